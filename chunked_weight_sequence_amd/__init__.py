@@ -9,6 +9,13 @@ library is missing or the tensors are not on the GPU, the call raises.
     O, W, loss = linear_minibatch(Q, K, V, minibatch=16, eta=0.1)  # TTT-Linear
     cache = surprisal_route(loss, K, V, chunk=64)                 # SR-TTT routing
     Vhat = lm_target(X0, conv_w, W_target, chunk=512)            # In-Place TTT target
+
+The attention half of a block, over a packed prompt and then token by token:
+
+    inv_freq, rope_scale = rope_frequencies(128, base=1e6)
+    q, k = qk_norm_rope(Q, K, pos, inv_freq, V=V, K_cache=Kc, V_cache=Vc, slots=slots)
+    O = attention_packed(q, k, V, cu_seqlens)
+    O = attention_decode(q, Kc, Vc, page_table, lengths, page_size=64)
 """
 from __future__ import annotations
 
@@ -19,17 +26,21 @@ __all__ = [
     "lib", "library_path", "TTTError", "abi_version", "status_string",
     "chunk_scan", "chunk_scan_workspace_bytes", "chunk_scan_profile",
     "linear_minibatch", "surprisal_route", "lm_target", "gated_z", "cache_readout", "chunk_scan_docs",
-    "chunk_scan_handover_timeouts", "scan_test_overrides", "chunk_scan_noalloc", "EXPORTED",
+    "chunk_scan_handover_timeouts", "scan_test_overrides", "chunk_scan_noalloc",
+    "rope_frequencies", "qk_norm_rope", "attention_packed", "attention_decode", "EXPORTED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libttt_mi355x.so")
 
 TTT_F32, TTT_BF16 = 0, 1
+ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 SCAN_PHASES = ("stage", "corr", "update", "apply")
 
 # name -> (restype, argtypes); mirrors include/ttt_mi355x.h
 _p, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_d, _ll = ctypes.c_double, ctypes.c_longlong
 _SCAN_ARGS = [_p, _p, _i, _p, _i, _p, _i, _p, _i, _i, _i, _i, _i, _f, _p, _sz, _p]
 EXPORTED = {
     "ttt_chunk_scan": (_i, _SCAN_ARGS),
@@ -50,6 +61,15 @@ EXPORTED = {
                                _p]),
     "ttt_chunk_scan_handover_timeouts": (_i, [_i, _i, _i, _i, _i, _i, _p, _sz, _p, _p]),
     "ttt_scan_test_overrides": (_i, [_i, _i, _i]),
+    "ttt_rope_frequencies": (_i, [_p, _i, _d, _i, _d, _i, _d, _d, _p]),
+    "ttt_qk_norm_rope": (_i, [_p, _ll, _p, _ll, _p, _ll, _i, _p, _p, _f, _p, _p, _i, _i, _f,
+                              _p, _ll, _p, _ll, _p, _p, _p, _ll, _i, _i, _i, _i, _p]),
+    "ttt_attention_packed": (_i, [_p, _ll, _p, _ll, _p, _ll, _i, _p, _ll, _p, _p, _p,
+                                  _i, _i, _i, _i, _i, _i, _f, _i, _p, _sz, _p]),
+    "ttt_attention_packed_workspace": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "ttt_attention_decode": (_i, [_p, _ll, _p, _p, _i, _p, _ll, _p, _p, _i, _i, _i, _p,
+                                  _i, _i, _i, _i, _f, _i, _p, _sz, _p]),
+    "ttt_attention_decode_workspace": (_sz, [_i, _i, _i, _i, _i, _i]),
     "ttt_status_string": (ctypes.c_char_p, [_i]),
     "ttt_abi_version": (_i, []),
 }
@@ -464,3 +484,207 @@ def cache_readout(Q, K, V, routed_mask, ttt_out, alpha, H: int, chunk: int, capa
         _ptr(_dev(out, "out")), _dtype_code(out), _ptr(alpha), B, T, H, dh, chunk, capacity,
         float(scale), _stream(Q)))
     return out
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = None,
+                     factor: float = 1.0, original_length: int = 0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device=None):
+    """Frequencies of a rotation of `rot` channels for qk_norm_rope: (inv_freq [rot / 2] float64 on
+    `device` (default: the current GPU), rope_scale). scaling: None, "linear", "ntk" or "yarn"
+    (which needs original_length, the context the model was trained with)."""
+    torch = _torch()
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, got {scaling!r}")
+    out = (ctypes.c_double * max(1, int(rot) // 2))()
+    scale = ctypes.c_float(1.0)
+    _check(lib().ttt_rope_frequencies(ctypes.addressof(out), int(rot), float(base),
+                                      ROPE_SCALINGS[scaling], float(factor), int(original_length),
+                                      float(beta_fast), float(beta_slow),
+                                      ctypes.addressof(scale)))
+    return (torch.tensor(list(out), dtype=torch.float64, device=device or "cuda"), scale.value)
+
+
+def _rows(t, name: str, heads=None, dh=None, dtype=None, device=None, n=None):
+    """Checks a [tokens, heads, dh] GPU tensor whose tokens may lie apart (a slice of one buffer);
+    returns its token stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dh], got {tuple(shape)}")
+    if (n is not None and shape[0] != n) or (heads is not None and shape[1] != heads) or \
+            (dh is not None and shape[2] != dh):
+        raise ValueError(f"{name} must be [{n}, {heads}, {dh}], got {tuple(shape)}")
+    if shape[0] >= 1 << 31:
+        raise ValueError(f"{name} has too many tokens: {shape[0]}")
+    if (shape[2] > 1 and stride[2] != 1) or (shape[1] > 1 and stride[1] != shape[2]):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _vec(t, name: str, shape, dtype, device):
+    """Checks a dense tensor of exactly this shape, dtype and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor on {device}, got "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _int_in(value, name: str, lo: int, hi: int) -> int:
+    """An argument that the C ABI takes as an int: refused where ctypes would cut it."""
+    if not lo <= value <= hi:
+        raise ValueError(f"{name} must lie in [{lo}, {hi}], got {value}")
+    return int(value)
+
+
+def _launch(fn, args, device):
+    """Calls fn(*args, stream) with `device` current and its current stream; checks the status."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if code != 0:
+        raise TTTError(status_string(code))
+
+
+def qk_norm_rope(Q, K, pos, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 layout: str = "half", rope_scale: float = 1.0, V=None, K_cache=None,
+                 V_cache=None, slots=None, Q_out=None, K_out=None):
+    """Per-head RMS norm (where a weight is given) and rotation of Q [N,Hq,dh] and K [N,Hkv,dh]
+    (bf16 or fp32; tokens may be slices of one buffer) at positions pos [N] int32. inv_freq
+    [rot / 2] float64 and rope_scale as from rope_frequencies; layout "half" or "interleaved".
+    With slots [N] int32, token t's rotated K row and its V row are also written to row slots[t] of
+    K_cache and V_cache [n_slots,Hkv,dh] (slots outside are skipped; the others must be distinct).
+    Q_out / K_out may be Q / K (in place). Returns (Q_out, K_out)."""
+    torch = _torch()
+    qs = _rows(Q, "Q")
+    N, Hq, dh = Q.shape
+    dt, dev = Q.dtype, Q.device
+    code = _dtype_code(dt)
+    ks = _rows(K, "K", None, dh, dt, dev, N)
+    Hkv = K.shape[1]
+    _vec(pos, "pos", (N,), torch.int32, dev)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    half = inv_freq.shape[0]
+    _vec(inv_freq, "inv_freq", (half,), torch.float64, dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _vec(w, name, (dh,), torch.float32, dev)
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {list(ROPE_LAYOUTS)}, got {layout!r}")
+    vs = n_slots = 0
+    if slots is not None:
+        if V is None or K_cache is None or V_cache is None:
+            raise ValueError("slots needs V, K_cache and V_cache")
+        _vec(slots, "slots", (N,), torch.int32, dev)
+        vs = _rows(V, "V", Hkv, dh, dt, dev, N)
+        n_slots = K_cache.shape[0]
+        _vec(K_cache, "K_cache", (n_slots, Hkv, dh), dt, dev)
+        _vec(V_cache, "V_cache", (n_slots, Hkv, dh), dt, dev)
+    elif V is not None or K_cache is not None or V_cache is not None:
+        raise ValueError("V, K_cache and V_cache are for a call with slots")
+    if Q_out is None:
+        Q_out = torch.empty((N, Hq, dh), dtype=dt, device=dev)
+    if K_out is None:
+        K_out = torch.empty((N, Hkv, dh), dtype=dt, device=dev)
+    qos = _rows(Q_out, "Q_out", Hq, dh, dt, dev, N)
+    kos = _rows(K_out, "K_out", Hkv, dh, dt, dev, N)
+    _launch(lib().ttt_qk_norm_rope,
+            (Q.data_ptr(), qs, K.data_ptr(), ks, _ptr(V), vs, code, _ptr(q_weight),
+             _ptr(k_weight), eps, pos.data_ptr(), inv_freq.data_ptr() if half else None, 2 * half,
+             ROPE_LAYOUTS[layout], rope_scale, Q_out.data_ptr(), qos, K_out.data_ptr(), kos,
+             _ptr(K_cache), _ptr(V_cache), _ptr(slots), n_slots, N, Hq, Hkv, dh), dev)
+    return Q_out, K_out
+
+
+def attention_packed(Q, K, V, cu_q, cu_k=None, *, scale=None, window: int = 0, O=None,
+                     with_lse: bool = False, lse=None, workspace=None):
+    """Causal attention over packed sequences. Q [Nq,Hq,dh], K and V [Nk,Hkv,dh] bf16 (tokens may
+    be slices of one buffer), dh 64 or 128, Hq a multiple of Hkv; cu_q, cu_k [n_seq + 1] int32
+    offsets on the GPU (cu_k None: the same as cu_q). A sequence's last query stands at its last
+    key; window > 0 limits every query to the last `window` keys up to its own. scale: 1 / sqrt(dh)
+    by default. Returns O [Nq,Hq,dh], with (with_lse, or lse given) lse [Nq,Hq] fp32 beside it."""
+    torch = _torch()
+    qs = _rows(Q, "Q")
+    Nq, Hq, dh = Q.shape
+    dt, dev = Q.dtype, Q.device
+    ks = _rows(K, "K", None, dh, dt, dev)
+    Nk, Hkv, _ = K.shape
+    vs = _rows(V, "V", Hkv, dh, dt, dev, Nk)
+    n_seq = cu_q.shape[0] - 1
+    _vec(cu_q, "cu_q", (n_seq + 1,), torch.int32, dev)
+    if cu_k is None:
+        cu_k = cu_q
+    else:
+        _vec(cu_k, "cu_k", (n_seq + 1,), torch.int32, dev)
+    if O is None:
+        O = torch.empty((Nq, Hq, dh), dtype=dt, device=dev)
+    os_ = _rows(O, "O", Hq, dh, dt, dev, Nq)
+    window = _int_in(window, "window", 0, 1 << 30)
+    if lse is not None:
+        _vec(lse, "lse", (Nq, Hq), torch.float32, dev)
+    elif with_lse:
+        lse = torch.empty((Nq, Hq), dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(workspace, lib().ttt_attention_packed_workspace(
+        n_seq, Nq, Nk, Hq, Hkv, dh), dev)
+    _launch(lib().ttt_attention_packed,
+            (Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs, _dtype_code(dt), O.data_ptr(),
+             os_, _ptr(lse), cu_q.data_ptr(), cu_k.data_ptr(), n_seq, Nq, Nk, Hq, Hkv, dh,
+             dh ** -0.5 if scale is None else scale, window, _ptr(ws), ws_bytes), dev)
+    return O if lse is None else (O, lse)
+
+
+def attention_decode(Q, K_cache, V_cache, page_table, lengths, page_size: int, *, scale=None,
+                     window: int = 0, O=None, with_lse: bool = False, lse=None, workspace=None):
+    """One-token attention over a paged cache. Q [S,Hq,dh] bf16; K_cache, V_cache
+    [n_slots,Hkv,dh] (rows of page p: p * page_size ..); page_table [S,max_pages] int32;
+    lengths [S] int32: cached tokens of each sequence, its query's own among them. Returns
+    O [S,Hq,dh], with (with_lse, or lse given) lse [S,Hq] fp32 beside it."""
+    torch = _torch()
+    qs = _rows(Q, "Q")
+    S, Hq, dh = Q.shape
+    dt, dev = Q.dtype, Q.device
+    n_slots, Hkv = K_cache.shape[0], K_cache.shape[1]
+    _vec(K_cache, "K_cache", (n_slots, Hkv, dh), dt, dev)
+    _vec(V_cache, "V_cache", (n_slots, Hkv, dh), dt, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seq, max_pages]")
+    max_pages = page_table.shape[1]
+    _vec(page_table, "page_table", (S, max_pages), torch.int32, dev)
+    _vec(lengths, "lengths", (S,), torch.int32, dev)
+    page_size = _int_in(page_size, "page_size", 1, 65536)
+    window = _int_in(window, "window", 0, 1 << 30)
+    if O is None:
+        O = torch.empty((S, Hq, dh), dtype=dt, device=dev)
+    os_ = _rows(O, "O", Hq, dh, dt, dev, S)
+    if lse is not None:
+        _vec(lse, "lse", (S, Hq), torch.float32, dev)
+    elif with_lse:
+        lse = torch.empty((S, Hq), dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(workspace, lib().ttt_attention_decode_workspace(
+        S, max_pages, page_size, Hq, Hkv, dh), dev)
+    _launch(lib().ttt_attention_decode,
+            (Q.data_ptr(), qs, K_cache.data_ptr(), V_cache.data_ptr(), _dtype_code(dt),
+             O.data_ptr(), os_, _ptr(lse), page_table.data_ptr(), max_pages, page_size,
+             n_slots // page_size, lengths.data_ptr(), S, Hq, Hkv, dh,
+             dh ** -0.5 if scale is None else scale, window, _ptr(ws), ws_bytes), dev)
+    return O if lse is None else (O, lse)
+
+
+def _workspace(given, need: int, device):
+    """The caller's workspace, or a new one of `need` bytes (None where nothing is needed)."""
+    if given is not None:
+        if not given.is_cuda or not given.is_contiguous() or given.device != device:
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return given, given.numel() * given.element_size()
+    if need == 0:
+        return None, 0
+    return _torch().empty(need, dtype=_torch().uint8, device=device), need

@@ -575,6 +575,238 @@ TTT_EXPORT ttt_status ttt_cache_readout(const void* Q, const void* K, const void
   return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
 }
 
+namespace {
+// Rows of `len` bytes, one every `stride` bytes.
+struct Rows {
+  const void* p;
+  size_t n, stride, len;
+};
+Range span(Rows r) { return {r.p, r.p && r.n ? (r.n - 1) * r.stride + r.len : 0}; }
+// Whether two sets of rows share a byte. Rows with one stride, such as column slices of one buffer, are
+// compared within a row; rows with different strides count as overlapping if their spans do.
+bool overlap(Rows a, Rows b) {
+  if (!overlap(span(a), span(b))) return false;
+  if (a.stride != b.stride || a.n == 1 || b.n == 1) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  const size_t s = a.stride, d = y >= x ? (y - x) % s : (s - (x - y) % s) % s;
+  return !(d >= a.len && d + b.len <= s);  // b's rows start d bytes into a's period
+}
+Rows whole(const void* p, size_t bytes) { return {p, size_t(p ? 1 : 0), bytes, bytes}; }
+
+bool stride_ok(long long s, long long heads_dh, size_t esz, long long most) {
+  return s >= heads_dh && s <= most && (size_t(s) * esz) % 16 == 0;
+}
+}  // namespace
+
+TTT_EXPORT ttt_status ttt_rope_frequencies(double* inv_freq, int rot, double base,
+                                           ttt_rope_scaling scaling, double factor,
+                                           int original_length, double beta_fast,
+                                           double beta_slow, float* rope_scale) {
+  if (!inv_freq) return TTT_E_NULL;
+  const int kind = int(scaling);
+  if (kind < TTT_ROPE_PLAIN || kind > TTT_ROPE_YARN) return TTT_E_SHAPE;
+  if (rot < 2 || rot > 256 || rot % 2 || !(base > 1.) || !std::isfinite(base) || !(factor >= 1.) ||
+      !std::isfinite(factor))
+    return TTT_E_SHAPE;
+  if (kind == TTT_ROPE_NTK && rot < 4) return TTT_E_SHAPE;
+  if (kind == TTT_ROPE_YARN && (original_length < 1 || !(beta_slow > 0.) ||
+                                !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
+    return TTT_E_SHAPE;
+  if (kind == TTT_ROPE_NTK) base *= std::pow(factor, double(rot) / (rot - 2));
+  // the (fractional) pair that turns n times in original_length positions
+  auto pair_of = [&](double n) {
+    return rot * std::log(original_length / (n * 6.283185307179586)) / (2. * std::log(base));
+  };
+  double low = 0., high = 0.;
+  if (kind == TTT_ROPE_YARN) {
+    low = std::fmax(std::floor(pair_of(beta_fast)), 0.);
+    high = std::fmin(std::ceil(pair_of(beta_slow)), rot - 1.);
+    if (high <= low) high = low + 1e-3;
+  }
+  for (int j = 0; j < rot / 2; ++j) {
+    const double f = std::pow(base, -2. * j / rot);
+    double share = kind == TTT_ROPE_LINEAR ? 1. : 0.;  // of the interpolated frequency
+    if (kind == TTT_ROPE_YARN) share = std::fmin(std::fmax((j - low) / (high - low), 0.), 1.);
+    inv_freq[j] = f * (1. - share) + f / factor * share;
+  }
+  if (rope_scale)
+    *rope_scale = kind == TTT_ROPE_YARN && factor > 1. ? float(0.1 * std::log(factor) + 1.) : 1.f;
+  return TTT_OK;
+}
+
+TTT_EXPORT ttt_status ttt_qk_norm_rope(const void* Q, long long q_stride, const void* K,
+                                       long long k_stride, const void* V, long long v_stride,
+                                       ttt_dtype dtype, const float* q_weight,
+                                       const float* k_weight, float eps, const int* pos,
+                                       const double* inv_freq, int rot, ttt_rope_layout layout,
+                                       float rope_scale, void* Q_out, long long qo_stride,
+                                       void* K_out, long long ko_stride, void* K_cache,
+                                       void* V_cache, const int* slots, long long n_slots, int N,
+                                       int Hq, int Hkv, int dh, hipStream_t stream) {
+  if (!valid_dtype(dtype)) return TTT_E_DTYPE;
+  if (!Q || !K || !pos || !Q_out || (rot > 0 && !inv_freq)) return TTT_E_NULL;
+  if (slots ? !V || !K_cache || !V_cache : !K_out) return TTT_E_NULL;
+  if (!slots && (V || K_cache || V_cache)) return TTT_E_NULL;
+  if (N < 1 || N > (1 << 26) || Hq < 1 || Hkv < 1 || Hq > (1 << 16) || Hkv > (1 << 16) ||
+      dh < 16 || dh > 256 || dh % 16 || rot < 0 || rot > dh || rot % 16 ||
+      (Hq + 2ll * Hkv) * dh > (1 << 20))
+    return TTT_E_SHAPE;
+  if ((layout != TTT_ROPE_HALF && layout != TTT_ROPE_INTERLEAVED) || !(eps >= 0.f) ||
+      !std::isfinite(eps) || !std::isfinite(rope_scale))
+    return TTT_E_SHAPE;
+  const size_t esz = dsize(dtype);
+  const long long most = 1ll << 31, wq = (long long)Hq * dh, wk = (long long)Hkv * dh;
+  if (!stride_ok(q_stride, wq, esz, most) || !stride_ok(k_stride, wk, esz, most) ||
+      !stride_ok(qo_stride, wq, esz, most) || (K_out && !stride_ok(ko_stride, wk, esz, most)) ||
+      (slots && !stride_ok(v_stride, wk, esz, most)))
+    return TTT_E_SHAPE;
+  if (slots && (n_slots < 1 || n_slots > 0x7FFFFFFFll)) return TTT_E_SHAPE;
+  for (const void* p : {Q, K, V, (const void*)q_weight, (const void*)k_weight, (const void*)pos,
+                        (const void*)inv_freq, (const void*)Q_out, (const void*)K_out,
+                        (const void*)K_cache, (const void*)V_cache, (const void*)slots})
+    if (!aligned16(p)) return TTT_E_ALIGN;
+  const size_t n = size_t(N);
+  const Rows rq{Q, n, size_t(q_stride) * esz, size_t(wq) * esz},
+      rk{K, n, size_t(k_stride) * esz, size_t(wk) * esz},
+      rv{V, slots ? n : 0, size_t(v_stride) * esz, size_t(wk) * esz},
+      oq{Q_out, n, size_t(qo_stride) * esz, size_t(wq) * esz},
+      ok{K_out, K_out ? n : 0, size_t(ko_stride) * esz, size_t(wk) * esz},
+      ck = whole(K_cache, slots ? size_t(n_slots) * wk * esz : 0),
+      cv = whole(V_cache, slots ? size_t(n_slots) * wk * esz : 0);
+  const Rows ins[] = {rq, rk, rv, whole(q_weight, size_t(dh) * 4), whole(k_weight, size_t(dh) * 4),
+                      whole(pos, n * 4), whole(inv_freq, size_t(rot) * 4),
+                      whole(slots, n * 4)};
+  const Rows outs[] = {oq, ok, ck, cv};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 8; ++i) {
+      // in place: the same rows, each head read by the lanes that write it
+      if (i == o && o < 2 && outs[o].p == ins[i].p && outs[o].stride == ins[i].stride) continue;
+      if (overlap(outs[o], ins[i])) return TTT_E_ALIAS;
+    }
+    for (int p = 0; p < o; ++p)
+      if (overlap(outs[o], outs[p])) return TTT_E_ALIAS;
+  }
+  ttt::NormRopeArgs a{Q, K, V, long(q_stride), long(k_stride), long(v_stride), dtype == TTT_BF16,
+                      q_weight, k_weight, eps, pos, inv_freq, rot, layout == TTT_ROPE_INTERLEAVED,
+                      rope_scale, Q_out, K_out, long(qo_stride), long(ko_stride), K_cache, V_cache,
+                      slots, long(n_slots), N, Hq, Hkv, dh, stream};
+  (void)hipGetLastError();
+  const hipError_t e = ttt::norm_rope(a);
+  return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
+}
+
+namespace {
+bool heads_ok(int Hq, int Hkv, int dh) {
+  return Hq >= 1 && Hkv >= 1 && Hq <= (1 << 16) && Hq % Hkv == 0 && dh >= 1 &&
+         (long long)Hq * dh <= (1 << 22);
+}
+bool packed_ok(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh) {
+  return heads_ok(Hq, Hkv, dh) && n_seq >= 1 && n_seq <= (1 << 20) && Nq >= 1 && Nk >= 1 &&
+         Nq <= (1 << 26) && Nk <= (1 << 26) && (long long)Nq * Hq < (1ll << 31);
+}
+bool decode_ok(int n_seq, int max_pages, int page, int Hq, int Hkv, int dh) {
+  return heads_ok(Hq, Hkv, dh) && n_seq >= 1 && n_seq <= (1 << 20) && max_pages >= 1 && page >= 1 &&
+         (long long)max_pages * page <= (1 << 30) && (long long)n_seq * Hq <= (1 << 26);
+}
+bool page_ok(int page) { return page >= 16 && page <= 65536 && (page & (page - 1)) == 0; }
+bool scale_ok(float s) { return s > 0.f && std::isfinite(s); }
+}  // namespace
+
+TTT_EXPORT size_t ttt_attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh) {
+  if (!packed_ok(n_seq, Nq, Nk, Hq, Hkv, dh) || (dh != 64 && dh != 128)) return 0;
+  return ttt::attention_packed_workspace(n_seq, Nq, Nk, Hq, Hkv, dh);
+}
+
+TTT_EXPORT ttt_status ttt_attention_packed(const void* Q, long long q_stride, const void* K,
+                                           long long k_stride, const void* V, long long v_stride,
+                                           ttt_dtype dtype, void* O, long long o_stride,
+                                           float* lse, const int* cu_q, const int* cu_k, int n_seq,
+                                           int Nq, int Nk, int Hq, int Hkv, int dh, float scale,
+                                           int window, void* workspace, size_t workspace_bytes,
+                                           hipStream_t stream) {
+  if (!valid_dtype(dtype)) return TTT_E_DTYPE;
+  if (!Q || !K || !V || !O || !cu_q || !cu_k) return TTT_E_NULL;
+  if (!packed_ok(n_seq, Nq, Nk, Hq, Hkv, dh) || window < 0 || window > (1 << 30) || !scale_ok(scale))
+    return TTT_E_SHAPE;
+  if (dtype != TTT_BF16 || (dh != 64 && dh != 128)) return TTT_E_UNSUPPORTED;
+  const long long most = 1 << 23, wq = (long long)Hq * dh, wk = (long long)Hkv * dh;
+  if (!stride_ok(q_stride, wq, 2, most) || !stride_ok(k_stride, wk, 2, most) ||
+      !stride_ok(v_stride, wk, 2, most) || !stride_ok(o_stride, wq, 2, most))
+    return TTT_E_SHAPE;
+  for (const void* p : {Q, K, V, (const void*)O, (const void*)lse, (const void*)cu_q,
+                        (const void*)cu_k, (const void*)workspace})
+    if (!aligned16(p)) return TTT_E_ALIGN;
+  const size_t need = ttt::attention_packed_workspace(n_seq, Nq, Nk, Hq, Hkv, dh);
+  if (need && (!workspace || workspace_bytes < need)) return TTT_E_WORKSPACE;
+  const size_t nq = size_t(Nq), nk = size_t(Nk);
+  const Rows ins[] = {{Q, nq, size_t(q_stride) * 2, size_t(wq) * 2},
+                      {K, nk, size_t(k_stride) * 2, size_t(wk) * 2},
+                      {V, nk, size_t(v_stride) * 2, size_t(wk) * 2},
+                      whole(cu_q, size_t(n_seq + 1) * 4), whole(cu_k, size_t(n_seq + 1) * 4)};
+  const Rows outs[] = {{O, nq, size_t(o_stride) * 2, size_t(wq) * 2},
+                       whole(lse, nq * Hq * 4), whole(need ? workspace : nullptr, need)};
+  for (int o = 0; o < 3; ++o) {
+    for (const Rows& i : ins)
+      if (overlap(outs[o], i)) return TTT_E_ALIAS;
+    for (int p = 0; p < o; ++p)
+      if (overlap(outs[o], outs[p])) return TTT_E_ALIAS;
+  }
+  ttt::PackedArgs a{Q, K, V, long(q_stride), long(k_stride), long(v_stride), O, long(o_stride), lse,
+                    cu_q, cu_k, n_seq, Nq, Nk, Hq, Hkv, dh, scale, window, workspace, stream};
+  (void)hipGetLastError();
+  const hipError_t e = ttt::attention_packed(a);
+  return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
+}
+
+TTT_EXPORT size_t ttt_attention_decode_workspace(int n_seq, int max_pages, int page_size, int Hq,
+                                                 int Hkv, int dh) {
+  if (!decode_ok(n_seq, max_pages, page_size, Hq, Hkv, dh) || !page_ok(page_size) ||
+      (dh != 64 && dh != 128))
+    return 0;
+  return ttt::attention_decode_workspace(n_seq, max_pages, page_size, Hq, Hkv, dh);
+}
+
+TTT_EXPORT ttt_status ttt_attention_decode(const void* Q, long long q_stride, const void* K_cache,
+                                           const void* V_cache, ttt_dtype dtype, void* O,
+                                           long long o_stride, float* lse, const int* page_table,
+                                           int max_pages, int page_size, int n_pages,
+                                           const int* lengths, int n_seq, int Hq, int Hkv, int dh,
+                                           float scale, int window, void* workspace,
+                                           size_t workspace_bytes, hipStream_t stream) {
+  if (!valid_dtype(dtype)) return TTT_E_DTYPE;
+  if (!Q || !K_cache || !V_cache || !O || !page_table || !lengths) return TTT_E_NULL;
+  if (!decode_ok(n_seq, max_pages, page_size, Hq, Hkv, dh) || n_pages < 1 ||
+      (long long)n_pages * page_size > (1ll << 36) || window < 0 || window > (1 << 30) || !scale_ok(scale))
+    return TTT_E_SHAPE;
+  if (dtype != TTT_BF16 || (dh != 64 && dh != 128) || !page_ok(page_size)) return TTT_E_UNSUPPORTED;
+  const long long most = 1 << 23, wq = (long long)Hq * dh;
+  if (!stride_ok(q_stride, wq, 2, most) || !stride_ok(o_stride, wq, 2, most)) return TTT_E_SHAPE;
+  for (const void* p : {Q, K_cache, V_cache, (const void*)O, (const void*)lse,
+                        (const void*)page_table, (const void*)lengths, (const void*)workspace})
+    if (!aligned16(p)) return TTT_E_ALIGN;
+  const size_t need =
+      ttt::attention_decode_workspace(n_seq, max_pages, page_size, Hq, Hkv, dh);
+  if (need && (!workspace || workspace_bytes < need)) return TTT_E_WORKSPACE;
+  const size_t ns = size_t(n_seq), cache = size_t(n_pages) * page_size * Hkv * dh * 2;
+  const Rows ins[] = {{Q, ns, size_t(q_stride) * 2, size_t(wq) * 2}, whole(K_cache, cache),
+                      whole(V_cache, cache), whole(page_table, ns * max_pages * 4),
+                      whole(lengths, ns * 4)};
+  const Rows outs[] = {{O, ns, size_t(o_stride) * 2, size_t(wq) * 2},
+                       whole(lse, ns * Hq * 4), whole(need ? workspace : nullptr, need)};
+  for (int o = 0; o < 3; ++o) {
+    for (const Rows& i : ins)
+      if (overlap(outs[o], i)) return TTT_E_ALIAS;
+    for (int p = 0; p < o; ++p)
+      if (overlap(outs[o], outs[p])) return TTT_E_ALIAS;
+  }
+  ttt::DecodeArgs a{Q, long(q_stride), K_cache, V_cache, O, long(o_stride), lse, page_table,
+                    lengths, max_pages, page_size, n_pages, n_seq, Hq, Hkv, dh, scale, window,
+                    workspace, stream};
+  (void)hipGetLastError();
+  const hipError_t e = ttt::attention_decode(a);
+  return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
+}
+
 TTT_EXPORT const char* ttt_status_string(ttt_status s) {
   switch (s) {
     case TTT_OK: return "TTT_OK: success";

@@ -1,0 +1,97 @@
+// Device pieces shared by the attention kernels (attention.hip, decode.hip).
+//
+// A wave works on 32-row blocks of keys against 32 queries per block of columns:
+//     S^T = K Q^T    v_mfma_f32_32x32x16_bf16, keys as the A operand (from LDS), queries as B
+//                    (registers): lane l then holds query l % 32 and keys 8 (j / 4) + 4 (l / 32) + j % 4
+//     O^T += V^T P^T the same instruction: the exponentials of a lane, rounded to bf16 in pairs,
+//                    are the B operand as they stand if the 16 keys of a product are taken in the
+//                    order 8 (e / 4) + 4 (l / 32) + e % 4, e = 0..7; the V^T fragments are formed
+//                    in that order by transposing LDS reads. P never leaves the registers.
+// The softmax statistics of a query are in lanes l and l + 32, its output column in the same
+// lanes: a maximum needs one exchange between the halves, a rescale is a per-lane factor.
+//
+// LDS tiles are rows of dh bf16 in 16-byte chunks, filled by direct copies (64 lanes x 16 bytes in
+// a row), so rows are not padded; chunk c of row r sits at slot c ^ ksw(r) (K) or c ^ vsw(r) (V),
+// which spreads the 8 lanes of a 16-byte read pass, and the 32 lanes of a transposing one, over
+// all banks.
+#pragma once
+#include "common.hpp"
+#include "dma.hpp"
+
+namespace ttt {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int DH>
+__device__ __forceinline__ constexpr int ksw(int r) { return r & 7; }
+template <int DH>
+__device__ __forceinline__ constexpr int vsw(int r) { return DH == 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1); }
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+__device__ __forceinline__ uint2 tr_read(const char* p) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p));
+}
+
+// Value of the lane 32 away.
+__device__ __forceinline__ float other_half(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  // r[0]: the low half's values in both halves; r[1]: the high half's
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Byte offsets, inside a tile, of a lane's K and V^T fragments.
+template <int DH>
+struct FragOff {
+  static constexpr int kN = 4, vN = DH / 32;
+  uint32_t k[kN], v[vN];
+  __device__ __forceinline__ explicit FragOff(int lane) {
+    const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      k[i] = uint32_t(r * DH * 2 + (((2 * i + h) ^ ksw<DH>(r)) << 4));
+    const int vr = 4 * h + ((lane & 15) >> 2);
+    const int c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+#pragma unroll
+    for (int i = 0; i < vN; ++i)
+      v[i] = uint32_t(vr * DH * 2 + (((4 * i + c) ^ vsw<DH>(vr)) << 4) + 8 * (lane & 1));
+  }
+  // K fragment of 32-row block kb, contraction step ks (channels 16 ks ..)
+  __device__ __forceinline__ uint4 key(const char* tile, int kb, int ks) const {
+    return *reinterpret_cast<const uint4*>(tile + k[ks & 3] + kb * 32 * DH * 2 + (ks >> 2) * 128);
+  }
+  // V^T fragment of channels 32 dt .., the 16 keys 16 s ..
+  __device__ __forceinline__ uint4 value(const char* tile, int s, int dt) const {
+    const uint2 lo = tr_read(tile + v[dt] + s * 16 * DH * 2);
+    const uint2 hi = tr_read(tile + v[dt] + (s * 16 + 8) * DH * 2);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+};
+
+// The wave's share of copying `ROWS` rows of K or V into LDS: NW waves, copy i of wave w fills
+// 1 KB at (i * NW + w) KB.
+template <int DH, int ROWS, int NW, bool IS_V>
+struct TileCopy {
+  static constexpr int RPI = 1024 / (DH * 2);        // rows per copy instruction
+  static constexpr int N = ROWS / RPI / NW;          // instructions per wave
+  __device__ __forceinline__ static int row(int i, int wave, int lane) {
+    return (i * NW + wave) * RPI + lane / (64 / RPI);
+  }
+  __device__ __forceinline__ static uint32_t chunk(int i, int wave, int lane) {
+    const int r = row(i, wave, lane), p = lane % (64 / RPI);
+    return uint32_t(p ^ (IS_V ? vsw<DH>(r) : ksw<DH>(r))) << 4;
+  }
+};
+
+}  // namespace ttt

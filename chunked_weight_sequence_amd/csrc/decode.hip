@@ -1,0 +1,311 @@
+// One-token attention over a paged cache, grouped heads, bf16, and the joining of partial
+// results that a split over the keys leaves (also used by attention.hip).
+//
+// Sequence s holds n = lengths[s] tokens; token j is row table[s][j / page] * page + j % page of
+// the caches [n_pages * page][Hkv][dh]. Its query sees the last `window` of them (all without a
+// window): o = sum_j softmax_j(scale q . k_j) v_j, lse = log sum_j exp(scale q . k_j); o = 0 and
+// lse = -inf where nothing is visible. Tokens of a page outside [0, n_pages) are left out.
+//
+// Bound by HBM: every visible K and V row is read once. A workgroup takes a piece of one
+// sequence and one key head, with up to 32 of the query heads that share it as the columns of
+// S^T (attn.hpp); its 4 waves walk 32-key tiles independently, each through its own two-stage LDS
+// ring of direct copies (no barrier in the loop), and join their sums through LDS at the end.
+// Copies are whole rows, so each instruction reads 1 KB in full lines. Rows that are masked
+// (behind the last token, before the window) are replaced by a visible row of the tile in the
+// copy itself: what lies in them, NaN included, never enters a product.
+#include "attn.hpp"
+#include "launch.hpp"
+
+namespace ttt {
+namespace {
+
+constexpr int DC_BN = 32, DC_MAX_SPLITS = 64;
+
+// a row of zeros: what stands for the tokens of a page that does not exist
+__device__ const uint4 dc_zeros[16] = {};
+
+struct DecodeDev {
+  const uint16_t* Q;
+  long qs;
+  const char *Kc, *Vc;
+  uint16_t* O;
+  long os;
+  float* lse;
+  const int *table, *lengths;
+  int max_pages, psh, n_pages;
+  int n_seq, Hq, Hkv, G;
+  float scale;
+  int window;
+  int splits;
+  float* part;
+};
+
+// The page table through the scalar cache: a vector load in the key loop would make the compiler
+// wait for every copy in flight, since the vector-memory counter counts them together.
+typedef const __attribute__((address_space(4))) int const_int;
+
+template <int DH>
+__global__ __launch_bounds__(256, 1) void k_attention_decode(DecodeDev a) {
+  constexpr int TILE = DC_BN * DH * 2, KS = DH / 16, DT = DH / 32, RPI = 1024 / (DH * 2);
+  constexpr int NI = 16 / RPI;  // copies per 16-token half of a tile
+  __shared__ __align__(1024) char sm[4][2][2][TILE];  // wave, stage, K / V
+  __shared__ float2 ml_s[4][32];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int h = lane >> 5, col = lane & 31;
+  int id = blockIdx.x;
+  const int kvh = id % a.Hkv;
+  id /= a.Hkv;
+  const int split = id % a.splits;
+  id /= a.splits;
+  const int seq = id % a.n_seq, g0 = (id / a.n_seq) * 32;
+  const int gn = min(a.G - g0, 32);
+
+  const int psh = a.psh;
+  const long cap = long(a.max_pages) << psh;
+  const int n = int(min(long(max(a.lengths[seq], 0)), cap));
+  const int first = a.window > 0 ? max(0, n - a.window) : 0;
+  int t0 = first / DC_BN, t1 = n > first ? (n + DC_BN - 1) / DC_BN : t0;
+  {
+    const int per = (t1 - t0 + a.splits - 1) / a.splits;
+    t0 = min(t0 + split * per, t1);
+    t1 = min(t0 + per, t1);
+  }
+  uint4 qf[KS];
+  {
+    const uint16_t* p = a.Q + long(seq) * a.qs + (kvh * a.G + g0 + min(col, gn - 1)) * DH + 8 * h;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const uint4*>(p + 16 * s);
+  }
+  const_int* table =
+      (const_int*)(reinterpret_cast<uintptr_t>(a.table) + size_t(seq) * a.max_pages * 4);
+  const uint32_t rowb = uint32_t(a.Hkv) * DH * 2;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32(&sm[wave][0][0][0]));
+  const int lrow = lane / (64 / RPI), lchunk = lane % (64 / RPI);
+  // Copies tile t into a stage; returns which 16-token halves exist (bit 0, bit 1).
+  auto issue = [&](int t, int stage) {
+    int good = 0;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int f = t * DC_BN + 16 * hf;
+      int lo = max(f, first), hi = min(f + 15, n - 1);
+      if (lo > hi) lo = hi = min(max(f, first), n - 1);
+      const int page = table[__builtin_amdgcn_readfirstlane(lo >> psh)];
+      const bool ok = page >= 0 && page < a.n_pages;
+      good |= int(ok) << hf;
+      // row of token `lo`; page size is a power of two of at least 16, so a half is in one page
+      const long row = ok ? (long(page) << psh) + (lo & ((1 << psh) - 1)) : 0;
+      const long at = row * rowb + kvh * DH * 2;
+      const char* kb = ok ? a.Kc + at : reinterpret_cast<const char*>(dc_zeros);
+      const char* vb = ok ? a.Vc + at : reinterpret_cast<const char*>(dc_zeros);
+      const uint32_t rb = ok ? rowb : 0;
+      const uint32_t dst = lds0 + stage * 2 * TILE + hf * (TILE / 2);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = 16 * hf + i * RPI + lrow;  // row of the tile
+        const uint32_t o = uint32_t(min(max(t * DC_BN + r, lo), hi) - lo) * rb;
+        dma16(o + uint32_t((lchunk ^ ksw<DH>(r)) << 4), kb, dst + i * 1024);
+        dma16(o + uint32_t((lchunk ^ vsw<DH>(r)) << 4), vb, dst + TILE + i * 1024);
+      }
+    }
+    return good;
+  };
+
+  const FragOff<DH> fo(lane);
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  const float c = a.scale * kLog2e;
+
+  int good = 0, t = t0 + wave, stage = 0;
+  if (t < t1) good = issue(t, 0);
+  for (; t < t1; t += 4, stage ^= 1) {
+    int good_next = 0;
+    // this tile's stage was read two rounds ago: those reads are done before it is refilled
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (t + 4 < t1) {
+      good_next = issue(t + 4, stage ^ 1);
+      wait_vm<4 * NI>();
+    } else {
+      wait_vm<0>();
+    }
+    const char* kt = &sm[wave][stage][0][0];
+    const char* vt = &sm[wave][stage][1][0];
+    f32x16 s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) s = mfma32x32x16(fo.key(kt, 0, ks), qf[ks], s);
+    const int j0 = t * DC_BN;
+    if (good != 3 || j0 < first || j0 + DC_BN > n) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = j0 + 8 * (i / 4) + 4 * h + (i & 3);
+        if (j < first || j >= n || !((good >> (i / 8)) & 1)) s[i] = -INFINITY;
+      }
+    }
+    float mx = m;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i]);
+    mx = max_halves(mx);
+    const float base = mx == -INFINITY ? 0.f : mx * c;
+    const float al = exp2_fast(fmaf(m, c, -base));
+    float p[16], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      p[i] = exp2_fast(fmaf(s[i], c, -base));
+      sum += p[i];
+    }
+    l = l * al + sum;
+    m = mx;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] *= al;
+#pragma unroll
+    for (int s2 = 0; s2 < 2; ++s2) {
+      const uint4 pf = make_uint4(pack2bf(p[8 * s2], p[8 * s2 + 1]), pack2bf(p[8 * s2 + 2], p[8 * s2 + 3]),
+                                  pack2bf(p[8 * s2 + 4], p[8 * s2 + 5]), pack2bf(p[8 * s2 + 6], p[8 * s2 + 7]));
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] = mfma32x32x16(fo.value(vt, s2, d), pf, o[d]);
+    }
+    good = good_next;
+  }
+
+  // join the four waves: [wave][column][channel] fp32 in the ring that no copy fills any more
+  l = sum_halves(l);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __syncthreads();
+  float* js = reinterpret_cast<float*>(&sm[0][0][0][0]);
+  if (col < gn) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<float4*>(js + (wave * 32 + col) * DH + 32 * d + 2 * i + 4 * h) =
+            make_float4(o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]);
+    if (h == 0) ml_s[wave][col] = make_float2(m, l);
+  }
+  __syncthreads();
+  const long nrows = long(a.n_seq) * a.Hq;
+  for (int e = tid; e < gn * (DH / 4); e += 256) {
+    const int g = e / (DH / 4), d4 = e % (DH / 4) * 4;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mx = fmaxf(mx, ml_s[w][g].x);
+    const float base = mx == -INFINITY ? 0.f : mx * c;
+    float lt = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 x = ml_s[w][g];
+      const float f = exp2_fast(fmaf(x.x, c, -base));
+      const float4 v = *reinterpret_cast<const float4*>(js + (w * 32 + g) * DH + d4);
+      lt = fmaf(f, x.y, lt);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    const int hq = kvh * a.G + g0 + g;
+    const long rr = long(seq) * a.Hq + hq;
+    if (a.splits > 1) {
+      *reinterpret_cast<float4*>(a.part + (split * nrows + rr) * DH + d4) = acc;
+      if (d4 == 0)
+        *reinterpret_cast<float2*>(a.part + a.splits * nrows * DH + (split * nrows + rr) * 2) =
+            make_float2(mx, lt);
+    } else {
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      *reinterpret_cast<uint2*>(a.O + long(seq) * a.os + hq * DH + d4) =
+          make_uint2(pack2bf(acc.x * inv, acc.y * inv), pack2bf(acc.z * inv, acc.w * inv));
+      if (a.lse && d4 == 0) a.lse[rr] = lt == 0.f ? -INFINITY : mx * a.scale + __logf(lt);
+    }
+  }
+}
+
+// Joins the `splits` partial sums of each row (token, head); one wave per row. Fixed order, so the
+// same inputs give the same bits.
+template <int DH>
+__global__ __launch_bounds__(256) void k_attention_join(const float* part, int splits, long nrows,
+                                                        int Hq, uint16_t* O, long os, float* lse,
+                                                        float scale) {
+  const int lane = threadIdx.x & 63;
+  const long rr = long(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (rr >= nrows) return;
+  const float c = scale * kLog2e;
+  float2 x = make_float2(-INFINITY, 0.f);
+  if (lane < splits)
+    x = *reinterpret_cast<const float2*>(part + splits * nrows * DH + (lane * nrows + rr) * 2);
+  float mx = x.x;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) mx = fmaxf(mx, __shfl_xor(mx, d));
+  const float base = mx == -INFINITY ? 0.f : mx * c;
+  const float f = exp2_fast(fmaf(x.x, c, -base));
+  float lt = f * x.y;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) lt += __shfl_xor(lt, d);
+  constexpr int E = DH / 64;
+  float acc[E] = {};
+  const float* p = part + rr * DH + lane * E;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float w = __shfl(f, s);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, p[s * nrows * DH + e], acc[e]);
+  }
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  uint16_t* out = O + (rr / Hq) * os + (rr % Hq) * DH + lane * E;
+  if constexpr (E == 2)
+    *reinterpret_cast<uint32_t*>(out) = pack2bf(acc[0] * inv, acc[1] * inv);
+  else
+    out[0] = f2bf(acc[0] * inv);
+  if (lse && lane == 0) lse[rr] = lt == 0.f ? -INFINITY : mx * scale + __logf(lt);
+}
+
+int decode_splits(int n_seq, int max_pages, int page, int Hkv, int G) {
+  const long wgs = long(n_seq) * Hkv * ((G + 31) / 32);
+  const long want = (1024 + wgs - 1) / wgs, most = (long(max_pages) * page + 127) / 128;
+  const long n = want < most ? want : most;
+  return int(n < 1 ? 1 : n > DC_MAX_SPLITS ? DC_MAX_SPLITS : n);
+}
+
+}  // namespace
+
+hipError_t attention_join(const float* part, int splits, long nrows, int Hq, int dh, void* O, long os,
+                          float* lse, float scale, hipStream_t stream) {
+  const dim3 grid(unsigned((nrows + 3) / 4));
+  if (dh == 128)
+    hipLaunchKernelGGL((k_attention_join<128>), grid, dim3(256), 0, stream, part, splits, nrows, Hq,
+                       static_cast<uint16_t*>(O), os, lse, scale);
+  else
+    hipLaunchKernelGGL((k_attention_join<64>), grid, dim3(256), 0, stream, part, splits, nrows, Hq,
+                       static_cast<uint16_t*>(O), os, lse, scale);
+  return hipGetLastError();
+}
+
+size_t attention_decode_workspace(int n_seq, int max_pages, int page, int Hq, int Hkv, int dh) {
+  const int ns = decode_splits(n_seq, max_pages, page, Hkv, Hq / Hkv);
+  return ns > 1 ? size_t(ns) * n_seq * Hq * (dh + 2) * 4 : 0;
+}
+
+hipError_t attention_decode(const DecodeArgs& a) {
+  const int G = a.Hq / a.Hkv;
+  DecodeDev d{static_cast<const uint16_t*>(a.Q), a.qs, static_cast<const char*>(a.Kc),
+              static_cast<const char*>(a.Vc), static_cast<uint16_t*>(a.O), a.os, a.lse, a.table,
+              a.lengths, a.max_pages, __builtin_ctz(unsigned(a.page)), a.n_pages, a.n_seq, a.Hq,
+              a.Hkv, G, a.scale, a.window,
+              decode_splits(a.n_seq, a.max_pages, a.page, a.Hkv, G), static_cast<float*>(a.ws)};
+  const dim3 grid(unsigned(a.Hkv) * d.splits * a.n_seq * ((G + 31) / 32));
+  if (a.dh == 128)
+    hipLaunchKernelGGL((k_attention_decode<128>), grid, dim3(256), 0, a.stream, d);
+  else
+    hipLaunchKernelGGL((k_attention_decode<64>), grid, dim3(256), 0, a.stream, d);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || d.splits == 1) return e;
+  return attention_join(d.part, d.splits, long(a.n_seq) * a.Hq, a.Hq, a.dh, a.O, a.os, a.lse,
+                        a.scale, a.stream);
+}
+
+}  // namespace ttt

@@ -199,4 +199,68 @@ struct ClipArgs {
 size_t clip_workspace(int B, int T, int D, int C, bool in_bf16);
 hipError_t clip_targets(const ClipArgs& a);
 
+// Per-head norm and rotation of queries and keys, with the cache write. Strides in elements.
+struct NormRopeArgs {
+  const void *Q, *K, *V;         // token t's heads at + t * stride
+  long qs, ks, vs;
+  bool bf16;
+  const float *qw, *kw;          // [dh] or null (no norm)
+  float eps;
+  const int* pos;                // [N]
+  const double* inv_freq;        // [rot / 2]
+  int rot;
+  bool interleaved;
+  float rope_scale;
+  void *Qo, *Ko;                 // Ko may be null
+  long qos, kos;
+  void *Kc, *Vc;                 // [n_slots, Hkv, dh] or null
+  const int* slots;              // [N] or null
+  long n_slots;
+  int N, Hq, Hkv, dh;
+  hipStream_t stream;
+};
+hipError_t norm_rope(const NormRopeArgs& a);
+
+// Causal attention over packed sequences, grouped heads.
+struct PackedArgs {
+  const void *Q, *K, *V;         // token t's heads at + t * stride, bf16
+  long qs, ks, vs;
+  void* O;
+  long os;
+  float* lse;                    // [Nq, Hq] or null
+  const int *cu_q, *cu_k;        // [n_seq + 1]
+  int n_seq, Nq, Nk, Hq, Hkv, dh;
+  float scale;
+  int window;                    // 0: all earlier keys
+  void* ws;
+  hipStream_t stream;
+};
+size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh);
+hipError_t attention_packed(const PackedArgs& a);
+
+// Joins `splits` (<= 64) partial results of nrows = tokens * Hq rows: part holds unnormalised fp32
+// sums [splits][nrows][dh], then (maximum logit, sum) [splits][nrows][2] (decode.hip).
+hipError_t attention_join(const float* part, int splits, long nrows, int Hq, int dh, void* O, long os,
+                          float* lse, float scale, hipStream_t stream);
+
+// One query per sequence over a paged cache.
+struct DecodeArgs {
+  const void* Q;                 // sequence s's heads at + s * qs, bf16
+  long qs;
+  const void *Kc, *Vc;           // [n_pages * page, Hkv, dh]
+  void* O;
+  long os;
+  float* lse;                    // [n_seq, Hq] or null
+  const int* table;              // [n_seq, max_pages]
+  const int* lengths;            // [n_seq]
+  int max_pages, page, n_pages;
+  int n_seq, Hq, Hkv, dh;
+  float scale;
+  int window;
+  void* ws;
+  hipStream_t stream;
+};
+size_t attention_decode_workspace(int n_seq, int max_pages, int page, int Hq, int Hkv, int dh);
+hipError_t attention_decode(const DecodeArgs& a);
+
 }  // namespace ttt

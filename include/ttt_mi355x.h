@@ -16,11 +16,14 @@
  *
  * and the steps next to them on the path, declared further down: ttt_chunk_scan_docs (document
  * resets and update clipping), ttt_lm_target (the LM-aligned target), ttt_gated_z (the scan's
- * input Z) and ttt_cache_readout (the residual-cache readout).
+ * input Z) and ttt_cache_readout (the residual-cache readout); and the attention half of the
+ * blocks whose MLP half the scan is: ttt_qk_norm_rope, ttt_attention_packed and
+ * ttt_attention_decode.
  *
  * Conventions shared by every entry point:
  *   - Tensor pointers are DEVICE pointers owned by the caller; the library never allocates,
- *     frees or keeps them. Tensors are dense, row-major, with the stated shapes.
+ *     frees or keeps them. Tensors are dense, row-major, with the stated shapes; where a call
+ *     takes a stride, only consecutive tokens may lie further apart (slices of one buffer).
  *   - Every pointer must be 16-byte aligned (TTT_E_ALIGN otherwise).
  *   - Arguments are validated on the host before anything is enqueued. On any status other than
  *     TTT_OK nothing has been launched and no output has been written.
@@ -43,7 +46,7 @@
 extern "C" {
 #endif
 
-#define TTT_ABI_VERSION 7
+#define TTT_ABI_VERSION 8
 
 typedef enum {
   TTT_OK = 0,
@@ -357,6 +360,124 @@ ttt_status ttt_cache_readout(const void* Q, const void* K, const void* V, ttt_dt
                              const unsigned char* routed_mask, const void* ttt_out, void* out,
                              ttt_dtype out_dtype, const float* alpha, int B, int T, int H,
                              int dh, int chunk, int capacity, float scale, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* The attention half of a block: In-Place TTT keeps full or sliding-window attention beside the
+ * fast weights ("In-Place Test-Time Training", iplexlaw.co.kr blog on arXiv 2604.06169, sections
+ * 3 and 7). Three calls, used in this order: queries and keys are normalised and rotated and the
+ * cache is written (ttt_qk_norm_rope); a packed prompt attends to itself, or to its earlier part
+ * too (ttt_attention_packed); later tokens attend one at a time to the paged cache
+ * (ttt_attention_decode).
+ *
+ * A cache is a pair of arrays [n_slots, Hkv, dh]; slot s belongs to page s / page_size. */
+
+/* Frequencies of the rotation, on the HOST (no device work): inv_freq[j], j < rot / 2, in radians
+ * per position (the angle of pair j at position p is p * inv_freq[j]).
+ *   TTT_ROPE_PLAIN   base^(-2j / rot)
+ *   TTT_ROPE_LINEAR  the same / factor (positions interpolated)
+ *   TTT_ROPE_NTK     the same with base * factor^(rot / (rot - 2))
+ *   TTT_ROPE_YARN    the plain one for pairs that turn more than beta_fast times in
+ *                    original_length positions, the linear one for those that turn less than
+ *                    beta_slow times, a linear ramp over the pair index in between; and
+ *                    *rope_scale = 0.1 ln(factor) + 1 (1 for the others and for factor <= 1)
+ *   inv_freq   host double[rot / 2]; rope_scale: host float or NULL
+ *   rot: even, 2 .. 256 (TTT_ROPE_NTK: at least 4); base > 1; factor >= 1; for TTT_ROPE_YARN
+ *   original_length >= 1 and 0 < beta_slow < beta_fast (all else TTT_E_SHAPE). */
+typedef enum {
+  TTT_ROPE_PLAIN = 0, TTT_ROPE_LINEAR = 1, TTT_ROPE_NTK = 2, TTT_ROPE_YARN = 3
+} ttt_rope_scaling;
+ttt_status ttt_rope_frequencies(double* inv_freq, int rot, double base, ttt_rope_scaling scaling,
+                                double factor, int original_length, double beta_fast,
+                                double beta_slow, float* rope_scale);
+
+/* Per-head RMS norm and rotation of queries and keys in one pass, with the cache write. For token
+ * t and every head x [dh] of Q and of K:
+ *     y = x * rsqrt(mean(x^2) + eps) * w           (only where the weight w is given; else y = x)
+ *     (a, b) -> rope_scale * (a cos - b sin, a sin + b cos)   at the angle pos[t] * inv_freq[j]
+ * for pair j of the head's first `rot` channels: channels (j, j + rot/2) in TTT_ROPE_HALF,
+ * (2j, 2j + 1) in TTT_ROPE_INTERLEAVED. Channels from rot on keep y. fp32 arithmetic (the angle's
+ * reduction in fp64), rounded once to dtype.
+ *   Q      [N, Hq, dh], K [N, Hkv, dh]; dtype TTT_F32 or TTT_BF16; token t at + t * stride
+ *   V      [N, Hkv, dh], with slots only
+ *   q_weight, k_weight  [dh] fp32, either may be NULL
+ *   pos    [N] int32, any values; inv_freq [rot / 2] fp64 on the DEVICE (may be NULL if rot = 0)
+ *   Q_out  [N, Hq, dh], K_out [N, Hkv, dh] (K_out may be NULL with slots)
+ *   slots  [N] int32 or NULL. Token t's rotated K row and its V row (copied bit for bit) go to
+ *          rows slots[t] of K_cache and V_cache [n_slots, Hkv, dh]; a slot outside
+ *          [0, n_slots) writes nothing (padding). The slots inside have to be distinct: of two
+ *          tokens with the same slot either's values may remain, piece by piece.
+ *          V, K_cache and V_cache are required with slots and must be NULL without.
+ *   Strides are in elements: at least heads * dh, multiples of 16 bytes, at most 2^31.
+ *   dh: a multiple of 16 up to 256; rot: a multiple of 16, 0 .. dh; N <= 2^26;
+ *   (Hq + 2 Hkv) * dh <= 2^20; eps >= 0 and rope_scale finite (else TTT_E_SHAPE).
+ *   In place: Q_out may be Q and K_out may be K with the same strides. Any other overlap of an
+ *   output with an input or another output gives TTT_E_ALIAS; interleaved slices of one buffer
+ *   (equal strides, disjoint columns) do not overlap. */
+typedef enum { TTT_ROPE_HALF = 0, TTT_ROPE_INTERLEAVED = 1 } ttt_rope_layout;
+ttt_status ttt_qk_norm_rope(const void* Q, long long q_stride, const void* K, long long k_stride,
+                            const void* V, long long v_stride, ttt_dtype dtype,
+                            const float* q_weight, const float* k_weight, float eps,
+                            const int* pos, const double* inv_freq, int rot,
+                            ttt_rope_layout layout, float rope_scale,
+                            void* Q_out, long long qo_stride, void* K_out, long long ko_stride,
+                            void* K_cache, void* V_cache, const int* slots, long long n_slots,
+                            int N, int Hq, int Hkv, int dh, hipStream_t stream);
+
+/* Causal attention over packed sequences with grouped heads. Sequence s has the queries
+ * [cu_q[s], cu_q[s+1]) and the keys [cu_k[s], cu_k[s+1]), lq and lk of them; its last query stands
+ * at its last key (lk > lq: the earlier keys are a prompt's earlier part; lk < lq: the first
+ * queries see nothing). Query i of a sequence sees its key j when
+ *     j <= i + lk - lq   and, with window > 0,   j > i + lk - lq - window
+ * and query head h reads key head h / (Hq / Hkv):
+ *     o = sum_j softmax_j(scale * q . k_j) v_j        lse = ln sum_j exp(scale * q . k_j)
+ * A query that sees nothing (or only logits of -inf) gets o = 0 and lse = -inf.
+ * Logits, exponentials, maxima and sums in fp32; the weights enter the value product as bf16.
+ *   Q  [Nq, Hq, dh], K and V [Nk, Hkv, dh], O [Nq, Hq, dh], all dtype (TTT_BF16; TTT_F32 gives
+ *      TTT_E_UNSUPPORTED); token t at + t * stride
+ *   lse    [Nq, Hq] fp32 or NULL
+ *   cu_q, cu_k  [n_seq + 1] int32 on the device, non-decreasing, cu_q within [0, Nq] and cu_k
+ *      within [0, Nk] (values outside are clamped, a decreasing pair is an empty sequence: no
+ *      access leaves the buffers, but which rows are written is then unspecified). cu_k may be
+ *      cu_q. Empty sequences are allowed. Rows of O and lse before cu_q[0] and from cu_q[n_seq]
+ *      on are left as they were.
+ *   K and V hold Nk rows. Only the values of a sequence's own keys can reach its rows.
+ *   Hq % Hkv == 0; dh 64 or 128 (else TTT_E_UNSUPPORTED); 1 <= Nq, Nk <= 2^26;
+ *   1 <= n_seq <= 2^20; Nq * Hq < 2^31; 0 <= window <= 2^30; scale finite and > 0;
+ *   strides in elements: at least heads * dh, multiples of 8, at most 2^23.
+ *   O must not overlap an input; lse must not overlap anything.
+ *   workspace: at least ttt_attention_packed_workspace(...) bytes (may be NULL when that is 0);
+ *      contents on entry do not matter. Calls that overlap in time (two captured graphs that
+ *      may run at once too) need one each. */
+ttt_status ttt_attention_packed(const void* Q, long long q_stride, const void* K,
+                                long long k_stride, const void* V, long long v_stride,
+                                ttt_dtype dtype, void* O, long long o_stride, float* lse,
+                                const int* cu_q, const int* cu_k, int n_seq, int Nq, int Nk,
+                                int Hq, int Hkv, int dh, float scale, int window,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* Bytes of workspace ttt_attention_packed needs (0 if none, or for sizes it would reject): fp32
+ * partial results where few rows meet many keys and the keys are split over workgroups. */
+size_t ttt_attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh);
+
+/* One-token attention over a paged cache: the same formula with one query per sequence, which
+ * stands at the last of its lengths[s] cached tokens. Token j of sequence s is row
+ *     page_table[s][j / page_size] * page_size + j % page_size
+ * of K_cache and V_cache [n_pages * page_size, Hkv, dh] (rows behind n_pages * page_size are
+ * never read). lengths[s] <= 0 gives o = 0, lse = -inf; a length over max_pages * page_size is
+ * cut to it; tokens of a page outside [0, n_pages) are left out. Rows that a sequence does not
+ * see (behind its length, before its window) may hold anything, NaN included; their entries in
+ * page_table too.
+ *   Q  [n_seq, Hq, dh], O [n_seq, Hq, dh], dtype as above, sequence s at + s * stride
+ *   page_table [n_seq, max_pages] int32, lengths [n_seq] int32, lse [n_seq, Hq] fp32 or NULL
+ *   page_size: a power of two, 16 .. 65536 (else TTT_E_UNSUPPORTED); max_pages * page_size <=
+ *   2^30; n_pages * page_size <= 2^36; n_seq <= 2^20, n_seq * Hq <= 2^26; the other limits, overlaps and the workspace as above. */
+ttt_status ttt_attention_decode(const void* Q, long long q_stride, const void* K_cache,
+                                const void* V_cache, ttt_dtype dtype, void* O, long long o_stride,
+                                float* lse, const int* page_table, int max_pages, int page_size,
+                                int n_pages, const int* lengths, int n_seq, int Hq, int Hkv,
+                                int dh, float scale, int window, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+size_t ttt_attention_decode_workspace(int n_seq, int max_pages, int page_size, int Hq, int Hkv,
+                                      int dh);
 
 /* ------------------------------------------------------------------------------------------ */
 const char* ttt_status_string(ttt_status s);  /* static string, never NULL */
