@@ -544,12 +544,14 @@ def _int_in(value, name: str, lo: int, hi: int) -> int:
 
 def _launch(fn, args, device):
     """Calls fn(*args, stream) with `device` current and its current stream; checks the status."""
+    # the raw stream handle: torch.cuda.current_stream() builds an object, 4 us of a 16 us call
     torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, torch.cuda.current_stream().cuda_stream)
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            code = fn(*args, torch.cuda.current_stream().cuda_stream)
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if code != 0:
         raise TTTError(status_string(code))
 

@@ -18,6 +18,7 @@ namespace ttt {
 namespace {
 
 constexpr int AP_BN = 64;
+constexpr float AP_SLACK = 8.f;  // log2
 
 struct PackedDev {
   const uint16_t *Q, *K, *V;
@@ -55,10 +56,40 @@ __device__ __forceinline__ int ap_find(const PackedDev& a, int tile, int BM, int
   }
 }
 
-template <int DH, int QT>
-__global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void k_attention_packed(PackedDev a) {
-  constexpr int BM = 128 * QT, TILE = AP_BN * DH * 2, KS = DH / 16, DT = DH / 32;
-  __shared__ __align__(1024) char sm[2][2][TILE];
+// S^T tile of 32 keys by 32 queries into ordinary registers, where the exponentials are taken; the
+// queries sit in accumulator registers. Inline assembly, because the compiler would put every
+// product's result into accumulator registers and copy 64 values a tile. The result may be read a
+// whole phase later only (ap_settle).
+__device__ __forceinline__ void ap_mma0(f32x16& d, const uint4& k, const uint4& q) {
+  asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0"
+      : "=&v"(d) : "v"(__builtin_bit_cast(bf16x8, k)), "a"(__builtin_bit_cast(bf16x8, q)));
+}
+__device__ __forceinline__ void ap_mma(f32x16& d, const uint4& k, const uint4& q) {
+  asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
+      : "+v"(d) : "v"(__builtin_bit_cast(bf16x8, k)), "a"(__builtin_bit_cast(bf16x8, q)));
+}
+// The products that wrote these have left the matrix pipe: 16 + 16 wait states, where an 8-pass
+// product needs 11 before its result is read.
+__device__ __forceinline__ void ap_settle(f32x16 (&s)[2][2]) {
+  asm volatile("s_nop 15\n\ts_nop 15" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
+}
+// o *= f in accumulator registers, where the products keep it. Assembly again: as an ordinary product
+// the compiler copies the accumulator out in every round, before it knows whether it has to be scaled.
+__device__ __forceinline__ void ap_rescale(f32x16& o, float f) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x = o[i], t;
+    asm volatile("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %1, %2\n\tv_accvgpr_write_b32 %0, %1"
+                 : "+a"(x), "=&v"(t) : "v"(f));
+    o[i] = x;
+  }
+}
+__device__ __forceinline__ void ap_fence() { __builtin_amdgcn_sched_barrier(0); }
+
+template <int DH>
+__global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
+  constexpr int QT = 2, BM = 128 * QT, TILE = AP_BN * DH * 2, KS = DH / 16, DT = DH / 32;
+  __shared__ __align__(1024) char sm[2][2][TILE];  // [stage][K / V]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int h = lane >> 5;
   const int kvh = blockIdx.x % a.Hkv;
@@ -99,39 +130,39 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void k_attention_packed(Packe
     t1 = min(t0 + per, t1);
   }
   const int wr = row0 + wave * 32 * QT;
-  const int wlo = min(wr, rows - 1), whi = min(wr + 32 * QT, rows) - 1;
-  const bool wave_on = wr < rows;
-  const int hi_min = wlo / a.G + off, hi_max = (whi < wlo ? wlo : whi) / a.G + off;
-  const int lo_max = a.window > 0 ? hi_max - a.window + 1 : 0;
-  const int lo_min = a.window > 0 ? hi_min - a.window + 1 : 0;
+  const int hi_min = min(wr, rows - 1) / a.G + off;
+  const int lo_max = a.window > 0 ? min(wr + 32 * QT - 1, rows - 1) / a.G + off - a.window + 1 : 0;
 
-  using CK = TileCopy<DH, AP_BN, 4, false>;
-  using CV = TileCopy<DH, AP_BN, 4, true>;
+  // Copies: instruction i of a wave fills tile rows (4 i + wave) * RPI ..; a row past the sequence's
+  // last is replaced by that one (in another order of its chunks, and masked).
+  constexpr int RPI = 1024 / (DH * 2), NI = AP_BN / RPI / 4;
+  const int crow = wave * RPI + lane / (64 / RPI), cp = lane % (64 / RPI);
+  const uint32_t kchunk = uint32_t(cp ^ ksw<DH>(crow)) << 4, vchunk = uint32_t(cp ^ vsw<DH>(crow)) << 4;
   const char* Kb = reinterpret_cast<const char*>(a.K + long(k0) * a.ks + kvh * DH);
   const char* Vb = reinterpret_cast<const char*>(a.V + long(k0) * a.vs + kvh * DH);
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32(&sm[0][0][0]));
-  auto issue = [&](int t, int buf) {
-    const int first = t * AP_BN, last = lk - 1 - first;
-    const char* kb = Kb + long(first) * a.ks * 2;
-    const char* vb = Vb + long(first) * a.vs * 2;
-    const uint32_t kd = lds0 + buf * 2 * TILE + wave * 1024, vd = kd + TILE;
+  const uint32_t kstep = uint32_t(a.ks) * 2, vstep = uint32_t(a.vs) * 2;
+  const uint32_t krow = crow * kstep, vrow = crow * vstep;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32(&sm[0][0][0])) + wave * 1024;
+  auto copy = [&](int t, const char* base, uint32_t step, uint32_t mine, uint32_t chunk, uint32_t dst) {
 #pragma unroll
-    for (int i = 0; i < CK::N; ++i)
-      dma16(uint32_t(min(CK::row(i, wave, lane), last)) * uint32_t(a.ks * 2) +
-                CK::chunk(i, wave, lane), kb, kd + i * 4096);
-#pragma unroll
-    for (int i = 0; i < CV::N; ++i)
-      dma16(uint32_t(min(CV::row(i, wave, lane), last)) * uint32_t(a.vs * 2) +
-                CV::chunk(i, wave, lane), vb, vd + i * 4096);
+    for (int i = 0; i < NI; ++i) {
+      const int first = min(t * AP_BN + i * 4 * RPI, lk - 1);
+      const uint32_t last = uint32_t(min(lk - 1 - first, 4 * RPI)) * step;
+      dma16(min(mine, last) + chunk, base + size_t(first) * step, dst + i * 4096);
+    }
   };
+  auto copy_k = [&](int t, int buf) { copy(t, Kb, kstep, krow, kchunk, lds0 + buf * 2 * TILE); };
+  auto copy_v = [&](int t, int buf) { copy(t, Vb, vstep, vrow, vchunk, lds0 + buf * 2 * TILE + TILE); };
 
   const FragOff<DH> fo(lane);
   f32x16 o[DT][QT];
-  float m[QT], l[QT];
+  float m[QT], l[QT][4], base[QT];
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
     m[b] = -INFINITY;
-    l[b] = 0.f;
+    base[b] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l[b][i] = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -139,89 +170,165 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void k_attention_packed(Packe
   }
   const float c = a.scale * kLog2e;
 
-  if (t0 < t1) issue(t0, 0);
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1;
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (t + 1 < t1) issue(t + 1, buf ^ 1);
+  // Masks tile t if its edge crosses the wave's rows (and then takes the maxima again), and moves
+  // the reference maximum where the tile's exceeds it by 2^AP_SLACK: until then exponentials of
+  // up to 2^AP_SLACK are summed as they are, and no sum has to be rescaled.
+  auto rebase = [&](int t, f32x16 (&s)[2][QT], float (&mx)[QT]) {
     const int kv0 = t * AP_BN;
-    if (!wave_on || kv0 > hi_max || kv0 + AP_BN - 1 < lo_min) continue;
-    const char* kt = &sm[buf][0][0];
-    const char* vt = &sm[buf][1][0];
-    f32x16 s[2][QT];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int b = 0; b < QT; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[kb][b][i] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        const uint4 kf = fo.key(kt, kb, ks);
-#pragma unroll
-        for (int b = 0; b < QT; ++b) s[kb][b] = mfma32x32x16(kf, qf[b][ks], s[kb][b]);
-      }
     if (kv0 + AP_BN - 1 > hi_min || kv0 < lo_max) {
+      asm volatile("" ::: "memory");  // a branch, not 128 selects in every round
 #pragma unroll
-      for (int b = 0; b < QT; ++b)
+      for (int b = 0; b < QT; ++b) {
+        const int top = hi[b] - kv0 - 4 * h, bot = lo[b] - kv0 - 4 * h;
+        mx[b] = -INFINITY;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int j = kv0 + 32 * kb + 8 * (i / 4) + 4 * h + (i & 3);
-            if (j > hi[b] || j < lo[b]) s[kb][b][i] = -INFINITY;
+            const int j = 32 * kb + 8 * (i / 4) + (i & 3);
+            if (j > top || j < bot) s[kb][b][i] = -INFINITY;
+            mx[b] = fmaxf(mx[b], s[kb][b][i]);
           }
+      }
     }
-    uint4 pf[QT][4];
+    bool grow = false;
 #pragma unroll
     for (int b = 0; b < QT; ++b) {
-      float mx = m[b];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][b][i]);
-      mx = max_halves(mx);
-      const float base = mx == -INFINITY ? 0.f : mx * c;
-      const float al = exp2_fast(fmaf(m[b], c, -base));
-      float sum = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        float p[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          p[i] = exp2_fast(fmaf(s[kb][b][i], c, -base));
-          sum += p[i];
-        }
-        pf[b][2 * kb] = make_uint4(pack2bf(p[0], p[1]), pack2bf(p[2], p[3]), pack2bf(p[4], p[5]),
-                                   pack2bf(p[6], p[7]));
-        pf[b][2 * kb + 1] = make_uint4(pack2bf(p[8], p[9]), pack2bf(p[10], p[11]),
-                                       pack2bf(p[12], p[13]), pack2bf(p[14], p[15]));
-      }
-      l[b] = l[b] * al + sum;
-      if (__any(mx != m[b])) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[d][b][i] *= al;
-      }
-      m[b] = mx;
+      mx[b] = max_halves(mx[b]);
+      grow |= (mx[b] - m[b]) * c > AP_SLACK;  // false for -inf - -inf
     }
+    if (__any(grow)) {
+      asm volatile("s_nop 15\n\ts_nop 15");  // the last products have written the accumulator
 #pragma unroll
-    for (int s4 = 0; s4 < 4; ++s4)
+      for (int b = 0; b < QT; ++b) {
+        const float mn = fmaxf(mx[b], m[b]);
+        base[b] = mn == -INFINITY ? 0.f : mn * c;
+        const float al = exp2_fast(fmaf(m[b], c, -base[b]));
+        m[b] = mn;
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const uint4 vf = fo.value(vt, s4, d);
+        for (int i = 0; i < 4; ++i) l[b][i] *= al;
 #pragma unroll
-        for (int b = 0; b < QT; ++b) o[d][b] = mfma32x32x16(vf, pf[b][s4], o[d][b]);
+        for (int d = 0; d < DT; ++d) ap_rescale(o[d][b], al);
       }
+      asm volatile("s_nop 7");  // written before a product reads it
+    }
+  };
+
+  // One round: the scores of the next tile (phase A) and the products with this tile's values
+  // (phase B) keep the matrix pipe busy while the exponentials of this tile, then the maxima of the
+  // next, are taken in the gaps. A phase is a row of groups of two products; the fences hold each
+  // group's share of vector work beside it.
+  constexpr int NA = 2 * KS, NB = 4 * DT, UNITS = 32, UA = DH == 128 ? 24 : 16;
+  auto round = [&](const char* kt, const char* vt, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT],
+                   float (&mx)[QT]) {
+    uint32_t pw[2][QT][8];  // bf16 pairs: [key block][query block]
+    auto unit = [&](int u) {  // two neighbouring exponentials
+      const int kb = u >> 4, b = (u >> 3) & 1, i = 2 * (u & 7);
+      const float p0 = exp2_fast(fmaf(s[kb][b][i], c, -base[b]));
+      const float p1 = exp2_fast(fmaf(s[kb][b][i + 1], c, -base[b]));
+      l[b][i & 2] += p0;
+      l[b][(i & 2) + 1] += p1;
+      pw[kb][b][i / 2] = pack2bf(p0, p1);
+    };
+    uint4 kf[3], vf[3];
+    kf[0] = fo.key(kt, 0, 0);
+    kf[1] = fo.key(kt, 1, 0);
+#pragma unroll
+    for (int g = 0; g < NA; ++g) {
+      ap_fence();
+      if (g + 2 < NA) kf[(g + 2) % 3] = fo.key(kt, (g + 2) & 1, (g + 2) >> 1);
+      else vf[g + 2 - NA] = fo.value(vt, 0, g + 2 - NA);
+#pragma unroll
+      for (int b = 0; b < QT; ++b) {
+        if (g < 2) ap_mma0(sn[g & 1][b], kf[g % 3], qf[b][g >> 1]);
+        else ap_mma(sn[g & 1][b], kf[g % 3], qf[b][g >> 1]);
+      }
+#pragma unroll
+      for (int u = g * UA / NA; u < (g + 1) * UA / NA; ++u) unit(u);
+    }
+    float m4[QT] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int g = 0; g < NB; ++g) {
+      ap_fence();
+      const int st = g / DT, d = g % DT;
+      if (g == NB / 2) {
+        ap_settle(sn);
+        ap_fence();
+      }
+      if (g + 2 < NB) vf[(g + 2) % 3] = fo.value(vt, (g + 2) / DT, (g + 2) % DT);
+#pragma unroll
+      for (int b = 0; b < QT; ++b) {
+        const uint32_t* w = &pw[st >> 1][b][4 * (st & 1)];
+        o[d][b] = mfma32x32x16(vf[g % 3], make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
+      }
+      if (g < NB / 2) {
+#pragma unroll
+        for (int u = UA + g * (UNITS - UA) / (NB / 2); u < UA + (g + 1) * (UNITS - UA) / (NB / 2); ++u)
+          unit(u);
+      } else {
+        constexpr int PER = 64 / (NB / 2);  // values of S^T per group
+#pragma unroll
+        for (int e = (g - NB / 2) * PER; e < (g - NB / 2 + 1) * PER; ++e)
+          m4[e >> 5] = fmaxf(m4[e >> 5], sn[(e >> 4) & 1][e >> 5][e & 15]);
+      }
+    }
+    ap_fence();
+    mx[0] = m4[0];
+    mx[1] = m4[1];
+  };
+
+  // K of tile t + 1 and V of tile t are in LDS when round t begins; behind the last tile the scores
+  // are of whatever K rows are there and are not used.
+  f32x16 s0[2][QT], s1[2][QT];
+  float mx[QT];
+  auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) {
+    constexpr int B = decltype(buf)::value;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (t + 1 < t1) copy_v(t + 1, B ^ 1);
+    if (t + 2 < t1) copy_k(t + 2, B);
+    round(&sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx);
+    if (t + 1 < t1) rebase(t + 1, sn, mx);
+  };
+  // the queries are in accumulator registers, some wait states before the first product
+#pragma unroll
+  for (int b = 0; b < QT; ++b)
+#pragma unroll
+    for (int k = 0; k < KS; ++k) asm volatile("" : "+a"(qf[b][k].x), "+a"(qf[b][k].y), "+a"(qf[b][k].z), "+a"(qf[b][k].w));
+  asm volatile("s_nop 7");
+  ap_fence();
+  if (t0 < t1) {
+    copy_k(t0, 0);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    copy_v(t0, 0);
+    if (t0 + 1 < t1) copy_k(t0 + 1, 1);
+#pragma unroll
+    for (int g = 0; g < NA; ++g) {
+      const uint4 kf = fo.key(&sm[0][0][0], g & 1, g >> 1);
+#pragma unroll
+      for (int b = 0; b < QT; ++b) {
+        if (g < 2) ap_mma0(s0[g & 1][b], kf, qf[b][g >> 1]);
+        else ap_mma(s0[g & 1][b], kf, qf[b][g >> 1]);
+      }
+    }
+    ap_fence();
+    ap_settle(s0);
+    ap_fence();
+#pragma unroll
+    for (int b = 0; b < QT; ++b) {
+      mx[b] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) mx[b] = fmaxf(mx[b], s0[e >> 4][b][e & 15]);
+    }
+    rebase(t0, s0, mx);
+  }
+  for (int t = t0; t < t1; t += 2) {
+    step(t, std::integral_constant<int, 0>(), s0, s1);
+    if (t + 1 < t1) step(t + 1, std::integral_constant<int, 1>(), s1, s0);
   }
 
-  if (!wave_on) return;
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
-    const float lt = sum_halves(l[b]);
+    const float lt = sum_halves((l[b][0] + l[b][1]) + (l[b][2] + l[b][3]));
     if (row[b] >= rows) continue;
     const int qi = row[b] / a.G, hq = kvh * a.G + row[b] - qi * a.G;
     const long rr = long(q0 + qi) * a.Hq + hq;
@@ -266,9 +373,9 @@ hipError_t attention_packed(const PackedArgs& a) {
   d.tiles = int(long(a.Nq) * d.G / BM) + a.n_seq;
   const dim3 grid(unsigned(d.tiles) * a.Hkv);
   if (a.dh == 128)
-    hipLaunchKernelGGL((k_attention_packed<128, 2>), grid, dim3(256), 0, a.stream, d);
+    hipLaunchKernelGGL((k_attention_packed<128>), grid, dim3(256), 0, a.stream, d);
   else
-    hipLaunchKernelGGL((k_attention_packed<64, 2>), grid, dim3(256), 0, a.stream, d);
+    hipLaunchKernelGGL((k_attention_packed<64>), grid, dim3(256), 0, a.stream, d);
   return hipGetLastError();
 }
 
