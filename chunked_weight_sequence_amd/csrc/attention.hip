@@ -11,11 +11,15 @@
 // 1 / G as many queries. A workgroup of 4 waves owns BM = 128 * QT consecutive rows (32 * QT per
 // wave, as the columns of S^T) and walks the visible keys in tiles of 64 with the running maximum
 // and sum of a softmax in fp32.
+#include <type_traits>
+
 #include "attn.hpp"
 #include "launch.hpp"
 
 namespace ttt {
 namespace {
+
+#define AP_INLINE __attribute__((always_inline))
 
 constexpr int AP_BN = 64;
 constexpr float AP_SLACK = 8.f;  // log2
@@ -68,10 +72,12 @@ __device__ __forceinline__ void ap_mma(f32x16& d, const uint4& k, const uint4& q
   asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
       : "+v"(d) : "v"(__builtin_bit_cast(bf16x8, k)), "a"(__builtin_bit_cast(bf16x8, q)));
 }
-// The products that wrote these have left the matrix pipe: 16 + 16 wait states, where an 8-pass
-// product needs 11 before its result is read.
+// What follows reads these results of ap_mma: either at least three phases' quarters of products lie
+// between (NOPS false), or 16 + 16 wait states, where an 8-pass product needs 11, are put there.
+template <bool NOPS>
 __device__ __forceinline__ void ap_settle(f32x16 (&s)[2][2]) {
-  asm volatile("s_nop 15\n\ts_nop 15" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
+  if (NOPS) asm volatile("s_nop 15\n\ts_nop 15");
+  asm volatile("" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
 }
 // o *= f in accumulator registers, where the products keep it. Assembly again: as an ordinary product
 // the compiler copies the accumulator out in every round, before it knows whether it has to be scaled.
@@ -84,6 +90,24 @@ __device__ __forceinline__ void ap_rescale(f32x16& o, float f) {
     o[i] = x;
   }
 }
+// A copy that the compiler leaves where it stands (see ap_hide).
+__device__ __forceinline__ void ap_move(f32x16& to, const f32x16& from) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x;
+    asm volatile("v_mov_b32 %0, %1" : "=v"(x) : "v"(from[i]));
+    to[i] = x;
+  }
+}
+// x = -inf where `hidden`, in place: as an ordinary selection it would be another register, and every
+// tile, masked or not, would be copied to where the masked ones end.
+__device__ __forceinline__ void ap_hide(float& x, bool hidden) {
+  asm volatile("s_nop 1\n\tv_cndmask_b32 %0, %0, %1, %2"
+               : "+v"(x) : "v"(-INFINITY), "s"(__ballot(hidden)));
+}
+// Waits until at most N of the wave's LDS reads are under way (they return in order).
+template <int N>
+__device__ __forceinline__ void ap_wait() { __builtin_amdgcn_s_waitcnt(0xC07F | (N << 8)); }
 __device__ __forceinline__ void ap_fence() { __builtin_amdgcn_sched_barrier(0); }
 
 template <int DH>
@@ -141,42 +165,48 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
   const char* Kb = reinterpret_cast<const char*>(a.K + long(k0) * a.ks + kvh * DH);
   const char* Vb = reinterpret_cast<const char*>(a.V + long(k0) * a.vs + kvh * DH);
   const uint32_t kstep = uint32_t(a.ks) * 2, vstep = uint32_t(a.vs) * 2;
-  const uint32_t krow = crow * kstep, vrow = crow * vstep;
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32(&sm[0][0][0])) + wave * 1024;
-  auto copy = [&](int t, const char* base, uint32_t step, uint32_t mine, uint32_t chunk, uint32_t dst) {
+  uint32_t koff[NI], voff[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int first = min(t * AP_BN + i * 4 * RPI, lk - 1);
-      const uint32_t last = uint32_t(min(lk - 1 - first, 4 * RPI)) * step;
-      dma16(min(mine, last) + chunk, base + size_t(first) * step, dst + i * 4096);
+  for (int i = 0; i < NI; ++i) {
+    koff[i] = (i * 4 * RPI + crow) * kstep + kchunk;
+    voff[i] = (i * 4 * RPI + crow) * vstep + vchunk;
+  }
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32(&sm[0][0][0])) + wave * 1024;
+  auto copy = [&](int t, const char* base, uint32_t step, const uint32_t (&off)[NI], uint32_t chunk,
+                  uint32_t dst) AP_INLINE {
+    const char* tb = base + size_t(t * AP_BN) * step;
+    if ((t + 1) * AP_BN <= lk) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) dma16(off[i], tb, dst + i * 4096);
+    } else {
+      const uint32_t last = uint32_t(lk - 1 - t * AP_BN) * step;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) dma16(min(off[i] - chunk, last) + chunk, tb, dst + i * 4096);
     }
   };
-  auto copy_k = [&](int t, int buf) { copy(t, Kb, kstep, krow, kchunk, lds0 + buf * 2 * TILE); };
-  auto copy_v = [&](int t, int buf) { copy(t, Vb, vstep, vrow, vchunk, lds0 + buf * 2 * TILE + TILE); };
+  auto copy_k = [&](int t, int buf) AP_INLINE { copy(t, Kb, kstep, koff, kchunk, lds0 + buf * 2 * TILE); };
+  auto copy_v = [&](int t, int buf) AP_INLINE { copy(t, Vb, vstep, voff, vchunk, lds0 + buf * 2 * TILE + TILE); };
 
   const FragOff<DH> fo(lane);
   f32x16 o[DT][QT];
-  float m[QT], l[QT][4], base[QT];
+  // reference maximum, the largest logit that it serves, its exponent, the sum of the weights
+  float m[QT], most[QT], base[QT], l[QT][2];
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
-    m[b] = -INFINITY;
+    m[b] = most[b] = -INFINITY;
     base[b] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) l[b][i] = 0.f;
+    l[b][0] = l[b][1] = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][b][i] = 0.f;
   }
-  const float c = a.scale * kLog2e;
+  const float c = a.scale * kLog2e, slack = AP_SLACK / c;
 
-  // Masks tile t if its edge crosses the wave's rows (and then takes the maxima again), and moves
-  // the reference maximum where the tile's exceeds it by 2^AP_SLACK: until then exponentials of
-  // up to 2^AP_SLACK are summed as they are, and no sum has to be rescaled.
-  auto rebase = [&](int t, f32x16 (&s)[2][QT], float (&mx)[QT]) {
+  // Masks tile t, if its edge crosses the wave's rows, and takes its maxima again.
+  auto mask = [&](int t, f32x16 (&s)[2][QT], float (&mx)[QT]) AP_INLINE {
     const int kv0 = t * AP_BN;
     if (kv0 + AP_BN - 1 > hi_min || kv0 < lo_max) {
-      asm volatile("" ::: "memory");  // a branch, not 128 selects in every round
 #pragma unroll
       for (int b = 0; b < QT; ++b) {
         const int top = hi[b] - kv0 - 4 * h, bot = lo[b] - kv0 - 4 * h;
@@ -186,27 +216,29 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int j = 32 * kb + 8 * (i / 4) + (i & 3);
-            if (j > top || j < bot) s[kb][b][i] = -INFINITY;
-            mx[b] = fmaxf(mx[b], s[kb][b][i]);
+            float x = s[kb][b][i];
+            ap_hide(x, j > top || j < bot);
+            s[kb][b][i] = x;
+            mx[b] = fmaxf(mx[b], x);
           }
       }
     }
-    bool grow = false;
-#pragma unroll
-    for (int b = 0; b < QT; ++b) {
-      mx[b] = max_halves(mx[b]);
-      grow |= (mx[b] - m[b]) * c > AP_SLACK;  // false for -inf - -inf
-    }
-    if (__any(grow)) {
+  };
+  // Moves the reference maximum where a logit exceeds it by 2^AP_SLACK: until then exponentials of
+  // up to 2^AP_SLACK are summed as they are, and nothing has to be rescaled.
+  auto rebase = [&](const float (&mx)[QT]) AP_INLINE {
+    // each half of a query's lanes looks at its own keys
+    if (__any(mx[0] > most[0] || mx[1] > most[1])) {
       asm volatile("s_nop 15\n\ts_nop 15");  // the last products have written the accumulator
 #pragma unroll
       for (int b = 0; b < QT; ++b) {
-        const float mn = fmaxf(mx[b], m[b]);
+        const float mn = fmaxf(max_halves(mx[b]), m[b]);
         base[b] = mn == -INFINITY ? 0.f : mn * c;
         const float al = exp2_fast(fmaf(m[b], c, -base[b]));
         m[b] = mn;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) l[b][i] *= al;
+        most[b] = mn + slack;
+        l[b][0] *= al;
+        l[b][1] *= al;
 #pragma unroll
         for (int d = 0; d < DT; ++d) ap_rescale(o[d][b], al);
       }
@@ -216,78 +248,111 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
 
   // One round: the scores of the next tile (phase A) and the products with this tile's values
   // (phase B) keep the matrix pipe busy while the exponentials of this tile, then the maxima of the
-  // next, are taken in the gaps. A phase is a row of groups of two products; the fences hold each
-  // group's share of vector work beside it.
-  constexpr int NA = 2 * KS, NB = 4 * DT, UNITS = 32, UA = DH == 128 ? 24 : 16;
-  auto round = [&](const char* kt, const char* vt, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT],
-                   float (&mx)[QT]) {
+  // next, are taken in the gaps. A slot is one product and its share of the vector work, held
+  // together by fences; operands are read four products ahead. NEXT: there is a next tile.
+  constexpr int SA = 4 * KS, SB = 8 * DT;      // slots of the phases
+  constexpr int OPS = 96, OA = 54;             // steps of exponentials: in all, in phase A
+  auto round = [&](auto next, const char* kt, const char* vt, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT],
+                   float (&mx)[QT], auto&& copies) AP_INLINE {
+    constexpr bool NEXT = decltype(next)::value;
     uint32_t pw[2][QT][8];  // bf16 pairs: [key block][query block]
-    auto unit = [&](int u) {  // two neighbouring exponentials
-      const int kb = u >> 4, b = (u >> 3) & 1, i = 2 * (u & 7);
-      const float p0 = exp2_fast(fmaf(s[kb][b][i], c, -base[b]));
-      const float p1 = exp2_fast(fmaf(s[kb][b][i + 1], c, -base[b]));
-      l[b][i & 2] += p0;
-      l[b][(i & 2) + 1] += p1;
-      pw[kb][b][i / 2] = pack2bf(p0, p1);
-    };
-    uint4 kf[3], vf[3];
-    kf[0] = fo.key(kt, 0, 0);
-    kf[1] = fo.key(kt, 1, 0);
-#pragma unroll
-    for (int g = 0; g < NA; ++g) {
-      ap_fence();
-      if (g + 2 < NA) kf[(g + 2) % 3] = fo.key(kt, (g + 2) & 1, (g + 2) >> 1);
-      else vf[g + 2 - NA] = fo.value(vt, 0, g + 2 - NA);
-#pragma unroll
-      for (int b = 0; b < QT; ++b) {
-        if (g < 2) ap_mma0(sn[g & 1][b], kf[g % 3], qf[b][g >> 1]);
-        else ap_mma(sn[g & 1][b], kf[g % 3], qf[b][g >> 1]);
+    float p0 = 0.f, p1 = 0.f;
+    auto op = [&](int n) AP_INLINE {  // unit n / 3: two neighbouring weights, in the order phase B takes them
+      const int u = n / 3, kb = u >> 4, b = (u >> 2) & 1, i = 8 * ((u >> 3) & 1) + 2 * (u & 3);
+      if (n % 3 == 0) p0 = exp2_fast(fmaf(s[kb][b][i], c, -base[b]));
+      if (n % 3 == 1) p1 = exp2_fast(fmaf(s[kb][b][i + 1], c, -base[b]));
+      if (n % 3 == 2) {
+        pw[kb][b][i / 2] = pack2bf(p0, p1);
+        l[b][0] += p0;
+        l[b][1] += p1;
+        asm volatile("" : "+v"(l[b][0]), "+v"(l[b][1]));  // here, not behind the round
       }
+    };
+    constexpr int first = NEXT ? 0 : OA;
 #pragma unroll
-      for (int u = g * UA / NA; u < (g + 1) * UA / NA; ++u) unit(u);
+    for (int n = 0; n < first; ++n) op(n);
+    uint4 kf[2][2], vf[2][2];
+    if (NEXT) {
+      kf[0][0] = fo.key(kt, 0, 0);
+      kf[0][1] = fo.key(kt, 1, 0);
+#pragma unroll
+      for (int k = 0; k < SA; ++k) {
+        const int ks = k / 4, kb = (k >> 1) & 1, b = k & 1;
+        ap_fence();
+        if (k % 4 == 0) {
+          if (ks + 1 < KS) {
+            kf[(ks + 1) & 1][0] = fo.key(kt, 0, ks + 1);
+            kf[(ks + 1) & 1][1] = fo.key(kt, 1, ks + 1);
+            ap_wait<2>();
+          } else {
+            vf[0][0] = fo.value(vt, 0, 0);
+            vf[0][1] = fo.value(vt, 0, 1);
+            ap_wait<4>();
+          }
+          ap_fence();
+        }
+        if (k == 4) copies();
+        if (ks == 0) ap_mma0(sn[kb][b], kf[0][kb], qf[b][0]);
+        else ap_mma(sn[kb][b], kf[ks & 1][kb], qf[b][ks]);
+#pragma unroll
+        for (int n = k * OA / SA; n < (k + 1) * OA / SA; ++n) op(n);
+      }
+    } else {
+      vf[0][0] = fo.value(vt, 0, 0);
+      vf[0][1] = fo.value(vt, 0, 1);
     }
-    float m4[QT] = {-INFINITY, -INFINITY};
+    float m2[QT] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int g = 0; g < NB; ++g) {
+    for (int k = 0; k < SB; ++k) {
+      constexpr int PW = SB / 4, SE = 3 * PW;  // slots per 16 keys; slots with exponentials
+      const int st = k / PW, d = (k % PW) >> 1, b = k & 1, pr = k / 4;
       ap_fence();
-      const int st = g / DT, d = g % DT;
-      if (g == NB / 2) {
-        ap_settle(sn);
+      if (k % 4 == 0) {
+        if (pr + 1 < SB / 4) {
+          const int st1 = (k + 4) / PW, d1 = ((k + 4) % PW) >> 1;
+          vf[(pr + 1) & 1][0] = fo.value(vt, st1, d1);
+          vf[(pr + 1) & 1][1] = fo.value(vt, st1, d1 + 1);
+          ap_wait<4>();
+        } else {
+          ap_wait<0>();
+        }
         ap_fence();
       }
-      if (g + 2 < NB) vf[(g + 2) % 3] = fo.value(vt, (g + 2) / DT, (g + 2) % DT);
-#pragma unroll
-      for (int b = 0; b < QT; ++b) {
-        const uint32_t* w = &pw[st >> 1][b][4 * (st & 1)];
-        o[d][b] = mfma32x32x16(vf[g % 3], make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
+      if (NEXT && k == SE) {
+        ap_settle<false>(sn);
+        ap_fence();
       }
-      if (g < NB / 2) {
+      const uint32_t* w = &pw[st >> 1][b][4 * (st & 1)];
+      o[d][b] = mfma32x32x16(vf[pr & 1][d & 1], make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
+      if (k < SE) {
 #pragma unroll
-        for (int u = UA + g * (UNITS - UA) / (NB / 2); u < UA + (g + 1) * (UNITS - UA) / (NB / 2); ++u)
-          unit(u);
-      } else {
-        constexpr int PER = 64 / (NB / 2);  // values of S^T per group
+        for (int n = OA + k * (OPS - OA) / SE; n < OA + (k + 1) * (OPS - OA) / SE; ++n) op(n);
+      } else if (NEXT) {
+        constexpr int PER = 64 / PW;  // values of the next scores per slot
+        const int e0 = (k - SE) * PER, q = e0 >> 5;
 #pragma unroll
-        for (int e = (g - NB / 2) * PER; e < (g - NB / 2 + 1) * PER; ++e)
-          m4[e >> 5] = fmaxf(m4[e >> 5], sn[(e >> 4) & 1][e >> 5][e & 15]);
+        for (int e = e0; e < e0 + PER; e += 2)
+          m2[q] = fmaxf(fmaxf(m2[q], sn[(e >> 4) & 1][q][e & 15]), sn[(e >> 4) & 1][q][(e & 15) + 1]);
+        asm volatile("" : "+v"(m2[q]));  // here, not behind the phase
       }
     }
     ap_fence();
-    mx[0] = m4[0];
-    mx[1] = m4[1];
+    mx[0] = m2[0];
+    mx[1] = m2[1];
   };
 
-  // K of tile t + 1 and V of tile t are in LDS when round t begins; behind the last tile the scores
-  // are of whatever K rows are there and are not used.
+  // K of tile t + 1 and V of tile t are in LDS when round t begins
   f32x16 s0[2][QT], s1[2][QT];
   float mx[QT];
-  auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) {
+  auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) AP_INLINE {
     constexpr int B = decltype(buf)::value;
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (t + 1 < t1) copy_v(t + 1, B ^ 1);
-    if (t + 2 < t1) copy_k(t + 2, B);
-    round(&sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx);
-    if (t + 1 < t1) rebase(t + 1, sn, mx);
+    round(std::true_type(), &sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx, [&] {
+      copy_v(t + 1, B ^ 1);
+      if (t + 2 < t1) copy_k(t + 2, B);
+    });
+    mask(t + 1, sn, mx);
+    rebase(mx);
   };
   // the queries are in accumulator registers, some wait states before the first product
 #pragma unroll
@@ -302,7 +367,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
     copy_v(t0, 0);
     if (t0 + 1 < t1) copy_k(t0 + 1, 1);
 #pragma unroll
-    for (int g = 0; g < NA; ++g) {
+    for (int g = 0; g < 2 * KS; ++g) {
       const uint4 kf = fo.key(&sm[0][0][0], g & 1, g >> 1);
 #pragma unroll
       for (int b = 0; b < QT; ++b) {
@@ -311,7 +376,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
       }
     }
     ap_fence();
-    ap_settle(s0);
+    ap_settle<true>(s0);
     ap_fence();
 #pragma unroll
     for (int b = 0; b < QT; ++b) {
@@ -319,16 +384,31 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
 #pragma unroll
       for (int e = 0; e < 32; ++e) mx[b] = fmaxf(mx[b], s0[e >> 4][b][e & 15]);
     }
-    rebase(t0, s0, mx);
+    mask(t0, s0, mx);
+    rebase(mx);
   }
-  for (int t = t0; t < t1; t += 2) {
-    step(t, std::integral_constant<int, 0>(), s0, s1);
-    if (t + 1 < t1) step(t + 1, std::integral_constant<int, 1>(), s1, s0);
+  using B0 = std::integral_constant<int, 0>;
+  using B1 = std::integral_constant<int, 1>;
+  for (int t = t0; t + 1 < t1; t += 2) {
+    step(t, B0(), s0, s1);
+    if (t + 2 < t1) {
+      step(t + 1, B1(), s1, s0);
+    } else {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int b = 0; b < QT; ++b) ap_move(s0[kb][b], s1[kb][b]);
+    }
+  }
+  if (t0 < t1) {  // the last tile
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const char* vt = &sm[(t1 - 1 - t0) & 1][1][0];
+    round(std::false_type(), vt, vt, s0, s1, mx, [] {});
   }
 
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
-    const float lt = sum_halves((l[b][0] + l[b][1]) + (l[b][2] + l[b][3]));
+    const float lt = sum_halves(l[b][0] + l[b][1]);
     if (row[b] >= rows) continue;
     const int qi = row[b] / a.G, hq = kvh * a.G + row[b] - qi * a.G;
     const long rr = long(q0 + qi) * a.Hq + hq;
