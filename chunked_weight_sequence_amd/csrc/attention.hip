@@ -99,16 +99,47 @@ __device__ __forceinline__ void ap_move(f32x16& to, const f32x16& from) {
     to[i] = x;
   }
 }
-// x = -inf where `hidden`, in place: as an ordinary selection it would be another register, and every
-// tile, masked or not, would be copied to where the masked ones end.
-__device__ __forceinline__ void ap_hide(float& x, bool hidden) {
-  asm volatile("s_nop 1\n\tv_cndmask_b32 %0, %0, %1, %2"
-               : "+v"(x) : "v"(-INFINITY), "s"(__ballot(hidden)));
+// x = -inf where j > last (or j < first), in place: as an ordinary selection the result would be
+// another register, and every tile, masked or not, would be copied to where the masked ones end.
+__device__ __forceinline__ void ap_hide_after(float& x, int j, int last) {
+  asm volatile("v_cmp_gt_i32 vcc, %1, %2\n\ts_nop 1\n\tv_cndmask_b32 %0, %0, %3, vcc"
+               : "+v"(x) : "n"(j), "v"(last), "v"(-INFINITY) : "vcc");
+}
+__device__ __forceinline__ void ap_hide_before(float& x, int j, int first) {
+  asm volatile("v_cmp_lt_i32 vcc, %1, %2\n\ts_nop 1\n\tv_cndmask_b32 %0, %0, %3, vcc"
+               : "+v"(x) : "n"(j), "v"(first), "v"(-INFINITY) : "vcc");
 }
 // Waits until at most N of the wave's LDS reads are under way (they return in order).
 template <int N>
 __device__ __forceinline__ void ap_wait() { __builtin_amdgcn_s_waitcnt(0xC07F | (N << 8)); }
 __device__ __forceinline__ void ap_fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// How the 96 steps of a tile's exponentials (14 clocks each) are dealt out over the slots of a round:
+// in proportion to what a slot's product (33 clocks) leaves free beside its own issue, operand reads
+// and copies. at[k] .. at[k + 1]: slot k's steps (phase A, then the first three quarters of phase
+// B); at[0] of them come before the first product, while its operands are on their way from LDS.
+template <int KS, int DT, int NI>
+struct ApPlan {
+  static constexpr int SA = 4 * KS, SB = 8 * DT, OPS = 96, FIRST = 6;
+  int at[SA + 3 * SB / 4 + 1];
+  // slot of the i-th copy (V, then K)
+  static constexpr int copy_slot(int i) { return 4 * (i / 3) + i % 3 + 1; }
+  static constexpr int room(int k) {
+    int r = k < SA ? (k % 4 == 0 ? 14 : 28) : (k % 4 == 0 ? 6 : 28);
+    for (int i = 0; i < 2 * NI; ++i)
+      if (k == copy_slot(i)) r = 8;
+    return r;
+  }
+  constexpr ApPlan() : at() {
+    int total = 0, sum = 0;
+    for (int k = 0; k < SA + 3 * SB / 4; ++k) total += room(k);
+    for (int k = 0; k < SA + 3 * SB / 4; ++k) {
+      at[k] = FIRST + (sum * (OPS - FIRST) + total / 2) / total;
+      sum += room(k);
+    }
+    at[SA + 3 * SB / 4] = OPS;
+  }
+};
 
 template <int DH>
 __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
@@ -157,35 +188,48 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
   const int hi_min = min(wr, rows - 1) / a.G + off;
   const int lo_max = a.window > 0 ? min(wr + 32 * QT - 1, rows - 1) / a.G + off - a.window + 1 : 0;
 
-  // Copies: instruction i of a wave fills tile rows (4 i + wave) * RPI ..; a row past the sequence's
-  // last is replaced by that one (in another order of its chunks, and masked).
-  constexpr int RPI = 1024 / (DH * 2), NI = AP_BN / RPI / 4;
-  const int crow = wave * RPI + lane / (64 / RPI), cp = lane % (64 / RPI);
-  const uint32_t kchunk = uint32_t(cp ^ ksw<DH>(crow)) << 4, vchunk = uint32_t(cp ^ vsw<DH>(crow)) << 4;
-  const char* Kb = reinterpret_cast<const char*>(a.K + long(k0) * a.ks + kvh * DH);
-  const char* Vb = reinterpret_cast<const char*>(a.V + long(k0) * a.vs + kvh * DH);
+  // Copies: wave w fills tile rows 64 / 4 w .. in NI instructions of RPI rows. A row past the
+  // sequence's last is replaced by that one (and masked). Offsets are 3 KB up, the bases 3 KB down,
+  // so that no offset is negative when dma16_at adds its 1024 i.
+  constexpr int RPI = 1024 / (DH * 2), NI = AP_BN / RPI / 4, BACK = 3072;
+  const int crow = wave * (AP_BN / 4) + lane / (64 / RPI), cp = lane % (64 / RPI);
   const uint32_t kstep = uint32_t(a.ks) * 2, vstep = uint32_t(a.vs) * 2;
   uint32_t koff[NI], voff[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    koff[i] = (i * 4 * RPI + crow) * kstep + kchunk;
-    voff[i] = (i * 4 * RPI + crow) * vstep + vchunk;
+    const int r = crow + i * RPI;
+    koff[i] = r * kstep + ((cp ^ ksw<DH>(r)) << 4) + (BACK - 1024 * i);
+    voff[i] = r * vstep + ((cp ^ vsw<DH>(r)) << 4) + (BACK - 1024 * i);
   }
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32(&sm[0][0][0])) + wave * 1024;
-  auto copy = [&](int t, const char* base, uint32_t step, const uint32_t (&off)[NI], uint32_t chunk,
-                  uint32_t dst) AP_INLINE {
-    const char* tb = base + size_t(t * AP_BN) * step;
-    if ((t + 1) * AP_BN <= lk) {
+  const int tlast = t1 - 1, over = (tlast + 1) * AP_BN - lk;  // rows of the last tile that are not there
+  auto cut = [&](uint32_t (&off)[NI], uint32_t step) AP_INLINE {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) dma16(off[i], tb, dst + i * 4096);
-    } else {
-      const uint32_t last = uint32_t(lk - 1 - t * AP_BN) * step;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) dma16(min(off[i] - chunk, last) + chunk, tb, dst + i * 4096);
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t d = uint32_t(max(crow + i * RPI - (AP_BN - 1 - over), 0)) * step;
+      asm volatile("v_sub_u32 %0, %0, %1" : "+v"(off[i]) : "v"(d));
     }
   };
-  auto copy_k = [&](int t, int buf) AP_INLINE { copy(t, Kb, kstep, koff, kchunk, lds0 + buf * 2 * TILE); };
-  auto copy_v = [&](int t, int buf) AP_INLINE { copy(t, Vb, vstep, voff, vchunk, lds0 + buf * 2 * TILE + TILE); };
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32(&sm[0][0][0])) + wave * (TILE / 4);
+  // the next tiles to copy; K stays at the last one, which is then copied again and not read
+  const char* kp = reinterpret_cast<const char*>(a.K + (long(k0) + t0 * AP_BN) * a.ks + kvh * DH) - BACK;
+  const char* vp = reinterpret_cast<const char*>(a.V + (long(k0) + t0 * AP_BN) * a.vs + kvh * DH) - BACK;
+  const size_t ktile = size_t(AP_BN) * kstep, vtile = size_t(AP_BN) * vstep;
+  auto copy_k = [&](auto i, int buf) AP_INLINE {
+    constexpr int I = decltype(i)::value;
+    dma16_at<I>(koff[I], kp, lds0 + buf * 2 * TILE);
+  };
+  auto copy_v = [&](auto i, int buf) AP_INLINE {
+    constexpr int I = decltype(i)::value;
+    dma16_at<I>(voff[I], vp, lds0 + buf * 2 * TILE + TILE);
+  };
+  auto each = [&](auto&& f) AP_INLINE {
+    f(std::integral_constant<int, 0>());
+    f(std::integral_constant<int, 1>());
+    if constexpr (NI == 4) {
+      f(std::integral_constant<int, 2>());
+      f(std::integral_constant<int, 3>());
+    }
+  };
 
   const FragOff<DH> fo(lane);
   f32x16 o[DT][QT];
@@ -203,25 +247,41 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
   }
   const float c = a.scale * kLog2e, slack = AP_SLACK / c;
 
-  // Masks tile t, if its edge crosses the wave's rows, and takes its maxima again.
+  // Masks tile t where an edge crosses the wave's rows, and takes its maxima again.
+  auto maxima = [&](const f32x16 (&s)[2][QT], float (&mx)[QT]) AP_INLINE {
+#pragma unroll
+    for (int b = 0; b < QT; ++b) {
+      mx[b] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 32; e += 2)
+        mx[b] = fmaxf(fmaxf(mx[b], s[e >> 4][b][e & 15]), s[e >> 4][b][(e & 15) + 1]);
+    }
+  };
   auto mask = [&](int t, f32x16 (&s)[2][QT], float (&mx)[QT]) AP_INLINE {
     const int kv0 = t * AP_BN;
-    if (kv0 + AP_BN - 1 > hi_min || kv0 < lo_max) {
+    const bool after = kv0 + AP_BN - 1 > hi_min, before = kv0 < lo_max;
+    if (after || before) {
+      if (after) {
 #pragma unroll
-      for (int b = 0; b < QT; ++b) {
-        const int top = hi[b] - kv0 - 4 * h, bot = lo[b] - kv0 - 4 * h;
-        mx[b] = -INFINITY;
+        for (int b = 0; b < QT; ++b)
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = 32 * kb + 8 * (i / 4) + (i & 3);
-            float x = s[kb][b][i];
-            ap_hide(x, j > top || j < bot);
-            s[kb][b][i] = x;
-            mx[b] = fmaxf(mx[b], x);
+          for (int e = 0; e < 32; ++e) {
+            float x = s[e >> 4][b][e & 15];
+            ap_hide_after(x, 32 * (e >> 4) + 8 * ((e & 15) / 4) + (e & 3), hi[b] - kv0 - 4 * h);
+            s[e >> 4][b][e & 15] = x;
           }
       }
+      if (before) {
+#pragma unroll
+        for (int b = 0; b < QT; ++b)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x = s[e >> 4][b][e & 15];
+            ap_hide_before(x, 32 * (e >> 4) + 8 * ((e & 15) / 4) + (e & 3), lo[b] - kv0 - 4 * h);
+            s[e >> 4][b][e & 15] = x;
+          }
+      }
+      maxima(s, mx);
     }
   };
   // Moves the reference maximum where a logit exceeds it by 2^AP_SLACK: until then exponentials of
@@ -248,13 +308,16 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
 
   // One round: the scores of the next tile (phase A) and the products with this tile's values
   // (phase B) keep the matrix pipe busy while the exponentials of this tile, then the maxima of the
-  // next, are taken in the gaps. A slot is one product and its share of the vector work, held
-  // together by fences; operands are read four products ahead. NEXT: there is a next tile.
-  constexpr int SA = 4 * KS, SB = 8 * DT;      // slots of the phases
-  constexpr int OPS = 96, OA = 54;             // steps of exponentials: in all, in phase A
-  auto round = [&](auto next, const char* kt, const char* vt, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT],
-                   float (&mx)[QT], auto&& copies) AP_INLINE {
+  // next, are taken in the gaps. A slot is one product and its share of the other work, held
+  // together by fences; operands are read four products ahead. NEXT: there is a next tile, and
+  // phase A also copies K of the one after it and V of the next.
+  using Plan = ApPlan<KS, DT, NI>;
+  constexpr int SA = Plan::SA, SB = Plan::SB;
+  auto round = [&](auto next, auto buf, const char* kt, const char* vt, f32x16 (&s)[2][QT],
+                   f32x16 (&sn)[2][QT], float (&mx)[QT]) AP_INLINE {
     constexpr bool NEXT = decltype(next)::value;
+    constexpr int BUF = decltype(buf)::value;
+    constexpr Plan plan{};
     uint32_t pw[2][QT][8];  // bf16 pairs: [key block][query block]
     float p0 = 0.f, p1 = 0.f;
     auto op = [&](int n) AP_INLINE {  // unit n / 3: two neighbouring weights, in the order phase B takes them
@@ -268,13 +331,18 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
         asm volatile("" : "+v"(l[b][0]), "+v"(l[b][1]));  // here, not behind the round
       }
     };
-    constexpr int first = NEXT ? 0 : OA;
-#pragma unroll
-    for (int n = 0; n < first; ++n) op(n);
     uint4 kf[2][2], vf[2][2];
     if (NEXT) {
       kf[0][0] = fo.key(kt, 0, 0);
       kf[0][1] = fo.key(kt, 1, 0);
+      ap_fence();
+    } else {
+      vf[0][0] = fo.value(vt, 0, 0);
+      vf[0][1] = fo.value(vt, 0, 1);
+    }
+#pragma unroll
+    for (int n = 0; n < (NEXT ? plan.at[0] : plan.at[SA]); ++n) op(n);
+    if (NEXT) {
 #pragma unroll
       for (int k = 0; k < SA; ++k) {
         const int ks = k / 4, kb = (k >> 1) & 1, b = k & 1;
@@ -291,15 +359,15 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
           }
           ap_fence();
         }
-        if (k == 4) copies();
         if (ks == 0) ap_mma0(sn[kb][b], kf[0][kb], qf[b][0]);
         else ap_mma(sn[kb][b], kf[ks & 1][kb], qf[b][ks]);
+        each([&](auto i) AP_INLINE {
+          if (k == Plan::copy_slot(decltype(i)::value)) copy_v(i, BUF ^ 1);
+          if (k == Plan::copy_slot(NI + decltype(i)::value)) copy_k(i, BUF);
+        });
 #pragma unroll
-        for (int n = k * OA / SA; n < (k + 1) * OA / SA; ++n) op(n);
+        for (int n = plan.at[k]; n < plan.at[k + 1]; ++n) op(n);
       }
-    } else {
-      vf[0][0] = fo.value(vt, 0, 0);
-      vf[0][1] = fo.value(vt, 0, 1);
     }
     float m2[QT] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -326,7 +394,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
       o[d][b] = mfma32x32x16(vf[pr & 1][d & 1], make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
       if (k < SE) {
 #pragma unroll
-        for (int n = OA + k * (OPS - OA) / SE; n < OA + (k + 1) * (OPS - OA) / SE; ++n) op(n);
+        for (int n = plan.at[SA + k]; n < plan.at[SA + k + 1]; ++n) op(n);
       } else if (NEXT) {
         constexpr int PER = 64 / PW;  // values of the next scores per slot
         const int e0 = (k - SE) * PER, q = e0 >> 5;
@@ -347,13 +415,30 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
   auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) AP_INLINE {
     constexpr int B = decltype(buf)::value;
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    round(std::true_type(), &sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx, [&] {
-      copy_v(t + 1, B ^ 1);
-      if (t + 2 < t1) copy_k(t + 2, B);
-    });
+    vp += vtile;
+    if (t + 2 < t1) kp += ktile;
+    if (t + 2 >= tlast) {
+      if (t + 2 == tlast) cut(koff, kstep);
+      if (t + 1 == tlast) cut(voff, vstep);
+    }
+    round(std::true_type(), buf, &sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx);
     mask(t + 1, sn, mx);
     rebase(mx);
   };
+  // the first copies: K and V of the first tile, K of the second
+  if (t0 < t1) {
+    if (t0 == tlast) {
+      cut(koff, kstep);
+      cut(voff, vstep);
+    }
+    each([&](auto i) AP_INLINE { copy_k(i, 0); });
+    each([&](auto i) AP_INLINE { copy_v(i, 0); });
+    if (t0 < tlast) {
+      kp += ktile;
+      if (t0 + 1 == tlast) cut(koff, kstep);
+      each([&](auto i) AP_INLINE { copy_k(i, 1); });
+    }
+  }
   // the queries are in accumulator registers, some wait states before the first product
 #pragma unroll
   for (int b = 0; b < QT; ++b)
@@ -362,10 +447,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
   asm volatile("s_nop 7");
   ap_fence();
   if (t0 < t1) {
-    copy_k(t0, 0);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    copy_v(t0, 0);
-    if (t0 + 1 < t1) copy_k(t0 + 1, 1);
 #pragma unroll
     for (int g = 0; g < 2 * KS; ++g) {
       const uint4 kf = fo.key(&sm[0][0][0], g & 1, g >> 1);
@@ -378,12 +460,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
     ap_fence();
     ap_settle<true>(s0);
     ap_fence();
-#pragma unroll
-    for (int b = 0; b < QT; ++b) {
-      mx[b] = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) mx[b] = fmaxf(mx[b], s0[e >> 4][b][e & 15]);
-    }
+    maxima(s0, mx);
     mask(t0, s0, mx);
     rebase(mx);
   }
@@ -403,7 +480,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
   if (t0 < t1) {  // the last tile
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     const char* vt = &sm[(t1 - 1 - t0) & 1][1][0];
-    round(std::false_type(), vt, vt, s0, s1, mx, [] {});
+    round(std::false_type(), B0(), vt, vt, s0, s1, mx);
   }
 
 #pragma unroll
