@@ -19,6 +19,12 @@
 namespace ttt {
 namespace {
 
+#ifndef AP_SEL
+#define AP_SEL(dh) (dh == 128)
+#endif
+#ifndef AP_OCC
+#define AP_OCC 2
+#endif
 #define AP_INLINE __attribute__((always_inline))
 
 constexpr int AP_BN = 64;
@@ -74,13 +80,15 @@ __device__ __forceinline__ void ap_mma(f32x16& d, const uint4& k, const uint4& q
 }
 // What follows reads these results of ap_mma: either at least three phases' quarters of products lie
 // between (NOPS false), or 16 + 16 wait states, where an 8-pass product needs 11, are put there.
-template <bool NOPS>
-__device__ __forceinline__ void ap_settle(f32x16 (&s)[2][2]) {
+template <bool NOPS, int QT>
+__device__ __forceinline__ void ap_settle(f32x16 (&s)[2][QT]) {
   if (NOPS) asm volatile("s_nop 15\n\ts_nop 15");
-  asm volatile("" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
+#pragma unroll
+  for (int b = 0; b < QT; ++b) asm volatile("" : "+v"(s[0][b]), "+v"(s[1][b]));
 }
-// o *= f in accumulator registers, where the products keep it. Assembly again: as an ordinary product
-// the compiler copies the accumulator out in every round, before it knows whether it has to be scaled.
+// o *= f in the accumulator registers where the products keep it, behind a branch. Assembly: as an
+// ordinary product the compiler copies the accumulator out in every round, before it knows whether it
+// has to be scaled.
 __device__ __forceinline__ void ap_rescale(f32x16& o, float f) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -89,6 +97,39 @@ __device__ __forceinline__ void ap_rescale(f32x16& o, float f) {
                  : "+a"(x), "=&v"(t) : "v"(f));
     o[i] = x;
   }
+}
+// The same with the branch inside the assembly, for the round where the products that follow at once
+// would make the compiler copy the accumulator on both sides of a branch that it sees: o *= f
+// where any lane wants it (`lanes` not 0). The wait states in front let the last products
+// write it (8 passes: 11 needed), those behind let it settle for the next (2).
+__device__ __forceinline__ void ap_rescale_if(f32x16& o, float f, uint64_t lanes) {
+  float x[16], t;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = o[i];
+  asm volatile(
+      "s_cmp_eq_u64 %18, 0\n\ts_cbranch_scc1 1f\n\ts_nop 15\n\t"
+      "v_accvgpr_read_b32 %16, %0\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %0, %16\n\t"
+      "v_accvgpr_read_b32 %16, %1\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %1, %16\n\t"
+      "v_accvgpr_read_b32 %16, %2\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %2, %16\n\t"
+      "v_accvgpr_read_b32 %16, %3\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %3, %16\n\t"
+      "v_accvgpr_read_b32 %16, %4\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %4, %16\n\t"
+      "v_accvgpr_read_b32 %16, %5\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %5, %16\n\t"
+      "v_accvgpr_read_b32 %16, %6\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %6, %16\n\t"
+      "v_accvgpr_read_b32 %16, %7\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %7, %16\n\t"
+      "v_accvgpr_read_b32 %16, %8\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %8, %16\n\t"
+      "v_accvgpr_read_b32 %16, %9\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %9, %16\n\t"
+      "v_accvgpr_read_b32 %16, %10\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %10, %16\n\t"
+      "v_accvgpr_read_b32 %16, %11\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %11, %16\n\t"
+      "v_accvgpr_read_b32 %16, %12\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %12, %16\n\t"
+      "v_accvgpr_read_b32 %16, %13\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %13, %16\n\t"
+      "v_accvgpr_read_b32 %16, %14\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %14, %16\n\t"
+      "v_accvgpr_read_b32 %16, %15\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %15, %16\n\t"
+      "s_nop 3\n1:"
+      : "+a"(x[0]), "+a"(x[1]), "+a"(x[2]), "+a"(x[3]), "+a"(x[4]), "+a"(x[5]), "+a"(x[6]), "+a"(x[7]), "+a"(x[8]), "+a"(x[9]), "+a"(x[10]), "+a"(x[11]), "+a"(x[12]), "+a"(x[13]), "+a"(x[14]), "+a"(x[15]), "=&v"(t)
+      : "v"(f), "s"(lanes)
+      : "scc");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = x[i];
 }
 // A copy that the compiler leaves where it stands (see ap_hide).
 __device__ __forceinline__ void ap_move(f32x16& to, const f32x16& from) {
@@ -141,9 +182,9 @@ struct ApPlan {
   }
 };
 
-template <int DH>
-__global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
-  constexpr int QT = 2, BM = 128 * QT, TILE = AP_BN * DH * 2, KS = DH / 16, DT = DH / 32;
+template <int DH, int QT, bool PIPE>
+__global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_attention_packed(PackedDev a) {
+  constexpr int BM = 128 * QT, TILE = AP_BN * DH * 2, KS = DH / 16, DT = DH / 32;
   __shared__ __align__(1024) char sm[2][2][TILE];  // [stage][K / V]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int h = lane >> 5;
@@ -286,146 +327,51 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
   };
   // Moves the reference maximum where a logit exceeds it by 2^AP_SLACK: until then exponentials of
   // up to 2^AP_SLACK are summed as they are, and nothing has to be rescaled.
+  auto move = [&](const float (&mx)[QT], int b) AP_INLINE {  // returns the factor of the sums
+    const float old = m[b], mn = fmaxf(max_halves(mx[b]), old);
+    base[b] = mn == -INFINITY ? 0.f : mn * c;
+    m[b] = mn;
+    most[b] = mn + slack;
+    return exp2_fast(fmaf(old, c, -base[b]));
+  };
   auto rebase = [&](const float (&mx)[QT]) AP_INLINE {
-    // each half of a query's lanes looks at its own keys
-    if (__any(mx[0] > most[0] || mx[1] > most[1])) {
-      asm volatile("s_nop 15\n\ts_nop 15");  // the last products have written the accumulator
+    bool grow = false;  // each half of a query's lanes looks at its own keys
 #pragma unroll
-      for (int b = 0; b < QT; ++b) {
-        const float mn = fmaxf(max_halves(mx[b]), m[b]);
-        base[b] = mn == -INFINITY ? 0.f : mn * c;
-        const float al = exp2_fast(fmaf(m[b], c, -base[b]));
-        m[b] = mn;
-        most[b] = mn + slack;
-        l[b][0] *= al;
-        l[b][1] *= al;
+    for (int b = 0; b < QT; ++b) grow = grow || mx[b] > most[b];
+    const uint64_t lanes = __ballot(grow);
+    if constexpr (PIPE) {
+      if (lanes) {
+        asm volatile("s_nop 15\n\ts_nop 15");  // the last products have written the accumulator
 #pragma unroll
-        for (int d = 0; d < DT; ++d) ap_rescale(o[d][b], al);
+        for (int b = 0; b < QT; ++b) {
+          const float al = move(mx, b);
+          l[b][0] *= al;
+          l[b][1] *= al;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) ap_rescale(o[d][b], al);
+        }
+        asm volatile("s_nop 7");  // written before a product reads it
       }
-      asm volatile("s_nop 7");  // written before a product reads it
-    }
-  };
-
-  // One round: the scores of the next tile (phase A) and the products with this tile's values
-  // (phase B) keep the matrix pipe busy while the exponentials of this tile, then the maxima of the
-  // next, are taken in the gaps. A slot is one product and its share of the other work, held
-  // together by fences; operands are read four products ahead. NEXT: there is a next tile, and
-  // phase A also copies K of the one after it and V of the next.
-  using Plan = ApPlan<KS, DT, NI>;
-  constexpr int SA = Plan::SA, SB = Plan::SB;
-  auto round = [&](auto next, auto buf, const char* kt, const char* vt, f32x16 (&s)[2][QT],
-                   f32x16 (&sn)[2][QT], float (&mx)[QT]) AP_INLINE {
-    constexpr bool NEXT = decltype(next)::value;
-    constexpr int BUF = decltype(buf)::value;
-    constexpr Plan plan{};
-    uint32_t pw[2][QT][8];  // bf16 pairs: [key block][query block]
-    float p0 = 0.f, p1 = 0.f;
-    auto op = [&](int n) AP_INLINE {  // unit n / 3: two neighbouring weights, in the order phase B takes them
-      const int u = n / 3, kb = u >> 4, b = (u >> 2) & 1, i = 8 * ((u >> 3) & 1) + 2 * (u & 3);
-      if (n % 3 == 0) p0 = exp2_fast(fmaf(s[kb][b][i], c, -base[b]));
-      if (n % 3 == 1) p1 = exp2_fast(fmaf(s[kb][b][i + 1], c, -base[b]));
-      if (n % 3 == 2) {
-        pw[kb][b][i / 2] = pack2bf(p0, p1);
-        l[b][0] += p0;
-        l[b][1] += p1;
-        asm volatile("" : "+v"(l[b][0]), "+v"(l[b][1]));  // here, not behind the round
-      }
-    };
-    uint4 kf[2][2], vf[2][2];
-    if (NEXT) {
-      kf[0][0] = fo.key(kt, 0, 0);
-      kf[0][1] = fo.key(kt, 1, 0);
-      ap_fence();
     } else {
-      vf[0][0] = fo.value(vt, 0, 0);
-      vf[0][1] = fo.value(vt, 0, 1);
-    }
+      float al[QT];
 #pragma unroll
-    for (int n = 0; n < (NEXT ? plan.at[0] : plan.at[SA]); ++n) op(n);
-    if (NEXT) {
+      for (int b = 0; b < QT; ++b) al[b] = 1.f;
+      if (lanes) {
 #pragma unroll
-      for (int k = 0; k < SA; ++k) {
-        const int ks = k / 4, kb = (k >> 1) & 1, b = k & 1;
-        ap_fence();
-        if (k % 4 == 0) {
-          if (ks + 1 < KS) {
-            kf[(ks + 1) & 1][0] = fo.key(kt, 0, ks + 1);
-            kf[(ks + 1) & 1][1] = fo.key(kt, 1, ks + 1);
-            ap_wait<2>();
-          } else {
-            vf[0][0] = fo.value(vt, 0, 0);
-            vf[0][1] = fo.value(vt, 0, 1);
-            ap_wait<4>();
-          }
-          ap_fence();
+        for (int b = 0; b < QT; ++b) {
+          al[b] = move(mx, b);
+          l[b][0] *= al[b];
+          l[b][1] *= al[b];
         }
-        if (ks == 0) ap_mma0(sn[kb][b], kf[0][kb], qf[b][0]);
-        else ap_mma(sn[kb][b], kf[ks & 1][kb], qf[b][ks]);
-        each([&](auto i) AP_INLINE {
-          if (k == Plan::copy_slot(decltype(i)::value)) copy_v(i, BUF ^ 1);
-          if (k == Plan::copy_slot(NI + decltype(i)::value)) copy_k(i, BUF);
-        });
-#pragma unroll
-        for (int n = plan.at[k]; n < plan.at[k + 1]; ++n) op(n);
       }
+#pragma unroll
+      for (int b = 0; b < QT; ++b)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) ap_rescale_if(o[d][b], al[b], lanes);
     }
-    float m2[QT] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int k = 0; k < SB; ++k) {
-      constexpr int PW = SB / 4, SE = 3 * PW;  // slots per 16 keys; slots with exponentials
-      const int st = k / PW, d = (k % PW) >> 1, b = k & 1, pr = k / 4;
-      ap_fence();
-      if (k % 4 == 0) {
-        if (pr + 1 < SB / 4) {
-          const int st1 = (k + 4) / PW, d1 = ((k + 4) % PW) >> 1;
-          vf[(pr + 1) & 1][0] = fo.value(vt, st1, d1);
-          vf[(pr + 1) & 1][1] = fo.value(vt, st1, d1 + 1);
-          ap_wait<4>();
-        } else {
-          ap_wait<0>();
-        }
-        ap_fence();
-      }
-      if (NEXT && k == SE) {
-        ap_settle<false>(sn);
-        ap_fence();
-      }
-      const uint32_t* w = &pw[st >> 1][b][4 * (st & 1)];
-      o[d][b] = mfma32x32x16(vf[pr & 1][d & 1], make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
-      if (k < SE) {
-#pragma unroll
-        for (int n = plan.at[SA + k]; n < plan.at[SA + k + 1]; ++n) op(n);
-      } else if (NEXT) {
-        constexpr int PER = 64 / PW;  // values of the next scores per slot
-        const int e0 = (k - SE) * PER, q = e0 >> 5;
-#pragma unroll
-        for (int e = e0; e < e0 + PER; e += 2)
-          m2[q] = fmaxf(fmaxf(m2[q], sn[(e >> 4) & 1][q][e & 15]), sn[(e >> 4) & 1][q][(e & 15) + 1]);
-        asm volatile("" : "+v"(m2[q]));  // here, not behind the phase
-      }
-    }
-    ap_fence();
-    mx[0] = m2[0];
-    mx[1] = m2[1];
   };
 
-  // K of tile t + 1 and V of tile t are in LDS when round t begins
-  f32x16 s0[2][QT], s1[2][QT];
-  float mx[QT];
-  auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) AP_INLINE {
-    constexpr int B = decltype(buf)::value;
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    vp += vtile;
-    if (t + 2 < t1) kp += ktile;
-    if (t + 2 >= tlast) {
-      if (t + 2 == tlast) cut(koff, kstep);
-      if (t + 1 == tlast) cut(voff, vstep);
-    }
-    round(std::true_type(), buf, &sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx);
-    mask(t + 1, sn, mx);
-    rebase(mx);
-  };
-  // the first copies: K and V of the first tile, K of the second
+  // the first copies: K and V of the first tile
   if (t0 < t1) {
     if (t0 == tlast) {
       cut(koff, kstep);
@@ -433,11 +379,6 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
     }
     each([&](auto i) AP_INLINE { copy_k(i, 0); });
     each([&](auto i) AP_INLINE { copy_v(i, 0); });
-    if (t0 < tlast) {
-      kp += ktile;
-      if (t0 + 1 == tlast) cut(koff, kstep);
-      each([&](auto i) AP_INLINE { copy_k(i, 1); });
-    }
   }
   // the queries are in accumulator registers, some wait states before the first product
 #pragma unroll
@@ -446,41 +387,223 @@ __global__ __launch_bounds__(256, 1) void k_attention_packed(PackedDev a) {
     for (int k = 0; k < KS; ++k) asm volatile("" : "+a"(qf[b][k].x), "+a"(qf[b][k].y), "+a"(qf[b][k].z), "+a"(qf[b][k].w));
   asm volatile("s_nop 7");
   ap_fence();
-  if (t0 < t1) {
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  auto scores = [&](const char* kt, f32x16 (&s)[2][QT]) AP_INLINE {
 #pragma unroll
-    for (int g = 0; g < 2 * KS; ++g) {
-      const uint4 kf = fo.key(&sm[0][0][0], g & 1, g >> 1);
-#pragma unroll
-      for (int b = 0; b < QT; ++b) {
-        if (g < 2) ap_mma0(s0[g & 1][b], kf, qf[b][g >> 1]);
-        else ap_mma(s0[g & 1][b], kf, qf[b][g >> 1]);
-      }
-    }
-    ap_fence();
-    ap_settle<true>(s0);
-    ap_fence();
-    maxima(s0, mx);
-    mask(t0, s0, mx);
-    rebase(mx);
-  }
-  using B0 = std::integral_constant<int, 0>;
-  using B1 = std::integral_constant<int, 1>;
-  for (int t = t0; t + 1 < t1; t += 2) {
-    step(t, B0(), s0, s1);
-    if (t + 2 < t1) {
-      step(t + 1, B1(), s1, s0);
-    } else {
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint4 kf[2] = {fo.key(kt, 0, ks), fo.key(kt, 1, ks)};
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int b = 0; b < QT; ++b) ap_move(s0[kb][b], s1[kb][b]);
+        for (int b = 0; b < QT; ++b) {
+          if (ks == 0) ap_mma0(s[kb][b], kf[kb], qf[b][0]);
+          else ap_mma(s[kb][b], kf[kb], qf[b][ks]);
+        }
     }
-  }
-  if (t0 < t1) {  // the last tile
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const char* vt = &sm[(t1 - 1 - t0) & 1][1][0];
-    round(std::false_type(), B0(), vt, vt, s0, s1, mx);
+    ap_fence();
+    ap_settle<true>(s);
+    ap_fence();
+  };
+  float mx[QT];
+  f32x16 s0[2][QT];
+  using B0 = std::integral_constant<int, 0>;
+  using B1 = std::integral_constant<int, 1>;
+  if constexpr (PIPE) {
+    // One round: the scores of the next tile (phase A) and the products with this tile's values
+    // (phase B) keep the matrix pipe busy while the exponentials of this tile, then the maxima of the
+    // next, are taken in the gaps. A slot is one product and its share of the other work, held
+    // together by fences; operands are read four products ahead. NEXT: there is a next tile, and
+    // phase A also copies K of the one after it and V of the next.
+    using Plan = ApPlan<KS, DT, NI>;
+    constexpr int SA = Plan::SA, SB = Plan::SB;
+    auto round = [&](auto next, auto buf, const char* kt, const char* vt, f32x16 (&s)[2][QT],
+                     f32x16 (&sn)[2][QT], float (&mx)[QT]) AP_INLINE {
+      constexpr bool NEXT = decltype(next)::value;
+      constexpr int BUF = decltype(buf)::value;
+      constexpr Plan plan{};
+      uint32_t pw[2][QT][8];  // bf16 pairs: [key block][query block]
+      float p0 = 0.f, p1 = 0.f;
+      auto op = [&](int n) AP_INLINE {  // unit n / 3: two neighbouring weights, in the order phase B takes them
+        const int u = n / 3, kb = u >> 4, b = (u >> 2) & 1, i = 8 * ((u >> 3) & 1) + 2 * (u & 3);
+        if (n % 3 == 0) p0 = exp2_fast(fmaf(s[kb][b][i], c, -base[b]));
+        if (n % 3 == 1) p1 = exp2_fast(fmaf(s[kb][b][i + 1], c, -base[b]));
+        if (n % 3 == 2) {
+          pw[kb][b][i / 2] = pack2bf(p0, p1);
+          l[b][0] += p0;
+          l[b][1] += p1;
+          asm volatile("" : "+v"(l[b][0]), "+v"(l[b][1]));  // here, not behind the round
+        }
+      };
+      uint4 kf[2][2], vf[2][2];
+      if (NEXT) {
+        kf[0][0] = fo.key(kt, 0, 0);
+        kf[0][1] = fo.key(kt, 1, 0);
+        ap_fence();
+      } else {
+        vf[0][0] = fo.value(vt, 0, 0);
+        vf[0][1] = fo.value(vt, 0, 1);
+      }
+#pragma unroll
+      for (int n = 0; n < (NEXT ? plan.at[0] : plan.at[SA]); ++n) op(n);
+      if (NEXT) {
+#pragma unroll
+        for (int k = 0; k < SA; ++k) {
+          const int ks = k / 4, kb = (k >> 1) & 1, b = k & 1;
+          ap_fence();
+          if (k % 4 == 0) {
+            if (ks + 1 < KS) {
+              kf[(ks + 1) & 1][0] = fo.key(kt, 0, ks + 1);
+              kf[(ks + 1) & 1][1] = fo.key(kt, 1, ks + 1);
+              ap_wait<2>();
+            } else {
+              vf[0][0] = fo.value(vt, 0, 0);
+              vf[0][1] = fo.value(vt, 0, 1);
+              ap_wait<4>();
+            }
+            ap_fence();
+          }
+          if (ks == 0) ap_mma0(sn[kb][b], kf[0][kb], qf[b][0]);
+          else ap_mma(sn[kb][b], kf[ks & 1][kb], qf[b][ks]);
+          each([&](auto i) AP_INLINE {
+            if (k == Plan::copy_slot(decltype(i)::value)) copy_v(i, BUF ^ 1);
+            if (k == Plan::copy_slot(NI + decltype(i)::value)) copy_k(i, BUF);
+          });
+#pragma unroll
+          for (int n = plan.at[k]; n < plan.at[k + 1]; ++n) op(n);
+        }
+      }
+      float m2[QT] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < SB; ++k) {
+        constexpr int PW = SB / 4, SE = 3 * PW;  // slots per 16 keys; slots with exponentials
+        const int st = k / PW, d = (k % PW) >> 1, b = k & 1, pr = k / 4;
+        ap_fence();
+        if (k % 4 == 0) {
+          if (pr + 1 < SB / 4) {
+            const int st1 = (k + 4) / PW, d1 = ((k + 4) % PW) >> 1;
+            vf[(pr + 1) & 1][0] = fo.value(vt, st1, d1);
+            vf[(pr + 1) & 1][1] = fo.value(vt, st1, d1 + 1);
+            ap_wait<4>();
+          } else {
+            ap_wait<0>();
+          }
+          ap_fence();
+        }
+        if (NEXT && k == SE) {
+          ap_settle<false>(sn);
+          ap_fence();
+        }
+        const uint32_t* w = &pw[st >> 1][b][4 * (st & 1)];
+        o[d][b] = mfma32x32x16(vf[pr & 1][d & 1], make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
+        if (k < SE) {
+#pragma unroll
+          for (int n = plan.at[SA + k]; n < plan.at[SA + k + 1]; ++n) op(n);
+        } else if (NEXT) {
+          constexpr int PER = 64 / PW;  // values of the next scores per slot
+          const int e0 = (k - SE) * PER, q = e0 >> 5;
+#pragma unroll
+          for (int e = e0; e < e0 + PER; e += 2)
+            m2[q] = fmaxf(fmaxf(m2[q], sn[(e >> 4) & 1][q][e & 15]), sn[(e >> 4) & 1][q][(e & 15) + 1]);
+          asm volatile("" : "+v"(m2[q]));  // here, not behind the phase
+        }
+      }
+      ap_fence();
+      mx[0] = m2[0];
+      mx[1] = m2[1];
+    };
+
+    // K of tile t + 1 and V of tile t are in LDS when round t begins
+    f32x16 s1[2][QT];
+    auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) AP_INLINE {
+      constexpr int B = decltype(buf)::value;
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      vp += vtile;
+      if (t + 2 < t1) kp += ktile;
+      if (t + 2 >= tlast) {
+        if (t + 2 == tlast) cut(koff, kstep);
+        if (t + 1 == tlast) cut(voff, vstep);
+      }
+      round(std::true_type(), buf, &sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx);
+      mask(t + 1, sn, mx);
+      rebase(mx);
+    };
+    if (t0 < t1) {
+      if (t0 < tlast) {
+        kp += ktile;
+        if (t0 + 1 == tlast) cut(koff, kstep);
+        each([&](auto i) AP_INLINE { copy_k(i, 1); });
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * NI) : "memory");  // K of the first tile
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+      }
+      scores(&sm[0][0][0], s0);
+      maxima(s0, mx);
+      mask(t0, s0, mx);
+#pragma unroll
+      for (int b = 0; b < QT; ++b) move(mx, b);
+    }
+    for (int t = t0; t + 1 < t1; t += 2) {
+      step(t, B0(), s0, s1);
+      if (t + 2 < t1) {
+        step(t + 1, B1(), s1, s0);
+      } else {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int b = 0; b < QT; ++b) ap_move(s0[kb][b], s1[kb][b]);
+      }
+    }
+    if (t0 < t1) {  // the last tile
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const char* vt = &sm[(t1 - 1 - t0) & 1][1][0];
+      round(std::false_type(), B0(), vt, vt, s0, s1, mx);
+    }
+  } else {
+    // Two workgroups on a compute unit: while one wave of a SIMD takes exponentials, the other's
+    // products run.
+    for (int t = t0; t < t1; ++t) {
+      const int B = (t - t0) & 1;
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (t < tlast) {
+        kp += ktile;
+        vp += vtile;
+        if (t + 1 == tlast) {
+          cut(koff, kstep);
+          cut(voff, vstep);
+        }
+        each([&](auto i) AP_INLINE { copy_k(i, B ^ 1); });
+        each([&](auto i) AP_INLINE { copy_v(i, B ^ 1); });
+      }
+      scores(&sm[B][0][0], s0);
+      maxima(s0, mx);
+      mask(t, s0, mx);
+      rebase(mx);
+      const char* vt = &sm[B][1][0];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        uint32_t pw[QT][8];
+#pragma unroll
+        for (int b = 0; b < QT; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float p0 = exp2_fast(fmaf(s0[kb][b][i], c, -base[b]));
+            const float p1 = exp2_fast(fmaf(s0[kb][b][i + 1], c, -base[b]));
+            l[b][0] += p0;
+            l[b][1] += p1;
+            pw[b][i / 2] = pack2bf(p0, p1);
+          }
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const uint4 vf = fo.value(vt, 2 * kb + st, d);
+#pragma unroll
+            for (int b = 0; b < QT; ++b) {
+              const uint32_t* w = &pw[b][4 * st];
+              o[d][b] = mfma32x32x16(vf, make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
+            }
+          }
+      }
+    }
   }
 
 #pragma unroll
@@ -526,13 +649,18 @@ hipError_t attention_packed(const PackedArgs& a) {
               static_cast<const uint16_t*>(a.V), a.qs, a.ks, a.vs, static_cast<uint16_t*>(a.O),
               a.os, a.lse, a.cu_q, a.cu_k, a.n_seq, a.Nq, a.Nk, a.Hq, a.Hkv, a.Hq / a.Hkv,
               a.scale, a.window, 0, 1, nullptr};
-  const int BM = 256;
+  const bool pipe = AP_SEL(a.dh);
+  const int BM = pipe ? 256 : 128;
   d.tiles = int(long(a.Nq) * d.G / BM) + a.n_seq;
-  const dim3 grid(unsigned(d.tiles) * a.Hkv);
-  if (a.dh == 128)
-    hipLaunchKernelGGL((k_attention_packed<128>), grid, dim3(256), 0, a.stream, d);
+  const dim3 grid(unsigned(d.tiles) * a.Hkv * d.splits);
+  if (a.dh == 128 && pipe)
+    hipLaunchKernelGGL((k_attention_packed<128, 2, true>), grid, dim3(256), 0, a.stream, d);
+  else if (a.dh == 128)
+    hipLaunchKernelGGL((k_attention_packed<128, 1, false>), grid, dim3(256), 0, a.stream, d);
+  else if (pipe)
+    hipLaunchKernelGGL((k_attention_packed<64, 2, true>), grid, dim3(256), 0, a.stream, d);
   else
-    hipLaunchKernelGGL((k_attention_packed<64>), grid, dim3(256), 0, a.stream, d);
+    hipLaunchKernelGGL((k_attention_packed<64, 1, false>), grid, dim3(256), 0, a.stream, d);
   return hipGetLastError();
 }
 
