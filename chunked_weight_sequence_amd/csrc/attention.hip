@@ -28,6 +28,9 @@ namespace {
 #define AP_INLINE __attribute__((always_inline))
 
 constexpr int AP_BN = 64;
+#ifndef AP_PIECE
+#define AP_PIECE 512
+#endif
 constexpr float AP_SLACK = 8.f;  // log2
 
 struct PackedDev {
@@ -44,26 +47,45 @@ struct PackedDev {
   float* part;  // splits > 1: [splits][Nq * Hq][dh] sums, then [splits][Nq * Hq] (m, l)
 };
 
-// Sequence that holds row tile `tile`: sequence s owns the ids [base(s), base(s + 1)) with
-// base(s) = cu_q[s] * G / BM + s, at least as many as it has tiles. A 64-way search over the
-// wave's lanes; -1 if no sequence starts at or below `tile`.
-__device__ __forceinline__ long ap_base(const PackedDev& a, int s, int BM) {
-  const int c = min(max(a.cu_q[s], 0), a.Nq);
-  return long(c) * a.G / BM + s;
-}
-__device__ __forceinline__ int ap_find(const PackedDev& a, int tile, int BM, int lane) {
-  int lo = 0, len = a.n_seq;
-  while (true) {
-    const int step = (len + 63) / 64;
-    const int s = lo + lane * step;
-    const bool below = lane * step < len && ap_base(a, s, BM) <= tile;
-    const int n = __popcll(__ballot(below));
-    if (n == 0) return -1;
-    const int at = (n - 1) * step;
-    if (step == 1) return lo + at;
-    len = min(step, len - at);
-    lo += at;
+// The sequence that holds row tile `tile`, and its offsets (clamped to the buffers). Sequence s owns
+// the ids [base(s), base(s + 1)), base(s) = cu_q[s] * G / BM + s: at least as many as it has tiles.
+struct Seq {
+  int s, q0, q1, k0, k1;  // s < 0: no sequence starts at or below `tile`
+};
+__device__ __forceinline__ Seq ap_find(const PackedDev& a, int tile, int BM, int lane) {
+  const auto base = [&](int cu, int s) { return int(uint32_t(cu) * uint32_t(a.G) / uint32_t(BM)) + s; };
+  const auto clampq = [&](int s) { return min(max(a.cu_q[s], 0), a.Nq); };
+  Seq r;
+  if (a.n_seq < 64) {  // one load for everything: lane s has sequence s
+    const int s = min(lane, a.n_seq);
+    const int cq = clampq(s), ck = min(max(a.cu_k[s], 0), a.Nk);
+    r.s = __popcll(__ballot(lane < a.n_seq && base(cq, s) <= tile)) - 1;
+    const int at = max(r.s, 0);
+    r.q0 = __builtin_amdgcn_readlane(cq, at);
+    r.q1 = __builtin_amdgcn_readlane(cq, at + 1);
+    r.k0 = __builtin_amdgcn_readlane(ck, at);
+    r.k1 = __builtin_amdgcn_readlane(ck, at + 1);
+  } else {  // 64-way search
+    int lo = 0, len = a.n_seq;
+    while (true) {
+      const int step = (len + 63) / 64, s = lo + lane * step;
+      const bool in = lane * step < len;
+      const int n = __popcll(__ballot(in && base(clampq(in ? s : lo), s) <= tile));
+      r.s = n == 0 ? -1 : lo + (n - 1) * step;
+      if (n == 0 || step == 1) break;
+      len = min(step, len - (n - 1) * step);
+      lo = r.s;
+    }
+    r.s = __builtin_amdgcn_readfirstlane(r.s);
+    const int at = max(r.s, 0);
+    r.q0 = clampq(at);
+    r.q1 = clampq(at + 1);
+    r.k0 = min(max(a.cu_k[at], 0), a.Nk);
+    r.k1 = min(max(a.cu_k[at + 1], 0), a.Nk);
   }
+  r.q1 = max(r.q1, r.q0);
+  r.k1 = max(r.k1, r.k0);
+  return r;
 }
 
 // S^T tile of 32 keys by 32 queries into ordinary registers, where the exponentials are taken; the
@@ -185,7 +207,10 @@ struct ApPlan {
 template <int DH, int QT, bool PIPE>
 __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_attention_packed(PackedDev a) {
   constexpr int BM = 128 * QT, TILE = AP_BN * DH * 2, KS = DH / 16, DT = DH / 32;
-  __shared__ __align__(1024) char sm[2][2][TILE];  // [stage][K / V]
+  // [stage][K / V]; then, PIPE only, one region per wave that holds its queries at the start and its
+  // results at the end (otherwise they pass through a stage that is not in use)
+  __shared__ __align__(1024) char smem[4 * TILE + (PIPE ? BM * DH * 2 : 0)];
+  char(&sm)[2][2][TILE] = *reinterpret_cast<char(*)[2][2][TILE]>(smem);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int h = lane >> 5;
   const int kvh = blockIdx.x % a.Hkv;
@@ -193,30 +218,33 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
   const int split = rest % a.splits;
   const int tile = a.tiles - 1 - rest / a.splits;
 
-  const int seq = __builtin_amdgcn_readfirstlane(ap_find(a, tile, BM, lane));
-  if (seq < 0) return;
-  const int q0 = min(max(a.cu_q[seq], 0), a.Nq), q1 = min(max(a.cu_q[seq + 1], q0), a.Nq);
-  const int k0 = min(max(a.cu_k[seq], 0), a.Nk), k1 = min(max(a.cu_k[seq + 1], k0), a.Nk);
-  const int rows = (q1 - q0) * a.G, lk = k1 - k0, off = lk - (q1 - q0);
-  const long row0l = (tile - (long(q0) * a.G / BM + seq)) * BM;
-  if (row0l < 0 || row0l >= rows) return;
-  const int row0 = int(row0l);
+  const Seq sq = ap_find(a, tile, BM, lane);
+  if (sq.s < 0) return;
+  const int q0 = sq.q0, k0 = sq.k0, G = a.G;
+  const int rows = (sq.q1 - q0) * G, lk = sq.k1 - k0, off = lk - (sq.q1 - q0);
+  const int row0 = (tile - sq.s - int(uint32_t(q0) * uint32_t(G) / uint32_t(BM))) * BM;
+  if (row0 < 0 || row0 >= rows) return;
+  // Row x of the workgroup is query qa + v / G, head v % G, v = first + x. The quotient in fp32: v is
+  // below 2^17, so its error, 2^-22 v / G, is less than the 1 / (2 G) to the next whole number.
+  const int qa = row0 / G, first = row0 - qa * G, rows_here = min(BM, rows - row0);
+  const float inv_g = 1.f / float(G);
+  const auto query = [&](int x) { return int((float(first + x) + 0.5f) * inv_g); };  // less qa
 
-  // the lane's query column of each block: its row, its last and first visible keys
-  int row[QT], hi[QT], lo[QT];
-  uint4 qf[QT][KS];
+  const FragOff<DH> fo(lane);
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(smem));
+  constexpr int WROWS = 32 * QT;                      // rows of a wave
+  const int wrow = wave * WROWS;
+  char* const mine = smem + (PIPE ? 4 * TILE : 2 * TILE) + wrow * DH * 2;  // for the queries
+  // the lane's query column of each block: its last and first visible keys
+  int hi[QT], lo[QT];
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
-    row[b] = row0 + (wave * QT + b) * 32 + (lane & 31);
-    const int r = min(row[b], rows - 1), qi = r / a.G, g = r - qi * a.G;
+    const int qi = qa + query(min(wrow + 32 * b + (lane & 31), rows_here - 1));
     hi[b] = qi + off;
     lo[b] = a.window > 0 ? qi + off - a.window + 1 : 0;
-    const uint16_t* p = a.Q + long(q0 + qi) * a.qs + (kvh * a.G + g) * DH + 8 * h;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) qf[b][s] = *reinterpret_cast<const uint4*>(p + 16 * s);
   }
   // key tiles of the workgroup, and the wave's own limits
-  const int qa = row0 / a.G, qb = (min(row0 + BM, rows) - 1) / a.G;
+  const int qb = qa + query(rows_here - 1);
   const int kend = min(lk, qb + off + 1);
   const int kbeg = a.window > 0 ? max(0, qa + off - a.window + 1) : 0;
   int t0 = kbeg / AP_BN, t1 = kend > kbeg ? (kend + AP_BN - 1) / AP_BN : t0;
@@ -225,9 +253,9 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
     t0 = min(t0 + split * per, t1);
     t1 = min(t0 + per, t1);
   }
-  const int wr = row0 + wave * 32 * QT;
-  const int hi_min = min(wr, rows - 1) / a.G + off;
-  const int lo_max = a.window > 0 ? min(wr + 32 * QT - 1, rows - 1) / a.G + off - a.window + 1 : 0;
+  const int hi_min = qa + query(min(wrow, rows_here - 1)) + off;
+  const int lo_max =
+      a.window > 0 ? qa + query(min(wrow + WROWS, rows_here) - 1) + off - a.window + 1 : 0;
 
   // Copies: wave w fills tile rows 64 / 4 w .. in NI instructions of RPI rows. A row past the
   // sequence's last is replaced by that one (and masked). Offsets are 3 KB up, the bases 3 KB down,
@@ -250,7 +278,7 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
       asm volatile("v_sub_u32 %0, %0, %1" : "+v"(off[i]) : "v"(d));
     }
   };
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32(&sm[0][0][0])) + wave * (TILE / 4);
+  const uint32_t lds0 = lds + wave * (TILE / 4);
   // the next tiles to copy; K stays at the last one, which is then copied again and not read
   const char* kp = reinterpret_cast<const char*>(a.K + (long(k0) + t0 * AP_BN) * a.ks + kvh * DH) - BACK;
   const char* vp = reinterpret_cast<const char*>(a.V + (long(k0) + t0 * AP_BN) * a.vs + kvh * DH) - BACK;
@@ -272,7 +300,6 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
     }
   };
 
-  const FragOff<DH> fo(lane);
   f32x16 o[DT][QT];
   // reference maximum, the largest logit that it serves, its exponent, the sum of the weights
   float m[QT], most[QT], base[QT], l[QT][2];
@@ -371,21 +398,41 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
     }
   };
 
-  // the first copies: K and V of the first tile
+  // the first copies: K of the first tile, the wave's queries (rows as K's: chunk c of row r at slot
+  // c ^ ksw(r)), V of the first tile
+  uint4 qf[QT][KS];
   if (t0 < t1) {
     if (t0 == tlast) {
       cut(koff, kstep);
       cut(voff, vstep);
     }
     each([&](auto i) AP_INLINE { copy_k(i, 0); });
+    const uint16_t* Qh = a.Q + long(q0 + qa) * a.qs + long(kvh) * G * DH;
+    const uint32_t qdst = lds + uint32_t(mine - smem);
+#pragma unroll
+    for (int i = 0; i < WROWS / RPI; ++i) {
+      const int r = i * RPI + lane / (64 / RPI), x = min(wrow + r, rows_here - 1), qi = query(x);
+      dma16_far(Qh + long(qi) * a.qs + (first + x - qi * G) * DH + 8 * (cp ^ ksw<DH>(r)),
+                __builtin_amdgcn_readfirstlane(qdst + i * 1024));
+    }
     each([&](auto i) AP_INLINE { copy_v(i, 0); });
+    if (PIPE && t0 < tlast) {
+      kp += ktile;
+      if (t0 + 1 == tlast) cut(koff, kstep);
+      each([&](auto i) AP_INLINE { copy_k(i, 1); });
+      wait_vm<2 * NI>();
+    } else {
+      wait_vm<NI>();
+    }
   }
-  // the queries are in accumulator registers, some wait states before the first product
 #pragma unroll
   for (int b = 0; b < QT; ++b)
 #pragma unroll
-    for (int k = 0; k < KS; ++k) asm volatile("" : "+a"(qf[b][k].x), "+a"(qf[b][k].y), "+a"(qf[b][k].z), "+a"(qf[b][k].w));
-  asm volatile("s_nop 7");
+    for (int k = 0; k < KS; ++k) {
+      qf[b][k] = fo.key(mine, b, k);
+      asm volatile("" : "+a"(qf[b][k].x), "+a"(qf[b][k].y), "+a"(qf[b][k].z), "+a"(qf[b][k].w));
+    }
+  asm volatile("s_nop 7");  // in accumulator registers some wait states before the first product
   ap_fence();
   auto scores = [&](const char* kt, f32x16 (&s)[2][QT]) AP_INLINE {
 #pragma unroll
@@ -527,14 +574,7 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
       rebase(mx);
     };
     if (t0 < t1) {
-      if (t0 < tlast) {
-        kp += ktile;
-        if (t0 + 1 == tlast) cut(koff, kstep);
-        each([&](auto i) AP_INLINE { copy_k(i, 1); });
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * NI) : "memory");  // K of the first tile
-      } else {
-        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-      }
+      asm volatile("s_barrier" ::: "memory");  // every wave's part of the first K tile is there
       scores(&sm[0][0][0], s0);
       maxima(s0, mx);
       mask(t0, s0, mx);
@@ -606,13 +646,18 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
     }
   }
 
+  // Results. Partial ones go out as they are; others by way of LDS, in whole rows: chunk c (16 bytes)
+  // of a row at slot c ^ (row % (chunks of a row)).
+  constexpr int CH = DH / 8;
+  char* const out = PIPE ? mine : smem + (((t1 - t0) & 1) ? 2 * TILE : 0) + wrow * DH * 2;
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
     const float lt = sum_halves(l[b][0] + l[b][1]);
-    if (row[b] >= rows) continue;
-    const int qi = row[b] / a.G, hq = kvh * a.G + row[b] - qi * a.G;
-    const long rr = long(q0 + qi) * a.Hq + hq;
+    const int r = 32 * b + (lane & 31), x = wrow + r, qi = query(x);
+    const bool on = x < rows_here;
+    const long rr = long(q0 + qa + qi) * a.Hq + kvh * G + first + x - qi * G;
     if (a.splits > 1) {
+      if (!on) continue;
       const long n = long(a.Nq) * a.Hq;
       float* po = a.part + (long(split) * n + rr) * DH + 4 * h;
 #pragma unroll
@@ -628,40 +673,78 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
       continue;
     }
     const float inv = lt == 0.f ? 0.f : 1.f / lt;
-    uint16_t* po = a.O + long(q0 + qi) * a.os + hq * DH + 4 * h;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<uint2*>(po + 32 * d + 2 * i) =
+        *reinterpret_cast<uint2*>(out + r * DH * 2 + (((4 * d + i / 4) ^ (r % CH)) << 4) + 8 * h) =
             make_uint2(pack2bf(o[d][b][i] * inv, o[d][b][i + 1] * inv),
                        pack2bf(o[d][b][i + 2] * inv, o[d][b][i + 3] * inv));
-    if (a.lse && h == 0) a.lse[rr] = lt == 0.f ? -INFINITY : m[b] * a.scale + __logf(lt);
+    if (a.lse && h == 0 && on) a.lse[rr] = lt == 0.f ? -INFINITY : m[b] * a.scale + __logf(lt);
+  }
+  if (a.splits > 1) return;
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  uint16_t* Oh = a.O + long(q0 + qa) * a.os + long(kvh) * G * DH;
+#pragma unroll
+  for (int i = 0; i < WROWS / RPI; ++i) {
+    const int r = i * RPI + lane / (64 / RPI), x = wrow + r, qi = query(x);
+    const uint4 v = *reinterpret_cast<const uint4*>(out + r * DH * 2 + ((cp ^ (r % CH)) << 4));
+    if (x < rows_here)
+      *reinterpret_cast<uint4*>(Oh + long(qi) * a.os + (first + x - qi * G) * DH + 8 * cp) = v;
   }
 }
 
 }  // namespace
 
-size_t attention_packed_workspace(int, int, int, int, int, int) { return 0; }
+// What a call launches: rows per workgroup (256: the pipelined kernel, one workgroup to a compute
+// unit; 128: the other, two) and pieces of the key axis.
+namespace {
+struct PackedPlan {
+  bool pipe;
+  int tiles, splits;
+};
+PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
+  PackedPlan p;
+  const long rows = long(Nq) * (Hq / Hkv);
+  p.pipe = AP_SEL(dh);
+  const int BM = p.pipe ? 256 : 128;
+  p.tiles = int(rows / BM) + n_seq;
+  // Fewer tiles than places for workgroups: the keys are split over more of them, as long as a piece
+  // has AP_PIECE keys of an average sequence.
+  const long places = p.pipe ? 256 : 512;
+  const long wgs = ((rows + BM - 1) / BM + n_seq - 1) * Hkv;
+  long keys = (Nk + n_seq - 1) / n_seq;
+  if (window > 0 && keys > window + BM) keys = window + BM;
+  long n = places / wgs;
+  if (n > keys / AP_PIECE) n = keys / AP_PIECE;
+  p.splits = int(n < 1 ? 1 : n > 64 ? 64 : n);
+  return p;
+}
+}  // namespace
+
+size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh) {
+  const int n = packed_plan(n_seq, Nq, Nk, Hq, Hkv, dh, 0).splits;  // with a window at most as many
+  return n > 1 ? size_t(n) * Nq * Hq * (dh + 2) * 4 : 0;
+}
 
 hipError_t attention_packed(const PackedArgs& a) {
-  PackedDev d{static_cast<const uint16_t*>(a.Q), static_cast<const uint16_t*>(a.K),
-              static_cast<const uint16_t*>(a.V), a.qs, a.ks, a.vs, static_cast<uint16_t*>(a.O),
-              a.os, a.lse, a.cu_q, a.cu_k, a.n_seq, a.Nq, a.Nk, a.Hq, a.Hkv, a.Hq / a.Hkv,
-              a.scale, a.window, 0, 1, nullptr};
-  const bool pipe = AP_SEL(a.dh);
-  const int BM = pipe ? 256 : 128;
-  d.tiles = int(long(a.Nq) * d.G / BM) + a.n_seq;
-  const dim3 grid(unsigned(d.tiles) * a.Hkv * d.splits);
-  if (a.dh == 128 && pipe)
+  const PackedPlan p = packed_plan(a.n_seq, a.Nq, a.Nk, a.Hq, a.Hkv, a.dh, a.window);
+  const PackedDev d{static_cast<const uint16_t*>(a.Q), static_cast<const uint16_t*>(a.K),
+                    static_cast<const uint16_t*>(a.V), a.qs, a.ks, a.vs,
+                    static_cast<uint16_t*>(a.O), a.os, a.lse, a.cu_q, a.cu_k, a.n_seq, a.Nq, a.Nk,
+                    a.Hq, a.Hkv, a.Hq / a.Hkv, a.scale, a.window, p.tiles, p.splits,
+                    static_cast<float*>(a.ws)};
+  const dim3 grid(unsigned(p.tiles) * a.Hkv * p.splits);
+  if (a.dh == 128 && p.pipe)
     hipLaunchKernelGGL((k_attention_packed<128, 2, true>), grid, dim3(256), 0, a.stream, d);
   else if (a.dh == 128)
     hipLaunchKernelGGL((k_attention_packed<128, 1, false>), grid, dim3(256), 0, a.stream, d);
-  else if (pipe)
-    hipLaunchKernelGGL((k_attention_packed<64, 2, true>), grid, dim3(256), 0, a.stream, d);
   else
     hipLaunchKernelGGL((k_attention_packed<64, 1, false>), grid, dim3(256), 0, a.stream, d);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  return attention_join(d.part, p.splits, a.cu_q, a.n_seq, long(a.Nq) * a.Hq, a.Hq, a.dh, a.O, a.os,
+                        a.lse, a.scale, a.stream);
 }
 
 }  // namespace ttt

@@ -228,12 +228,14 @@ __global__ __launch_bounds__(256, 1) void k_attention_decode(DecodeDev a) {
 // Joins the `splits` partial sums of each row (token, head); one wave per row. Fixed order, so the
 // same inputs give the same bits.
 template <int DH>
-__global__ __launch_bounds__(256) void k_attention_join(const float* part, int splits, long nrows,
+__global__ __launch_bounds__(256) void k_attention_join(const float* part, int splits,
+                                                        const int* cu_q, int n_seq, long nrows,
                                                         int Hq, uint16_t* O, long os, float* lse,
                                                         float scale) {
   const int lane = threadIdx.x & 63;
   const long rr = long(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (rr >= nrows) return;
+  if (cu_q && (rr / Hq < cu_q[0] || rr / Hq >= cu_q[n_seq])) return;  // a row of no sequence
   const float c = scale * kLog2e;
   float2 x = make_float2(-INFINITY, 0.f);
   if (lane < splits)
@@ -273,14 +275,17 @@ int decode_splits(int n_seq, int max_pages, int page, int Hkv, int G) {
 
 }  // namespace
 
-hipError_t attention_join(const float* part, int splits, long nrows, int Hq, int dh, void* O, long os,
-                          float* lse, float scale, hipStream_t stream) {
+hipError_t attention_join(const float* part, int splits, const int* cu_q, int n_seq, long nrows,
+                          int Hq, int dh, void* O, long os, float* lse, float scale,
+                          hipStream_t stream) {
   const dim3 grid(unsigned((nrows + 3) / 4));
   if (dh == 128)
-    hipLaunchKernelGGL((k_attention_join<128>), grid, dim3(256), 0, stream, part, splits, nrows, Hq,
+    hipLaunchKernelGGL((k_attention_join<128>), grid, dim3(256), 0, stream, part, splits, cu_q,
+                       n_seq, nrows, Hq,
                        static_cast<uint16_t*>(O), os, lse, scale);
   else
-    hipLaunchKernelGGL((k_attention_join<64>), grid, dim3(256), 0, stream, part, splits, nrows, Hq,
+    hipLaunchKernelGGL((k_attention_join<64>), grid, dim3(256), 0, stream, part, splits, cu_q,
+                       n_seq, nrows, Hq,
                        static_cast<uint16_t*>(O), os, lse, scale);
   return hipGetLastError();
 }
@@ -304,7 +309,7 @@ hipError_t attention_decode(const DecodeArgs& a) {
     hipLaunchKernelGGL((k_attention_decode<64>), grid, dim3(256), 0, a.stream, d);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || d.splits == 1) return e;
-  return attention_join(d.part, d.splits, long(a.n_seq) * a.Hq, a.Hq, a.dh, a.O, a.os, a.lse,
+  return attention_join(d.part, d.splits, nullptr, 0, long(a.n_seq) * a.Hq, a.Hq, a.dh, a.O, a.os, a.lse,
                         a.scale, a.stream);
 }
 

@@ -40,6 +40,11 @@ __device__ __forceinline__ void dma16_at(uint32_t voff, const char* sbase, uint3
     asm volatile("global_load_lds_dwordx4 %0, %1 offset:%2" ::"v"(voff), "s"(sbase), "n"(I * 1024));
 }
 
+// One copy with a 64-bit address per lane, M0 written a wait state ahead.
+__device__ __forceinline__ void dma16_far(const void* p, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(m0));
+}
+
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");

@@ -239,9 +239,11 @@ size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, in
 hipError_t attention_packed(const PackedArgs& a);
 
 // Joins `splits` (<= 64) partial results of nrows = tokens * Hq rows: part holds unnormalised fp32
-// sums [splits][nrows][dh], then (maximum logit, sum) [splits][nrows][2] (decode.hip).
-hipError_t attention_join(const float* part, int splits, long nrows, int Hq, int dh, void* O, long os,
-                          float* lse, float scale, hipStream_t stream);
+// sums [splits][nrows][dh], then (maximum logit, sum) [splits][nrows][2] (decode.hip). With cu_q,
+// only the rows of tokens in [cu_q[0], cu_q[n_seq]).
+hipError_t attention_join(const float* part, int splits, const int* cu_q, int n_seq, long nrows,
+                          int Hq, int dh, void* O, long os, float* lse, float scale,
+                          hipStream_t stream);
 
 // One query per sequence over a paged cache.
 struct DecodeArgs {
