@@ -19,18 +19,9 @@
 namespace ttt {
 namespace {
 
-#ifndef AP_SEL
-#define AP_SEL(dh) (dh == 128)
-#endif
-#ifndef AP_OCC
-#define AP_OCC 2
-#endif
 #define AP_INLINE __attribute__((always_inline))
 
 constexpr int AP_BN = 64;
-#ifndef AP_PIECE
-#define AP_PIECE 512
-#endif
 constexpr float AP_SLACK = 8.f;  // log2
 
 struct PackedDev {
@@ -205,7 +196,7 @@ struct ApPlan {
 };
 
 template <int DH, int QT, bool PIPE>
-__global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_attention_packed(PackedDev a) {
+__global__ __launch_bounds__(256, PIPE ? 1 : 2) void k_attention_packed(PackedDev a) {
   constexpr int BM = 128 * QT, TILE = AP_BN * DH * 2, KS = DH / 16, DT = DH / 32;
   // [stage][K / V]; then, PIPE only, one region per wave that holds its queries at the start and its
   // results at the end (otherwise they pass through a stage that is not in use)
@@ -229,6 +220,10 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
   const int qa = row0 / G, first = row0 - qa * G, rows_here = min(BM, rows - row0);
   const float inv_g = 1.f / float(G);
   const auto query = [&](int x) { return int((float(first + x) + 0.5f) * inv_g); };  // less qa
+  // element offset of row x from head kvh * G of query qa (one 32 x 32 bit product)
+  const auto element = [&](int x, uint32_t stride) {
+    return uint64_t(uint32_t(query(x))) * (stride - uint32_t(G * DH)) + uint32_t((first + x) * DH);
+  };
 
   const FragOff<DH> fo(lane);
   const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(smem));
@@ -411,8 +406,8 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
     const uint32_t qdst = lds + uint32_t(mine - smem);
 #pragma unroll
     for (int i = 0; i < WROWS / RPI; ++i) {
-      const int r = i * RPI + lane / (64 / RPI), x = min(wrow + r, rows_here - 1), qi = query(x);
-      dma16_far(Qh + long(qi) * a.qs + (first + x - qi * G) * DH + 8 * (cp ^ ksw<DH>(r)),
+      const int r = i * RPI + lane / (64 / RPI);
+      dma16_far(Qh + element(min(wrow + r, rows_here - 1), uint32_t(a.qs)) + 8 * (cp ^ ksw<DH>(r)),
                 __builtin_amdgcn_readfirstlane(qdst + i * 1024));
     }
     each([&](auto i) AP_INLINE { copy_v(i, 0); });
@@ -687,10 +682,9 @@ __global__ __launch_bounds__(256, PIPE ? 1 : DH == 64 ? AP_OCC : 2) void k_atten
   uint16_t* Oh = a.O + long(q0 + qa) * a.os + long(kvh) * G * DH;
 #pragma unroll
   for (int i = 0; i < WROWS / RPI; ++i) {
-    const int r = i * RPI + lane / (64 / RPI), x = wrow + r, qi = query(x);
+    const int r = i * RPI + lane / (64 / RPI), x = wrow + r;
     const uint4 v = *reinterpret_cast<const uint4*>(out + r * DH * 2 + ((cp ^ (r % CH)) << 4));
-    if (x < rows_here)
-      *reinterpret_cast<uint4*>(Oh + long(qi) * a.os + (first + x - qi * G) * DH + 8 * cp) = v;
+    if (x < rows_here) *reinterpret_cast<uint4*>(Oh + element(x, uint32_t(a.os)) + 8 * cp) = v;
   }
 }
 
@@ -703,27 +697,42 @@ struct PackedPlan {
   bool pipe;
   int tiles, splits;
 };
+// Pieces that the keys of a row are split into: as many workgroups as the chip has places for, where
+// row tiles alone are fewer, as long as a piece has 320 keys of an average row (5 tiles, about 5 us;
+// joining costs about 4 us: 1024 tokens, one sequence, 32/8 heads of 128: 31 us unsplit, 37 us split
+// in pieces of 256; 512 tokens after 15872: 323 us unsplit, 122 us split).
+int packed_splits(bool pipe, long rows, int n_seq, int Hkv, long seen) {
+  const int BM = pipe ? 256 : 128;
+  const long wgs = ((rows + BM - 1) / BM + n_seq - 1) * Hkv;
+  long n = (pipe ? 256 : 512) / wgs;
+  if (n > seen / 320) n = seen / 320;
+  return int(n < 1 ? 1 : n > 64 ? 64 : n);
+}
+// Keys that an average row sees.
+long packed_seen(int n_seq, int Nq, int Nk, int window) {
+  const long seen = (Nk > Nq / 2 ? Nk - Nq / 2 : Nk) / n_seq;
+  return window > 0 && window < seen ? window : seen;
+}
 PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
   PackedPlan p;
-  const long rows = long(Nq) * (Hq / Hkv);
-  p.pipe = AP_SEL(dh);
-  const int BM = p.pipe ? 256 : 128;
-  p.tiles = int(rows / BM) + n_seq;
-  // Fewer tiles than places for workgroups: the keys are split over more of them, as long as a piece
-  // has AP_PIECE keys of an average sequence.
-  const long places = p.pipe ? 256 : 512;
-  const long wgs = ((rows + BM - 1) / BM + n_seq - 1) * Hkv;
-  long keys = (Nk + n_seq - 1) / n_seq;
-  if (window > 0 && keys > window + BM) keys = window + BM;
-  long n = places / wgs;
-  if (n > keys / AP_PIECE) n = keys / AP_PIECE;
-  p.splits = int(n < 1 ? 1 : n > 64 ? 64 : n);
+  const long rows = long(Nq) * (Hq / Hkv), seen = packed_seen(n_seq, Nq, Nk, window);
+  // The pipelined kernel starts and ends slowly (14000 clocks that nothing overlaps; a tile takes it
+  // 2900): heads of 128 and rows of at least 320 keys. Measured, pipelined against not, 32/8 heads
+  // of 128: 16384 tokens 1.74 / 2.07 ms, 11 documents in 8192 tokens 110 / 121 us, 40 in 4096 37 /
+  // 31 us, 9000 tokens with a window of 128 76 / 57 us. Heads of 64, which the vector unit bounds:
+  // 8191 tokens, window 2048, 188 / 150 us.
+  p.pipe = dh == 128 && seen >= 320 && rows > 128;
+  p.tiles = int(rows / (p.pipe ? 256 : 128)) + n_seq;
+  p.splits = packed_splits(p.pipe, rows, n_seq, Hkv, seen);
   return p;
 }
 }  // namespace
 
 size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh) {
-  const int n = packed_plan(n_seq, Nq, Nk, Hq, Hkv, dh, 0).splits;  // with a window at most as many
+  // the window is not known here: the most that any choice takes
+  const long rows = long(Nq) * (Hq / Hkv), seen = packed_seen(n_seq, Nq, Nk, 0);
+  const int a = packed_splits(true, rows, n_seq, Hkv, seen), b = packed_splits(false, rows, n_seq, Hkv, seen);
+  const int n = a > b ? a : b;
   return n > 1 ? size_t(n) * Nq * Hq * (dh + 2) * 4 : 0;
 }
 
