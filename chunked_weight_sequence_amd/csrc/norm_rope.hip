@@ -31,17 +31,23 @@ struct Raw {
   uint4 v[n];
 };
 
+// A 16-byte read from global memory (head_at's pointer does not tell the compiler which memory).
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+  const u32x4_t v = *(const __attribute__((address_space(1))) u32x4_t*)reinterpret_cast<uintptr_t>(p);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
 template <typename T>
 __device__ __forceinline__ Raw<T> raw_load(const T* p, int e0, int e1) {
   Raw<T> r;
   if constexpr (sizeof(T) == 2) {
-    r.v[0] = *reinterpret_cast<const uint4*>(p + e0);
-    r.v[1] = *reinterpret_cast<const uint4*>(p + e1);
+    r.v[0] = ld16(p + e0);
+    r.v[1] = ld16(p + e1);
   } else {
-    r.v[0] = *reinterpret_cast<const uint4*>(p + e0);
-    r.v[1] = *reinterpret_cast<const uint4*>(p + e0 + 4);
-    r.v[2] = *reinterpret_cast<const uint4*>(p + e1);
-    r.v[3] = *reinterpret_cast<const uint4*>(p + e1 + 4);
+    r.v[0] = ld16(p + e0);
+    r.v[1] = ld16(p + e0 + 4);
+    r.v[2] = ld16(p + e1);
+    r.v[3] = ld16(p + e1 + 4);
   }
   return r;
 }
@@ -96,30 +102,65 @@ __device__ __forceinline__ Raw<T> raw_pack(const float (&x)[16]) {
   return r;
 }
 
-// lsh: log2 of the lanes per head; wpt: waves per token (1: four tokens per workgroup, 4: one)
+// Where head h of a token lies: queries, then keys, then values. Selected by value, no array or
+// closure of pointers: the compiler would put one into LDS and read the workgroup's size from the
+// dispatch packet, which lies in host memory (15 us for the last of the chip's XCDs).
+template <typename T>
+__device__ __forceinline__ const T* head_at(const T* q, const T* k, const T* v, int h, int Hq, int Hqk,
+                                            int dh) {
+  const uintptr_t p = h < Hq ? uintptr_t(q) : h < Hqk ? uintptr_t(k) : uintptr_t(v);
+  const int i = h < Hq ? h : h < Hqk ? h - Hq : h - Hqk;
+  return reinterpret_cast<const T*>(p) + long(i) * dh;
+}
+
+// A lane's 16 weights of the norm.
+struct Weights {
+  float4 v[4];
+  __device__ __forceinline__ void load(const float* p, int e0, int e1) {
+    if (!p) return;  // no norm: not read
+    v[0] = *reinterpret_cast<const float4*>(p + e0);
+    v[1] = *reinterpret_cast<const float4*>(p + e0 + 4);
+    v[2] = *reinterpret_cast<const float4*>(p + e1);
+    v[3] = *reinterpret_cast<const float4*>(p + e1 + 4);
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const float4& q = v[i >> 2];
+    return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+  }
+};
+
+// lsh: log2 of the lanes per head; wsh: log2 of the waves per token (a workgroup of 4 waves takes
+// 4 >> wsh tokens)
 template <typename T, bool INTER>
-__global__ __launch_bounds__(256) void k_norm_rope(NormRopeArgs a, int lsh, int wpt) {
+__global__ __launch_bounds__(256) void k_norm_rope(NormRopeArgs a, int lsh, int wsh) {
   __shared__ float2 cs[4][NR_MAX_HALF];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int tpb = 4 / wpt, half = a.rot >> 1;
+  const int tpb = 4 >> wsh, half = a.rot >> 1;
   const long t0 = long(blockIdx.x) * tpb;
-  const long t = t0 + wave / wpt;
+  const long t = t0 + (wave >> wsh);
   const bool on = t < a.N;  // wave-uniform
 
-  const int L = 1 << lsh, c = lane & (L - 1), step = wpt << (6 - lsh);
+  const int L = 1 << lsh, c = lane & (L - 1), hpw = 64 >> lsh, step = hpw << wsh;
   const bool live = c < (a.dh >> 4), rotates = c < (a.rot >> 4);
   const int e0 = (INTER || !rotates) ? 16 * c : 8 * c;
   const int e1 = (INTER || !rotates) ? e0 + 8 : half + e0;
   const int Hq = a.Hq, Hqk = a.Hq + a.Hkv, dh = a.dh;
   const int heads = Hqk + (a.Vc ? a.Hkv : 0);
   const T* q = static_cast<const T*>(a.Q) + t * a.qs;
-  const T* k = static_cast<const T*>(a.K) + t * a.ks - long(Hq) * dh;
-  const T* v = static_cast<const T*>(a.V) + t * a.vs - long(Hqk) * dh;
-  auto src = [=](int i) { return (i < Hq ? q : i < Hqk ? k : v) + long(i) * dh; };
-  int h = (wave % wpt) * (64 >> lsh) + (lane >> lsh);
+  const T* k = static_cast<const T*>(a.K) + t * a.ks;
+  const T* v = static_cast<const T*>(a.V) + t * a.vs;
+  const float *qwp = a.qw, *kwp = a.kw;
+  const bool qn = qwp != nullptr, kn = kwp != nullptr;
+  const int h0 = (wave & ((1 << wsh) - 1)) * hpw;
+  int h = h0 + (lane >> lsh);
+
+  // everything that comes from memory is asked for before the angles are worked out
   Raw<T> cur{};
-  if (on && live && h < heads) cur = raw_load(src(h), e0, e1);
+  if (on && live && h < heads) cur = raw_load(head_at(q, k, v, h, Hq, Hqk, dh), e0, e1);
   const int slot = (on && a.slots) ? a.slots[t] : -1;
+  bool isq = h < Hq;
+  Weights w;
+  if (live) w.load(isq ? qwp : kwp, e0, e1);
 
   for (int i = tid; i < tpb * half; i += 256) {
     const int tt = i / half, f = i - tt * half;
@@ -134,31 +175,24 @@ __global__ __launch_bounds__(256) void k_norm_rope(NormRopeArgs a, int lsh, int 
   if (!on) return;
   float2 turn[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) turn[i] = rotates ? cs[wave / wpt][8 * c + i] : make_float2(1.f, 0.f);
-  const float *qwp = a.qw, *kwp = a.kw;
-  const bool qn = qwp != nullptr, kn = kwp != nullptr;
-  float qw[16], kw[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int e = i < 8 ? e0 + i : e1 + i - 8;
-    qw[i] = qn && live ? qwp[e] : 1.f;
-    kw[i] = kn && live ? kwp[e] : 1.f;
-  }
-  const float inv_dh = 1.f / float(a.dh);
+  for (int i = 0; i < 8; ++i) turn[i] = rotates ? cs[wave >> wsh][8 * c + i] : make_float2(1.f, 0.f);
+  const float inv_dh = 1.f / float(dh);
   const bool cached = a.slots && slot >= 0 && slot < a.n_slots;
   T* qo = static_cast<T*>(a.Qo) + t * a.qos;
   T* ko = static_cast<T*>(a.Ko) + t * a.kos;
-  T* kc = static_cast<T*>(a.Kc) + long(slot) * a.Hkv * a.dh;
-  T* vc = static_cast<T*>(a.Vc) + long(slot) * a.Hkv * a.dh;
+  T* kc = static_cast<T*>(a.Kc) + long(slot) * a.Hkv * dh;
+  T* vc = static_cast<T*>(a.Vc) + long(slot) * a.Hkv * dh;
   // every lane of a wave makes the same number of rounds: the lanes of a head exchange sums
-  const int rounds = (heads - (wave % wpt) * (64 >> lsh) + step - 1) / step;
-  for (int r = 0; r < rounds; ++r, h += step) {
+  for (int r = h0; r < heads; r += step, h += step) {
     const bool here = live && h < heads;
     Raw<T> next{};
-    if (live && h + step < heads) next = raw_load(src(h + step), e0, e1);
+    if (live && h + step < heads) next = raw_load(head_at(q, k, v, h + step, Hq, Hqk, dh), e0, e1);
+    if (isq && h >= Hq) {  // the lane's heads have moved on to the keys
+      isq = false;
+      if (live) w.load(kwp, e0, e1);
+    }
     float x[16];
     raw_unpack<T>(cur, x);
-    const bool isq = h < Hq;
     if (isq ? qn : kn) {
       float ss = 0.f;
 #pragma unroll
@@ -166,7 +200,7 @@ __global__ __launch_bounds__(256) void k_norm_rope(NormRopeArgs a, int lsh, int 
       for (int d = 1; d < L; d *= 2) ss += __shfl_xor(ss, d);
       const float rs = rsqrtf(ss * inv_dh + a.eps);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = x[i] * rs * (isq ? qw[i] : kw[i]);
+      for (int i = 0; i < 16; ++i) x[i] = x[i] * rs * w.at(i);
     }
     if (rotates) {
 #pragma unroll
@@ -198,18 +232,20 @@ __global__ __launch_bounds__(256) void k_norm_rope(NormRopeArgs a, int lsh, int 
 hipError_t norm_rope(const NormRopeArgs& a) {
   int lsh = 0;
   while ((16 << lsh) < a.dh) ++lsh;
-  // Four waves on a token while that still leaves the chip short of waves (N tokens on 1024
-  // SIMDs); one wave per token past that, so that the angles of four tokens are one per thread.
-  const int wpt = a.N <= 2048 ? 4 : 1, tpb = 4 / wpt;
+  // Up to four waves on a token, as many as its heads fill, while that still leaves the chip short of
+  // waves (N tokens on 1024 SIMDs); one wave per token past that, so that the angles of four tokens
+  // are one per thread.
+  const int waves = (((a.Hq + a.Hkv + (a.Vc ? a.Hkv : 0)) << lsh) + 63) / 64;
+  const int wsh = a.N > 2048 || waves < 2 ? 0 : waves < 4 ? 1 : 2, tpb = 4 >> wsh;
   const dim3 grid(unsigned((a.N + tpb - 1) / tpb)), block(256);
   if (a.bf16 && a.interleaved)
-    hipLaunchKernelGGL((k_norm_rope<uint16_t, true>), grid, block, 0, a.stream, a, lsh, wpt);
+    hipLaunchKernelGGL((k_norm_rope<uint16_t, true>), grid, block, 0, a.stream, a, lsh, wsh);
   else if (a.bf16)
-    hipLaunchKernelGGL((k_norm_rope<uint16_t, false>), grid, block, 0, a.stream, a, lsh, wpt);
+    hipLaunchKernelGGL((k_norm_rope<uint16_t, false>), grid, block, 0, a.stream, a, lsh, wsh);
   else if (a.interleaved)
-    hipLaunchKernelGGL((k_norm_rope<float, true>), grid, block, 0, a.stream, a, lsh, wpt);
+    hipLaunchKernelGGL((k_norm_rope<float, true>), grid, block, 0, a.stream, a, lsh, wsh);
   else
-    hipLaunchKernelGGL((k_norm_rope<float, false>), grid, block, 0, a.stream, a, lsh, wpt);
+    hipLaunchKernelGGL((k_norm_rope<float, false>), grid, block, 0, a.stream, a, lsh, wsh);
   return hipGetLastError();
 }
 
