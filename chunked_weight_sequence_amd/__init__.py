@@ -507,30 +507,32 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = N
 def _rows(t, name: str, heads=None, dh=None, dtype=None, device=None, n=None):
     """Checks a [tokens, heads, dh] GPU tensor whose tokens may lie apart (a slice of one buffer);
     returns its token stride in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
     shape, stride = t.shape, t.stride()
     if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, dh], got {tuple(shape)}")
-    if (n is not None and shape[0] != n) or (heads is not None and shape[1] != heads) or \
-            (dh is not None and shape[2] != dh):
-        raise ValueError(f"{name} must be [{n}, {heads}, {dh}], got {tuple(shape)}")
-    if shape[0] >= 1 << 31:
-        raise ValueError(f"{name} has too many tokens: {shape[0]}")
-    if (shape[2] > 1 and stride[2] != 1) or (shape[1] > 1 and stride[1] != shape[2]):
+    N, H, D = shape
+    if device is None:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if N >= 1 << 31:
+            raise ValueError(f"{name} has too many tokens: {N}")
+    else:
+        if (n is not None and N != n) or (heads is not None and H != heads) or D != dh:
+            raise ValueError(f"{name} must be [{n}, {heads}, {dh}], got {tuple(shape)}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if (stride[2] != 1 and D > 1) or (stride[1] != D and H > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
+    return stride[0] if N > 1 else H * D
 
 
 def _vec(t, name: str, shape, dtype, device):
     """Checks a dense tensor of exactly this shape, dtype and device."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor on {device}, got "
                          f"{tuple(t.shape)} on {t.device}")
 
@@ -594,11 +596,13 @@ def qk_norm_rope(Q, K, pos, inv_freq, *, q_weight=None, k_weight=None, eps: floa
     elif V is not None or K_cache is not None or V_cache is not None:
         raise ValueError("V, K_cache and V_cache are for a call with slots")
     if Q_out is None:
-        Q_out = torch.empty((N, Hq, dh), dtype=dt, device=dev)
+        Q_out, qos = Q.new_empty((N, Hq, dh)), Hq * dh
+    else:
+        qos = _rows(Q_out, "Q_out", Hq, dh, dt, dev, N)
     if K_out is None:
-        K_out = torch.empty((N, Hkv, dh), dtype=dt, device=dev)
-    qos = _rows(Q_out, "Q_out", Hq, dh, dt, dev, N)
-    kos = _rows(K_out, "K_out", Hkv, dh, dt, dev, N)
+        K_out, kos = K.new_empty((N, Hkv, dh)), Hkv * dh
+    else:
+        kos = _rows(K_out, "K_out", Hkv, dh, dt, dev, N)
     _launch(lib().ttt_qk_norm_rope,
             (Q.data_ptr(), qs, K.data_ptr(), ks, _ptr(V), vs, code, _ptr(q_weight),
              _ptr(k_weight), eps, pos.data_ptr(), inv_freq.data_ptr() if half else None, 2 * half,
@@ -620,6 +624,8 @@ def attention_packed(Q, K, V, cu_q, cu_k=None, *, scale=None, window: int = 0, O
     dt, dev = Q.dtype, Q.device
     ks = _rows(K, "K", None, dh, dt, dev)
     Nk, Hkv, _ = K.shape
+    if Nk >= 1 << 31:
+        raise ValueError(f"K has too many tokens: {Nk}")
     vs = _rows(V, "V", Hkv, dh, dt, dev, Nk)
     n_seq = cu_q.shape[0] - 1
     _vec(cu_q, "cu_q", (n_seq + 1,), torch.int32, dev)
@@ -628,8 +634,9 @@ def attention_packed(Q, K, V, cu_q, cu_k=None, *, scale=None, window: int = 0, O
     else:
         _vec(cu_k, "cu_k", (n_seq + 1,), torch.int32, dev)
     if O is None:
-        O = torch.empty((Nq, Hq, dh), dtype=dt, device=dev)
-    os_ = _rows(O, "O", Hq, dh, dt, dev, Nq)
+        O, os_ = Q.new_empty((Nq, Hq, dh)), Hq * dh
+    else:
+        os_ = _rows(O, "O", Hq, dh, dt, dev, Nq)
     window = _int_in(window, "window", 0, 1 << 30)
     if lse is not None:
         _vec(lse, "lse", (Nq, Hq), torch.float32, dev)
@@ -665,8 +672,9 @@ def attention_decode(Q, K_cache, V_cache, page_table, lengths, page_size: int, *
     page_size = _int_in(page_size, "page_size", 1, 65536)
     window = _int_in(window, "window", 0, 1 << 30)
     if O is None:
-        O = torch.empty((S, Hq, dh), dtype=dt, device=dev)
-    os_ = _rows(O, "O", Hq, dh, dt, dev, S)
+        O, os_ = Q.new_empty((S, Hq, dh)), Hq * dh
+    else:
+        os_ = _rows(O, "O", Hq, dh, dt, dev, S)
     if lse is not None:
         _vec(lse, "lse", (S, Hq), torch.float32, dev)
     elif with_lse:
