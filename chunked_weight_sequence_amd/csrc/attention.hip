@@ -111,39 +111,6 @@ __device__ __forceinline__ void ap_rescale(f32x16& o, float f) {
     o[i] = x;
   }
 }
-// The same with the branch inside the assembly, for the round where the products that follow at once
-// would make the compiler copy the accumulator on both sides of a branch that it sees: o *= f
-// where any lane wants it (`lanes` not 0). The wait states in front let the last products
-// write it (8 passes: 11 needed), those behind let it settle for the next (2).
-__device__ __forceinline__ void ap_rescale_if(f32x16& o, float f, uint64_t lanes) {
-  float x[16], t;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = o[i];
-  asm volatile(
-      "s_cmp_eq_u64 %18, 0\n\ts_cbranch_scc1 1f\n\ts_nop 15\n\t"
-      "v_accvgpr_read_b32 %16, %0\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %0, %16\n\t"
-      "v_accvgpr_read_b32 %16, %1\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %1, %16\n\t"
-      "v_accvgpr_read_b32 %16, %2\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %2, %16\n\t"
-      "v_accvgpr_read_b32 %16, %3\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %3, %16\n\t"
-      "v_accvgpr_read_b32 %16, %4\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %4, %16\n\t"
-      "v_accvgpr_read_b32 %16, %5\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %5, %16\n\t"
-      "v_accvgpr_read_b32 %16, %6\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %6, %16\n\t"
-      "v_accvgpr_read_b32 %16, %7\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %7, %16\n\t"
-      "v_accvgpr_read_b32 %16, %8\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %8, %16\n\t"
-      "v_accvgpr_read_b32 %16, %9\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %9, %16\n\t"
-      "v_accvgpr_read_b32 %16, %10\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %10, %16\n\t"
-      "v_accvgpr_read_b32 %16, %11\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %11, %16\n\t"
-      "v_accvgpr_read_b32 %16, %12\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %12, %16\n\t"
-      "v_accvgpr_read_b32 %16, %13\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %13, %16\n\t"
-      "v_accvgpr_read_b32 %16, %14\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %14, %16\n\t"
-      "v_accvgpr_read_b32 %16, %15\n\tv_mul_f32 %16, %16, %17\n\tv_accvgpr_write_b32 %15, %16\n\t"
-      "s_nop 3\n1:"
-      : "+a"(x[0]), "+a"(x[1]), "+a"(x[2]), "+a"(x[3]), "+a"(x[4]), "+a"(x[5]), "+a"(x[6]), "+a"(x[7]), "+a"(x[8]), "+a"(x[9]), "+a"(x[10]), "+a"(x[11]), "+a"(x[12]), "+a"(x[13]), "+a"(x[14]), "+a"(x[15]), "=&v"(t)
-      : "v"(f), "s"(lanes)
-      : "scc");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = x[i];
-}
 // A copy that the compiler leaves where it stands (see ap_hide).
 __device__ __forceinline__ void ap_move(f32x16& to, const f32x16& from) {
 #pragma unroll
@@ -168,18 +135,19 @@ template <int N>
 __device__ __forceinline__ void ap_wait() { __builtin_amdgcn_s_waitcnt(0xC07F | (N << 8)); }
 __device__ __forceinline__ void ap_fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// How the 96 steps of a tile's exponentials (14 clocks each) are dealt out over the slots of a round:
-// in proportion to what a slot's product (33 clocks) leaves free beside its own issue, operand reads
-// and copies. at[k] .. at[k + 1]: slot k's steps (phase A, then the first three quarters of phase
-// B); at[0] of them come before the first product, while its operands are on their way from LDS.
-template <int KS, int DT, int NI>
+// How the 48 QT steps of a tile's exponentials (14 clocks each) are dealt out over the slots of a
+// round: in proportion to what a slot's product (33 clocks) leaves free beside its own issue, operand
+// reads and copies. at[k] .. at[k + 1]: slot k's steps (phase A, then the first three quarters of
+// phase B); at[0] of them come before the first product, while its operands are on their way from LDS.
+template <int KS, int DT, int NI, int QT>
 struct ApPlan {
-  static constexpr int SA = 4 * KS, SB = 8 * DT, OPS = 96, FIRST = 6;
+  static constexpr int SA = 2 * QT * KS, SB = 4 * QT * DT, OPS = 48 * QT, FIRST = 3 * QT;
   int at[SA + 3 * SB / 4 + 1];
   // slot of the i-th copy (V, then K)
   static constexpr int copy_slot(int i) { return 4 * (i / 3) + i % 3 + 1; }
   static constexpr int room(int k) {
-    int r = k < SA ? (k % 4 == 0 ? 14 : 28) : (k % 4 == 0 ? 6 : 28);
+    const bool reads = k % (2 * QT) == 0;
+    int r = k < SA ? (reads ? 14 : 28) : (reads ? 6 : 28);
     for (int i = 0; i < 2 * NI; ++i)
       if (k == copy_slot(i)) r = 8;
     return r;
@@ -193,14 +161,83 @@ struct ApPlan {
     }
     at[SA + 3 * SB / 4] = OPS;
   }
+  // the weights of the 16 keys that a quarter of phase B multiplies are ready when it begins
+  constexpr bool in_time() const {
+    for (int s = 0; s < 4; ++s)
+      if (at[SA + s * SB / 4] < 12 * QT * (s + 1)) return false;
+    return true;
+  }
 };
 
-template <int DH, int QT, bool PIPE>
-__global__ __launch_bounds__(256, PIPE ? 1 : 2) void k_attention_packed(PackedDev a) {
+// One row (token q, head `head`) over the keys [j0, j1) of the sequence that begins at k0, none of
+// them masked, by a whole wave: the scores of 64 keys, a key per lane, then their values, two
+// channels per lane. The tiles multiply masked values by a weight of 0, which an infinity or a NaN
+// among them turns into a NaN; so a row whose sums are not finite although its scores are is summed
+// again here. About 3000 clocks per 64 keys: 16384 tokens of 32/8 heads of 128 with one infinite
+// value in the last token take no longer than without it, with one in the first token, which every
+// row sees, APROWMS.
+template <int DH>
+__device__ __forceinline__ void ap_row(const PackedDev& a, int q, int head, int kvh, int k0, int j0, int j1,
+                                       int split, int lane) {
+  const float c = a.scale * kLog2e;
+  const uint4* qp = reinterpret_cast<const uint4*>(a.Q + q * a.qs + head * DH);
+  const int ch = 2 * (lane % (DH / 2));
+  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+  for (int j = j0; j < j1; j += 64) {
+    const uint4* kp =
+        reinterpret_cast<const uint4*>(a.K + (long(k0) + min(j + lane, j1 - 1)) * a.ks + kvh * DH);
+    float s = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < DH / 8; ++i) {
+      const uint4 x = qp[i], y = kp[i];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(bf2f(uint16_t(u[e])), bf2f(uint16_t(v[e])), s);
+        s = fmaf(bf2f(uint16_t(u[e] >> 16)), bf2f(uint16_t(v[e] >> 16)), s);
+      }
+    }
+    if (j + lane >= j1) s = -INFINITY;
+    float mn = fmaxf(m, s);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) mn = fmaxf(mn, __shfl_xor(mn, d));
+    const float base = mn == -INFINITY ? 0.f : mn * c;
+    const float al = exp2_fast(fmaf(m, c, -base)), p = exp2_fast(fmaf(s, c, -base));
+    m = mn;
+    l = l * al + p;
+    o0 *= al;
+    o1 *= al;
+    const int n = min(64, j1 - j);
+    const uint16_t* vp = a.V + (long(k0) + j) * a.vs + kvh * DH + ch;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(vp + i * a.vs);
+      const float w = bf2f(f2bf(__shfl(p, i)));
+      o0 = fmaf(w, bf2f(uint16_t(v)), o0);
+      o1 = fmaf(w, bf2f(uint16_t(v >> 16)), o1);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d);
+  const long rr = long(q) * a.Hq + head, n = long(a.Nq) * a.Hq;
+  if (lane >= DH / 2) return;
+  if (a.splits > 1) {
+    *reinterpret_cast<float2*>(a.part + (split * n + rr) * DH + ch) = make_float2(o0, o1);
+    if (lane == 0)
+      *reinterpret_cast<float2*>(a.part + a.splits * n * DH + (split * n + rr) * 2) = make_float2(m, l);
+  } else {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint32_t*>(a.O + q * a.os + head * DH + ch) = pack2bf(o0 * inv, o1 * inv);
+  }
+}
+
+template <int DH, int QT>
+__global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(PackedDev a) {
   constexpr int BM = 128 * QT, TILE = AP_BN * DH * 2, KS = DH / 16, DT = DH / 32;
-  // [stage][K / V]; then, PIPE only, one region per wave that holds its queries at the start and its
+  // [stage][K / V]; then, with 256 rows, one region per wave that holds its queries at the start and its
   // results at the end (otherwise they pass through a stage that is not in use)
-  __shared__ __align__(1024) char smem[4 * TILE + (PIPE ? BM * DH * 2 : 0)];
+  constexpr bool OWN = QT == 2;
+  __shared__ __align__(1024) char smem[4 * TILE + (OWN ? BM * DH * 2 : 0)];
   char(&sm)[2][2][TILE] = *reinterpret_cast<char(*)[2][2][TILE]>(smem);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int h = lane >> 5;
@@ -229,7 +266,7 @@ __global__ __launch_bounds__(256, PIPE ? 1 : 2) void k_attention_packed(PackedDe
   const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(smem));
   constexpr int WROWS = 32 * QT;                      // rows of a wave
   const int wrow = wave * WROWS;
-  char* const mine = smem + (PIPE ? 4 * TILE : 2 * TILE) + wrow * DH * 2;  // for the queries
+  char* const mine = smem + (OWN ? 4 * TILE : 2 * TILE) + wrow * DH * 2;  // for the queries
   // the lane's query column of each block: its last and first visible keys
   int hi[QT], lo[QT];
 #pragma unroll
@@ -255,7 +292,7 @@ __global__ __launch_bounds__(256, PIPE ? 1 : 2) void k_attention_packed(PackedDe
   // Copies: wave w fills tile rows 64 / 4 w .. in NI instructions of RPI rows. A row past the
   // sequence's last is replaced by that one (and masked). Offsets are 3 KB up, the bases 3 KB down,
   // so that no offset is negative when dma16_at adds its 1024 i.
-  constexpr int RPI = 1024 / (DH * 2), NI = AP_BN / RPI / 4, BACK = 3072;
+  constexpr int RPI = 1024 / (DH * 2), NI = AP_BN / RPI / 4, BACK = 3 * 1024;
   const int crow = wave * (AP_BN / 4) + lane / (64 / RPI), cp = lane % (64 / RPI);
   const uint32_t kstep = uint32_t(a.ks) * 2, vstep = uint32_t(a.vs) * 2;
   uint32_t koff[NI], voff[NI];
@@ -360,36 +397,17 @@ __global__ __launch_bounds__(256, PIPE ? 1 : 2) void k_attention_packed(PackedDe
     bool grow = false;  // each half of a query's lanes looks at its own keys
 #pragma unroll
     for (int b = 0; b < QT; ++b) grow = grow || mx[b] > most[b];
-    const uint64_t lanes = __ballot(grow);
-    if constexpr (PIPE) {
-      if (lanes) {
-        asm volatile("s_nop 15\n\ts_nop 15");  // the last products have written the accumulator
+    if (__any(grow)) {
+      asm volatile("s_nop 15\n\ts_nop 15");  // the last products have written the accumulator
 #pragma unroll
-        for (int b = 0; b < QT; ++b) {
-          const float al = move(mx, b);
-          l[b][0] *= al;
-          l[b][1] *= al;
+      for (int b = 0; b < QT; ++b) {
+        const float al = move(mx, b);
+        l[b][0] *= al;
+        l[b][1] *= al;
 #pragma unroll
-          for (int d = 0; d < DT; ++d) ap_rescale(o[d][b], al);
-        }
-        asm volatile("s_nop 7");  // written before a product reads it
+        for (int d = 0; d < DT; ++d) ap_rescale(o[d][b], al);
       }
-    } else {
-      float al[QT];
-#pragma unroll
-      for (int b = 0; b < QT; ++b) al[b] = 1.f;
-      if (lanes) {
-#pragma unroll
-        for (int b = 0; b < QT; ++b) {
-          al[b] = move(mx, b);
-          l[b][0] *= al[b];
-          l[b][1] *= al[b];
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < QT; ++b)
-#pragma unroll
-        for (int d = 0; d < DT; ++d) ap_rescale_if(o[d][b], al[b], lanes);
+      asm volatile("s_nop 7");  // written before a product reads it
     }
   };
 
@@ -411,7 +429,7 @@ __global__ __launch_bounds__(256, PIPE ? 1 : 2) void k_attention_packed(PackedDe
                 __builtin_amdgcn_readfirstlane(qdst + i * 1024));
     }
     each([&](auto i) AP_INLINE { copy_v(i, 0); });
-    if (PIPE && t0 < tlast) {
+    if (OWN && t0 < tlast) {
       kp += ktile;
       if (t0 + 1 == tlast) cut(koff, kstep);
       each([&](auto i) AP_INLINE { copy_k(i, 1); });
@@ -449,205 +467,174 @@ __global__ __launch_bounds__(256, PIPE ? 1 : 2) void k_attention_packed(PackedDe
   f32x16 s0[2][QT];
   using B0 = std::integral_constant<int, 0>;
   using B1 = std::integral_constant<int, 1>;
-  if constexpr (PIPE) {
-    // One round: the scores of the next tile (phase A) and the products with this tile's values
-    // (phase B) keep the matrix pipe busy while the exponentials of this tile, then the maxima of the
-    // next, are taken in the gaps. A slot is one product and its share of the other work, held
-    // together by fences; operands are read four products ahead. NEXT: there is a next tile, and
-    // phase A also copies K of the one after it and V of the next.
-    using Plan = ApPlan<KS, DT, NI>;
-    constexpr int SA = Plan::SA, SB = Plan::SB;
-    auto round = [&](auto next, auto buf, const char* kt, const char* vt, f32x16 (&s)[2][QT],
-                     f32x16 (&sn)[2][QT], float (&mx)[QT]) AP_INLINE {
-      constexpr bool NEXT = decltype(next)::value;
-      constexpr int BUF = decltype(buf)::value;
-      constexpr Plan plan{};
-      uint32_t pw[2][QT][8];  // bf16 pairs: [key block][query block]
-      float p0 = 0.f, p1 = 0.f;
-      auto op = [&](int n) AP_INLINE {  // unit n / 3: two neighbouring weights, in the order phase B takes them
-        const int u = n / 3, kb = u >> 4, b = (u >> 2) & 1, i = 8 * ((u >> 3) & 1) + 2 * (u & 3);
-        if (n % 3 == 0) p0 = exp2_fast(fmaf(s[kb][b][i], c, -base[b]));
-        if (n % 3 == 1) p1 = exp2_fast(fmaf(s[kb][b][i + 1], c, -base[b]));
-        if (n % 3 == 2) {
-          pw[kb][b][i / 2] = pack2bf(p0, p1);
-          l[b][0] += p0;
-          l[b][1] += p1;
-          asm volatile("" : "+v"(l[b][0]), "+v"(l[b][1]));  // here, not behind the round
-        }
-      };
-      uint4 kf[2][2], vf[2][2];
-      if (NEXT) {
-        kf[0][0] = fo.key(kt, 0, 0);
-        kf[0][1] = fo.key(kt, 1, 0);
-        ap_fence();
-      } else {
-        vf[0][0] = fo.value(vt, 0, 0);
-        vf[0][1] = fo.value(vt, 0, 1);
+  // One round: the scores of the next tile (phase A) and the products with this tile's values
+  // (phase B) keep the matrix pipe busy while the exponentials of this tile, then the maxima of the
+  // next, are taken in the gaps. A slot is one product and its share of the other work, held
+  // together by fences; operands are read four products ahead. NEXT: there is a next tile, and
+  // phase A also copies K of the one after it and V of the next.
+  using Plan = ApPlan<KS, DT, NI, QT>;
+  static_assert(Plan().in_time(), "a product before its operand");
+  constexpr int SA = Plan::SA, SB = Plan::SB;
+  auto round = [&](auto next, auto buf, const char* kt, const char* vt, f32x16 (&s)[2][QT],
+                   f32x16 (&sn)[2][QT], float (&mx)[QT]) AP_INLINE {
+    constexpr bool NEXT = decltype(next)::value;
+    constexpr int BUF = decltype(buf)::value;
+    constexpr Plan plan{};
+    uint32_t pw[2][QT][8];  // bf16 pairs: [key block][query block]
+    float p0 = 0.f, p1 = 0.f;
+    auto op = [&](int n) AP_INLINE {  // unit n / 3: two neighbouring weights, in the order phase B takes them
+      const int u = n / 3, st = u / (4 * QT), kb = st >> 1, b = (u >> 2) % QT, i = 8 * (st & 1) + 2 * (u & 3);
+      if (n % 3 == 0) p0 = exp2_fast(fmaf(s[kb][b][i], c, -base[b]));
+      if (n % 3 == 1) p1 = exp2_fast(fmaf(s[kb][b][i + 1], c, -base[b]));
+      if (n % 3 == 2) {
+        pw[kb][b][i / 2] = pack2bf(p0, p1);
+        l[b][0] += p0;
+        l[b][1] += p1;
+        asm volatile("" : "+v"(l[b][0]), "+v"(l[b][1]));  // here, not behind the round
       }
-#pragma unroll
-      for (int n = 0; n < (NEXT ? plan.at[0] : plan.at[SA]); ++n) op(n);
-      if (NEXT) {
-#pragma unroll
-        for (int k = 0; k < SA; ++k) {
-          const int ks = k / 4, kb = (k >> 1) & 1, b = k & 1;
-          ap_fence();
-          if (k % 4 == 0) {
-            if (ks + 1 < KS) {
-              kf[(ks + 1) & 1][0] = fo.key(kt, 0, ks + 1);
-              kf[(ks + 1) & 1][1] = fo.key(kt, 1, ks + 1);
-              ap_wait<2>();
-            } else {
-              vf[0][0] = fo.value(vt, 0, 0);
-              vf[0][1] = fo.value(vt, 0, 1);
-              ap_wait<4>();
-            }
-            ap_fence();
-          }
-          if (ks == 0) ap_mma0(sn[kb][b], kf[0][kb], qf[b][0]);
-          else ap_mma(sn[kb][b], kf[ks & 1][kb], qf[b][ks]);
-          each([&](auto i) AP_INLINE {
-            if (k == Plan::copy_slot(decltype(i)::value)) copy_v(i, BUF ^ 1);
-            if (k == Plan::copy_slot(NI + decltype(i)::value)) copy_k(i, BUF);
-          });
-#pragma unroll
-          for (int n = plan.at[k]; n < plan.at[k + 1]; ++n) op(n);
-        }
-      }
-      float m2[QT] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int k = 0; k < SB; ++k) {
-        constexpr int PW = SB / 4, SE = 3 * PW;  // slots per 16 keys; slots with exponentials
-        const int st = k / PW, d = (k % PW) >> 1, b = k & 1, pr = k / 4;
-        ap_fence();
-        if (k % 4 == 0) {
-          if (pr + 1 < SB / 4) {
-            const int st1 = (k + 4) / PW, d1 = ((k + 4) % PW) >> 1;
-            vf[(pr + 1) & 1][0] = fo.value(vt, st1, d1);
-            vf[(pr + 1) & 1][1] = fo.value(vt, st1, d1 + 1);
-            ap_wait<4>();
-          } else {
-            ap_wait<0>();
-          }
-          ap_fence();
-        }
-        if (NEXT && k == SE) {
-          ap_settle<false>(sn);
-          ap_fence();
-        }
-        const uint32_t* w = &pw[st >> 1][b][4 * (st & 1)];
-        o[d][b] = mfma32x32x16(vf[pr & 1][d & 1], make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
-        if (k < SE) {
-#pragma unroll
-          for (int n = plan.at[SA + k]; n < plan.at[SA + k + 1]; ++n) op(n);
-        } else if (NEXT) {
-          constexpr int PER = 64 / PW;  // values of the next scores per slot
-          const int e0 = (k - SE) * PER, q = e0 >> 5;
-#pragma unroll
-          for (int e = e0; e < e0 + PER; e += 2)
-            m2[q] = fmaxf(fmaxf(m2[q], sn[(e >> 4) & 1][q][e & 15]), sn[(e >> 4) & 1][q][(e & 15) + 1]);
-          asm volatile("" : "+v"(m2[q]));  // here, not behind the phase
-        }
-      }
+    };
+    uint4 kf[2][2], vf[2][2];
+    if (NEXT) {
+      kf[0][0] = fo.key(kt, 0, 0);
+      kf[0][1] = fo.key(kt, 1, 0);
       ap_fence();
-      mx[0] = m2[0];
-      mx[1] = m2[1];
-    };
-
-    // K of tile t + 1 and V of tile t are in LDS when round t begins
-    f32x16 s1[2][QT];
-    auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) AP_INLINE {
-      constexpr int B = decltype(buf)::value;
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      vp += vtile;
-      if (t + 2 < t1) kp += ktile;
-      if (t + 2 >= tlast) {
-        if (t + 2 == tlast) cut(koff, kstep);
-        if (t + 1 == tlast) cut(voff, vstep);
-      }
-      round(std::true_type(), buf, &sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx);
-      mask(t + 1, sn, mx);
-      rebase(mx);
-    };
-    if (t0 < t1) {
-      asm volatile("s_barrier" ::: "memory");  // every wave's part of the first K tile is there
-      scores(&sm[0][0][0], s0);
-      maxima(s0, mx);
-      mask(t0, s0, mx);
-#pragma unroll
-      for (int b = 0; b < QT; ++b) move(mx, b);
+    } else {
+      vf[0][0] = fo.value(vt, 0, 0);
+      vf[0][1] = fo.value(vt, 0, 1);
     }
-    for (int t = t0; t + 1 < t1; t += 2) {
-      step(t, B0(), s0, s1);
-      if (t + 2 < t1) {
-        step(t + 1, B1(), s1, s0);
-      } else {
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+    for (int n = 0; n < (NEXT ? plan.at[0] : plan.at[SA]); ++n) op(n);
+    if (NEXT) {
 #pragma unroll
-          for (int b = 0; b < QT; ++b) ap_move(s0[kb][b], s1[kb][b]);
-      }
-    }
-    if (t0 < t1) {  // the last tile
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      const char* vt = &sm[(t1 - 1 - t0) & 1][1][0];
-      round(std::false_type(), B0(), vt, vt, s0, s1, mx);
-    }
-  } else {
-    // Two workgroups on a compute unit: while one wave of a SIMD takes exponentials, the other's
-    // products run.
-    for (int t = t0; t < t1; ++t) {
-      const int B = (t - t0) & 1;
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      if (t < tlast) {
-        kp += ktile;
-        vp += vtile;
-        if (t + 1 == tlast) {
-          cut(koff, kstep);
-          cut(voff, vstep);
+      for (int k = 0; k < SA; ++k) {
+        const int ks = k / (2 * QT), kb = (k / QT) & 1, b = k % QT;
+        ap_fence();
+        if (k % (2 * QT) == 0) {
+          if (ks + 1 < KS) {
+            kf[(ks + 1) & 1][0] = fo.key(kt, 0, ks + 1);
+            kf[(ks + 1) & 1][1] = fo.key(kt, 1, ks + 1);
+            ap_wait<2>();
+          } else {
+            vf[0][0] = fo.value(vt, 0, 0);
+            vf[0][1] = fo.value(vt, 0, 1);
+            ap_wait<4>();
+          }
+          ap_fence();
         }
-        each([&](auto i) AP_INLINE { copy_k(i, B ^ 1); });
-        each([&](auto i) AP_INLINE { copy_v(i, B ^ 1); });
-      }
-      scores(&sm[B][0][0], s0);
-      maxima(s0, mx);
-      mask(t, s0, mx);
-      rebase(mx);
-      const char* vt = &sm[B][1][0];
+        if (ks == 0) ap_mma0(sn[kb][b], kf[0][kb], qf[b][0]);
+        else ap_mma(sn[kb][b], kf[ks & 1][kb], qf[b][ks]);
+        each([&](auto i) AP_INLINE {
+          if (k == Plan::copy_slot(decltype(i)::value)) copy_v(i, BUF ^ 1);
+          if (k == Plan::copy_slot(NI + decltype(i)::value)) copy_k(i, BUF);
+        });
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        uint32_t pw[QT][8];
-#pragma unroll
-        for (int b = 0; b < QT; ++b)
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float p0 = exp2_fast(fmaf(s0[kb][b][i], c, -base[b]));
-            const float p1 = exp2_fast(fmaf(s0[kb][b][i + 1], c, -base[b]));
-            l[b][0] += p0;
-            l[b][1] += p1;
-            pw[b][i / 2] = pack2bf(p0, p1);
-          }
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const uint4 vf = fo.value(vt, 2 * kb + st, d);
-#pragma unroll
-            for (int b = 0; b < QT; ++b) {
-              const uint32_t* w = &pw[b][4 * st];
-              o[d][b] = mfma32x32x16(vf, make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
-            }
-          }
+        for (int n = plan.at[k]; n < plan.at[k + 1]; ++n) op(n);
       }
     }
+    float m2[QT];
+#pragma unroll
+    for (int b = 0; b < QT; ++b) m2[b] = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < SB; ++k) {
+      constexpr int PW = SB / 4, SE = 3 * PW;  // slots per 16 keys; slots with exponentials
+      const int st = k / PW, d = (k % PW) / QT, b = k % QT, pr = k / (2 * QT);
+      ap_fence();
+      if (k % (2 * QT) == 0) {
+        if (pr + 1 < SB / (2 * QT)) {
+          const int st1 = (k + 2 * QT) / PW, d1 = ((k + 2 * QT) % PW) / QT;
+          vf[(pr + 1) & 1][0] = fo.value(vt, st1, d1);
+          vf[(pr + 1) & 1][1] = fo.value(vt, st1, d1 + 1);
+          ap_wait<4>();
+        } else {
+          ap_wait<0>();
+        }
+        ap_fence();
+      }
+      if (NEXT && k == SE) {
+        ap_settle<false>(sn);
+        ap_fence();
+      }
+      const uint32_t* w = &pw[st >> 1][b][4 * (st & 1)];
+      o[d][b] = mfma32x32x16(vf[pr & 1][d & 1], make_uint4(w[0], w[1], w[2], w[3]), o[d][b]);
+      if (k < SE) {
+#pragma unroll
+        for (int n = plan.at[SA + k]; n < plan.at[SA + k + 1]; ++n) op(n);
+      } else if (NEXT) {
+        constexpr int PER = 32 * QT / PW;  // values of the next scores per slot
+        const int e0 = (k - SE) * PER, q = e0 >> 5;
+#pragma unroll
+        for (int e = e0; e < e0 + PER; e += 2)
+          m2[q] = fmaxf(fmaxf(m2[q], sn[(e >> 4) & 1][q][e & 15]), sn[(e >> 4) & 1][q][(e & 15) + 1]);
+        asm volatile("" : "+v"(m2[q]));  // here, not behind the phase
+      }
+    }
+    ap_fence();
+#pragma unroll
+    for (int b = 0; b < QT; ++b) mx[b] = m2[b];
+  };
+
+  // K of tile t + 1 and V of tile t are in LDS when round t begins
+  f32x16 s1[2][QT];
+  auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) AP_INLINE {
+    constexpr int B = decltype(buf)::value;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    vp += vtile;
+    if (t + 2 < t1) kp += ktile;
+    if (t + 2 >= tlast) {
+      if (t + 2 == tlast) cut(koff, kstep);
+      if (t + 1 == tlast) cut(voff, vstep);
+    }
+    round(std::true_type(), buf, &sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx);
+    mask(t + 1, sn, mx);
+    rebase(mx);
+  };
+  if (t0 < t1) {
+    // every wave's part of the first K tile is there, every wave has its queries
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (!OWN && t0 < tlast) {
+      kp += ktile;
+      if (t0 + 1 == tlast) cut(koff, kstep);
+      each([&](auto i) AP_INLINE { copy_k(i, 1); });
+    }
+    scores(&sm[0][0][0], s0);
+    maxima(s0, mx);
+    mask(t0, s0, mx);
+#pragma unroll
+    for (int b = 0; b < QT; ++b) move(mx, b);
+  }
+  for (int t = t0; t + 1 < t1; t += 2) {
+    step(t, B0(), s0, s1);
+    if (t + 2 < t1) {
+      step(t + 1, B1(), s1, s0);
+    } else {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int b = 0; b < QT; ++b) ap_move(s0[kb][b], s1[kb][b]);
+    }
+  }
+  if (t0 < t1) {  // the last tile
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const char* vt = &sm[(t1 - 1 - t0) & 1][1][0];
+    round(std::false_type(), B0(), vt, vt, s0, s1, mx);
   }
 
   // Results. Partial ones go out as they are; others by way of LDS, in whole rows: chunk c (16 bytes)
   // of a row at slot c ^ (row % (chunks of a row)).
   constexpr int CH = DH / 8;
-  char* const out = PIPE ? mine : smem + (((t1 - t0) & 1) ? 2 * TILE : 0) + wrow * DH * 2;
+  char* const out = OWN ? mine : smem + (((t1 - t0) & 1) ? 2 * TILE : 0) + wrow * DH * 2;
+  uint64_t again[QT];  // lanes whose columns have to be summed again
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
     const float lt = sum_halves(l[b][0] + l[b][1]);
+    // A value that a row does not see has the weight 0 in its products, and 0 times an infinity or a
+    // NaN is no 0: see ap_row.
+    float zero = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) zero = fmaf(o[d][b][i], 0.f, zero);
+    again[b] = __ballot(zero != 0.f && lt == lt && wrow + 32 * b + (lane & 31) < rows_here);
     const int r = 32 * b + (lane & 31), x = wrow + r, qi = query(x);
     const bool on = x < rows_here;
     const long rr = long(q0 + qa + qi) * a.Hq + kvh * G + first + x - qi * G;
@@ -677,61 +664,79 @@ __global__ __launch_bounds__(256, PIPE ? 1 : 2) void k_attention_packed(PackedDe
                        pack2bf(o[d][b][i + 2] * inv, o[d][b][i + 3] * inv));
     if (a.lse && h == 0 && on) a.lse[rr] = lt == 0.f ? -INFINITY : m[b] * a.scale + __logf(lt);
   }
-  if (a.splits > 1) return;
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  uint16_t* Oh = a.O + long(q0 + qa) * a.os + long(kvh) * G * DH;
+  if (a.splits == 1) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    uint16_t* Oh = a.O + long(q0 + qa) * a.os + long(kvh) * G * DH;
 #pragma unroll
-  for (int i = 0; i < WROWS / RPI; ++i) {
-    const int r = i * RPI + lane / (64 / RPI), x = wrow + r;
-    const uint4 v = *reinterpret_cast<const uint4*>(out + r * DH * 2 + ((cp ^ (r % CH)) << 4));
-    if (x < rows_here) *reinterpret_cast<uint4*>(Oh + element(x, uint32_t(a.os)) + 8 * cp) = v;
+    for (int i = 0; i < WROWS / RPI; ++i) {
+      const int r = i * RPI + lane / (64 / RPI), x = wrow + r;
+      const uint4 v = *reinterpret_cast<const uint4*>(out + r * DH * 2 + ((cp ^ (r % CH)) << 4));
+      if (x < rows_here) *reinterpret_cast<uint4*>(Oh + element(x, uint32_t(a.os)) + 8 * cp) = v;
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < QT; ++b) {
+    uint32_t rest = uint32_t(again[b] | again[b] >> 32);
+    if (rest) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what is written over is there
+    while (rest) {
+      const int x = wrow + 32 * b + __builtin_ctz(rest);
+      rest &= rest - 1;
+      const int qi = qa + query(x), head = kvh * G + first + x - (qi - qa) * G;
+      const int to = qi + off, from = a.window > 0 ? max(to - a.window + 1, 0) : 0;
+      ap_row<DH>(a, q0 + qi, head, kvh, k0, max(from, t0 * AP_BN), min(to + 1, t1 * AP_BN), split, lane);
+    }
   }
 }
 
 }  // namespace
 
-// What a call launches: rows per workgroup (256: the pipelined kernel, one workgroup to a compute
-// unit; 128: the other, two) and pieces of the key axis.
+// What a call launches: rows per workgroup (128 QT) and pieces of the key axis.
 namespace {
 struct PackedPlan {
-  bool pipe;
-  int tiles, splits;
+  int qt, tiles, splits;
 };
-// Pieces that the keys of a row are split into: as many workgroups as the chip has places for, where
-// row tiles alone are fewer, as long as a piece has 320 keys of an average row (5 tiles, about 5 us;
-// joining costs about 4 us: 1024 tokens, one sequence, 32/8 heads of 128: 31 us unsplit, 37 us split
-// in pieces of 256; 512 tokens after 15872: 323 us unsplit, 122 us split).
-int packed_splits(bool pipe, long rows, int n_seq, int Hkv, long seen) {
-  const int BM = pipe ? 256 : 128;
-  const long wgs = ((rows + BM - 1) / BM + n_seq - 1) * Hkv;
-  long n = (pipe ? 256 : 512) / wgs;
-  if (n > seen / 320) n = seen / 320;
-  return int(n < 1 ? 1 : n > 64 ? 64 : n);
-}
 // Keys that an average row sees.
 long packed_seen(int n_seq, int Nq, int Nk, int window) {
   const long seen = (Nk > Nq / 2 ? Nk - Nq / 2 : Nk) / n_seq;
   return window > 0 && window < seen ? window : seen;
 }
+// Workgroups that have rows, if the sequences are alike; the chip holds 512 / QT of them.
+long packed_wgs(int qt, int n_seq, int Nq, int Hq, int Hkv) {
+  const long rows = long(Nq) * (Hq / Hkv), BM = 128 * qt;
+  return ((rows + BM - 1) / BM + n_seq - 1) * Hkv;
+}
+// Pieces that the keys of a row are split into: as many workgroups as the chip has places for, where
+// row tiles alone are fewer, as long as a piece has 320 keys of an average row (5 tiles, about 5 us;
+// joining costs about 4 us: 1024 tokens, one sequence, 32/8 heads of 128: 31 us unsplit, 37 us split
+// in pieces of 256; 512 tokens after 15872: 323 us unsplit, 122 us split).
+int packed_splits(int qt, int n_seq, int Nq, int Nk, int Hq, int Hkv, int window) {
+  long n = 512 / qt / packed_wgs(qt, n_seq, Nq, Hq, Hkv);
+  const long most = packed_seen(n_seq, Nq, Nk, window) / 320;
+  if (n > most) n = most;
+  return int(n < 1 ? 1 : n > 64 ? 64 : n);
+}
 PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
-  PackedPlan p;
-  const long rows = long(Nq) * (Hq / Hkv), seen = packed_seen(n_seq, Nq, Nk, window);
-  // The pipelined kernel starts and ends slowly (14000 clocks that nothing overlaps; a tile takes it
-  // 2900): heads of 128 and rows of at least 320 keys. Measured, pipelined against not, 32/8 heads
-  // of 128: 16384 tokens 1.74 / 2.07 ms, 11 documents in 8192 tokens 110 / 121 us, 40 in 4096 37 /
-  // 31 us, 9000 tokens with a window of 128 76 / 57 us. Heads of 64, which the vector unit bounds:
-  // 8191 tokens, window 2048, 188 / 150 us.
-  p.pipe = dh == 128 && seen >= 320 && rows > 128;
-  p.tiles = int(rows / (p.pipe ? 256 : 128)) + n_seq;
-  p.splits = packed_splits(p.pipe, rows, n_seq, Hkv, seen);
+  // 256 rows share each tile read from LDS, which costs least power (long rows are bound by that), but
+  // leave the chip's 256 places unevenly filled and nothing to run while a workgroup starts and ends
+  // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least
+  // 9 of 10 places. Measured, 256 rows against 128, 32/8 heads of 128: 16384 tokens 1.76 / 1.87 ms,
+  // 512 after 15872 127 / 134 us, but 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105
+  // us, 12000 tokens of 4/1 heads in 2 documents 205 / 153 us. Heads of 64, which the vector unit
+  // bounds: 8191 tokens, window 2048, 188 / 145 us.
+  PackedPlan p{1, 0, 1};
+  if (dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
+    const long n = packed_wgs(2, n_seq, Nq, Hq, Hkv) * packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, window);
+    if (10 * n >= 9 * 256 * ((n + 255) / 256)) p.qt = 2;
+  }
+  p.tiles = int(long(Nq) * (Hq / Hkv) / (128 * p.qt)) + n_seq;
+  p.splits = packed_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, window);
   return p;
 }
 }  // namespace
 
 size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh) {
   // the window is not known here: the most that any choice takes
-  const long rows = long(Nq) * (Hq / Hkv), seen = packed_seen(n_seq, Nq, Nk, 0);
-  const int a = packed_splits(true, rows, n_seq, Hkv, seen), b = packed_splits(false, rows, n_seq, Hkv, seen);
+  const int a = packed_splits(1, n_seq, Nq, Nk, Hq, Hkv, 0), b = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, 0);
   const int n = a > b ? a : b;
   return n > 1 ? size_t(n) * Nq * Hq * (dh + 2) * 4 : 0;
 }
@@ -744,12 +749,12 @@ hipError_t attention_packed(const PackedArgs& a) {
                     a.Hq, a.Hkv, a.Hq / a.Hkv, a.scale, a.window, p.tiles, p.splits,
                     static_cast<float*>(a.ws)};
   const dim3 grid(unsigned(p.tiles) * a.Hkv * p.splits);
-  if (a.dh == 128 && p.pipe)
-    hipLaunchKernelGGL((k_attention_packed<128, 2, true>), grid, dim3(256), 0, a.stream, d);
+  if (p.qt == 2)
+    hipLaunchKernelGGL((k_attention_packed<128, 2>), grid, dim3(256), 0, a.stream, d);
   else if (a.dh == 128)
-    hipLaunchKernelGGL((k_attention_packed<128, 1, false>), grid, dim3(256), 0, a.stream, d);
+    hipLaunchKernelGGL((k_attention_packed<128, 1>), grid, dim3(256), 0, a.stream, d);
   else
-    hipLaunchKernelGGL((k_attention_packed<64, 1, false>), grid, dim3(256), 0, a.stream, d);
+    hipLaunchKernelGGL((k_attention_packed<64, 1>), grid, dim3(256), 0, a.stream, d);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   return attention_join(d.part, p.splits, a.cu_q, a.n_seq, long(a.Nq) * a.Hq, a.Hq, a.dh, a.O, a.os,
