@@ -700,43 +700,60 @@ long packed_seen(int n_seq, int Nq, int Nk, int window) {
   const long seen = (Nk > Nq / 2 ? Nk - Nq / 2 : Nk) / n_seq;
   return window > 0 && window < seen ? window : seen;
 }
-// Workgroups that have rows, if the sequences are alike; the chip holds 512 / QT of them.
+// Workgroups that have rows, if the sequences are alike.
 long packed_wgs(int qt, int n_seq, int Nq, int Hq, int Hkv) {
   const long rows = long(Nq) * (Hq / Hkv), BM = 128 * qt;
   return ((rows + BM - 1) / BM + n_seq - 1) * Hkv;
 }
-// Pieces that the keys of a row are split into: as many workgroups as the chip has places for, where
-// row tiles alone are fewer, as long as a piece has 320 keys of an average row (5 tiles, about 5 us;
-// joining costs about 4 us: 1024 tokens, one sequence, 32/8 heads of 128: 31 us unsplit, 37 us split
-// in pieces of 256; 512 tokens after 15872: 323 us unsplit, 122 us split).
-int packed_splits(int qt, int n_seq, int Nq, int Nk, int Hq, int Hkv, int window) {
-  long n = 512 / qt / packed_wgs(qt, n_seq, Nq, Hq, Hkv);
-  const long most = packed_seen(n_seq, Nq, Nk, window) / 320;
-  if (n > most) n = most;
-  return int(n < 1 ? 1 : n > 64 ? 64 : n);
+// Pieces that the keys of a row are split into, if row tiles alone leave compute units free: the number that
+// makes the longest row's tiles (0.75 us each, 1.5 with 256 rows, 0.5 for heads of 64) and the joining
+// (5 us, and the partial sums written and read at 4 TB/s) cost least, each piece at least 256 keys.
+// Measured, 32/8 heads of 128: 512 tokens after 15872, 323 us whole, 125 us in 4; 64 tokens after 16000,
+// 35 us in 32 pieces, 31 us in 16; 1024 tokens 20 us whole, 35 us in 2; 2048 tokens of 8/4 heads of 64
+// 24 us whole, 28 us in 2.
+int packed_splits(int qt, int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
+  long keys = Nk / n_seq;
+  if (window > 0 && window < keys) keys = window;
+  // a compute unit each, where a workgroup counts for as much as an average row has of the longest
+  const long seen = packed_seen(n_seq, Nq, Nk, window);
+  long most = 256 * keys / (packed_wgs(qt, n_seq, Nq, Hq, Hkv) * (seen < 1 ? 1 : seen));
+  if (most > keys / 256) most = keys / 256;
+  if (most > 64) most = 64;
+  const double tiles = keys / 64 * (qt == 2 ? 1.5 : dh == 64 ? 0.5 : 0.75);
+  const double join = double(Nq) * Hq * dh * 8 / 4e6;
+  int best = 1;
+  double cost = tiles;
+  for (int n = 2; n <= most; ++n) {
+    const double t = tiles / n + 5 + n * join;
+    if (t < cost) cost = t, best = n;
+  }
+  return best;
 }
 PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
   // 256 rows share each tile read from LDS, which costs least power (long rows are bound by that), but
   // leave the chip's 256 places unevenly filled and nothing to run while a workgroup starts and ends
   // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least
-  // 9 of 10 places. Measured, 256 rows against 128, 32/8 heads of 128: 16384 tokens 1.76 / 1.87 ms,
-  // 512 after 15872 127 / 134 us, but 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105
-  // us, 12000 tokens of 4/1 heads in 2 documents 205 / 153 us. Heads of 64, which the vector unit
-  // bounds: 8191 tokens, window 2048, 188 / 145 us.
+  // 9 of 10 places, in pieces of at least 1024. Measured, 256 rows against 128, 32/8 heads of 128: 16384 tokens
+  // 1.76 / 1.87 ms, 512 after 15872 126 / 138 us, 256 after 16000 75 / 80 us; but 64 after 16000 37 / 31
+  // us, 200 after 4000 31 / 28 us, 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105 us, 12000 tokens of 4/1 heads in
+  // 2 documents 205 / 153 us. Heads of 64, which the vector unit bounds: 8191 tokens, window 2048,
+  // 188 / 145 us.
   PackedPlan p{1, 0, 1};
   if (dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
-    const long n = packed_wgs(2, n_seq, Nq, Hq, Hkv) * packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, window);
-    if (10 * n >= 9 * 256 * ((n + 255) / 256)) p.qt = 2;
+    const int pieces = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, window);
+    const long n = packed_wgs(2, n_seq, Nq, Hq, Hkv) * pieces;
+    if (packed_seen(n_seq, Nq, Nk, window) >= 1024 * pieces && 10 * n >= 9 * 256 * ((n + 255) / 256)) p.qt = 2;
   }
   p.tiles = int(long(Nq) * (Hq / Hkv) / (128 * p.qt)) + n_seq;
-  p.splits = packed_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, window);
+  p.splits = packed_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
   return p;
 }
 }  // namespace
 
 size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh) {
-  // the window is not known here: the most that any choice takes
-  const int a = packed_splits(1, n_seq, Nq, Nk, Hq, Hkv, 0), b = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, 0);
+  // the window is not known here; with one there are no more pieces than without
+  const int a = packed_splits(1, n_seq, Nq, Nk, Hq, Hkv, dh, 0);
+  const int b = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, 0);
   const int n = a > b ? a : b;
   return n > 1 ? size_t(n) * Nq * Hq * (dh + 2) * 4 : 0;
 }

@@ -34,12 +34,6 @@ __device__ __forceinline__ uint2 tr_read(const char* p) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p));
 }
 
-// Value of the lane 32 away.
-__device__ __forceinline__ float other_half(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  // r[0]: the low half's values in both halves; r[1]: the high half's
-  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
-}
 __device__ __forceinline__ float max_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
@@ -76,21 +70,6 @@ struct FragOff {
     const uint2 lo = tr_read(tile + v[dt] + s * 16 * DH * 2);
     const uint2 hi = tr_read(tile + v[dt] + (s * 16 + 8) * DH * 2);
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
-  }
-};
-
-// The wave's share of copying `ROWS` rows of K or V into LDS: NW waves, copy i of wave w fills
-// 1 KB at (i * NW + w) KB.
-template <int DH, int ROWS, int NW, bool IS_V>
-struct TileCopy {
-  static constexpr int RPI = 1024 / (DH * 2);        // rows per copy instruction
-  static constexpr int N = ROWS / RPI / NW;          // instructions per wave
-  __device__ __forceinline__ static int row(int i, int wave, int lane) {
-    return (i * NW + wave) * RPI + lane / (64 / RPI);
-  }
-  __device__ __forceinline__ static uint32_t chunk(int i, int wave, int lane) {
-    const int r = row(i, wave, lane), p = lane % (64 / RPI);
-    return uint32_t(p ^ (IS_V ? vsw<DH>(r) : ksw<DH>(r))) << 4;
   }
 };
 

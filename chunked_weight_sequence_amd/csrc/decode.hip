@@ -8,11 +8,13 @@
 //
 // Bound by HBM: every visible K and V row is read once. A workgroup takes a piece of one
 // sequence and one key head, with up to 32 of the query heads that share it as the columns of
-// S^T (attn.hpp); its 4 waves walk 32-key tiles independently, each through its own two-stage LDS
+// S^T (attn.hpp); its 2 or 4 waves walk 32-key tiles independently, each through its own two-stage LDS
 // ring of direct copies (no barrier in the loop), and join their sums through LDS at the end.
 // Copies are whole rows, so each instruction reads 1 KB in full lines. Rows that are masked
 // (behind the last token, before the window) are replaced by a visible row of the tile in the
 // copy itself: what lies in them, NaN included, never enters a product.
+#include <type_traits>
+
 #include "attn.hpp"
 #include "launch.hpp"
 
@@ -44,12 +46,12 @@ struct DecodeDev {
 // wait for every copy in flight, since the vector-memory counter counts them together.
 typedef const __attribute__((address_space(4))) int const_int;
 
-template <int DH>
-__global__ __launch_bounds__(256, 1) void k_attention_decode(DecodeDev a) {
+template <int DH, int W>
+__global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
   constexpr int TILE = DC_BN * DH * 2, KS = DH / 16, DT = DH / 32, RPI = 1024 / (DH * 2);
   constexpr int NI = 16 / RPI;  // copies per 16-token half of a tile
-  __shared__ __align__(1024) char sm[4][2][2][TILE];  // wave, stage, K / V
-  __shared__ float2 ml_s[4][32];
+  __shared__ __align__(1024) char sm[W][2][2][TILE];  // wave, stage, K / V
+  __shared__ float2 ml_s[W][32];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int h = lane >> 5, col = lane & 31;
   int id = blockIdx.x;
@@ -82,7 +84,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_decode(DecodeDev a) {
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32(&sm[wave][0][0][0]));
   const int lrow = lane / (64 / RPI), lchunk = lane % (64 / RPI);
   // Copies tile t into a stage; returns which 16-token halves exist (bit 0, bit 1).
-  auto issue = [&](int t, int stage) {
+  auto issue = [&](int t, int stage) __attribute__((always_inline)) {
     int good = 0;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
@@ -99,13 +101,25 @@ __global__ __launch_bounds__(256, 1) void k_attention_decode(DecodeDev a) {
       const char* vb = ok ? a.Vc + at : reinterpret_cast<const char*>(dc_zeros);
       const uint32_t rb = ok ? rowb : 0;
       const uint32_t dst = lds0 + stage * 2 * TILE + hf * (TILE / 2);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = 16 * hf + i * RPI + lrow;  // row of the tile
-        const uint32_t o = uint32_t(min(max(t * DC_BN + r, lo), hi) - lo) * rb;
-        dma16(o + uint32_t((lchunk ^ ksw<DH>(r)) << 4), kb, dst + i * 1024);
-        dma16(o + uint32_t((lchunk ^ vsw<DH>(r)) << 4), vb, dst + TILE + i * 1024);
-      }
+      // the instruction adds 1024 i to both addresses: that much less here, and 3 KB more, which the
+      // bases lack, so that no offset is negative
+      constexpr uint32_t BACK = 3 * 1024;
+      const auto copies = [&](const char* base, uint32_t m0, auto swizzle) __attribute__((always_inline)) {
+        const auto one = [&](auto i) __attribute__((always_inline)) {
+          constexpr int I = decltype(i)::value;
+          const int r = 16 * hf + I * RPI + lrow;  // row of the tile
+          const uint32_t o = uint32_t(min(max(t * DC_BN + r, lo), hi) - lo) * rb;
+          dma16_at<I>(o + uint32_t((lchunk ^ swizzle(r)) << 4) + (BACK - 1024 * I), base - BACK, m0);
+        };
+        one(std::integral_constant<int, 0>());
+        one(std::integral_constant<int, 1>());
+        if constexpr (NI == 4) {
+          one(std::integral_constant<int, 2>());
+          one(std::integral_constant<int, 3>());
+        }
+      };
+      copies(kb, dst, [](int r) { return ksw<DH>(r); });
+      copies(vb, dst + TILE, [](int r) { return vsw<DH>(r); });
     }
     return good;
   };
@@ -121,12 +135,12 @@ __global__ __launch_bounds__(256, 1) void k_attention_decode(DecodeDev a) {
 
   int good = 0, t = t0 + wave, stage = 0;
   if (t < t1) good = issue(t, 0);
-  for (; t < t1; t += 4, stage ^= 1) {
+  for (; t < t1; t += W, stage ^= 1) {
     int good_next = 0;
     // this tile's stage was read two rounds ago: those reads are done before it is refilled
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (t + 4 < t1) {
-      good_next = issue(t + 4, stage ^ 1);
+    if (t + W < t1) {
+      good_next = issue(t + W, stage ^ 1);
       wait_vm<4 * NI>();
     } else {
       wait_vm<0>();
@@ -174,7 +188,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_decode(DecodeDev a) {
     good = good_next;
   }
 
-  // join the four waves: [wave][column][channel] fp32 in the ring that no copy fills any more
+  // join the waves: [wave][column][channel] fp32 in the ring that no copy fills any more
   l = sum_halves(l);
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __syncthreads();
@@ -190,16 +204,16 @@ __global__ __launch_bounds__(256, 1) void k_attention_decode(DecodeDev a) {
   }
   __syncthreads();
   const long nrows = long(a.n_seq) * a.Hq;
-  for (int e = tid; e < gn * (DH / 4); e += 256) {
+  for (int e = tid; e < gn * (DH / 4); e += 64 * W) {
     const int g = e / (DH / 4), d4 = e % (DH / 4) * 4;
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mx = fmaxf(mx, ml_s[w][g].x);
+    for (int w = 0; w < W; ++w) mx = fmaxf(mx, ml_s[w][g].x);
     const float base = mx == -INFINITY ? 0.f : mx * c;
     float lt = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float2 x = ml_s[w][g];
       const float f = exp2_fast(fmaf(x.x, c, -base));
       const float4 v = *reinterpret_cast<const float4*>(js + (w * 32 + g) * DH + d4);
@@ -225,21 +239,39 @@ __global__ __launch_bounds__(256, 1) void k_attention_decode(DecodeDev a) {
   }
 }
 
-// Joins the `splits` partial sums of each row (token, head); one wave per row. Fixed order, so the
-// same inputs give the same bits.
+// Joins the `splits` partial sums of each row (token, head); one wave per row, four channels per
+// lane, so that a wave has 2 (dh 128) or 4 splits side by side. What it waits for is one round of
+// memory: the statistics and the first 8 loads of sums per lane are asked for together. Fixed order,
+// so the same inputs give the same bits.
 template <int DH>
 __global__ __launch_bounds__(256) void k_attention_join(const float* part, int splits,
                                                         const int* cu_q, int n_seq, long nrows,
                                                         int Hq, uint16_t* O, long os, float* lse,
                                                         float scale) {
-  const int lane = threadIdx.x & 63;
-  const long rr = long(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  constexpr int LP = DH / 4, SP = 64 / LP, U = 8;  // lanes per split, splits side by side, loads at once
+  const int lane = threadIdx.x & 63, sub = lane / LP, ch = 4 * (lane % LP);
+  const long rr = long(blockIdx.x) * (blockDim.x / 64) + (threadIdx.x >> 6);
   if (rr >= nrows) return;
-  if (cu_q && (rr / Hq < cu_q[0] || rr / Hq >= cu_q[n_seq])) return;  // a row of no sequence
-  const float c = scale * kLog2e;
+  const float* p = part + rr * DH + ch;
+  const long step = nrows * DH;
   float2 x = make_float2(-INFINITY, 0.f);
   if (lane < splits)
-    x = *reinterpret_cast<const float2*>(part + splits * nrows * DH + (lane * nrows + rr) * 2);
+    x = *reinterpret_cast<const float2*>(part + splits * step + (lane * nrows + rr) * 2);
+  float4 v[U];
+  const auto load = [&](int s0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int s = s0 + u * SP + sub;
+      if (s < splits) v[u] = *reinterpret_cast<const float4*>(p + s * step);
+    }
+  };
+  load(0);
+  if (cu_q) {  // a row of no sequence
+    const int t = int(rr / Hq);
+    if (t < cu_q[0] || t >= cu_q[n_seq]) return;
+  }
+  const float c = scale * kLog2e;
   float mx = x.x;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) mx = fmaxf(mx, __shfl_xor(mx, d));
@@ -248,29 +280,55 @@ __global__ __launch_bounds__(256) void k_attention_join(const float* part, int s
   float lt = f * x.y;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) lt += __shfl_xor(lt, d);
-  constexpr int E = DH / 64;
-  float acc[E] = {};
-  const float* p = part + rr * DH + lane * E;
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
-    const float w = __shfl(f, s);
+  float acc[4] = {};
+  for (int s0 = 0; s0 < splits; s0 += U * SP) {
+    if (s0) load(s0);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, p[s * nrows * DH + e], acc[e]);
+    for (int u = 0; u < U; ++u) {
+      const float w = __shfl(f, (s0 + u * SP + sub) & 63);
+      acc[0] = fmaf(w, v[u].x, acc[0]);
+      acc[1] = fmaf(w, v[u].y, acc[1]);
+      acc[2] = fmaf(w, v[u].z, acc[2]);
+      acc[3] = fmaf(w, v[u].w, acc[3]);
+    }
   }
+#pragma unroll
+  for (int d = LP; d < 64; d *= 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], d);
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  uint16_t* out = O + (rr / Hq) * os + (rr % Hq) * DH + lane * E;
-  if constexpr (E == 2)
-    *reinterpret_cast<uint32_t*>(out) = pack2bf(acc[0] * inv, acc[1] * inv);
-  else
-    out[0] = f2bf(acc[0] * inv);
+  if (sub == 0)
+    *reinterpret_cast<uint2*>(O + (rr / Hq) * os + (rr % Hq) * DH + ch) =
+        make_uint2(pack2bf(acc[0] * inv, acc[1] * inv), pack2bf(acc[2] * inv, acc[3] * inv));
   if (lse && lane == 0) lse[rr] = lt == 0.f ? -INFINITY : mx * scale + __logf(lt);
 }
 
-int decode_splits(int n_seq, int max_pages, int page, int Hkv, int G) {
+// What a call launches: waves per workgroup and pieces per sequence, from the most that the page
+// table can hold, since only the device knows the lengths.
+struct DecodePlan {
+  int waves, splits;
+};
+DecodePlan decode_plan(int n_seq, int max_pages, int page, int Hkv, int G, int dh, int window) {
   const long wgs = long(n_seq) * Hkv * ((G + 31) / 32);
-  const long want = (1024 + wgs - 1) / wgs, most = (long(max_pages) * page + 127) / 128;
-  const long n = want < most ? want : most;
-  return int(n < 1 ? 1 : n > DC_MAX_SPLITS ? DC_MAX_SPLITS : n);
+  long keys = long(max_pages) * page;
+  if (window > 0 && window < keys) keys = window;
+  // The ring of 4 waves of heads of 128 takes a compute unit's LDS; with 2 waves, one workgroup starts
+  // or ends while the other streams, which counts when each unit has several: from 1536 tokens per
+  // unit on. 4 / 2 waves, 32/8 heads of 128: 100 x 512 tokens 47 / 39 us, 200 x 500 96 / 91, 64 x
+  // 1000 45 / 43, but 1 x 32768 28 / 29, 1 x 4096 8.3 / 9.8.
+  const int waves = dh == 128 && wgs * keys >= 256 * 1536 ? 2 : 4;
+  // As many pieces as fill the chip, of at least 128 tokens (a tile per wave), and up to four times
+  // as many, since lengths differ and the last to end counts, where a piece still has 1024 (heads of
+  // 64, whose tiles are half as large: 512). Measured in pieces for four times the chip's workgroups
+  // of 4 waves / for once, without the second limit: 16 x 32768 tokens 365 / 374 us, 33 of up to 5000,
+  // 16/4 heads of 64, 21 / 33 us, but 64 x 1000 52 / 45 us, 4 x 2000 11.8 / 9.6 us.
+  const auto pieces = [&](long want, long least) {
+    const long n = (want + wgs - 1) / wgs, most = keys / least;
+    return n < most ? n : most;
+  };
+  const long chip = 1024 / waves;
+  const long a = pieces(chip, 128), b = pieces(4 * chip, dh == 128 ? 1024 : 512), n = a > b ? a : b;
+  return {waves, int(n < 1 ? 1 : n > DC_MAX_SPLITS ? DC_MAX_SPLITS : n)};
 }
 
 }  // namespace
@@ -278,35 +336,36 @@ int decode_splits(int n_seq, int max_pages, int page, int Hkv, int G) {
 hipError_t attention_join(const float* part, int splits, const int* cu_q, int n_seq, long nrows,
                           int Hq, int dh, void* O, long os, float* lse, float scale,
                           hipStream_t stream) {
-  const dim3 grid(unsigned((nrows + 3) / 4));
-  if (dh == 128)
-    hipLaunchKernelGGL((k_attention_join<128>), grid, dim3(256), 0, stream, part, splits, cu_q,
-                       n_seq, nrows, Hq,
-                       static_cast<uint16_t*>(O), os, lse, scale);
-  else
-    hipLaunchKernelGGL((k_attention_join<64>), grid, dim3(256), 0, stream, part, splits, cu_q,
-                       n_seq, nrows, Hq,
-                       static_cast<uint16_t*>(O), os, lse, scale);
+  // few rows: a wave per workgroup, on as many compute units
+  const int waves = nrows < 1024 ? 1 : 4;
+  const dim3 grid(unsigned((nrows + waves - 1) / waves)), block(64 * waves);
+  const auto k = dh == 128 ? k_attention_join<128> : k_attention_join<64>;
+  hipLaunchKernelGGL(k, grid, block, 0, stream, part, splits, cu_q, n_seq, nrows, Hq,
+                     static_cast<uint16_t*>(O), os, lse, scale);
   return hipGetLastError();
 }
 
 size_t attention_decode_workspace(int n_seq, int max_pages, int page, int Hq, int Hkv, int dh) {
-  const int ns = decode_splits(n_seq, max_pages, page, Hkv, Hq / Hkv);
+  // the window is not known here: without one there are no fewer pieces than with it
+  const int ns = decode_plan(n_seq, max_pages, page, Hkv, Hq / Hkv, dh, 0).splits;
   return ns > 1 ? size_t(ns) * n_seq * Hq * (dh + 2) * 4 : 0;
 }
 
 hipError_t attention_decode(const DecodeArgs& a) {
   const int G = a.Hq / a.Hkv;
-  DecodeDev d{static_cast<const uint16_t*>(a.Q), a.qs, static_cast<const char*>(a.Kc),
+  const DecodePlan p = decode_plan(a.n_seq, a.max_pages, a.page, a.Hkv, G, a.dh, a.window);
+  const DecodeDev d{static_cast<const uint16_t*>(a.Q), a.qs, static_cast<const char*>(a.Kc),
               static_cast<const char*>(a.Vc), static_cast<uint16_t*>(a.O), a.os, a.lse, a.table,
               a.lengths, a.max_pages, __builtin_ctz(unsigned(a.page)), a.n_pages, a.n_seq, a.Hq,
               a.Hkv, G, a.scale, a.window,
-              decode_splits(a.n_seq, a.max_pages, a.page, a.Hkv, G), static_cast<float*>(a.ws)};
+              p.splits, static_cast<float*>(a.ws)};
   const dim3 grid(unsigned(a.Hkv) * d.splits * a.n_seq * ((G + 31) / 32));
-  if (a.dh == 128)
-    hipLaunchKernelGGL((k_attention_decode<128>), grid, dim3(256), 0, a.stream, d);
+  if (a.dh == 64)
+    hipLaunchKernelGGL((k_attention_decode<64, 4>), grid, dim3(256), 0, a.stream, d);
+  else if (p.waves == 4)
+    hipLaunchKernelGGL((k_attention_decode<128, 4>), grid, dim3(256), 0, a.stream, d);
   else
-    hipLaunchKernelGGL((k_attention_decode<64>), grid, dim3(256), 0, a.stream, d);
+    hipLaunchKernelGGL((k_attention_decode<128, 2>), grid, dim3(128), 0, a.stream, d);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || d.splits == 1) return e;
   return attention_join(d.part, d.splits, nullptr, 0, long(a.n_seq) * a.Hq, a.Hq, a.dh, a.O, a.os, a.lse,
