@@ -83,13 +83,13 @@ __device__ __forceinline__ Seq ap_find(const PackedDev& a, int tile, int BM, int
 // queries sit in accumulator registers. Inline assembly, because the compiler would put every
 // product's result into accumulator registers and copy 64 values a tile. The result may be read a
 // whole phase later only (ap_settle).
-__device__ __forceinline__ void ap_mma0(f32x16& d, const uint4& k, const uint4& q) {
+__device__ __forceinline__ void ap_mma0(f32x16& d, const uint4& k, const bf16x8& q) {
   asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0"
-      : "=&v"(d) : "v"(__builtin_bit_cast(bf16x8, k)), "a"(__builtin_bit_cast(bf16x8, q)));
+      : "=&v"(d) : "v"(__builtin_bit_cast(bf16x8, k)), "a"(q));
 }
-__device__ __forceinline__ void ap_mma(f32x16& d, const uint4& k, const uint4& q) {
+__device__ __forceinline__ void ap_mma(f32x16& d, const uint4& k, const bf16x8& q) {
   asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
-      : "+v"(d) : "v"(__builtin_bit_cast(bf16x8, k)), "a"(__builtin_bit_cast(bf16x8, q)));
+      : "+v"(d) : "v"(__builtin_bit_cast(bf16x8, k)), "a"(q));
 }
 // What follows reads these results of ap_mma: either at least three phases' quarters of products lie
 // between (NOPS false), or 16 + 16 wait states, where an 8-pass product needs 11, are put there.
@@ -169,65 +169,104 @@ struct ApPlan {
   }
 };
 
-// One row (token q, head `head`) over the keys [j0, j1) of the sequence that begins at k0, none of
-// them masked, by a whole wave: the scores of 64 keys, a key per lane, then their values, two
-// channels per lane. The tiles multiply masked values by a weight of 0, which an infinity or a NaN
-// among them turns into a NaN; so a row whose sums are not finite although its scores are is summed
-// again here. About 3000 clocks per 64 keys: 16384 tokens of 32/8 heads of 128 with one infinite
-// value in the last token take no longer than without it, with one in the first token, which every
-// row sees, APROWMS.
-template <int DH>
-__device__ __forceinline__ void ap_row(const PackedDev& a, int q, int head, int kvh, int k0, int j0, int j1,
-                                       int split, int lane) {
-  const float c = a.scale * kLog2e;
-  const uint4* qp = reinterpret_cast<const uint4*>(a.Q + q * a.qs + head * DH);
-  const int ch = 2 * (lane % (DH / 2));
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int j = j0; j < j1; j += 64) {
-    const uint4* kp =
-        reinterpret_cast<const uint4*>(a.K + (long(k0) + min(j + lane, j1 - 1)) * a.ks + kvh * DH);
-    float s = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < DH / 8; ++i) {
-      const uint4 x = qp[i], y = kp[i];
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+// Sums the values of one block of 32 rows again, with care for infinities and NaN: the tiles multiply a
+// value that a row does not see by a weight of 0, and 0 times an infinity or a NaN is a NaN. Here such
+// values are multiplied as 0, and what the rows that see them get is found by products of 1 and 0:
+// which of +inf, -inf and NaN a row sees at all. The maxima and sums of the first pass are right and
+// stay. By the wave alone, 32 keys [j, j + 32) of [j0, j1) at a time: K straight into registers, V by
+// way of its own 32 rows of LDS. 16384 tokens of 32/8 heads of 128 take 1.8 ms; with one infinity in the
+// last token 4.4 ms, in the first, which every row of a head sees, 15 ms, with nothing but NaN in V 26 ms.
+template <int DH, int QT>
+__device__ __forceinline__ void ap_again(f32x16 (&o)[DH / 32][QT], int b, const bf16x8 (&qf)[DH / 16], const char* tile,
+                                         const uint16_t* K, long ks, const uint16_t* V, long vs, int j0,
+                                         int j1, int lo, int hi, float c, float base, int lane) {
+  constexpr int KS = DH / 16, DT = DH / 32, RPI = 1024 / (DH * 2);
+  const FragOff<DH> fo(lane);
+  const uint32_t lds = lds_u32(tile);
+  const int h = lane >> 5;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s = fmaf(bf2f(uint16_t(u[e])), bf2f(uint16_t(v[e])), s);
-        s = fmaf(bf2f(uint16_t(u[e] >> 16)), bf2f(uint16_t(v[e] >> 16)), s);
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][b][i] = 0.f;
+  for (int j = j0; j < j1; j += 32) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last tile has been read
+#pragma unroll 1
+    for (int i = 0; i < 32 / RPI; ++i) {
+      const int r = i * RPI + lane / (64 / RPI), ch = (lane % (64 / RPI)) ^ vsw<DH>(r);
+      dma16_far(V + min(j + r, j1 - 1) * vs + 8 * ch, __builtin_amdgcn_readfirstlane(lds + i * 1024));
+    }
+    const uint16_t* kp = K + min(j + (lane & 31), j1 - 1) * ks + 8 * h;
+    f32x16 s;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const uint4 kf = *reinterpret_cast<const uint4*>(kp + 16 * k);
+      if (k == 0) ap_mma0(s, kf, qf[0]);
+      else ap_mma(s, kf, qf[k]);
+      if (k % 4 == 3) ap_fence();  // not all loads at once: the registers are the main loop's
+    }
+    asm volatile("s_nop 15\n\ts_nop 15" : "+v"(s));
+    uint32_t pw[8], seen = 0;  // bit i: the row sees its i-th key
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      float p[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int key = j + 8 * (i / 4) + 4 * h + (i & 3) + e;
+        const bool in = key >= lo && key <= hi && key < j1;
+        p[e] = in ? exp2_fast(fmaf(s[i + e], c, -base)) : 0.f;
+        seen |= uint32_t(in) << (i + e);
+      }
+      pw[i / 2] = pack2bf(p[0], p[1]);
+    }
+    wait_vm<0>();
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      // +inf, -inf and NaN as 1, 2^8 and 2^16: their sum over 32 keys, exact in fp32, tells which a row
+      // sees
+      uint32_t code[2][4];
+      bool odd = false;
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const uint4 v = fo.value(tile, st, d);
+        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          code[st][e] = 0;
+#pragma unroll
+          for (int half = 0; half < 32; half += 16) {
+            const uint32_t y = x[e] >> half & 0xFFFF;
+            if ((y & 0x7F80) != 0x7F80) continue;
+            odd = true;
+            code[st][e] |= uint32_t(y == 0x7F80 ? 0x3F80 : y == 0xFF80 ? 0x4380 : 0x4780) << half;
+            x[e] &= 0xFFFF0000u >> half;
+          }
+        }
+        o[d][b] = mfma32x32x16(make_uint4(x[0], x[1], x[2], x[3]),
+                               make_uint4(pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]), o[d][b]);
+      }
+      if (!__any(odd)) continue;
+      f32x16 n;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) n[i] = 0.f;
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        uint32_t one[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t two = seen >> (8 * st + 2 * e) & 3;
+          one[e] = ((two & 1) | (two & 2) << 15) * 0x3F80;
+        }
+        n = mfma32x32x16(make_uint4(code[st][0], code[st][1], code[st][2], code[st][3]),
+                         make_uint4(one[0], one[1], one[2], one[3]), n);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int k = int(n[i]);
+        if (k & 0xFF) o[d][b][i] += INFINITY;
+        if (k & 0xFF00) o[d][b][i] -= INFINITY;
+        if (k >> 16) o[d][b][i] = NAN;
       }
     }
-    if (j + lane >= j1) s = -INFINITY;
-    float mn = fmaxf(m, s);
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) mn = fmaxf(mn, __shfl_xor(mn, d));
-    const float base = mn == -INFINITY ? 0.f : mn * c;
-    const float al = exp2_fast(fmaf(m, c, -base)), p = exp2_fast(fmaf(s, c, -base));
-    m = mn;
-    l = l * al + p;
-    o0 *= al;
-    o1 *= al;
-    const int n = min(64, j1 - j);
-    const uint16_t* vp = a.V + (long(k0) + j) * a.vs + kvh * DH + ch;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(vp + i * a.vs);
-      const float w = bf2f(f2bf(__shfl(p, i)));
-      o0 = fmaf(w, bf2f(uint16_t(v)), o0);
-      o1 = fmaf(w, bf2f(uint16_t(v >> 16)), o1);
-    }
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d);
-  const long rr = long(q) * a.Hq + head, n = long(a.Nq) * a.Hq;
-  if (lane >= DH / 2) return;
-  if (a.splits > 1) {
-    *reinterpret_cast<float2*>(a.part + (split * n + rr) * DH + ch) = make_float2(o0, o1);
-    if (lane == 0)
-      *reinterpret_cast<float2*>(a.part + a.splits * n * DH + (split * n + rr) * 2) = make_float2(m, l);
-  } else {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint32_t*>(a.O + q * a.os + head * DH + ch) = pack2bf(o0 * inv, o1 * inv);
   }
 }
 
@@ -413,7 +452,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
 
   // the first copies: K of the first tile, the wave's queries (rows as K's: chunk c of row r at slot
   // c ^ ksw(r)), V of the first tile
-  uint4 qf[QT][KS];
+  bf16x8 qf[QT][KS];
   if (t0 < t1) {
     if (t0 == tlast) {
       cut(koff, kstep);
@@ -442,8 +481,8 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   for (int b = 0; b < QT; ++b)
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      qf[b][k] = fo.key(mine, b, k);
-      asm volatile("" : "+a"(qf[b][k].x), "+a"(qf[b][k].y), "+a"(qf[b][k].z), "+a"(qf[b][k].w));
+      qf[b][k] = __builtin_bit_cast(bf16x8, fo.key(mine, b, k));
+      asm volatile("" : "+a"(qf[b][k]));
     }
   asm volatile("s_nop 7");  // in accumulator registers some wait states before the first product
   ap_fence();
@@ -622,33 +661,36 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   // Results. Partial ones go out as they are; others by way of LDS, in whole rows: chunk c (16 bytes)
   // of a row at slot c ^ (row % (chunks of a row)).
   constexpr int CH = DH / 8;
+  int ln = threadIdx.x & 63;
+  asm volatile("" : "+v"(ln));  // what follows from it is computed here, not kept through the loop
   char* const out = OWN ? mine : smem + (((t1 - t0) & 1) ? 2 * TILE : 0) + wrow * DH * 2;
-  uint64_t again[QT];  // lanes whose columns have to be summed again
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
     const float lt = sum_halves(l[b][0] + l[b][1]);
-    // A value that a row does not see has the weight 0 in its products, and 0 times an infinity or a
-    // NaN is no 0: see ap_row.
     float zero = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) zero = fmaf(o[d][b][i], 0.f, zero);
-    again[b] = __ballot(zero != 0.f && lt == lt && wrow + 32 * b + (lane & 31) < rows_here);
-    const int r = 32 * b + (lane & 31), x = wrow + r, qi = query(x);
+    if (__any(zero != 0.f && lt == lt)) {  // not finite, although the weights are
+      ap_again<DH>(o, b, qf[b], out + 32 * b * DH * 2, a.K + long(k0) * a.ks + kvh * DH, a.ks,
+                   a.V + long(k0) * a.vs + kvh * DH, a.vs, t0 * AP_BN, min(t1 * AP_BN, lk), lo[b], hi[b],
+                   c, base[b], ln);
+    }
+    const int r = 32 * b + (ln & 31), x = wrow + r, qi = query(x);
     const bool on = x < rows_here;
     const long rr = long(q0 + qa + qi) * a.Hq + kvh * G + first + x - qi * G;
     if (a.splits > 1) {
       if (!on) continue;
       const long n = long(a.Nq) * a.Hq;
-      float* po = a.part + (long(split) * n + rr) * DH + 4 * h;
+      float* po = a.part + (long(split) * n + rr) * DH + 4 * (ln >> 5);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
           *reinterpret_cast<float4*>(po + 32 * d + 2 * i) =
               make_float4(o[d][b][i], o[d][b][i + 1], o[d][b][i + 2], o[d][b][i + 3]);
-      if (h == 0) {
+      if (ln < 32) {
         float* ml = a.part + long(a.splits) * n * DH + (long(split) * n + rr) * 2;
         *reinterpret_cast<float2*>(ml) = make_float2(m[b], lt);
       }
@@ -659,31 +701,19 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<uint2*>(out + r * DH * 2 + (((4 * d + i / 4) ^ (r % CH)) << 4) + 8 * h) =
+        *reinterpret_cast<uint2*>(out + r * DH * 2 + (((4 * d + i / 4) ^ (r % CH)) << 4) + 8 * (ln >> 5)) =
             make_uint2(pack2bf(o[d][b][i] * inv, o[d][b][i + 1] * inv),
                        pack2bf(o[d][b][i + 2] * inv, o[d][b][i + 3] * inv));
-    if (a.lse && h == 0 && on) a.lse[rr] = lt == 0.f ? -INFINITY : m[b] * a.scale + __logf(lt);
+    if (a.lse && ln < 32 && on) a.lse[rr] = lt == 0.f ? -INFINITY : m[b] * a.scale + __logf(lt);
   }
   if (a.splits == 1) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     uint16_t* Oh = a.O + long(q0 + qa) * a.os + long(kvh) * G * DH;
 #pragma unroll
     for (int i = 0; i < WROWS / RPI; ++i) {
-      const int r = i * RPI + lane / (64 / RPI), x = wrow + r;
-      const uint4 v = *reinterpret_cast<const uint4*>(out + r * DH * 2 + ((cp ^ (r % CH)) << 4));
-      if (x < rows_here) *reinterpret_cast<uint4*>(Oh + element(x, uint32_t(a.os)) + 8 * cp) = v;
-    }
-  }
-#pragma unroll
-  for (int b = 0; b < QT; ++b) {
-    uint32_t rest = uint32_t(again[b] | again[b] >> 32);
-    if (rest) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what is written over is there
-    while (rest) {
-      const int x = wrow + 32 * b + __builtin_ctz(rest);
-      rest &= rest - 1;
-      const int qi = qa + query(x), head = kvh * G + first + x - (qi - qa) * G;
-      const int to = qi + off, from = a.window > 0 ? max(to - a.window + 1, 0) : 0;
-      ap_row<DH>(a, q0 + qi, head, kvh, k0, max(from, t0 * AP_BN), min(to + 1, t1 * AP_BN), split, lane);
+      const int r = i * RPI + ln / (64 / RPI), x = wrow + r;
+      const uint4 v = *reinterpret_cast<const uint4*>(out + r * DH * 2 + ((ln % CH ^ (r % CH)) << 4));
+      if (x < rows_here) *reinterpret_cast<uint4*>(Oh + element(x, uint32_t(a.os)) + 8 * (ln % CH)) = v;
     }
   }
 }

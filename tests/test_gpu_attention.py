@@ -167,6 +167,90 @@ def test_packed_neighbours_do_not_leak():
     np.testing.assert_array_equal(got[:, 2:][75:140], gen.bf16_bits_to_f32(ref[75:140, 2:]))
 
 
+def _some_rows(Q, K, V, cu_q, cu_k, scale, window, tokens, heads):
+    """The oracle at chosen tokens and heads: (o, lse, sums of weight * |v|) [tokens, heads, ..]."""
+    G = Q.shape[1] // K.shape[1]
+    out = []
+    for t in tokens:
+        s = int(np.searchsorted(cu_q, t, side="right")) - 1
+        last = t - cu_q[s] + (cu_k[s + 1] - cu_k[s]) - (cu_q[s + 1] - cu_q[s])
+        first = max(0, last - window + 1) if window else 0
+        ks = slice(cu_k[s] + first, cu_k[s] + max(first, last + 1))
+        out += [oa.attend(Q[t, h], K[ks, h // G], V[ks, h // G], scale) for h in heads]
+    shape = (len(tokens), len(heads))
+    return [np.array([x[i] for x in out]).reshape(*shape, *np.shape(out[0][i])) for i in range(3)]
+
+
+# long rows whose workgroups of 256 rows fill the compute units evenly: (lq, lk - lq, Hq, Hkv, window)
+WIDE = [([4200], [0], 15, 15, 0), ([4200], [0], 30, 15, 0), ([1000], [3000], 32, 32, 2500),
+        ([2100, 2050], [2000, 2100], 32, 8, 0), ([300], [2500], 28, 28, 0)]
+
+
+@pytest.mark.parametrize("lq,more,Hq,Hkv,window", WIDE)
+def test_packed_long_rows(lq, more, Hq, Hkv, window):
+    print(f"case: packed long rows lq={lq} more={more} {Hq}/{Hkv} window={window}", flush=True)
+    dh, rng = 128, np.random.default_rng(sum(lq) + Hq)
+    cu_q, cu_k = _cu(lq), _cu(np.array(lq) + np.array(more))
+    Q = _draw(rng, cu_q[-1], Hq, dh)
+    K, V = _draw(rng, cu_k[-1], Hkv, dh), _draw(rng, cu_k[-1], Hkv, dh)
+    scale = 1.3 * dh ** -0.5
+    O, L = _packed(Q, K, V, cu_q, cu_k, scale, window)
+    tokens = sorted({0, 1, 63, 64, 127, 128, 255, 256, int(cu_q[-1]) - 1, int(cu_q[1]) - 1,
+                     *rng.integers(0, cu_q[-1], 12).tolist()})
+    heads = sorted({0, Hq - 1, *rng.integers(0, Hq, 3).tolist()})
+    q, k, v = _f(Q), _f(K), _f(V)
+    X = _logit_size(q[tokens], k, scale)[:, heads]
+    _check(O[tokens][:, heads], L[tokens][:, heads],
+           _some_rows(q, k, v, cu_q, cu_k, scale, window, tokens, heads), X, dh, "long rows")
+    got = host_f64(O)  # every row was written, none with what lies outside the convex hull of V
+    assert np.isfinite(got).all() and np.abs(got).max() <= np.abs(v).max() * (1 + 2.0 ** -6)
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("lq,more,Hq,Hkv,dh,window", [
+    ([150], [0], 4, 2, 128, 0), ([150], [0], 4, 2, 64, 0), ([90, 130], [30, 0], 3, 1, 64, 50),
+    ([40], [3000], 2, 1, 128, 0),                       # the keys are split
+    ([40], [3000], 2, 1, 128, 1000), ([300], [2500], 28, 28, 128, 0)])
+def test_packed_hidden_values_reach_nothing(lq, more, Hq, Hkv, dh, window, bad):
+    """Infinities and NaN among the own sequence's keys and values reach the rows that see them, and
+    no other row, although the same tiles are multiplied."""
+    print(f"case: packed hidden {bad} lq={lq} more={more} {Hq}/{Hkv}x{dh} window={window}", flush=True)
+    rng = np.random.default_rng(sum(lq) + dh)
+    cu_q, cu_k = _cu(lq), _cu(np.array(lq) + np.array(more))
+    Q = _draw(rng, cu_q[-1], Hq, dh)
+    K, V = _draw(rng, cu_k[-1], Hkv, dh), _draw(rng, cu_k[-1], Hkv, dh)
+    scale = dh ** -0.5
+    # key head 0: one value channel of a key in the middle of the first sequence's own part, another of
+    # a key near its start; a key vector 10 behind the middle
+    mid, near, key = int(cu_k[1]) - lq[0] // 2, 3, int(cu_k[1]) - lq[0] // 2 + 10
+    x, q, k, v = gen.f32_to_bf16_bits(np.float32([bad]))[0], _f(Q), _f(K), _f(V)
+    V1 = V.copy()
+    V1[mid, 0, 5], V1[near, 0, dh - 1] = x, x
+    K1 = K.copy()
+    K1[key, 0] = 0x7FC0
+    O, L = _packed(Q, K1, V1, cu_q, cu_k, scale, window)
+    G = Hq // Hkv
+    tokens = sorted({*range(min(lq[0], 150)), *rng.integers(0, cu_q[-1], 10).tolist()})
+    heads = sorted({0, G - 1, Hq - 1})
+    o, lse, a = _some_rows(q, k, v, cu_q, cu_k, scale, window, tokens, heads)
+    got, gl = O[tokens][:, heads].clone(), L[tokens][:, heads].clone()
+    for i, t in enumerate(tokens):
+        last = t + more[0] if t < lq[0] else -1
+        first = max(0, last - window + 1) if window else 0
+        for j, h in enumerate(heads):
+            if h >= G:
+                continue
+            if first <= key <= last:  # a logit is NaN: the row is
+                assert np.isnan(host_f64(got[i, j])).all() and np.isnan(host_f64(gl[i, j]))
+                got[i, j], gl[i, j], o[i, j], a[i, j], lse[i, j] = 0, 0, 0, 0, 0
+            for at, c in ((mid, 5), (near, dh - 1)):
+                if first <= at <= last and not first <= key <= last:
+                    np.testing.assert_equal(host_f64(got[i, j, c]), bad)
+                    got[i, j, c], o[i, j, c], a[i, j, c] = 0, 0, 0
+    k[key, 0] = 0
+    _check(got, gl, (o, lse, a), _logit_size(q[tokens], k, scale)[:, heads], dh, "hidden values")
+
+
 def test_packed_bad_offsets_stay_in_bounds():
     """Offsets outside the tensors or decreasing: nothing outside is read or written. The buffers are
     slices of larger ones, whose other rows would show a write."""
