@@ -596,11 +596,11 @@ def qk_norm_rope(Q, K, pos, inv_freq, *, q_weight=None, k_weight=None, eps: floa
     elif V is not None or K_cache is not None or V_cache is not None:
         raise ValueError("V, K_cache and V_cache are for a call with slots")
     if Q_out is None:
-        Q_out, qos = Q.new_empty((N, Hq, dh)), Hq * dh
+        Q_out, qos = torch.empty_like(Q), Hq * dh  # contiguous, also of a slice
     else:
         qos = _rows(Q_out, "Q_out", Hq, dh, dt, dev, N)
     if K_out is None:
-        K_out, kos = K.new_empty((N, Hkv, dh)), Hkv * dh
+        K_out, kos = torch.empty_like(K), Hkv * dh
     else:
         kos = _rows(K_out, "K_out", Hkv, dh, dt, dev, N)
     _launch(lib().ttt_qk_norm_rope,
@@ -634,14 +634,14 @@ def attention_packed(Q, K, V, cu_q, cu_k=None, *, scale=None, window: int = 0, O
     else:
         _vec(cu_k, "cu_k", (n_seq + 1,), torch.int32, dev)
     if O is None:
-        O, os_ = Q.new_empty((Nq, Hq, dh)), Hq * dh
+        O, os_ = torch.empty_like(Q), Hq * dh
     else:
         os_ = _rows(O, "O", Hq, dh, dt, dev, Nq)
     window = _int_in(window, "window", 0, 1 << 30)
     if lse is not None:
         _vec(lse, "lse", (Nq, Hq), torch.float32, dev)
     elif with_lse:
-        lse = torch.empty((Nq, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty(Nq, Hq, dtype=torch.float32, device=dev)
     ws, ws_bytes = _workspace(workspace, lib().ttt_attention_packed_workspace(
         n_seq, Nq, Nk, Hq, Hkv, dh), dev)
     _launch(lib().ttt_attention_packed,
@@ -672,13 +672,13 @@ def attention_decode(Q, K_cache, V_cache, page_table, lengths, page_size: int, *
     page_size = _int_in(page_size, "page_size", 1, 65536)
     window = _int_in(window, "window", 0, 1 << 30)
     if O is None:
-        O, os_ = Q.new_empty((S, Hq, dh)), Hq * dh
+        O, os_ = torch.empty_like(Q), Hq * dh
     else:
         os_ = _rows(O, "O", Hq, dh, dt, dev, S)
     if lse is not None:
         _vec(lse, "lse", (S, Hq), torch.float32, dev)
     elif with_lse:
-        lse = torch.empty((S, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty(S, Hq, dtype=torch.float32, device=dev)
     ws, ws_bytes = _workspace(workspace, lib().ttt_attention_decode_workspace(
         S, max_pages, page_size, Hq, Hkv, dh), dev)
     _launch(lib().ttt_attention_decode,
