@@ -10,7 +10,13 @@
 // r / G, head r % G, so one pass over the keys serves them all and a tile's causal edge spans
 // 1 / G as many queries. A workgroup of 4 waves owns BM = 128 * QT consecutive rows (32 * QT per
 // wave, as the columns of S^T) and walks the visible keys in tiles of 64 with the running maximum
-// and sum of a softmax in fp32.
+// and sum of a softmax in fp32. While the exponentials of one tile are taken (the vector unit: 760
+// clocks per tile and 32 rows), the matrix pipe works on the scores of the next and the values of this
+// one (33 clocks per 32x32x16 product: 1056 with heads of 128, 528 with 64). So heads of 128 are bound by
+// the matrix pipe, and by power where rows are long (the clock falls to 1.6 .. 2.0 GHz), heads of 64 by
+// the vector unit. 32/8 heads of 128: 16384 tokens 1.72 .. 1.88 ms (1170 .. 1280 TFLOP/s over the visible
+// pairs; a large matrix product 1350 .. 1550), 11 documents in 8192 tokens 105 .. 112 us, 512 tokens after
+// 15872 125 .. 134 us; 32/32 heads of 64, 8191 tokens, window 2048: 143 .. 154 us.
 #include <type_traits>
 
 #include "attn.hpp"
@@ -765,9 +771,9 @@ PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int w
   // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least
   // 9 of 10 places, in pieces of at least 1024. Measured, 256 rows against 128, 32/8 heads of 128: 16384 tokens
   // 1.76 / 1.87 ms, 512 after 15872 126 / 138 us, 256 after 16000 75 / 80 us; but 64 after 16000 37 / 31
-  // us, 200 after 4000 31 / 28 us, 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105 us, 12000 tokens of 4/1 heads in
-  // 2 documents 205 / 153 us. Heads of 64, which the vector unit bounds: 8191 tokens, window 2048,
-  // 188 / 145 us.
+  // us, 200 after 4000 31 / 28 us, 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105 us,
+  // 12000 tokens of 4/1 heads in 2 documents 205 / 153 us. Heads of 64, which the vector unit bounds:
+  // 8191 tokens, window 2048, 188 / 145 us.
   PackedPlan p{1, 0, 1};
   if (dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
     const int pieces = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, window);

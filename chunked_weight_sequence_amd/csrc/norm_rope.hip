@@ -14,7 +14,9 @@
 // power of two) share a head and sum its squares by lane exchange; a wave walks the heads of its
 // token 64 / L at a time, the next heads' loads in flight while these are worked on. The sines
 // and cosines are computed once per token (one angle per thread) and shared through LDS.
-// Bound by HBM: each input is read once and each output written once.
+// Bound by HBM: each input is read once and each output written once. 32768 tokens of 32/8 heads of 128
+// bf16 with the cache write, 872 MB: 166 us, 5.25 TB/s (a copy of 2 GiB: 4.9); 1023 tokens of 16/16 heads
+// of 64 in fp32, 17 MB: 6.2 us; 1 token 3.8 us, of which an empty launch is 2.
 #include <type_traits>
 
 #include "common.hpp"
@@ -234,7 +236,8 @@ hipError_t norm_rope(const NormRopeArgs& a) {
   while ((16 << lsh) < a.dh) ++lsh;
   // Up to four waves on a token, as many as its heads fill, while that still leaves the chip short of
   // waves (N tokens on 1024 SIMDs); one wave per token past that, so that the angles of four tokens
-  // are one per thread.
+  // are one per thread. Several / one, 32/8 heads of 128 with the cache write: 1 token 3.9 / 6.7 us, 1024
+  // tokens 7.2 / 9.5, 2048 tokens 12.3 / 11.6, 4096 tokens 20.2 / 18.3.
   const int waves = (((a.Hq + a.Hkv + (a.Vc ? a.Hkv : 0)) << lsh) + 63) / 64;
   const int wsh = a.N > 2048 || waves < 2 ? 0 : waves < 4 ? 1 : 2, tpb = 4 >> wsh;
   const dim3 grid(unsigned((a.N + tpb - 1) / tpb)), block(256);

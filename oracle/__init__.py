@@ -14,6 +14,8 @@ method, citing the passage it implements:
                   mini-batch, output in dual form (TTT layers page; DeltaNet equivalence).
 * ``route``       SR-TTT surprisal filter, EMA-smoothed 95th-percentile threshold, chunk-mean
                   condition and a fixed-capacity residual cache (SR-TTT page, section 2.1 and 5).
+* ``attention``   rotation frequencies, per-head norm and rotation, causal attention over packed
+                  sequences and over a paged cache (In-Place TTT page, sections 3 and 7).
 
 Parity pins (tests marked ``not gpu``) tie each function to closed forms, invariants, brute
 force on tiny inputs and library routines, never to itself.
