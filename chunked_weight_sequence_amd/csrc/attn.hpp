@@ -34,6 +34,23 @@ __device__ __forceinline__ uint2 tr_read(const char* p) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p));
 }
 
+// Direct copies (dma.hpp) in a row, 1 KB apart in LDS (m0 + 1024 I): the instruction's offset counts
+// for the global address and the LDS address alike, so M0 is written once, by the first (I = 0), a wait
+// state ahead. The I-th copy reads at sbase + voff + 1024 I.
+template <int I>
+__device__ __forceinline__ void dma16_at(uint32_t voff, const char* sbase, uint32_t m0) {
+  if constexpr (I == 0)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase),
+                 "s"(m0));
+  else
+    asm volatile("global_load_lds_dwordx4 %0, %1 offset:%2" ::"v"(voff), "s"(sbase), "n"(I * 1024));
+}
+
+// One direct copy with a 64-bit address per lane, M0 written a wait state ahead.
+__device__ __forceinline__ void dma16_far(const void* p, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(m0));
+}
+
 __device__ __forceinline__ float max_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
