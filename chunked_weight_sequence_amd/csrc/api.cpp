@@ -647,7 +647,8 @@ TTT_EXPORT ttt_status ttt_qk_norm_rope(const void* Q, long long q_stride, const 
   if (!Q || !K || !pos || !Q_out || (rot > 0 && !inv_freq)) return TTT_E_NULL;
   if (slots ? !V || !K_cache || !V_cache : !K_out) return TTT_E_NULL;
   if (!slots && (V || K_cache || V_cache)) return TTT_E_NULL;
-  if (N < 1 || N > (1 << 26) || Hq < 1 || Hkv < 1 || Hq > (1 << 16) || Hkv > (1 << 16) ||
+  // N: a launch counts its threads in 32 bits (64 a token)
+  if (N < 1 || N > (1 << 25) || Hq < 1 || Hkv < 1 || Hq > (1 << 16) || Hkv > (1 << 16) ||
       dh < 16 || dh > 256 || dh % 16 || rot < 0 || rot > dh || rot % 16 ||
       (Hq + 2ll * Hkv) * dh > (1 << 20))
     return TTT_E_SHAPE;
@@ -702,11 +703,14 @@ bool heads_ok(int Hq, int Hkv, int dh) {
 }
 bool packed_ok(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh) {
   return heads_ok(Hq, Hkv, dh) && n_seq >= 1 && n_seq <= (1 << 20) && Nq >= 1 && Nk >= 1 &&
-         Nq <= (1 << 26) && Nk <= (1 << 26) && (long long)Nq * Hq < (1ll << 31);
+         Nq <= (1 << 26) && Nk <= (1 << 26) &&
+         // a launch counts its threads in 32 bits: 256 per 128 rows, and per sequence and key head
+         (long long)Nq * Hq + 128ll * n_seq * Hkv < (1ll << 31);
 }
 bool decode_ok(int n_seq, int max_pages, int page, int Hq, int Hkv, int dh) {
   return heads_ok(Hq, Hkv, dh) && n_seq >= 1 && n_seq <= (1 << 20) && max_pages >= 1 && page >= 1 &&
-         (long long)max_pages * page <= (1 << 30) && (long long)n_seq * Hq <= (1 << 26);
+         (long long)max_pages * page <= (1 << 30) &&
+         (long long)n_seq * Hq < (1 << 24);  // 256 threads each at most, counted in 32 bits
 }
 bool page_ok(int page) { return page >= 16 && page <= 65536 && (page & (page - 1)) == 0; }
 bool scale_ok(float s) { return s > 0.f && std::isfinite(s); }

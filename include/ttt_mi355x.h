@@ -408,7 +408,7 @@ ttt_status ttt_rope_frequencies(double* inv_freq, int rot, double base, ttt_rope
  *          tokens with the same slot either's values may remain, piece by piece.
  *          V, K_cache and V_cache are required with slots and must be NULL without.
  *   Strides are in elements: at least heads * dh, multiples of 16 bytes, at most 2^31.
- *   dh: a multiple of 16 up to 256; rot: a multiple of 16, 0 .. dh; N <= 2^26;
+ *   dh: a multiple of 16 up to 256; rot: a multiple of 16, 0 .. dh; N <= 2^25;
  *   (Hq + 2 Hkv) * dh <= 2^20; eps >= 0 and rope_scale finite (else TTT_E_SHAPE).
  *   In place: Q_out may be Q and K_out may be K with the same strides. Any other overlap of an
  *   output with an input or another output gives TTT_E_ALIAS; interleaved slices of one buffer
@@ -443,7 +443,7 @@ ttt_status ttt_qk_norm_rope(const void* Q, long long q_stride, const void* K, lo
  *   K and V hold Nk rows. Only the keys and values that a row sees reach it, whatever the others hold
  *   (infinities and NaN too); rows whose sums are not finite take several times as long.
  *   Hq % Hkv == 0; dh 64 or 128 (else TTT_E_UNSUPPORTED); 1 <= Nq, Nk <= 2^26;
- *   1 <= n_seq <= 2^20; Nq * Hq < 2^31; 0 <= window <= 2^30; scale finite and > 0;
+ *   1 <= n_seq <= 2^20; Nq * Hq + 128 * n_seq * Hkv < 2^31; 0 <= window <= 2^30; scale finite and > 0;
  *   strides in elements: at least heads * dh, multiples of 8, at most 2^23.
  *   O must not overlap an input; lse must not overlap anything.
  *   workspace: at least ttt_attention_packed_workspace(...) bytes (may be NULL when that is 0);
@@ -470,7 +470,7 @@ size_t ttt_attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv
  *   Q  [n_seq, Hq, dh], O [n_seq, Hq, dh], dtype as above, sequence s at + s * stride
  *   page_table [n_seq, max_pages] int32, lengths [n_seq] int32, lse [n_seq, Hq] fp32 or NULL
  *   page_size: a power of two, 16 .. 65536 (else TTT_E_UNSUPPORTED); max_pages * page_size <=
- *   2^30; n_pages * page_size <= 2^36; n_seq <= 2^20, n_seq * Hq <= 2^26; the other limits,
+ *   2^30; n_pages * page_size <= 2^36; n_seq <= 2^20, n_seq * Hq < 2^24; the other limits,
  *   overlaps and the workspace as above. Where a row sees an infinite value, its result in that
  *   channel is that infinity or NaN. */
 ttt_status ttt_attention_decode(const void* Q, long long q_stride, const void* K_cache,

@@ -120,6 +120,16 @@ def test_decode_rejects_bad_arguments(kw, code):
     assert decode(**kw) == code
 
 
+def test_launches_past_32_bits_of_threads_are_refused():
+    """Empty sequences and one-head tokens reach them long before the tensors do."""
+    assert rope(N=(1 << 25) + 1, Hq=1, Hkv=1, dh=16, rot=0) == E_SHAPE
+    assert packed(n=1 << 20, Nq=1, Nk=1, Hq=16, Hkv=16) == E_SHAPE
+    assert packed(n=1 << 17, Nq=1, Nk=1, Hq=128, Hkv=128, dh=64) == E_SHAPE
+    assert packed(n=1, Nq=(1 << 26) - 4, Nk=1, Hq=32) == E_SHAPE   # the tokens alone would pass
+    assert decode(n=1 << 20, Hq=16, Hkv=16) == E_SHAPE
+    assert decode(n=1 << 18, Hq=64, Hkv=64, dh=64) == E_SHAPE
+
+
 def test_workspace_queries():
     lib = ttt.lib()
     one = lib.ttt_attention_decode_workspace(1, 64, 64, 32, 8, 128)
