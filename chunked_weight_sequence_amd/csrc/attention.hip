@@ -41,6 +41,7 @@ struct PackedDev {
   float scale;
   int window;
   int tiles, splits;
+  int half;     // row tiles from here on are taken from the other end (packed_plan)
   float* part;  // splits > 1: [splits][Nq * Hq][dh] sums, then [splits][Nq * Hq] (m, l)
 };
 
@@ -289,7 +290,8 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   const int kvh = blockIdx.x % a.Hkv;
   const int rest = blockIdx.x / a.Hkv;
   const int split = rest % a.splits;
-  const int tile = a.tiles - 1 - rest / a.splits;
+  const int turn = rest / a.splits;
+  const int tile = turn < a.half ? a.tiles - 1 - turn : turn - a.half;
 
   const Seq sq = ap_find(a, tile, BM, lane);
   if (sq.s < 0) return;
@@ -729,12 +731,17 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
 // What a call launches: rows per workgroup (128 QT) and pieces of the key axis.
 namespace {
 struct PackedPlan {
-  int qt, tiles, splits;
+  int qt, tiles, splits, half;
 };
 // Keys that an average row sees.
 long packed_seen(int n_seq, int Nq, int Nk, int window) {
   const long seen = (Nk > Nq / 2 ? Nk - Nq / 2 : Nk) / n_seq;
   return window > 0 && window < seen ? window : seen;
+}
+// Keys that the last row sees.
+long packed_keys(int n_seq, int Nk, int window) {
+  const long keys = Nk / n_seq;
+  return window > 0 && window < keys ? window : keys;
 }
 // Workgroups that have rows, if the sequences are alike.
 long packed_wgs(int qt, int n_seq, int Nq, int Hq, int Hkv) {
@@ -748,8 +755,7 @@ long packed_wgs(int qt, int n_seq, int Nq, int Hq, int Hkv) {
 // 35 us in 32 pieces, 31 us in 16; 1024 tokens 20 us whole, 35 us in 2; 2048 tokens of 8/4 heads of 64
 // 24 us whole, 28 us in 2.
 int packed_splits(int qt, int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
-  long keys = Nk / n_seq;
-  if (window > 0 && window < keys) keys = window;
+  const long keys = packed_keys(n_seq, Nk, window);
   // a compute unit each, where a workgroup counts for as much as an average row has of the longest
   const long seen = packed_seen(n_seq, Nq, Nk, window);
   long most = 256 * keys / (packed_wgs(qt, n_seq, Nq, Hq, Hkv) * (seen < 1 ? 1 : seen));
@@ -769,19 +775,28 @@ PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int w
   // 256 rows share each tile read from LDS, which costs least power (long rows are bound by that), but
   // leave the chip's 256 places unevenly filled and nothing to run while a workgroup starts and ends
   // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least
-  // 9 of 10 places, in pieces of at least 1024. Measured, 256 rows against 128, 32/8 heads of 128: 16384 tokens
+  // 9 of 10 places, in pieces of at least 1024, and that are many if their rows differ in length. Measured, 256 rows against 128, 32/8 heads of 128: 16384 tokens
   // 1.76 / 1.87 ms, 512 after 15872 126 / 138 us, 256 after 16000 75 / 80 us; but 64 after 16000 37 / 31
-  // us, 200 after 4000 31 / 28 us, 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105 us,
+  // us, 200 after 4000 31 / 28 us, 4096 tokens of 16/4 heads 98 / 74 us, 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105 us,
   // 12000 tokens of 4/1 heads in 2 documents 205 / 153 us. Heads of 64, which the vector unit bounds:
   // 8191 tokens, window 2048, 188 / 145 us.
-  PackedPlan p{1, 0, 1};
+  PackedPlan p{1, 0, 1, 0};
   if (dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
     const int pieces = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, window);
-    const long n = packed_wgs(2, n_seq, Nq, Hq, Hkv) * pieces;
-    if (packed_seen(n_seq, Nq, Nk, window) >= 1024 * pieces && 10 * n >= 9 * 256 * ((n + 255) / 256)) p.qt = 2;
+    const long wgs = packed_wgs(2, n_seq, Nq, Hq, Hkv), n = wgs * pieces;
+    const long seen = packed_seen(n_seq, Nq, Nk, window);
+    if (seen >= 1024 * pieces && 10 * n >= 9 * 256 * ((n + 255) / 256) &&
+        (wgs >= 384 || 4 * packed_keys(n_seq, Nk, window) <= 5 * seen))
+      p.qt = 2;
   }
   p.tiles = int(long(Nq) * (Hq / Hkv) / (128 * p.qt)) + n_seq;
   p.splits = packed_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
+  // Row tiles are taken from the last on, so that the longest rows start first. Where all workgroups
+  // start at once, two on a compute unit, the second half comes in the opposite order, so that each
+  // unit has a long and a short one: 2048 tokens of 32/8 heads of 128 44 -> 42 us, 1800 38 -> 35.6, 4000
+  // of 8/4 heads of 64 46 -> 44 us.
+  const long wgs = packed_wgs(p.qt, n_seq, Nq, Hq, Hkv) * p.splits;
+  p.half = p.qt == 1 && wgs > 256 && wgs <= 512 ? 256 / (Hkv * p.splits) : p.tiles;
   return p;
 }
 }  // namespace
@@ -799,7 +814,7 @@ hipError_t attention_packed(const PackedArgs& a) {
   const PackedDev d{static_cast<const uint16_t*>(a.Q), static_cast<const uint16_t*>(a.K),
                     static_cast<const uint16_t*>(a.V), a.qs, a.ks, a.vs,
                     static_cast<uint16_t*>(a.O), a.os, a.lse, a.cu_q, a.cu_k, a.n_seq, a.Nq, a.Nk,
-                    a.Hq, a.Hkv, a.Hq / a.Hkv, a.scale, a.window, p.tiles, p.splits,
+                    a.Hq, a.Hkv, a.Hq / a.Hkv, a.scale, a.window, p.tiles, p.splits, p.half,
                     static_cast<float*>(a.ws)};
   const dim3 grid(unsigned(p.tiles) * a.Hkv * p.splits);
   if (p.qt == 2)

@@ -183,7 +183,8 @@ def _some_rows(Q, K, V, cu_q, cu_k, scale, window, tokens, heads):
 
 # long rows whose workgroups of 256 rows fill the compute units evenly: (lq, lk - lq, Hq, Hkv, window)
 WIDE = [([4200], [0], 15, 15, 0), ([4200], [0], 30, 15, 0), ([1000], [3000], 32, 32, 2500),
-        ([2100, 2050], [2000, 2100], 32, 8, 0), ([300], [2500], 28, 28, 0)]
+        ([2100, 2050], [2000, 2100], 32, 8, 0), ([300], [2500], 28, 28, 0), ([4200], [0], 45, 45, 0),
+        ([2100, 2050], [2000, 2100], 60, 15, 0), ([256], [4200], 64, 8, 0), ([256], [16000], 32, 8, 0)]
 
 
 @pytest.mark.parametrize("lq,more,Hq,Hkv,window", WIDE)
@@ -195,7 +196,7 @@ def test_packed_long_rows(lq, more, Hq, Hkv, window):
     K, V = _draw(rng, cu_k[-1], Hkv, dh), _draw(rng, cu_k[-1], Hkv, dh)
     scale = 1.3 * dh ** -0.5
     O, L = _packed(Q, K, V, cu_q, cu_k, scale, window)
-    tokens = sorted({0, 1, 63, 64, 127, 128, 255, 256, int(cu_q[-1]) - 1, int(cu_q[1]) - 1,
+    tokens = sorted({0, 1, 63, 64, 127, 128, 255, int(cu_q[-1]) - 1, int(cu_q[1]) - 1,
                      *rng.integers(0, cu_q[-1], 12).tolist()})
     heads = sorted({0, Hq - 1, *rng.integers(0, Hq, 3).tolist()})
     q, k, v = _f(Q), _f(K), _f(V)
@@ -210,7 +211,7 @@ def test_packed_long_rows(lq, more, Hq, Hkv, window):
 @pytest.mark.parametrize("lq,more,Hq,Hkv,dh,window", [
     ([150], [0], 4, 2, 128, 0), ([150], [0], 4, 2, 64, 0), ([90, 130], [30, 0], 3, 1, 64, 50),
     ([40], [3000], 2, 1, 128, 0),                       # the keys are split
-    ([40], [3000], 2, 1, 128, 1000), ([300], [2500], 28, 28, 128, 0)])
+    ([40], [3000], 2, 1, 128, 1000), ([300], [2500], 28, 28, 128, 0), ([256], [4200], 64, 8, 128, 0)])
 def test_packed_hidden_values_reach_nothing(lq, more, Hq, Hkv, dh, window, bad):
     """Infinities and NaN among the own sequence's keys and values reach the rows that see them, and
     no other row, although the same tiles are multiplied."""
