@@ -88,6 +88,9 @@ PACKED = [
     ([700], [0], 8, 2, 128, 0),
     ([3, 2, 1, 600, 2], [0] * 5, 2, 1, 128, 0),
     ([40], [3000], 2, 1, 128, 0),                     # few rows, many keys
+    ([5, 3], [2, 0], 200, 1, 64, 0),                  # the heads of one query fill more than a row tile
+    ([2, 3], [3000, 2000], 300, 2, 128, 700),
+    ([64, 1, 0, 33], [1900, 2500, 1000, 0], 4, 2, 64, 0),   # split, of unlike lengths
 ]
 
 
@@ -358,6 +361,22 @@ def test_decode_stale_window_rows_bad_pages_and_lengths():
     for a, b in zip(run(Kc, Vc, table, [full + 99, -5, -(1 << 31)], 0),
                     run(Kc, Vc, table, [full, 0, 0], 0)):
         np.testing.assert_array_equal(a, b)
+
+
+def test_decode_pages_of_several_sequences():
+    """A page may stand in several rows of the table (a shared prefix), and twice in one."""
+    import torch
+    print("case: decode shared pages", flush=True)
+    rng = np.random.default_rng(11)
+    page, Hq, Hkv, dh = 32, 4, 2, 64
+    Kc, Vc = _draw(rng, 9 * page, Hkv, dh), _draw(rng, 9 * page, Hkv, dh)
+    table = np.array([[4, 1, 7, -1], [4, 1, 2, 8], [5, 5, 5, 5]], np.int32)
+    lens, Q = [80, 128, 100], _draw(rng, 3, Hq, dh)
+    O, L = ttt.attention_decode(dev(Q, "bf16"), dev(Kc, "bf16"), dev(Vc, "bf16"), _i32(table),
+                                _i32(lens), page, with_lse=True)
+    torch.cuda.synchronize()
+    X = dh ** -0.5 * np.abs(_f(Q)).sum(-1) * _seen(Kc, table, lens, page)
+    _check(O, L, oa.decode(_f(Q), _f(Kc), _f(Vc), table, lens, page, dh ** -0.5), X, dh, "shared")
 
 
 def test_decode_equals_the_packed_call_on_the_same_keys():

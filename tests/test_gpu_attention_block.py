@@ -242,6 +242,25 @@ def test_two_streams_and_given_workspaces():
                 call(workspace=bad)
 
 
+def test_split_rows_of_no_sequence_are_left():
+    import torch
+    print("case: split keys, rows of no sequence", flush=True)
+    rng = np.random.default_rng(7)
+    Nq, Nk, Hq, Hkv, dh = 40, 5000, 4, 1, 128
+    assert ttt.lib().ttt_attention_packed_workspace(2, Nq, Nk, Hq, Hkv, dh) > 0
+    q, k, v = _draw(rng, Nq, Hq, dh), _draw(rng, Nk, Hkv, dh), _draw(rng, Nk, Hkv, dh)
+    cq, ck = np.array([3, 20, 33]), np.array([40, 4000, 4990])
+    O = torch.full((Nq, Hq, dh), 7.0, dtype=torch.bfloat16, device="cuda")
+    L = torch.full((Nq, Hq), 7.0, device="cuda")
+    ttt.attention_packed(dev(q, "bf16"), dev(k, "bf16"), dev(v, "bf16"), _i32(cq), _i32(ck), O=O, lse=L)
+    torch.cuda.synchronize()
+    for x in (O[:3], O[33:], L[:3], L[33:]):
+        assert (x == 7).all()
+    tokens = list(range(3, 33))
+    want = _some_rows(_f(q), _f(k), _f(v), cq, ck, dh ** -0.5, 0, tokens, range(Hq))
+    _check(O[3:33], L[3:33], want, _logit_size(_f(q), _f(k), dh ** -0.5)[3:33], dh, "split")
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 4 GiB: rows at its end are written and read; a packed call whose rows lie
     far apart."""
