@@ -15,7 +15,7 @@
 // one (33 clocks per 32x32x16 product: 1056 with heads of 128, 528 with 64). So heads of 128 are bound by
 // the matrix pipe, and by power where rows are long (the clock falls to 1.6 .. 2.0 GHz), heads of 64 by
 // the vector unit. 32/8 heads of 128: 16384 tokens 1.69 .. 1.88 ms (1170 .. 1300 TFLOP/s over the visible
-// pairs; a large matrix product 1350 .. 1550), 11 documents in 8192 tokens 103 .. 112 us, 512 tokens after
+// pairs; a large matrix product 1350 .. 1550), 11 documents in 8192 tokens 103 .. 109 us, 512 tokens after
 // 15872 124 .. 134 us; 32/32 heads of 64, 8191 tokens, window 2048: 139 .. 154 us. A workgroup takes 4 us
 // to its first round (its sequence 0.6, set up 0.6, copies 1.5, queries to registers 0.5, first scores
 // 0.9), 1.2 .. 1.5 per tile of 128 rows with two on a unit, and 2 to write its rows.
@@ -43,49 +43,87 @@ struct PackedDev {
   float scale;
   int window;
   int tiles, splits;
-  int half;     // row tiles from here on are taken from the other end (packed_plan)
+  int half;     // pieces of work from here on are taken from the other end (packed_plan)
   float* part;  // splits > 1: [splits][Nq * Hq][dh] sums, then [splits][Nq * Hq] (m, l)
 };
 
-// The sequence that holds row tile `tile`, and its offsets (clamped to the buffers). Sequence s owns
-// the ids [base(s), base(s + 1)), base(s) = cu_q[s] * G / BM + s: at least as many as it has tiles.
-struct Seq {
-  int s, q0, q1, k0, k1;  // s < 0: no sequence starts at or below `tile`
+// The w-th piece of work: a sequence's offsets (clamped to the buffers) and which of its row tiles, its
+// last one first.
+struct Work {
+  int q0, q1, k0, k1, r;  // r < 0: there is no such tile
 };
-__device__ __forceinline__ Seq ap_find(const PackedDev& a, int tile, int BM, int lane) {
+__device__ __forceinline__ Work ap_find(const PackedDev& a, int w, int BM, int lane) {
+  // of sequences one after the other: s owns the ids [base(s), base(s + 1)), at least as many as it has
+  // tiles
   const auto base = [&](int cu, int s) { return int(uint32_t(cu) * uint32_t(a.G) / uint32_t(BM)) + s; };
   const auto clampq = [&](int s) { return min(max(a.cu_q[s], 0), a.Nq); };
-  Seq r;
-  if (a.n_seq < 64) {  // one load for everything: lane s has sequence s
+  const auto clampk = [&](int s) { return min(max(a.cu_k[s], 0), a.Nk); };
+  const int tile = a.tiles - 1 - w;
+  Work p;
+  p.r = -1;
+  int at = 0;
+  const auto tiles = [&](int lq) {
+    return int((uint32_t(max(lq, 0)) * uint32_t(a.G) + uint32_t(BM - 1)) / uint32_t(BM));
+  };
+  if (a.n_seq == 1) {
+    p.q0 = clampq(0);
+    p.q1 = clampq(1);
+    p.k0 = clampk(0);
+    p.k1 = clampk(1);
+    p.r = tiles(p.q1 - p.q0) - 1 - w;
+  } else if (a.n_seq < 64) {  // one load for everything: lane s has sequence s
     const int s = min(lane, a.n_seq);
-    const int cq = clampq(s), ck = min(max(a.cu_k[s], 0), a.Nk);
-    r.s = __popcll(__ballot(lane < a.n_seq && base(cq, s) <= tile)) - 1;
-    const int at = max(r.s, 0);
-    r.q0 = __builtin_amdgcn_readlane(cq, at);
-    r.q1 = __builtin_amdgcn_readlane(cq, at + 1);
-    r.k0 = __builtin_amdgcn_readlane(ck, at);
-    r.k1 = __builtin_amdgcn_readlane(ck, at + 1);
+    const int cq = clampq(s), ck = clampk(s);
+    if (a.n_seq <= 16) {
+      // The sequence with most keys first, so that what starts last is short (otherwise the last one
+      // first): 11 documents in 8192 tokens 103 / 106 us, 3 in 4096 63 / 67, 12 in 4096 33.5 / 32.9. Past
+      // 16 the order gains less than it costs (30 clocks a sequence).
+      const int cq1 = __builtin_amdgcn_update_dpp(0, cq, 0x130, 0xF, 0xF, true);  // of the lane above
+      const int ck1 = __builtin_amdgcn_update_dpp(0, ck, 0x130, 0xF, 0xF, true);
+      const int lk = max(ck1 - ck, 0);
+      const int n = tiles(cq1 - cq);
+      int before = 0;  // row tiles of the sequences that come first
+      for (int j = 0; j < a.n_seq; ++j) {
+        const int kj = __builtin_amdgcn_readlane(lk, j), nj = __builtin_amdgcn_readlane(n, j);
+        before += kj > lk || (kj == lk && j < lane) ? nj : 0;
+      }
+      const uint64_t on = __ballot(lane < a.n_seq && w >= before && w - before < n);
+      if (on) {
+        at = __builtin_ctzll(on);
+        p.r = __builtin_amdgcn_readlane(n, at) - 1 - (w - __builtin_amdgcn_readlane(before, at));
+      }
+    } else {
+      at = __popcll(__ballot(lane < a.n_seq && base(cq, s) <= tile)) - 1;
+      if (at >= 0) p.r = tile - base(__builtin_amdgcn_readlane(cq, at), at);
+      else at = 0;
+    }
+    p.q0 = __builtin_amdgcn_readlane(cq, at);
+    p.q1 = __builtin_amdgcn_readlane(cq, at + 1);
+    p.k0 = __builtin_amdgcn_readlane(ck, at);
+    p.k1 = __builtin_amdgcn_readlane(ck, at + 1);
   } else {  // 64-way search
     int lo = 0, len = a.n_seq;
+    bool some = true;
     while (true) {
       const int step = (len + 63) / 64, s = lo + lane * step;
       const bool in = lane * step < len;
       const int n = __popcll(__ballot(in && base(clampq(in ? s : lo), s) <= tile));
-      r.s = n == 0 ? -1 : lo + (n - 1) * step;
-      if (n == 0 || step == 1) break;
+      some = n > 0;
+      if (some) at = lo + (n - 1) * step;
+      if (!some || step == 1) break;
       len = min(step, len - (n - 1) * step);
-      lo = r.s;
+      lo = at;
     }
-    r.s = __builtin_amdgcn_readfirstlane(r.s);
-    const int at = max(r.s, 0);
-    r.q0 = clampq(at);
-    r.q1 = clampq(at + 1);
-    r.k0 = min(max(a.cu_k[at], 0), a.Nk);
-    r.k1 = min(max(a.cu_k[at + 1], 0), a.Nk);
+    at = __builtin_amdgcn_readfirstlane(at);
+    p.q0 = clampq(at);
+    p.q1 = clampq(at + 1);
+    p.k0 = clampk(at);
+    p.k1 = clampk(at + 1);
+    if (some) p.r = tile - base(p.q0, at);
   }
-  r.q1 = max(r.q1, r.q0);
-  r.k1 = max(r.k1, r.k0);
-  return r;
+  p.q1 = max(p.q1, p.q0);
+  p.k1 = max(p.k1, p.k0);
+  return p;
 }
 
 // S^T tile of 32 keys by 32 queries into ordinary registers, where the exponentials are taken; the
@@ -293,14 +331,13 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   const int rest = blockIdx.x / a.Hkv;
   const int split = rest % a.splits;
   const int turn = rest / a.splits;
-  const int tile = turn < a.half ? a.tiles - 1 - turn : turn - a.half;
 
-  const Seq sq = ap_find(a, tile, BM, lane);
-  if (sq.s < 0) return;
-  const int q0 = sq.q0, k0 = sq.k0, G = a.G;
-  const int rows = (sq.q1 - q0) * G, lk = sq.k1 - k0, off = lk - (sq.q1 - q0);
-  const int row0 = (tile - sq.s - int(uint32_t(q0) * uint32_t(G) / uint32_t(BM))) * BM;
-  if (row0 < 0 || row0 >= rows) return;
+  const Work wk = ap_find(a, turn < a.half ? turn : a.tiles - 1 - (turn - a.half), BM, lane);
+  if (wk.r < 0) return;
+  const int q0 = wk.q0, k0 = wk.k0, G = a.G;
+  const int rows = (wk.q1 - q0) * G, lk = wk.k1 - k0, off = lk - (wk.q1 - q0);
+  const int row0 = wk.r * BM;
+  if (row0 >= rows) return;
   // Row x of the workgroup is query qa + v / G, head v % G, v = first + x. The quotient in fp32: v is
   // below 2^17, so its error, 2^-22 v / G, is less than the 1 / (2 G) to the next whole number.
   const int qa = row0 / G, first = row0 - qa * G, rows_here = min(BM, rows - row0);
@@ -791,14 +828,15 @@ PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int w
         (wgs >= 384 || 4 * packed_keys(n_seq, Nk, window) <= 5 * seen))
       p.qt = 2;
   }
-  p.tiles = int(long(Nq) * (Hq / Hkv) / (128 * p.qt)) + n_seq;
+  const long rows = long(Nq) * (Hq / Hkv);
+  p.tiles = n_seq == 1 ? int((rows + 128 * p.qt - 1) / (128 * p.qt)) : int(rows / (128 * p.qt)) + n_seq;
   p.splits = packed_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
   // Row tiles are taken from the last on, so that the longest rows start first. Where all workgroups
-  // start at once, two on a compute unit, the second half comes in the opposite order, so that each
-  // unit has a long and a short one: 2048 tokens of 32/8 heads of 128 44 -> 42 us, 1800 38 -> 35.6, 4000
+  // start at once, two on a compute unit (three of heads of 64), those past the first 256 come in the
+  // opposite order, so that each unit has long and short ones: 2048 tokens of 32/8 heads of 128 44 -> 42 us, 1800 38 -> 35.6, 4000
   // of 8/4 heads of 64 46 -> 44 us.
   const long wgs = packed_wgs(p.qt, n_seq, Nq, Hq, Hkv) * p.splits;
-  p.half = p.qt == 1 && wgs > 256 && wgs <= 512 ? 256 / (Hkv * p.splits) : p.tiles;
+  p.half = p.qt == 1 && wgs > 256 && wgs <= (dh == 64 ? 768 : 512) ? 256 / (Hkv * p.splits) : p.tiles;
   return p;
 }
 }  // namespace
