@@ -224,8 +224,8 @@ struct ApPlan {
 // way of its own 32 rows of LDS. 16384 tokens of 32/8 heads of 128 take 1.8 ms; with one infinity in the
 // last token 4.4 ms, in the first, which every row of a head sees, 15 ms, with nothing but NaN in V 26 ms.
 template <int DH, int QT>
-__device__ __forceinline__ void ap_again(f32x16 (&o)[DH / 32][QT], int b, const bf16x8 (&qf)[DH / 16], const char* tile,
-                                         const uint16_t* K, long ks, const uint16_t* V, long vs, int j0,
+__device__ __forceinline__ void ap_again(f32x16 (&o)[DH / 32][QT], int b,
+                                         const bf16x8 (&qf)[DH / 16], const char* tile, const uint16_t* K, long ks, const uint16_t* V, long vs, int j0,
                                          int j1, int lo, int hi, float c, float base, int lane) {
   constexpr int KS = DH / 16, DT = DH / 32, RPI = 1024 / (DH * 2);
   const FragOff<DH> fo(lane);
@@ -813,12 +813,13 @@ int packed_splits(int qt, int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, in
 PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
   // 256 rows share each tile read from LDS, which costs least power (long rows are bound by that), but
   // leave the chip's 256 places unevenly filled and nothing to run while a workgroup starts and ends
-  // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least
-  // 9 of 10 places, in pieces of at least 1024, and that are many if their rows differ in length. Measured, 256 rows against 128, 32/8 heads of 128: 16384 tokens
-  // 1.76 / 1.87 ms, 512 after 15872 126 / 138 us, 256 after 16000 75 / 80 us; but 64 after 16000 37 / 31
-  // us, 200 after 4000 31 / 28 us, 4096 tokens of 16/4 heads 98 / 74 us, 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105 us,
-  // 12000 tokens of 4/1 heads in 2 documents 205 / 153 us. Heads of 64, which the vector unit bounds:
-  // 8191 tokens, window 2048, 188 / 145 us.
+  // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least 9
+  // of 10 places, in pieces of at least 1024, and that are many if their rows differ in length.
+  // Measured, 256 rows against 128, 32/8 heads of 128: 16384 tokens 1.76 / 1.87 ms, 512 after 15872 126
+  // / 138 us, 256 after 16000 75 / 80 us; but 64 after 16000 37 / 31 us, 200 after 4000 31 / 28 us,
+  // 4096 tokens of 16/4 heads 98 / 74 us, 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105
+  // us, 12000 tokens of 4/1 heads in 2 documents 205 / 153 us. Heads of 64, which the vector unit
+  // bounds: 8191 tokens, window 2048, 188 / 145 us.
   PackedPlan p{1, 0, 1, 0};
   if (dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
     const int pieces = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, window);
@@ -833,8 +834,8 @@ PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int w
   p.splits = packed_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
   // Row tiles are taken from the last on, so that the longest rows start first. Where all workgroups
   // start at once, two on a compute unit (three of heads of 64), those past the first 256 come in the
-  // opposite order, so that each unit has long and short ones: 2048 tokens of 32/8 heads of 128 44 -> 42 us, 1800 38 -> 35.6, 4000
-  // of 8/4 heads of 64 46 -> 44 us.
+  // opposite order, so that each unit has long and short ones: 2048 tokens of 32/8 heads of 128 44 ->
+  // 42 us, 1800 38 -> 35.6, 4000 of 8/4 heads of 64 46 -> 44 us.
   const long wgs = packed_wgs(p.qt, n_seq, Nq, Hq, Hkv) * p.splits;
   p.half = p.qt == 1 && wgs > 256 && wgs <= (dh == 64 ? 768 : 512) ? 256 / (Hkv * p.splits) : p.tiles;
   return p;
