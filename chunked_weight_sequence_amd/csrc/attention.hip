@@ -225,8 +225,10 @@ struct ApPlan {
 // last token 4.4 ms, in the first, which every row of a head sees, 15 ms, with nothing but NaN in V 26 ms.
 template <int DH, int QT>
 __device__ __forceinline__ void ap_again(f32x16 (&o)[DH / 32][QT], int b,
-                                         const bf16x8 (&qf)[DH / 16], const char* tile, const uint16_t* K, long ks, const uint16_t* V, long vs, int j0,
-                                         int j1, int lo, int hi, float c, float base, int lane) {
+                                         const bf16x8 (&qf)[DH / 16], const char* tile,
+                                         const uint16_t* K, long ks, const uint16_t* V, long vs,
+                                         int j0, int j1, int lo, int hi, float c, float base,
+                                         int lane) {
   constexpr int KS = DH / 16, DT = DH / 32, RPI = 1024 / (DH * 2);
   const FragOff<DH> fo(lane);
   const uint32_t lds = lds_u32(tile);
