@@ -20,6 +20,7 @@ The attention half of a block, over a packed prompt and then token by token:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -120,10 +121,10 @@ def _dtype_code(t) -> int:
     """Library dtype code of a tensor or a torch.dtype."""
     torch = _torch()
     dt = t if isinstance(t, torch.dtype) else t.dtype
-    if dt == torch.float32:
-        return TTT_F32
-    if dt == torch.bfloat16:
+    if dt is torch.bfloat16:
         return TTT_BF16
+    if dt is torch.float32:
+        return TTT_F32
     raise TypeError(f"unsupported dtype {dt}: use float32 or bfloat16")
 
 
@@ -642,8 +643,8 @@ def attention_packed(Q, K, V, cu_q, cu_k=None, *, scale=None, window: int = 0, O
         _vec(lse, "lse", (Nq, Hq), torch.float32, dev)
     elif with_lse:
         lse = torch.empty(Nq, Hq, dtype=torch.float32, device=dev)
-    ws, ws_bytes = _workspace(workspace, lib().ttt_attention_packed_workspace(
-        n_seq, Nq, Nk, Hq, Hkv, dh), dev)
+    ws, ws_bytes = _workspace(workspace, _workspace_bytes(
+        "ttt_attention_packed_workspace", n_seq, Nq, Nk, Hq, Hkv, dh), dev)
     _launch(lib().ttt_attention_packed,
             (Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs, _dtype_code(dt), O.data_ptr(),
              os_, _ptr(lse), cu_q.data_ptr(), cu_k.data_ptr(), n_seq, Nq, Nk, Hq, Hkv, dh,
@@ -679,14 +680,20 @@ def attention_decode(Q, K_cache, V_cache, page_table, lengths, page_size: int, *
         _vec(lse, "lse", (S, Hq), torch.float32, dev)
     elif with_lse:
         lse = torch.empty(S, Hq, dtype=torch.float32, device=dev)
-    ws, ws_bytes = _workspace(workspace, lib().ttt_attention_decode_workspace(
-        S, max_pages, page_size, Hq, Hkv, dh), dev)
+    ws, ws_bytes = _workspace(workspace, _workspace_bytes(
+        "ttt_attention_decode_workspace", S, max_pages, page_size, Hq, Hkv, dh), dev)
     _launch(lib().ttt_attention_decode,
             (Q.data_ptr(), qs, K_cache.data_ptr(), V_cache.data_ptr(), _dtype_code(dt),
              O.data_ptr(), os_, _ptr(lse), page_table.data_ptr(), max_pages, page_size,
              n_slots // page_size, lengths.data_ptr(), S, Hq, Hkv, dh,
              dh ** -0.5 if scale is None else scale, window, _ptr(ws), ws_bytes), dev)
     return O if lse is None else (O, lse)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(query: str, *sizes) -> int:
+    """A workspace query of the library, which depends on the sizes only (0.2 instead of 0.4 us)."""
+    return getattr(lib(), query)(*sizes)
 
 
 def _workspace(given, need: int, device):
