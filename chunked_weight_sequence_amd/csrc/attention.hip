@@ -868,7 +868,7 @@ hipError_t attention_packed(const PackedArgs& a) {
     hipLaunchKernelGGL((k_attention_packed<64, 1>), grid, dim3(256), 0, a.stream, d);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  return attention_join(d.part, p.splits, a.cu_q, a.n_seq, long(a.Nq) * a.Hq, a.Hq, a.dh, a.O, a.os,
+  return attention_join(d.part, p.splits, a.cu_q, a.n_seq, long(a.Nq) * a.Hq, a.Hq, a.Hkv, a.dh, a.O, a.os,
                         a.lse, a.scale, a.stream);
 }
 

@@ -242,7 +242,7 @@ hipError_t attention_packed(const PackedArgs& a);
 // sums [splits][nrows][dh], then (maximum logit, sum) [splits][nrows][2] (decode.hip). With cu_q,
 // only the rows of tokens in [cu_q[0], cu_q[n_seq]).
 hipError_t attention_join(const float* part, int splits, const int* cu_q, int n_seq, long nrows,
-                          int Hq, int dh, void* O, long os, float* lse, float scale,
+                          int Hq, int Hkv, int dh, void* O, long os, float* lse, float scale,
                           hipStream_t stream);
 
 // One query per sequence over a paged cache.
