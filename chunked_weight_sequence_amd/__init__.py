@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 __all__ = [
@@ -496,10 +497,12 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = N
     torch = _torch()
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, got {scaling!r}")
-    out = (ctypes.c_double * max(1, int(rot) // 2))()
+    rot = _int_in(rot, "rot", 2, 256)
+    original_length = _int_in(original_length, "original_length", 0, (1 << 31) - 1)
+    out = (ctypes.c_double * (rot // 2))()
     scale = ctypes.c_float(1.0)
-    _check(lib().ttt_rope_frequencies(ctypes.addressof(out), int(rot), float(base),
-                                      ROPE_SCALINGS[scaling], float(factor), int(original_length),
+    _check(lib().ttt_rope_frequencies(ctypes.addressof(out), rot, float(base),
+                                      ROPE_SCALINGS[scaling], float(factor), original_length,
                                       float(beta_fast), float(beta_slow),
                                       ctypes.addressof(scale)))
     return (torch.tensor(list(out), dtype=torch.float64, device=device or "cuda"), scale.value)
@@ -540,9 +543,10 @@ def _vec(t, name: str, shape, dtype, device):
 
 def _int_in(value, name: str, lo: int, hi: int) -> int:
     """An argument that the C ABI takes as an int: refused where ctypes would cut it."""
+    value = operator.index(value)
     if not lo <= value <= hi:
         raise ValueError(f"{name} must lie in [{lo}, {hi}], got {value}")
-    return int(value)
+    return value
 
 
 def _launch(fn, args, device):

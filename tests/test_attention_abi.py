@@ -155,3 +155,13 @@ def test_binding_refuses_cpu_tensors_and_unknown_names():
         ttt.attention_decode(q, q, q, cu[None], cu, 16)
     with pytest.raises(ValueError):
         ttt.rope_frequencies(64, scaling="other")
+    for bad in (0, 1, -64, 258, (1 << 40) + 64):
+        with pytest.raises(ValueError):
+            ttt.rope_frequencies(bad, device="cpu")
+    with pytest.raises(ttt.TTTError):
+        ttt.rope_frequencies(7, device="cpu")          # odd
+    with pytest.raises(TypeError):
+        ttt.rope_frequencies(64.0, device="cpu")
+    with pytest.raises(ValueError):
+        ttt.rope_frequencies(64, scaling="yarn", factor=4.0, original_length=(1 << 32) + 4096,
+                             device="cpu")
