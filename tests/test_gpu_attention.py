@@ -422,3 +422,42 @@ def test_attention_refuses_what_it_cannot_check_on_the_device():
         args.update(kw)
         with pytest.raises((ValueError, TypeError, ttt.TTTError)):
             ttt.attention_decode(**args)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_packed_random_shapes(seed):
+    rng = np.random.default_rng(1000 + seed)
+    dh, Hkv, G = int(rng.choice([64, 128])), int(rng.choice([1, 2, 3, 8])), int(rng.choice([1, 2, 4, 5]))
+    n = int(rng.choice([1, 2, 5, 16, 17, 40, 63, 64, 80]))
+    lq = rng.multinomial(int(rng.integers(1, 500)), rng.dirichlet(np.ones(n)))
+    more = rng.integers(-20, int(rng.choice([1, 60, 600])), n) * int(rng.integers(0, 2))
+    lk = np.maximum(lq + more, 0)
+    window = int(rng.choice([0, 0, 1, 30, 100]))
+    print(f"case: packed random {seed}: {n} sequences, {lq.sum()} queries, {lk.sum()} keys, "
+          f"{Hkv * G}/{Hkv}x{dh} window={window}", flush=True)
+    cu_q, cu_k = _cu(lq), _cu(lk)
+    Q = _draw(rng, cu_q[-1], Hkv * G, dh)
+    K, V = _draw(rng, max(cu_k[-1], 1), Hkv, dh), _draw(rng, max(cu_k[-1], 1), Hkv, dh)
+    scale = float(rng.uniform(0.5, 2)) * dh ** -0.5
+    O, L = _packed(Q, K, V, cu_q, cu_k, scale, window)
+    _check(O, L, oa.packed(_f(Q), _f(K), _f(V), cu_q, cu_k, scale, window),
+           _logit_size(_f(Q), _f(K), scale), dh, "packed")
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_decode_random_shapes(seed):
+    import torch
+    rng = np.random.default_rng(2000 + seed)
+    dh, Hkv, G = int(rng.choice([64, 128])), int(rng.choice([1, 2, 3, 8])), int(rng.choice([1, 4, 7, 33]))
+    S, page = int(rng.choice([1, 2, 9, 40])), int(rng.choice([16, 32, 128]))
+    lens = [int(x) for x in rng.integers(0, int(rng.choice([40, 400, 2000])) // S ** 0.5 + 2, S)]
+    window = int(rng.choice([0, 0, 1, 33, 200]))
+    print(f"case: decode random {seed}: lens={lens[:8]} page={page} {Hkv * G}/{Hkv}x{dh} "
+          f"window={window}", flush=True)
+    Kc, Vc, table = _cache(rng, lens, page, Hkv, dh)
+    Q, scale = _draw(rng, S, Hkv * G, dh), 1.2 * dh ** -0.5
+    O, L = ttt.attention_decode(dev(Q, "bf16"), dev(Kc, "bf16"), dev(Vc, "bf16"), _i32(table),
+                                _i32(lens), page, scale=scale, window=window, with_lse=True)
+    torch.cuda.synchronize()
+    X = scale * np.abs(_f(Q)).sum(-1) * _seen(Kc, table, lens, page)
+    _check(O, L, oa.decode(_f(Q), _f(Kc), _f(Vc), table, lens, page, scale, window), X, dh, "decode")
