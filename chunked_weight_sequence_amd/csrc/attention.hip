@@ -44,7 +44,7 @@ struct PackedDev {
   int window;
   int tiles, splits;
   int half;     // pieces of work from here on are taken from the other end (packed_plan)
-  float* part;  // splits > 1: [splits][Nq * Hq][dh] sums, then [splits][Nq * Hq] (m, l)
+  float* part;  // splits > 1: [splits][Nq * Hq][dh] means, then [splits][Nq * Hq] (m, l)
 };
 
 // The w-th piece of work: a sequence's offsets (clamped to the buffers) and which of its row tiles, its
@@ -220,7 +220,8 @@ struct ApPlan {
 // value that a row does not see by a weight of 0, and 0 times an infinity or a NaN is a NaN. Here such
 // values are multiplied as 0, and what the rows that see them get is found by products of 1 and 0:
 // which of +inf, -inf and NaN a row sees at all. The maxima and sums of the first pass are right and
-// stay. By the wave alone, 32 keys [j, j + 32) of [j0, j1) at a time: K straight into registers, V by
+// stay; the weights are divided by their sum here (inv: 1 / sum) before they meet the values, so that
+// finite values, whose mean is finite, do not pass fp32 on the way. By the wave alone, 32 keys [j, j + 32) of [j0, j1) at a time: K straight into registers, V by
 // way of its own 32 rows of LDS. 16384 tokens of 32/8 heads of 128 take 1.8 ms; with one infinity in the
 // last token 4.4 ms, in the first, which every row of a head sees, 15 ms, with nothing but NaN in V 26 ms.
 template <int DH, int QT>
@@ -228,7 +229,7 @@ __device__ __forceinline__ void ap_again(f32x16 (&o)[DH / 32][QT], int b,
                                          const bf16x8 (&qf)[DH / 16], const char* tile,
                                          const uint16_t* K, long ks, const uint16_t* V, long vs,
                                          int j0, int j1, int lo, int hi, float c, float base,
-                                         int lane) {
+                                         float inv, int lane) {
   constexpr int KS = DH / 16, DT = DH / 32, RPI = 1024 / (DH * 2);
   const FragOff<DH> fo(lane);
   const uint32_t lds = lds_u32(tile);
@@ -262,7 +263,7 @@ __device__ __forceinline__ void ap_again(f32x16 (&o)[DH / 32][QT], int b,
       for (int e = 0; e < 2; ++e) {
         const int key = j + 8 * (i / 4) + 4 * h + (i & 3) + e;
         const bool in = key >= lo && key <= hi && key < j1;
-        p[e] = in ? exp2_fast(fmaf(s[i + e], c, -base)) : 0.f;
+        p[e] = in ? exp2_fast(fmaf(s[i + e], c, -base)) * inv : 0.f;
         seen |= uint32_t(in) << (i + e);
       }
       pw[i / 2] = pack2bf(p[0], p[1]);
@@ -716,7 +717,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
     const float lt = sum_halves(l[b][0] + l[b][1]);
-    float zero = 0.f;
+    float inv = lt == 0.f ? 0.f : 1.f / lt, zero = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -724,7 +725,8 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
     if (__any(zero != 0.f && lt == lt)) {  // not finite, although the weights are
       ap_again<DH>(o, b, qf[b], out + 32 * b * DH * 2, a.K + long(k0) * a.ks + kvh * DH, a.ks,
                    a.V + long(k0) * a.vs + kvh * DH, a.vs, t0 * AP_BN, min(t1 * AP_BN, lk), lo[b], hi[b],
-                   c, base[b], ln);
+                   c, base[b], inv, ln);
+      inv = 1.f;
     }
     const int r = 32 * b + (ln & 31), x = wrow + r, qi = query(x);
     const bool on = x < rows_here;
@@ -738,14 +740,14 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
           *reinterpret_cast<float4*>(po + 32 * d + 2 * i) =
-              make_float4(o[d][b][i], o[d][b][i + 1], o[d][b][i + 2], o[d][b][i + 3]);
+              make_float4(o[d][b][i] * inv, o[d][b][i + 1] * inv, o[d][b][i + 2] * inv,
+                          o[d][b][i + 3] * inv);
       if (ln < 32) {
         float* ml = a.part + long(a.splits) * n * DH + (long(split) * n + rr) * 2;
         *reinterpret_cast<float2*>(ml) = make_float2(m[b], lt);
       }
       continue;
     }
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll

@@ -54,6 +54,7 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
   constexpr int NI = 16 / RPI;  // copies per 16-token half of a tile
   __shared__ __align__(1024) char sm[W][2][2][TILE];  // wave, stage, K / V
   __shared__ float2 ml_s[W][32];
+  __shared__ bool odd_s;  // a result is not finite, although its weights are
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int h = lane >> 5, col = lane & 31;
   int id = blockIdx.x;
@@ -135,109 +136,134 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
   float m = -INFINITY, l = 0.f;
   const float c = a.scale * kLog2e;
 
-  int good = 0, t = t0 + wave, stage = 0;
-  if (t < t1) good = issue(t, 0);
-  for (; t < t1; t += W, stage ^= 1) {
-    int good_next = 0;
-    // this tile's stage was read two rounds ago: those reads are done before it is refilled
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (t + W < t1) {
-      good_next = issue(t + W, stage ^ 1);
-      wait_vm<4 * NI>();
-    } else {
-      wait_vm<0>();
-    }
-    const char* kt = &sm[wave][stage][0][0];
-    const char* vt = &sm[wave][stage][1][0];
-    f32x16 s;
+  // The weights are relative to the running maximum and divided by their sum at the end, so sums of finite
+  // values can pass fp32 on the way although their mean does not. Where that shows in the results, they are
+  // taken a second time, with the weights divided by the sum of the first: exponents are lower by `add`, its
+  // logarithm.
+  float* js = reinterpret_cast<float*>(&sm[0][0][0][0]);
+  const long nrows = long(a.n_seq) * a.Hq;
+  float add = 0.f, whole = 0.f;
+  bool again = false;
+  if (tid == 0) odd_s = false;  // seen by all behind the first barrier
+  while (true) {
+    int good = 0, t = t0 + wave, stage = 0;
+    if (t < t1) good = issue(t, 0);
+    for (; t < t1; t += W, stage ^= 1) {
+      int good_next = 0;
+      // this tile's stage was read two rounds ago: those reads are done before it is refilled
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (t + W < t1) {
+        good_next = issue(t + W, stage ^ 1);
+        wait_vm<4 * NI>();
+      } else {
+        wait_vm<0>();
+      }
+      const char* kt = &sm[wave][stage][0][0];
+      const char* vt = &sm[wave][stage][1][0];
+      f32x16 s;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = 0.f;
+      for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) s = mfma32x32x16(fo.key(kt, 0, ks), qf[ks], s);
-    const int j0 = t * DC_BN;
-    if (good != 3 || j0 < first || j0 + DC_BN > n) {
+      for (int ks = 0; ks < KS; ++ks) s = mfma32x32x16(fo.key(kt, 0, ks), qf[ks], s);
+      const int j0 = t * DC_BN;
+      if (good != 3 || j0 < first || j0 + DC_BN > n) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = j0 + 8 * (i / 4) + 4 * h + (i & 3);
+          if (j < first || j >= n || !((good >> (i / 8)) & 1)) s[i] = -INFINITY;
+        }
+      }
+      float mx = m;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i]);
+      mx = max_halves(mx);
+      const float top = mx == -INFINITY ? 0.f : mx * c, base = top + add;
+      const float al = exp2_fast(fmaf(m, c, -top));
+      float p[16], sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int j = j0 + 8 * (i / 4) + 4 * h + (i & 3);
-        if (j < first || j >= n || !((good >> (i / 8)) & 1)) s[i] = -INFINITY;
+        p[i] = exp2_fast(fmaf(s[i], c, -base));
+        sum += p[i];
+      }
+      l = l * al + sum;
+      m = mx;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= al;
+#pragma unroll
+      for (int s2 = 0; s2 < 2; ++s2) {
+        const uint4 pf = make_uint4(pack2bf(p[8 * s2], p[8 * s2 + 1]), pack2bf(p[8 * s2 + 2], p[8 * s2 + 3]),
+                                    pack2bf(p[8 * s2 + 4], p[8 * s2 + 5]), pack2bf(p[8 * s2 + 6], p[8 * s2 + 7]));
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] = mfma32x32x16(fo.value(vt, s2, d), pf, o[d]);
+      }
+      good = good_next;
+    }
+    l = again ? whole : sum_halves(l);
+
+    // join the waves: [wave][column][channel] fp32 in the ring that no copy fills any more
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (col < gn) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(js + (wave * 32 + col) * DH + 32 * d + 2 * i + 4 * h) =
+              make_float4(o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]);
+      if (h == 0) ml_s[wave][col] = make_float2(m, l);
+    }
+    __syncthreads();
+    for (int e = tid; e < gn * (DH / 4); e += 64 * W) {
+      const int g = e / (DH / 4), d4 = e % (DH / 4) * 4;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < W; ++w) mx = fmaxf(mx, ml_s[w][g].x);
+      const float base = mx == -INFINITY ? 0.f : mx * c;
+      float lt = 0.f, part[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 x = ml_s[w][g];
+        part[w] = exp2_fast(fmaf(x.x, c, -base));
+        lt = fmaf(part[w], x.y, lt);
+      }
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {  // the wave's weight in the mean before its values: finite stays finite
+        const float f = (again ? part[w] * ml_s[w][g].y : part[w]) * inv;
+        const float4 v = *reinterpret_cast<const float4*>(js + (w * 32 + g) * DH + d4);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      if (lt < INFINITY && acc.x * 0.f + acc.y * 0.f + acc.z * 0.f + acc.w * 0.f != 0.f) odd_s = true;
+      const int hq = kvh * a.G + g0 + g;
+      const long rr = long(seq) * a.Hq + hq;
+      if (a.splits > 1) {
+        *reinterpret_cast<float4*>(a.part + (split * nrows + rr) * DH + d4) = acc;
+        if (d4 == 0)
+          *reinterpret_cast<float2*>(a.part + a.splits * nrows * DH + (split * nrows + rr) * 2) =
+              make_float2(mx, lt);
+      } else {
+        *reinterpret_cast<uint2*>(a.O + long(seq) * a.os + hq * DH + d4) =
+            make_uint2(pack2bf(acc.x, acc.y), pack2bf(acc.z, acc.w));
+        if (a.lse && d4 == 0) a.lse[rr] = lt == 0.f ? -INFINITY : mx * a.scale + __logf(lt);
       }
     }
-    float mx = m;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i]);
-    mx = max_halves(mx);
-    const float base = mx == -INFINITY ? 0.f : mx * c;
-    const float al = exp2_fast(fmaf(m, c, -base));
-    float p[16], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      p[i] = exp2_fast(fmaf(s[i], c, -base));
-      sum += p[i];
-    }
-    l = l * al + sum;
-    m = mx;
+    if (again) break;
+    __syncthreads();
+    if (!__builtin_amdgcn_readfirstlane(odd_s)) break;
+    again = true;
+    whole = l;
+    add = l > 0.f && l < INFINITY ? __log2f(l) : 0.f;
+    l = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[d][i] *= al;
-#pragma unroll
-    for (int s2 = 0; s2 < 2; ++s2) {
-      const uint4 pf = make_uint4(pack2bf(p[8 * s2], p[8 * s2 + 1]), pack2bf(p[8 * s2 + 2], p[8 * s2 + 3]),
-                                  pack2bf(p[8 * s2 + 4], p[8 * s2 + 5]), pack2bf(p[8 * s2 + 6], p[8 * s2 + 7]));
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[d] = mfma32x32x16(fo.value(vt, s2, d), pf, o[d]);
-    }
-    good = good_next;
-  }
-
-  // join the waves: [wave][column][channel] fp32 in the ring that no copy fills any more
-  l = sum_halves(l);
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __syncthreads();
-  float* js = reinterpret_cast<float*>(&sm[0][0][0][0]);
-  if (col < gn) {
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<float4*>(js + (wave * 32 + col) * DH + 32 * d + 2 * i + 4 * h) =
-            make_float4(o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]);
-    if (h == 0) ml_s[wave][col] = make_float2(m, l);
-  }
-  __syncthreads();
-  const long nrows = long(a.n_seq) * a.Hq;
-  for (int e = tid; e < gn * (DH / 4); e += 64 * W) {
-    const int g = e / (DH / 4), d4 = e % (DH / 4) * 4;
-    float mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < W; ++w) mx = fmaxf(mx, ml_s[w][g].x);
-    const float base = mx == -INFINITY ? 0.f : mx * c;
-    float lt = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float2 x = ml_s[w][g];
-      const float f = exp2_fast(fmaf(x.x, c, -base));
-      const float4 v = *reinterpret_cast<const float4*>(js + (w * 32 + g) * DH + d4);
-      lt = fmaf(f, x.y, lt);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
-    }
-    const int hq = kvh * a.G + g0 + g;
-    const long rr = long(seq) * a.Hq + hq;
-    if (a.splits > 1) {
-      *reinterpret_cast<float4*>(a.part + (split * nrows + rr) * DH + d4) = acc;
-      if (d4 == 0)
-        *reinterpret_cast<float2*>(a.part + a.splits * nrows * DH + (split * nrows + rr) * 2) =
-            make_float2(mx, lt);
-    } else {
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
-      *reinterpret_cast<uint2*>(a.O + long(seq) * a.os + hq * DH + d4) =
-          make_uint2(pack2bf(acc.x * inv, acc.y * inv), pack2bf(acc.z * inv, acc.w * inv));
-      if (a.lse && d4 == 0) a.lse[rr] = lt == 0.f ? -INFINITY : mx * a.scale + __logf(lt);
-    }
+      for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   }
 }
 
@@ -253,7 +279,8 @@ __device__ __forceinline__ long join_row(int block, int i, long nrows, int Hq, i
   return rr < nrows ? rr : -1;
 }
 
-// Joins the `splits` partial sums of each row (token, head); one wave per row, four channels per
+// Joins the `splits` partial means of each row (token, head), weighted by their share of the row's sum of
+// weights, so that no sum of finite values passes fp32; one wave per row, four channels per
 // lane, so that a wave has 2 (dh 128) or 4 splits side by side. What it waits for is one round of
 // memory: the statistics and the first 8 loads of sums per lane are asked for together (64 splits of 32
 // rows: 3.5 us, 15 us with the sums asked for one after the other once the weights are known). Fixed order,
@@ -291,10 +318,10 @@ __global__ __launch_bounds__(64 * W) void k_attention_join(const float* part, in
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) mx = fmaxf(mx, __shfl_xor(mx, d));
   const float base = mx == -INFINITY ? 0.f : mx * c;
-  const float f = exp2_fast(fmaf(x.x, c, -base));
-  float lt = f * x.y;
+  float f = exp2_fast(fmaf(x.x, c, -base)) * x.y, lt = f;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) lt += __shfl_xor(lt, d);
+  f *= lt == 0.f ? 0.f : 1.f / lt;
   float acc[4] = {};
   for (int s0 = 0; s0 < splits; s0 += U * SP) {
     if (s0) load(s0);
@@ -311,10 +338,9 @@ __global__ __launch_bounds__(64 * W) void k_attention_join(const float* part, in
   for (int d = LP; d < 64; d *= 2)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], d);
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
   if (sub == 0)
     *reinterpret_cast<uint2*>(O + (rr / Hq) * os + (rr % Hq) * DH + ch) =
-        make_uint2(pack2bf(acc[0] * inv, acc[1] * inv), pack2bf(acc[2] * inv, acc[3] * inv));
+        make_uint2(pack2bf(acc[0], acc[1]), pack2bf(acc[2], acc[3]));
   if (lse && lane == 0) lse[rr] = lt == 0.f ? -INFINITY : mx * scale + __logf(lt);
 }
 
@@ -355,16 +381,21 @@ __global__ __launch_bounds__(256) void k_attention_join_few(const float* part, i
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (u < splits) {
-      const float w = exp2_fast(fmaf(x[u].x, c, -base));
-      lt = fmaf(w, x[u].y, lt);
+      x[u].y *= exp2_fast(fmaf(x[u].x, c, -base));
+      lt += x[u].y;
+    }
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < splits) {
+      const float w = x[u].y * inv;
       acc[0] = fmaf(w, v[u].x, acc[0]);
       acc[1] = fmaf(w, v[u].y, acc[1]);
       acc[2] = fmaf(w, v[u].z, acc[2]);
       acc[3] = fmaf(w, v[u].w, acc[3]);
     }
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
   *reinterpret_cast<uint2*>(O + (rr / Hq) * os + (rr % Hq) * DH + ch) =
-      make_uint2(pack2bf(acc[0] * inv, acc[1] * inv), pack2bf(acc[2] * inv, acc[3] * inv));
+      make_uint2(pack2bf(acc[0], acc[1]), pack2bf(acc[2], acc[3]));
   if (lse && ch == 0) lse[rr] = lt == 0.f ? -INFINITY : mx * scale + __logf(lt);
 }
 

@@ -238,8 +238,9 @@ struct PackedArgs {
 size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh);
 hipError_t attention_packed(const PackedArgs& a);
 
-// Joins `splits` (<= 64) partial results of nrows = tokens * Hq rows: part holds unnormalised fp32
-// sums [splits][nrows][dh], then (maximum logit, sum) [splits][nrows][2] (decode.hip). With cu_q,
+// Joins `splits` (<= 64) partial results of nrows = tokens * Hq rows: part holds each piece's
+// weighted mean of its values in fp32 [splits][nrows][dh], then (maximum logit, sum of the weights)
+// [splits][nrows][2] (decode.hip). With cu_q,
 // only the rows of tokens in [cu_q[0], cu_q[n_seq]).
 hipError_t attention_join(const float* part, int splits, const int* cu_q, int n_seq, long nrows,
                           int Hq, int Hkv, int dh, void* O, long os, float* lse, float scale,

@@ -441,7 +441,8 @@ ttt_status ttt_qk_norm_rope(const void* Q, long long q_stride, const void* K, lo
  *      cu_q. Empty sequences are allowed. Rows of O and lse before cu_q[0] and from cu_q[n_seq]
  *      on are left as they were.
  *   K and V hold Nk rows. Only the keys and values that a row sees reach it, whatever the others hold
- *   (infinities and NaN too); rows whose sums are not finite take several times as long.
+ *   (infinities and NaN too). The mean of finite values is finite, up to the largest that bf16 holds.
+ *   Rows whose sums are not finite before they are divided take several times as long.
  *   Hq % Hkv == 0; dh 64 or 128 (else TTT_E_UNSUPPORTED); 1 <= Nq, Nk <= 2^26;
  *   1 <= n_seq <= 2^20; Nq * Hq + 128 * n_seq * Hkv < 2^31; 0 <= window <= 2^30; scale finite and > 0;
  *   strides in elements: at least heads * dh, multiples of 8, at most 2^23.
@@ -472,7 +473,8 @@ size_t ttt_attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv
  *   page_size: a power of two, 16 .. 65536 (else TTT_E_UNSUPPORTED); max_pages * page_size <=
  *   2^30; n_pages * page_size <= 2^36; n_seq <= 2^20, n_seq * Hq < 2^24; the other limits,
  *   overlaps and the workspace as above. Where a row sees an infinite value, its result in that
- *   channel is that infinity or NaN. */
+ *   channel is that infinity or NaN; the mean of finite values is finite. Sums that are not finite
+ *   before they are divided are taken a second time. */
 ttt_status ttt_attention_decode(const void* Q, long long q_stride, const void* K_cache,
                                 const void* V_cache, ttt_dtype dtype, void* O, long long o_stride,
                                 float* lse, const int* page_table, int max_pages, int page_size,

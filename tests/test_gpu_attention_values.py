@@ -1,0 +1,75 @@
+"""Packed and one-token attention at the ends of their ranges, against the fp64 oracle: values near the
+type's largest, scales near zero, logits past fp32, rows of very many keys, values that a row does not
+see. Tolerances as in test_gpu_attention.py, where a test does not derive its own."""
+import numpy as np
+import pytest
+
+import chunked_weight_sequence_amd as ttt
+import gen
+import oracle.attention as oa
+from helpers import dev, host_bits, host_f64, requires_gpu
+from test_gpu_attention import _cache, _check, _cu, _draw, _f, _i32, _logit_size, _packed, _seen, _some_rows
+
+pytestmark = [pytest.mark.gpu, requires_gpu]
+
+
+def _large(rng, *shape):
+    """Finite values of either sign up to 3.3e38 (bf16 ends at 3.39e38); channel 0 all of one sign."""
+    x = rng.uniform(-3.3e38, 3.3e38, shape)
+    x[..., 0] = rng.uniform(3.2e38, 3.3e38, shape[:-1])
+    return gen.f32_to_bf16_bits(x.astype(np.float32))
+
+
+@pytest.mark.parametrize("lq,more,Hq,Hkv,dh,window", [
+    ([150], [0], 4, 2, 128, 0), ([90, 130], [30, 0], 3, 1, 64, 50),
+    ([40], [3000], 2, 1, 128, 0), ([40], [3000], 2, 1, 64, 0),  # keys split, few pieces
+    ([2], [9000], 4, 4, 128, 0),                                # keys split, many pieces
+    ([4200], [0], 30, 15, 128, 0),                              # 256 rows to a workgroup
+    ([256], [4200], 64, 8, 128, 0)])                            # the same, keys split
+def test_packed_sums_of_large_values_stay_finite(lq, more, Hq, Hkv, dh, window):
+    """A weighted mean of finite values is finite, although their sum before the division is not."""
+    print(f"case: packed large values lq={lq} more={more} {Hq}/{Hkv}x{dh} window={window}", flush=True)
+    rng = np.random.default_rng(sum(lq) + dh)
+    cu_q, cu_k = _cu(lq), _cu(np.array(lq) + np.array(more))
+    Q, K, V = _draw(rng, cu_q[-1], Hq, dh), _draw(rng, cu_k[-1], Hkv, dh), _large(rng, cu_k[-1], Hkv, dh)
+    scale = dh ** -0.5
+    O, L = _packed(Q, K, V, cu_q, cu_k, scale, window)
+    tokens = sorted({0, 1, int(cu_q[-1]) - 1, *rng.integers(0, cu_q[-1], 30).tolist()})
+    heads = sorted({0, Hq // 2, Hq - 1})
+    q, k, v = _f(Q), _f(K), _f(V)
+    _check(O[tokens][:, heads], L[tokens][:, heads],
+           _some_rows(q, k, v, cu_q, cu_k, scale, window, tokens, heads),
+           _logit_size(q[tokens], k, scale)[:, heads], dh, "large values")
+    assert np.isfinite(host_f64(O)).all()
+
+
+def test_packed_a_large_value_behind_the_first_maximum():
+    """Weights relative to the first tile's maximum may reach 2^8: 2^7.8 times 2e36 passes fp32."""
+    print("case: packed, large value in a later tile", flush=True)
+    N, dh = 200, 64
+    Q, K, V = (np.zeros((N, 1, dh)) for _ in range(3))
+    Q[:, 0, 0], K[150, 0, 0], V[150, 0, 3] = 1.0, 5.40625, 2.0 ** 120.5
+    Q, K, V = (gen.f32_to_bf16_bits(x.astype(np.float32)) for x in (Q, K, V))
+    O, L = _packed(Q, K, V, [0, N], [0, N], 1.0, 0)
+    _check(O, L, oa.packed(_f(Q), _f(K), _f(V), [0, N], [0, N], 1.0),
+           _logit_size(_f(Q), _f(K), 1.0), dh, "later tile")
+
+
+@pytest.mark.parametrize("lens,page,Hq,Hkv,dh", [
+    ([0, 1, 33, 300], 16, 4, 4, 64), ([500, 129, 1000], 64, 14, 2, 128), ([2000], 256, 8, 8, 128),
+    ([400, 0, 399, 1] * 25, 16, 32, 16, 128)])                  # two waves to a workgroup
+def test_decode_sums_of_large_values_stay_finite(lens, page, Hq, Hkv, dh):
+    import torch
+    print(f"case: decode large values lens={lens[:8]} {Hq}/{Hkv}x{dh}", flush=True)
+    rng = np.random.default_rng(sum(lens) + dh)
+    Kc, Vc, table = _cache(rng, lens, page, Hkv, dh)
+    Vc = np.where(Vc == 0x7F80, Vc, _large(rng, *Vc.shape))
+    Q, scale = _draw(rng, len(lens), Hq, dh), dh ** -0.5
+    O, L = ttt.attention_decode(dev(Q, "bf16"), dev(Kc, "bf16"), dev(Vc, "bf16"), _i32(table),
+                                _i32(lens), page, scale=scale, with_lse=True)
+    torch.cuda.synchronize()
+    some = list(range(min(len(lens), 4)))
+    want = oa.decode(_f(Q[some]), _f(Kc), _f(Vc), table[some], np.array(lens)[some], page, scale)
+    X = scale * np.abs(_f(Q[some])).sum(-1) * _seen(Kc, table[some], np.array(lens)[some], page)
+    _check(O[some], L[some], want, X, dh, "large values")
+    assert np.isfinite(host_f64(O)).all()
