@@ -434,7 +434,8 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][b][i] = 0.f;
   }
-  const float c = a.scale * kLog2e, slack = AP_SLACK / c;
+  // finite for every scale: a row that has seen nothing yet has most = -inf + slack
+  const float c = a.scale * kLog2e, slack = fminf(AP_SLACK / c, 3.4e38f);
 
   // Masks tile t where an edge crosses the wave's rows, and takes its maxima again.
   auto maxima = [&](const f32x16 (&s)[2][QT], float (&mx)[QT]) AP_INLINE {

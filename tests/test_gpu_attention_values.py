@@ -73,3 +73,36 @@ def test_decode_sums_of_large_values_stay_finite(lens, page, Hq, Hkv, dh):
     X = scale * np.abs(_f(Q[some])).sum(-1) * _seen(Kc, table[some], np.array(lens)[some], page)
     _check(O[some], L[some], want, X, dh, "large values")
     assert np.isfinite(host_f64(O)).all()
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-40, 2.0 ** -149, 1e-30])
+@pytest.mark.parametrize("Nq,Nk,Hq,Hkv,dh,window", [(300, 300, 4, 2, 128, 20), (200, 150, 2, 1, 64, 30),
+                                                    (40, 3000, 2, 1, 128, 700), (4200, 4200, 30, 15, 128, 2500)])
+def test_packed_scales_near_zero(Nq, Nk, Hq, Hkv, dh, window, scale):
+    """All visible keys weigh the same: also for rows that see nothing of their first tile, whose window
+    begins behind it."""
+    print(f"case: packed scale={scale} {Nq}/{Nk} {Hq}/{Hkv}x{dh} window={window}", flush=True)
+    rng = np.random.default_rng(Nq)
+    Q, K, V = _draw(rng, Nq, Hq, dh), _draw(rng, Nk, Hkv, dh), _draw(rng, Nk, Hkv, dh)
+    scale = float(np.float32(scale))
+    O, L = _packed(Q, K, V, [0, Nq], [0, Nk], scale, window)
+    tokens, heads = sorted({*range(0, Nq, max(1, Nq // 60)), Nq - 1}), sorted({0, Hq - 1})
+    want = _some_rows(_f(Q), _f(K), _f(V), [0, Nq], [0, Nk], scale, window, tokens, heads)
+    _check(O[tokens][:, heads], L[tokens][:, heads], want,
+           _logit_size(_f(Q[tokens]), _f(K), scale)[:, heads], dh, "small scale")
+
+
+def test_decode_scales_near_zero():
+    import torch
+    print("case: decode scales near zero", flush=True)
+    rng = np.random.default_rng(12)
+    lens, page, Hq, Hkv, dh = [70, 0, 900], 16, 4, 2, 64
+    Kc, Vc, table = _cache(rng, lens, page, Hkv, dh)
+    Q = _draw(rng, 3, Hq, dh)
+    for scale in (1e-38, 2.0 ** -149, 1e-30):
+        scale = float(np.float32(scale))
+        O, L = ttt.attention_decode(dev(Q, "bf16"), dev(Kc, "bf16"), dev(Vc, "bf16"), _i32(table),
+                                    _i32(lens), page, scale=scale, with_lse=True)
+        torch.cuda.synchronize()
+        X = scale * np.abs(_f(Q)).sum(-1) * _seen(Kc, table, lens, page)
+        _check(O, L, oa.decode(_f(Q), _f(Kc), _f(Vc), table, lens, page, scale), X, dh, "small scale")
