@@ -718,7 +718,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
 #pragma unroll
   for (int b = 0; b < QT; ++b) {
     const float lt = sum_halves(l[b][0] + l[b][1]);
-    float inv = lt == 0.f ? 0.f : 1.f / lt, zero = 0.f;
+    float inv = inverse_sum(lt, m[b]), zero = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -756,7 +756,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
         *reinterpret_cast<uint2*>(out + r * DH * 2 + (((4 * d + i / 4) ^ (r % CH)) << 4) + 8 * (ln >> 5)) =
             make_uint2(pack2bf(o[d][b][i] * inv, o[d][b][i + 1] * inv),
                        pack2bf(o[d][b][i + 2] * inv, o[d][b][i + 3] * inv));
-    if (a.lse && ln < 32 && on) a.lse[rr] = lt == 0.f ? -INFINITY : m[b] * a.scale + __logf(lt);
+    if (a.lse && ln < 32 && on) a.lse[rr] = log_sum(lt, m[b], a.scale);
   }
   if (a.splits == 1) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -62,6 +62,16 @@ __device__ __forceinline__ float sum_halves(float x) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// 1 / l and m * scale + ln l of a row with the largest logit m (before the scale) and the sum of weights l: 0
+// and -inf for a row that sees nothing. Without weights below a finite maximum, the logits times log2(e)
+// passed fp32: NaN.
+__device__ __forceinline__ float inverse_sum(float l, float m) {
+  return l == 0.f ? (m == -INFINITY ? 0.f : NAN) : 1.f / l;
+}
+__device__ __forceinline__ float log_sum(float l, float m, float scale) {
+  return l == 0.f ? (m == -INFINITY ? -INFINITY : NAN) : m * scale + __logf(l);
+}
+
 // Byte offsets, inside a tile, of a lane's K and V^T fragments.
 template <int DH>
 struct FragOff {

@@ -228,7 +228,7 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
         part[w] = exp2_fast(fmaf(x.x, c, -base));
         lt = fmaf(part[w], x.y, lt);
       }
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const float inv = inverse_sum(lt, mx);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < W; ++w) {  // the wave's weight in the mean before its values: finite stays finite
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
       } else {
         *reinterpret_cast<uint2*>(a.O + long(seq) * a.os + hq * DH + d4) =
             make_uint2(pack2bf(acc.x, acc.y), pack2bf(acc.z, acc.w));
-        if (a.lse && d4 == 0) a.lse[rr] = lt == 0.f ? -INFINITY : mx * a.scale + __logf(lt);
+        if (a.lse && d4 == 0) a.lse[rr] = log_sum(lt, mx, a.scale);
       }
     }
     if (again) break;
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(64 * W) void k_attention_join(const float* part, in
   float f = exp2_fast(fmaf(x.x, c, -base)) * x.y, lt = f;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) lt += __shfl_xor(lt, d);
-  f *= lt == 0.f ? 0.f : 1.f / lt;
+  f *= inverse_sum(lt, mx);
   float acc[4] = {};
   for (int s0 = 0; s0 < splits; s0 += U * SP) {
     if (s0) load(s0);
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(64 * W) void k_attention_join(const float* part, in
   if (sub == 0)
     *reinterpret_cast<uint2*>(O + (rr / Hq) * os + (rr % Hq) * DH + ch) =
         make_uint2(pack2bf(acc[0], acc[1]), pack2bf(acc[2], acc[3]));
-  if (lse && lane == 0) lse[rr] = lt == 0.f ? -INFINITY : mx * scale + __logf(lt);
+  if (lse && lane == 0) lse[rr] = log_sum(lt, mx, scale);
 }
 
 // The same for up to 8 splits, which is where there are many rows: a row per 32 (dh 128) or 16 lanes, four
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(256) void k_attention_join_few(const float* part, i
       x[u].y *= exp2_fast(fmaf(x[u].x, c, -base));
       lt += x[u].y;
     }
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  const float inv = inverse_sum(lt, mx);
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (u < splits) {
@@ -396,7 +396,7 @@ __global__ __launch_bounds__(256) void k_attention_join_few(const float* part, i
     }
   *reinterpret_cast<uint2*>(O + (rr / Hq) * os + (rr % Hq) * DH + ch) =
       make_uint2(pack2bf(acc[0], acc[1]), pack2bf(acc[2], acc[3]));
-  if (lse && ch == 0) lse[rr] = lt == 0.f ? -INFINITY : mx * scale + __logf(lt);
+  if (lse && ch == 0) lse[rr] = log_sum(lt, mx, scale);
 }
 
 // What a call launches: waves per workgroup and pieces per sequence, from the most that the page

@@ -106,3 +106,25 @@ def test_decode_scales_near_zero():
         torch.cuda.synchronize()
         X = scale * np.abs(_f(Q)).sum(-1) * _seen(Kc, table, lens, page)
         _check(O, L, oa.decode(_f(Q), _f(Kc), _f(Vc), table, lens, page, scale), X, dh, "small scale")
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("Nq,Nk,dh", [(70, 70, 64), (40, 3000, 128)])
+def test_logits_past_fp32_are_not_taken_for_masked_ones(Nq, Nk, dh, sign):
+    """A logit of 2.6e38 is finite, times log2(e) it is not in fp32: the row is NaN, never o = 0 with
+    lse = -inf, which says that it sees nothing."""
+    import torch
+    print(f"case: logits of {sign} 2.6e38, {Nq}/{Nk}x{dh}", flush=True)
+    Q, K = (np.zeros((n, 1, dh), np.float32) for n in (Nq, Nk))
+    Q[..., 0], K[..., 0] = 1.6e19, sign * 1.6e19
+    Q, K = gen.f32_to_bf16_bits(Q), gen.f32_to_bf16_bits(K)
+    V = _draw(np.random.default_rng(1), Nk, 1, dh)
+    O, L = _packed(Q, K, V, [0, Nq], [0, Nk], 1.0, 0)
+    assert np.isnan(host_f64(O)).all() and not np.isneginf(host_f64(L)).any()
+    page = 16
+    Kc, Vc = (dev(x[:Nk // page * page], "bf16") for x in (K, V))
+    table = _i32(np.arange(Nk // page)[None])
+    O, L = ttt.attention_decode(dev(Q[:1], "bf16"), Kc, Vc, table, _i32([Nk // page * page]), page,
+                                scale=1.0, with_lse=True)
+    torch.cuda.synchronize()
+    assert np.isnan(host_f64(O)).all() and not np.isneginf(host_f64(L)).any()
