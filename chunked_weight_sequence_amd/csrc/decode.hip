@@ -178,7 +178,8 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i]);
       mx = max_halves(mx);
       const float top = mx == -INFINITY ? 0.f : mx * c, base = top + add;
-      const float al = exp2_fast(fmaf(m, c, -top));
+      // exactly 1 where the maximum stays: m c - top, the rounding of top, would change the sums tile by tile
+      const float al = mx == m ? 1.f : exp2_fast(fmaf(m, c, -top));
       float p[16], sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {

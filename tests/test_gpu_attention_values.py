@@ -128,3 +128,39 @@ def test_logits_past_fp32_are_not_taken_for_masked_ones(Nq, Nk, dh, sign):
                                 scale=1.0, with_lse=True)
     torch.cuda.synchronize()
     assert np.isnan(host_f64(O)).all() and not np.isneginf(host_f64(L)).any()
+
+
+@pytest.mark.parametrize("scale", [0.9, 1.3, 1.7])
+def test_decode_sums_of_many_equal_weights(scale):
+    """262144 tokens in one piece, all with one logit: the weights of all tiles are the same, however
+    many tiles pass without a new maximum. The sums are 4 of 2048 tiles' each: an addition is off by half
+    a step of the sum, so a mean by 2048 2^-24 at most, and lse by 2048 2^-24 beside _check's terms."""
+    import torch
+    print(f"case: decode, many equal weights, scale {scale}", flush=True)
+    S, Hkv, dh, page, n = 128, 8, 64, 64, 1 << 18
+    g = torch.Generator(device="cuda").manual_seed(3)
+    V = torch.randn((n, Hkv, dh), generator=g, device="cuda").to(torch.bfloat16)
+    V[: n // 2, :, 0], V[n // 2:, :, 0] = 1.0, -1.0  # early against late tokens: mean 0
+    key = _draw(np.random.default_rng(2), 1, Hkv, dh)
+    K = dev(key, "bf16").expand(n, Hkv, dh).contiguous()
+    q = _draw(np.random.default_rng(4), S, Hkv, dh, by=8.0)
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda").expand(S, n // page).contiguous()
+    lens = np.ones(S, np.int32)
+    lens[:3] = n
+    assert ttt.lib().ttt_attention_decode_workspace(S, n // page, page, Hkv, Hkv, dh) == 0  # one piece
+    O, L = ttt.attention_decode(dev(q, "bf16"), K, V, table, _i32(lens), page, scale=scale, with_lse=True)
+    torch.cuda.synchronize()
+    x = scale * (_f(q[:3]) * _f(key)).sum(-1)
+    mean = V.double().mean(0).cpu().numpy()
+    size = V.double().abs().mean(0).cpu().numpy()
+    X = scale * (np.abs(_f(q[:3])) * np.abs(_f(key))).sum(-1)
+    d = (dh + 4) * 2.0 ** -24 * X + 2048 * 2.0 ** -24
+    off = np.abs(host_f64(L[:3]) - (x + np.log(n)))
+    bound = d + 2.0 ** -20 + 4 * 2.0 ** -24 * (np.abs(x) + np.log(n) + X)
+    print(f"  lse {float((off / bound).max()):.3f}", flush=True)
+    ob = 1.01 * (2.0 ** -8 * (np.abs(mean) + size) + (4 * d[..., None] + 2.0 ** -19) * size)
+    # equal weights are rounded alike: the mean of channel 0 holds no rounding of bf16 weights
+    ob[..., 0] = 4 * 2048 * 2.0 ** -24
+    o = float((np.abs(host_f64(O[:3]) - mean) / ob).max())
+    print(f"  o {o:.3f}, channel 0 {np.abs(host_f64(O[:3, :, 0])).max():.2e}", flush=True)
+    assert (off <= bound).all() and o <= 1.0
