@@ -572,15 +572,21 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
     constexpr Plan plan{};
     uint32_t pw[2][QT][8];  // bf16 pairs: [key block][query block]
     float p0 = 0.f, p1 = 0.f;
+    // the tile's own sums, added to the row's once: 2^20 equal weights one by one lose 0.4%, and no time is won
+    float lt[QT][2] = {};
     auto op = [&](int n) AP_INLINE {  // unit n / 3: two neighbouring weights, in the order phase B takes them
       const int u = n / 3, st = u / (4 * QT), kb = st >> 1, b = (u >> 2) % QT, i = 8 * (st & 1) + 2 * (u & 3);
       if (n % 3 == 0) p0 = exp2_fast(fmaf(s[kb][b][i], c, -base[b]));
       if (n % 3 == 1) p1 = exp2_fast(fmaf(s[kb][b][i + 1], c, -base[b]));
       if (n % 3 == 2) {
         pw[kb][b][i / 2] = pack2bf(p0, p1);
-        l[b][0] += p0;
-        l[b][1] += p1;
-        asm volatile("" : "+v"(l[b][0]), "+v"(l[b][1]));  // here, not behind the round
+        lt[b][0] += p0;
+        lt[b][1] += p1;
+        asm volatile("" : "+v"(lt[b][0]), "+v"(lt[b][1]));  // here, not behind the round
+        if (st == 3 && (u & 3) == 3) {
+          l[b][0] += lt[b][0];
+          l[b][1] += lt[b][1];
+        }
       }
     };
     uint4 kf[2][2], vf[2][2];

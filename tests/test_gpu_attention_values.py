@@ -164,3 +164,28 @@ def test_decode_sums_of_many_equal_weights(scale):
     o = float((np.abs(host_f64(O[:3]) - mean) / ob).max())
     print(f"  o {o:.3f}, channel 0 {np.abs(host_f64(O[:3, :, 0])).max():.2e}", flush=True)
     assert (off <= bound).all() and o <= 1.0
+
+
+def test_packed_sums_of_many_equal_weights():
+    """2^20 keys of one logit but for a larger one in the first tile, one piece: each lane adds up some
+    2^18 equal weights. In sums of whole tiles (16384 of them) each addition is off by half a step: lse by
+    16384 / 2 2^-24 on the mean of a growing sum, doubled for what the tiles' own 16 additions lose."""
+    import torch
+    print("case: packed, many equal weights", flush=True)
+    Nq, Nk, Hq, dh = 256, 1 << 20, 128, 64
+    K = torch.zeros(Nk, 1, dh, dtype=torch.bfloat16, device="cuda")
+    K[0, 0, 0] = 1.0
+    V = torch.ones_like(K)
+    q = torch.zeros(Nq, Hq, dh, dtype=torch.bfloat16, device="cuda")
+    top = torch.linspace(0.1, 2.0, Hq, device="cuda").to(torch.bfloat16)
+    q[..., 0] = top
+    O, L = ttt.attention_packed(q, K, V, _i32([0, Nq]), _i32([0, Nk]), scale=1.0, with_lse=True)
+    torch.cuda.synchronize()
+    x = top.double().cpu().numpy()[None]
+    seen = Nk - Nq + 1 + np.arange(Nq)[:, None]  # keys of a row, the larger one among them
+    want = np.log(np.exp(x) + seen - 1)
+    off = np.abs(host_f64(L) - want).max()
+    print(f"  lse off by {off:.2e}", flush=True)
+    assert off <= 16384 * 2.0 ** -24 + 2.0 ** -20 + 8 * 2.0 ** -24 * 16
+    # bf16(weight) / weight: at most 2^-8 off, and the result's own rounding
+    assert np.abs(host_f64(O) - 1).max() <= 2.0 ** -7 + 2 * 16384 * 2.0 ** -24
