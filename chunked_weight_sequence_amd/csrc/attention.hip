@@ -216,28 +216,27 @@ struct ApPlan {
   }
 };
 
-// Sums the values of one block of 32 rows again, with care for infinities and NaN: the tiles multiply a
-// value that a row does not see by a weight of 0, and 0 times an infinity or a NaN is a NaN. Here such
-// values are multiplied as 0, and what the rows that see them get is found by products of 1 and 0:
-// which of +inf, -inf and NaN a row sees at all. The maxima and sums of the first pass are right and
-// stay; the weights are divided by their sum here (inv: 1 / sum) before they meet the values, so that
-// finite values, whose mean is finite, do not pass fp32 on the way. By the wave alone, 32 keys [j, j + 32) of [j0, j1) at a time: K straight into registers, V by
-// way of its own 32 rows of LDS. 16384 tokens of 32/8 heads of 128 take 1.8 ms; with one infinity in the
-// last token 4.4 ms, in the first, which every row of a head sees, 15 ms, with nothing but NaN in V 26 ms.
-template <int DH, int QT>
-__device__ __forceinline__ void ap_again(f32x16 (&o)[DH / 32][QT], int b,
-                                         const bf16x8 (&qf)[DH / 16], const char* tile,
-                                         const uint16_t* K, long ks, const uint16_t* V, long vs,
-                                         int j0, int j1, int lo, int hi, float c, float base,
-                                         float inv, int lane) {
-  constexpr int KS = DH / 16, DT = DH / 32, RPI = 1024 / (DH * 2);
-  const FragOff<DH> fo(lane);
+// The sums of 32 channels (32 d ..) of one block of 32 rows again, with care for infinities and NaN: the tiles
+// multiply a value that a row does not see by a weight of 0, and 0 times an infinity or a NaN is a NaN. Here
+// such values are multiplied as 0, and what the rows that see them get is found by products of 1 and 0:
+// which of +inf, -inf and NaN a row sees at all. The maxima and sums of the first pass are right and stay;
+// the weights are divided by their sum (inv: 1 / sum) before they meet the values, so that finite values,
+// whose mean is finite, do not pass fp32 on the way. By the wave alone, 32 keys [j, j + 32) of [j0, j1) at a
+// time: K straight into registers, V by way of its own 32 rows of LDS. 16384 tokens of 32/8 heads of 128
+// take 1.7 .. 2.3 ms; with one infinity in the last token 2.9 ms, in the first, which every row of a head sees,
+// 9.6 ms, with nothing but NaN in V 44 ms.
+template <int DH, int KS>
+__device__ __forceinline__ f32x16 ap_again(int d, const bf16x8 (&qf)[KS], const char* tile,
+                                           const uint16_t* K, long ks, const uint16_t* V, long vs, int j0,
+                                           int j1, int lo, int hi, float c, float base, float inv, int lane) {
+  constexpr int RPI = 1024 / (DH * 2);
+  asm volatile("" : "+v"(lane));  // nothing of this is worked out before
+  const char* const place = tile + FragOff<DH>::channels(lane, d);
   const uint32_t lds = lds_u32(tile);
   const int h = lane >> 5;
+  f32x16 o;
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][b][i] = 0.f;
+  for (int i = 0; i < 16; ++i) o[i] = 0.f;
   for (int j = j0; j < j1; j += 32) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last tile has been read
 #pragma unroll 1
@@ -269,55 +268,54 @@ __device__ __forceinline__ void ap_again(f32x16 (&o)[DH / 32][QT], int b,
       pw[i / 2] = pack2bf(p[0], p[1]);
     }
     wait_vm<0>();
+    ap_fence();
+    // +inf, -inf and NaN as 1, 2^8 and 2^16: their sum over 32 keys, exact in fp32, tells which a row sees
+    uint32_t code[2][4];
+    bool odd = false;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      // +inf, -inf and NaN as 1, 2^8 and 2^16: their sum over 32 keys, exact in fp32, tells which a row
-      // sees
-      uint32_t code[2][4];
-      bool odd = false;
+    for (int st = 0; st < 2; ++st) {
+      const uint4 v = FragOff<DH>::value_at(place, st);
+      uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const uint4 v = fo.value(tile, st, d);
-        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      for (int e = 0; e < 4; ++e) {
+        code[st][e] = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          code[st][e] = 0;
-#pragma unroll
-          for (int half = 0; half < 32; half += 16) {
-            const uint32_t y = x[e] >> half & 0xFFFF;
-            if ((y & 0x7F80) != 0x7F80) continue;
-            odd = true;
-            code[st][e] |= uint32_t(y == 0x7F80 ? 0x3F80 : y == 0xFF80 ? 0x4380 : 0x4780) << half;
-            x[e] &= 0xFFFF0000u >> half;
-          }
+        for (int half = 0; half < 32; half += 16) {
+          const uint32_t y = x[e] >> half & 0xFFFF;
+          if ((y & 0x7F80) != 0x7F80) continue;
+          odd = true;
+          code[st][e] |= uint32_t(y == 0x7F80 ? 0x3F80 : y == 0xFF80 ? 0x4380 : 0x4780) << half;
+          x[e] &= 0xFFFF0000u >> half;
         }
-        o[d][b] = mfma32x32x16(make_uint4(x[0], x[1], x[2], x[3]),
-                               make_uint4(pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]), o[d][b]);
       }
-      if (!__any(odd)) continue;
-      f32x16 n;
+      o = mfma32x32x16(make_uint4(x[0], x[1], x[2], x[3]),
+                       make_uint4(pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]), o);
+      ap_fence();
+    }
+    if (!__any(odd)) continue;
+    f32x16 n;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) n[i] = 0.f;
+    for (int i = 0; i < 16; ++i) n[i] = 0.f;
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        uint32_t one[4];
+    for (int st = 0; st < 2; ++st) {
+      uint32_t one[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t two = seen >> (8 * st + 2 * e) & 3;
-          one[e] = ((two & 1) | (two & 2) << 15) * 0x3F80;
-        }
-        n = mfma32x32x16(make_uint4(code[st][0], code[st][1], code[st][2], code[st][3]),
-                         make_uint4(one[0], one[1], one[2], one[3]), n);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t two = seen >> (8 * st + 2 * e) & 3;
+        one[e] = ((two & 1) | (two & 2) << 15) * 0x3F80;
       }
+      n = mfma32x32x16(make_uint4(code[st][0], code[st][1], code[st][2], code[st][3]),
+                       make_uint4(one[0], one[1], one[2], one[3]), n);
+    }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int k = int(n[i]);
-        if (k & 0xFF) o[d][b][i] += INFINITY;
-        if (k & 0xFF00) o[d][b][i] -= INFINITY;
-        if (k >> 16) o[d][b][i] = NAN;
-      }
+    for (int i = 0; i < 16; ++i) {
+      const int k = int(n[i]);
+      if (k & 0xFF) o[i] += INFINITY;
+      if (k & 0xFF00) o[i] -= INFINITY;
+      if (k >> 16) o[i] = NAN;
     }
   }
+  return o;
 }
 
 template <int DH, int QT>
@@ -730,9 +728,22 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
 #pragma unroll
       for (int i = 0; i < 16; ++i) zero = fmaf(o[d][b][i], 0.f, zero);
     if (__any(zero != 0.f && lt == lt)) {  // not finite, although the weights are
-      ap_again<DH>(o, b, qf[b], out + 32 * b * DH * 2, a.K + long(k0) * a.ks + kvh * DH, a.ks,
-                   a.V + long(k0) * a.vs + kvh * DH, a.vs, t0 * AP_BN, min(t1 * AP_BN, lk), lo[b], hi[b],
-                   c, base[b], inv, ln);
+      // Channels by 32, and only those with such a sum: an infinity or NaN in a tile reaches the sums of its
+      // channel in all 32 rows, and weights rounded at another maximum change the last bits of the other 31.
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) odd = odd || !(fabsf(o[d][b][i]) < INFINITY);
+        if (__any(odd && lt == lt)) {
+          o[d][b] = ap_again<DH>(d, qf[b], out + 32 * b * DH * 2, a.K + long(k0) * a.ks + kvh * DH, a.ks,
+                                 a.V + long(k0) * a.vs + kvh * DH, a.vs, t0 * AP_BN, min(t1 * AP_BN, lk),
+                                 lo[b], hi[b], c, base[b], inv, ln);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][b][i] *= inv;
+        }
+      }
       inv = 1.f;
     }
     const int r = 32 * b + (ln & 31), x = wrow + r, qi = query(x);

@@ -82,11 +82,14 @@ struct FragOff {
 #pragma unroll
     for (int i = 0; i < kN; ++i)
       k[i] = uint32_t(r * DH * 2 + (((2 * i + h) ^ ksw<DH>(r)) << 4));
-    const int vr = 4 * h + ((lane & 15) >> 2);
-    const int c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
 #pragma unroll
-    for (int i = 0; i < vN; ++i)
-      v[i] = uint32_t(vr * DH * 2 + (((4 * i + c) ^ vsw<DH>(vr)) << 4) + 8 * (lane & 1));
+    for (int i = 0; i < vN; ++i) v[i] = channels(lane, i);
+  }
+  // a lane's place of channels 32 dt ..
+  __device__ __forceinline__ static uint32_t channels(int lane, int dt) {
+    const int vr = 4 * (lane >> 5) + ((lane & 15) >> 2);
+    const int c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    return uint32_t(vr * DH * 2 + (((4 * dt + c) ^ vsw<DH>(vr)) << 4) + 8 * (lane & 1));
   }
   // K fragment of 32-row block kb, contraction step ks (channels 16 ks ..)
   __device__ __forceinline__ uint4 key(const char* tile, int kb, int ks) const {
@@ -94,8 +97,12 @@ struct FragOff {
   }
   // V^T fragment of channels 32 dt .., the 16 keys 16 s ..
   __device__ __forceinline__ uint4 value(const char* tile, int s, int dt) const {
-    const uint2 lo = tr_read(tile + v[dt] + s * 16 * DH * 2);
-    const uint2 hi = tr_read(tile + v[dt] + (s * 16 + 8) * DH * 2);
+    return value_at(tile + v[dt], s);
+  }
+  // the same from the lane's place of the channels
+  __device__ __forceinline__ static uint4 value_at(const char* place, int s) {
+    const uint2 lo = tr_read(place + s * 16 * DH * 2);
+    const uint2 hi = tr_read(place + (s * 16 + 8) * DH * 2);
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
   }
 };

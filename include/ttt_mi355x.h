@@ -441,9 +441,11 @@ ttt_status ttt_qk_norm_rope(const void* Q, long long q_stride, const void* K, lo
  *      access leaves the buffers, but which rows are written is then unspecified). cu_k may be
  *      cu_q. Empty sequences are allowed. Rows of O and lse before cu_q[0] and from cu_q[n_seq]
  *      on are left as they were.
- *   K and V hold Nk rows. Only the keys and values that a row sees reach it, whatever the others hold
- *   (infinities and NaN too). The mean of finite values is finite, up to the largest that bf16 holds.
- *   Rows whose sums are not finite before they are divided take several times as long.
+ *   K and V hold Nk rows. Only the keys and values that a row sees reach it, whatever the others hold,
+ *   infinities and NaN too. (Near a value that is neither finite nor seen, a row's sums of the 32
+ *   channels around it may be taken a second time, within the same bounds: last bits may differ.)
+ *   The mean of finite values is finite, up to the largest of bf16. Rows whose sums are not finite
+ *   before they are divided take several times as long.
  *   Hq % Hkv == 0; dh 64 or 128 (else TTT_E_UNSUPPORTED); 1 <= Nq, Nk <= 2^26;
  *   1 <= n_seq <= 2^20; Nq * Hq + 128 * n_seq * Hkv < 2^31; 0 <= window <= 2^30; scale finite and > 0;
  *   strides in elements: at least heads * dh, multiples of 8, at most 2^23.

@@ -189,3 +189,34 @@ def test_packed_sums_of_many_equal_weights():
     assert off <= 16384 * 2.0 ** -24 + 2.0 ** -20 + 8 * 2.0 ** -24 * 16
     # bf16(weight) / weight: at most 2^-8 off, and the result's own rounding
     assert np.abs(host_f64(O) - 1).max() <= 2.0 ** -7 + 2 * 16384 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+@pytest.mark.parametrize("lq,more,Hq,Hkv,dh,window", [
+    ([150], [0], 4, 2, 128, 0), ([150], [0], 4, 2, 64, 0), ([90, 130], [30, 0], 3, 1, 64, 50),
+    ([40], [3000], 2, 1, 128, 0), ([40], [3000], 2, 1, 128, 1000),   # the keys are split
+    ([4200], [0], 30, 15, 128, 0), ([1000], [3000], 64, 32, 128, 2500),  # 256 rows to a workgroup
+    ([256], [4200], 64, 8, 128, 0)])                                 # the same, split
+def test_packed_hidden_values_leave_the_bits_of_other_channels(lq, more, Hq, Hkv, dh, window, bad):
+    """Beside an infinity or NaN the 32 channels that hold it may be summed again, at another reference
+    maximum: every other channel, and every row of other heads and sequences, keeps its bits. The logits
+    rise, so that weights are taken at several maxima."""
+    print(f"case: packed hidden {bad}, bits, lq={lq} more={more} {Hq}/{Hkv}x{dh} window={window}", flush=True)
+    rng = np.random.default_rng(sum(lq) + dh)
+    cu_q, cu_k = _cu(lq), _cu(np.array(lq) + np.array(more))
+    Q, K = _draw(rng, cu_q[-1], Hq, dh), _draw(rng, cu_k[-1], Hkv, dh)
+    K = gen.f32_to_bf16_bits((_f(K) * np.linspace(0.2, 6, len(K))[:, None, None]).astype(np.float32))
+    V = _draw(rng, cu_k[-1], Hkv, dh)
+    at = int(cu_k[1]) - lq[0] // 2  # a key in the middle of the first sequence's own part
+    V1 = V.copy()
+    V1[at, 0, 5] = gen.f32_to_bf16_bits(np.float32([bad]))[0]
+    want, got = (_packed(Q, K, v, cu_q, cu_k, dh ** -0.5, window) for v in (V, V1))
+    np.testing.assert_array_equal(host_bits(got[1]), host_bits(want[1]))
+    want, got = host_bits(want[0]), host_bits(got[0])
+    last = np.arange(lq[0]) + more[0]
+    sees = (last >= at) & ((last - at < window) if window else True)
+    off = np.zeros(got.shape, bool)
+    off[:lq[0], :Hq // Hkv, :32] = True
+    assert 0 < sees.sum() < lq[0]
+    np.testing.assert_array_equal(got[~off], want[~off])
+    assert not np.isfinite(gen.bf16_bits_to_f32(got[:lq[0]][sees][:, :Hq // Hkv, 5])).any()
