@@ -6,7 +6,8 @@
 // for the rot / 2 pairs of the head's first `rot` channels: (j, j + rot/2) in the half layout,
 // (2j, 2j + 1) in the interleaved one. Channels past rot keep y. Everything is fp32 and rounded
 // once; the angle is reduced to a fraction of a turn in fp64, since a position of 2^20 times a
-// frequency of 1 leaves fp32 only four bits of the angle's fraction.
+// frequency of 1 leaves fp32 only four bits of the angle's fraction. Its sine and cosine are taken in
+// fp64 too for fp32 results; for bf16 ones, whose half step is 2^15 times as large, in fp32.
 //
 // A lane holds 16 channels of one head: one group of 16 channels holds 8 whole pairs in either
 // layout (8 channels j.. and 8 channels j + rot/2.. in the half layout), so rotation needs no
@@ -168,9 +169,15 @@ __global__ __launch_bounds__(256) void k_norm_rope(NormRopeArgs a, int lsh, int 
     const int tt = i / half, f = i - tt * half;
     if (t0 + tt < a.N) {
       const double turns = double(a.pos[t0 + tt]) * a.inv_freq[f] * 0.15915494309189533577;
-      float s, co;
-      sincospif(2.f * float(turns - rint(turns)), &s, &co);
-      cs[tt][f] = make_float2(co * a.rope_scale, s * a.rope_scale);
+      if constexpr (sizeof(T) == 4) {  // fp32 results show what sines in fp32 lose (1 token: 0.1 us more)
+        double s, co;
+        sincospi(2. * (turns - rint(turns)), &s, &co);
+        cs[tt][f] = make_float2(float(co * a.rope_scale), float(s * a.rope_scale));
+      } else {
+        float s, co;
+        sincospif(2.f * float(turns - rint(turns)), &s, &co);
+        cs[tt][f] = make_float2(co * a.rope_scale, s * a.rope_scale);
+      }
     }
   }
   __syncthreads();

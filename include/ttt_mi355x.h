@@ -396,7 +396,7 @@ ttt_status ttt_rope_frequencies(double* inv_freq, int rot, double base, ttt_rope
  *     (a, b) -> rope_scale * (a cos - b sin, a sin + b cos)   at the angle pos[t] * inv_freq[j]
  * for pair j of the head's first `rot` channels: channels (j, j + rot/2) in TTT_ROPE_HALF,
  * (2j, 2j + 1) in TTT_ROPE_INTERLEAVED. Channels from rot on keep y. fp32 arithmetic (the angle's
- * reduction in fp64), rounded once to dtype.
+ * reduction in fp64, for TTT_F32 its sine and cosine too), rounded once to dtype.
  *   Q      [N, Hq, dh], K [N, Hkv, dh]; dtype TTT_F32 or TTT_BF16; token t at + t * stride
  *   V      [N, Hkv, dh], with slots only
  *   q_weight, k_weight  [dh] fp32, either may be NULL

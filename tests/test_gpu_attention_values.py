@@ -220,3 +220,27 @@ def test_packed_hidden_values_leave_the_bits_of_other_channels(lq, more, Hq, Hkv
     assert 0 < sees.sum() < lq[0]
     np.testing.assert_array_equal(got[~off], want[~off])
     assert not np.isfinite(gen.bf16_bits_to_f32(got[:lq[0]][sees][:, :Hq // Hkv, 5])).any()
+
+
+@pytest.mark.parametrize("layout,dh,rot", [("half", 64, 64), ("interleaved", 64, 16), ("half", 256, 128)])
+def test_fp32_rotations_are_rounded_once(layout, dh, rot):
+    """The pair (1, 0) turns into the cosine and the sine: half a step of fp32 from the exact ones, beside
+    the fp64 angle's own error (2^20 times 2^-52 in radians)."""
+    import torch
+    print(f"case: fp32 rotation of (1, 0), {layout} {rot} of {dh}", flush=True)
+    rng = np.random.default_rng(rot)
+    N, half = 2000, rot // 2
+    pos = np.concatenate([rng.integers(0, 1 << 20, N - 4), [0, 1, -7, (1 << 20) - 1]])
+    a = np.arange(half) if layout == "half" else 2 * np.arange(half)
+    b = a + half if layout == "half" else a + 1
+    x = np.zeros((N, 1, dh), np.float32)
+    x[:, 0, a] = 1
+    freq, _ = oa.rope_frequencies(rot, 10000.0)
+    Q, _ = ttt.qk_norm_rope(dev(x, "f32"), dev(x, "f32"), _i32(pos), torch.tensor(freq, device="cuda"),
+                            layout=layout)
+    torch.cuda.synchronize()
+    got, angle = host_f64(Q)[:, 0], pos[:, None] * freq
+    for at, want in ((a, np.cos(angle)), (b, np.sin(angle))):
+        off = np.abs(got[:, at] - want) / (2.0 ** -24 * np.abs(want) + 2.0 ** -31)
+        print(f"  {off.max():.3f} of the bound", flush=True)
+        assert off.max() <= 1.0
