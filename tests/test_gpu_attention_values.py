@@ -8,6 +8,7 @@ import chunked_weight_sequence_amd as ttt
 import gen
 import oracle.attention as oa
 from helpers import dev, host_bits, host_f64, requires_gpu
+import test_gpu_norm_rope as norm_rope
 from test_gpu_attention import _cache, _check, _cu, _draw, _f, _i32, _logit_size, _packed, _seen, _some_rows
 
 pytestmark = [pytest.mark.gpu, requires_gpu]
@@ -244,3 +245,14 @@ def test_fp32_rotations_are_rounded_once(layout, dh, rot):
         off = np.abs(got[:, at] - want) / (2.0 ** -24 * np.abs(want) + 2.0 ** -31)
         print(f"  {off.max():.3f} of the bound", flush=True)
         assert off.max() <= 1.0
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,dh,rot,layout,dtype,norm,first,scale", [
+    (1024, 8, 2, 64, 32, "half", "bf16", "qk", 0, 1.0),        # four waves to a token, at most
+    (1025, 8, 4, 64, 32, "half", "bf16", "qk", 0, 1.0),        # two
+    (1025, 3, 3, 128, 16, "interleaved", "f32", "q", 77, 1.1),
+    (2048, 8, 4, 64, 32, "half", "f32", "k", 0, 1.0)])
+@pytest.mark.parametrize("how", ["plain", "in place"])
+def test_norm_and_rotation_with_fewer_waves_to_a_token(N, Hq, Hkv, dh, rot, layout, dtype, norm, first,
+                                                       scale, how):
+    norm_rope.test_norm_and_rotation(N, Hq, Hkv, dh, rot, layout, dtype, norm, first, scale, how)
