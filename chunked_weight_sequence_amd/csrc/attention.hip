@@ -44,6 +44,7 @@ struct PackedDev {
   int window;
   int tiles, splits;
   int half;     // pieces of work from here on are taken from the other end (packed_plan)
+  bool longest;  // sequences in the order of their keys (packed_plan)
   float* part;  // splits > 1: [splits][Nq * Hq][dh] means, then [splits][Nq * Hq] (m, l)
 };
 
@@ -74,10 +75,8 @@ __device__ __forceinline__ Work ap_find(const PackedDev& a, int w, int BM, int l
   } else if (a.n_seq < 64) {  // one load for everything: lane s has sequence s
     const int s = min(lane, a.n_seq);
     const int cq = clampq(s), ck = clampk(s);
-    if (a.n_seq <= 16) {
-      // The sequence with most keys first, so that what starts last is short (otherwise the last one
-      // first): 11 documents in 8192 tokens 103 / 106 us, 3 in 4096 63 / 67, 12 in 4096 33.5 / 32.9. Past
-      // 16 the order gains less than it costs (30 clocks a sequence).
+    if (a.longest) {
+      // the sequence with most keys first, so that what starts last is short (otherwise the last one first)
       const int cq1 = __builtin_amdgcn_update_dpp(0, cq, 0x130, 0xF, 0xF, true);  // of the lane above
       const int ck1 = __builtin_amdgcn_update_dpp(0, ck, 0x130, 0xF, 0xF, true);
       const int lk = max(ck1 - ck, 0);
@@ -793,6 +792,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
 namespace {
 struct PackedPlan {
   int qt, tiles, splits, half;
+  bool longest;
 };
 // Keys that an average row sees.
 long packed_seen(int n_seq, int Nq, int Nk, int window) {
@@ -842,7 +842,7 @@ PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int w
   // 4096 tokens of 16/4 heads 98 / 74 us, 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105
   // us, 12000 tokens of 4/1 heads in 2 documents 205 / 153 us. Heads of 64, which the vector unit
   // bounds: 8191 tokens, window 2048, 188 / 145 us.
-  PackedPlan p{1, 0, 1, 0};
+  PackedPlan p{1, 0, 1, 0, false};
   if (dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
     const int pieces = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, window);
     const long wgs = packed_wgs(2, n_seq, Nq, Hq, Hkv), n = wgs * pieces;
@@ -859,6 +859,14 @@ PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int w
   // opposite order, so that each unit has long and short ones: 2048 tokens of 32/8 heads of 128 44 ->
   // 42 us, 1800 38 -> 35.6, 4000 of 8/4 heads of 64 46 -> 44 us.
   const long wgs = packed_wgs(p.qt, n_seq, Nq, Hq, Hkv) * p.splits;
+  // Sequences with most keys first, where workgroups go more than once around the chip and so few times that
+  // the last to start counts, and finding the order (30 clocks a sequence in each) is little beside a row's
+  // tiles. Ordered / not, means over six draws of lengths: 16/8 heads of 128, 8 .. 14 sequences in 8800 tokens
+  // (1100 workgroups) 0.92 .. 0.94, in 16000 (2000) 0.95 .. 0.98; 32/8 heads, 5 .. 14 in 3200 .. 8000 tokens
+  // (800 .. 2000) 0.96 .. 1.005, 16 in 4096 0.99; 16/4 of 64 in 12000 (1500) 0.87 .. 0.96. But 5 .. 16 in 512 tokens (under 300)
+  // 1.02 .. 1.15, 24 in 4400 tokens (3 tiles a row) 1.10, 16 in 16384 with a window of 512 (4600) 1.06.
+  p.longest = n_seq > 1 && n_seq <= 16 && n_seq <= 4 * (packed_keys(n_seq, Nk, window) / AP_BN) &&
+              wgs > 512 && wgs <= 3200;
   p.half = p.qt == 1 && wgs > 256 && wgs <= (dh == 64 ? 768 : 512) ? 256 / (Hkv * p.splits) : p.tiles;
   return p;
 }
@@ -877,7 +885,7 @@ hipError_t attention_packed(const PackedArgs& a) {
   const PackedDev d{static_cast<const uint16_t*>(a.Q), static_cast<const uint16_t*>(a.K),
                     static_cast<const uint16_t*>(a.V), a.qs, a.ks, a.vs,
                     static_cast<uint16_t*>(a.O), a.os, a.lse, a.cu_q, a.cu_k, a.n_seq, a.Nq, a.Nk,
-                    a.Hq, a.Hkv, a.Hq / a.Hkv, a.scale, a.window, p.tiles, p.splits, p.half,
+                    a.Hq, a.Hkv, a.Hq / a.Hkv, a.scale, a.window, p.tiles, p.splits, p.half, p.longest,
                     static_cast<float*>(a.ws)};
   const dim3 grid(unsigned(p.tiles) * a.Hkv * p.splits);
   if (p.qt == 2)

@@ -256,3 +256,29 @@ def test_fp32_rotations_are_rounded_once(layout, dh, rot):
 def test_norm_and_rotation_with_fewer_waves_to_a_token(N, Hq, Hkv, dh, rot, layout, dtype, norm, first,
                                                        scale, how):
     norm_rope.test_norm_and_rotation(N, Hq, Hkv, dh, rot, layout, dtype, norm, first, scale, how)
+
+
+@pytest.mark.parametrize("Hq,Hkv,dh,more", [(32, 16, 64, 0), (32, 16, 128, 0), (20, 10, 128, 100)])
+def test_packed_sequences_taken_longest_first(Hq, Hkv, dh, more):
+    """Enough workgroups for that order; unlike lengths, two alike, empty sequences, rows of none."""
+    import torch
+    print(f"case: packed longest first {Hq}/{Hkv}x{dh} past {more}", flush=True)
+    rng = np.random.default_rng(dh + more)
+    lq = [0, 900, 33, 0, 1500, 128, 1, 900, 0]
+    cu_q, cu_k = _cu(lq, 5), _cu([n + more * (n > 0) for n in lq], 3)
+    Nq, Nk = cu_q[-1] + 7, cu_k[-1] + 2
+    Q, K, V = _draw(rng, Nq, Hq, dh), _draw(rng, Nk, Hkv, dh), _draw(rng, Nk, Hkv, dh)
+    O = torch.full((Nq, Hq, dh), 7.0, dtype=torch.bfloat16, device="cuda")
+    L = torch.full((Nq, Hq), 7.0, device="cuda")
+    _packed(Q, K, V, cu_q, cu_k, dh ** -0.5, 0, O=O, lse=L)
+    for x in (O[:5], O[-7:], L[:5], L[-7:]):
+        assert (x == 7).all()
+    on = slice(5, -7)
+    assert not (O[on] == 7).all(-1).any() and not (L[on] == 7).any()  # every row is written
+    tokens = sorted({*(cu_q[:-1][np.diff(cu_q) > 0]).tolist(), *(cu_q[1:][np.diff(cu_q) > 0] - 1).tolist(),
+                     *rng.integers(5, Nq - 7, 20).tolist()})
+    heads = [0, 1, Hq - 1]
+    q, k, v = _f(Q), _f(K), _f(V)
+    _check(O[tokens][:, heads], L[tokens][:, heads],
+           _some_rows(q, k, v, cu_q, cu_k, dh ** -0.5, 0, tokens, heads),
+           _logit_size(q[tokens], k, dh ** -0.5)[:, heads], dh, "longest first")
