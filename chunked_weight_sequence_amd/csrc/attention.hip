@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "attn.hpp"
+#include "attn_plan.hpp"
 #include "launch.hpp"
 
 namespace ttt {
@@ -29,7 +30,7 @@ namespace {
 
 #define AP_INLINE __attribute__((always_inline))
 
-constexpr int AP_BN = 64;
+constexpr int AP_BN = PLAN_TILE;
 constexpr float AP_SLACK = 8.f;  // log2
 
 struct PackedDev {
@@ -788,96 +789,8 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
 
 }  // namespace
 
-// What a call launches: rows per workgroup (128 QT) and pieces of the key axis.
-namespace {
-struct PackedPlan {
-  int qt, tiles, splits, half;
-  bool longest;
-};
-// Keys that an average row sees.
-long packed_seen(int n_seq, int Nq, int Nk, int window) {
-  const long seen = (Nk > Nq / 2 ? Nk - Nq / 2 : Nk) / n_seq;
-  return window > 0 && window < seen ? window : seen;
-}
-// Keys that the last row sees.
-long packed_keys(int n_seq, int Nk, int window) {
-  const long keys = Nk / n_seq;
-  return window > 0 && window < keys ? window : keys;
-}
-// Workgroups that have rows, if the sequences are alike.
-long packed_wgs(int qt, int n_seq, int Nq, int Hq, int Hkv) {
-  const long rows = long(Nq) * (Hq / Hkv), BM = 128 * qt;
-  return ((rows + BM - 1) / BM + n_seq - 1) * Hkv;
-}
-// Pieces that the keys of a row are split into, if row tiles alone leave compute units free: the number that
-// makes the longest row's tiles (0.75 us each, 1.5 with 256 rows, 0.5 for heads of 64) and the joining
-// (5 us, and the partial sums written and read at 4 TB/s) cost least, each piece at least 256 keys.
-// Measured, 32/8 heads of 128: 512 tokens after 15872, 323 us whole, 125 us in 4; 64 tokens after 16000,
-// 35 us in 32 pieces, 31 us in 16; 1024 tokens 20 us whole, 35 us in 2; 2048 tokens of 8/4 heads of 64
-// 24 us whole, 28 us in 2.
-int packed_splits(int qt, int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
-  const long keys = packed_keys(n_seq, Nk, window);
-  // a compute unit each, where a workgroup counts for as much as an average row has of the longest
-  const long seen = packed_seen(n_seq, Nq, Nk, window);
-  long most = 256 * keys / (packed_wgs(qt, n_seq, Nq, Hq, Hkv) * (seen < 1 ? 1 : seen));
-  if (most > keys / 256) most = keys / 256;
-  if (most > 64) most = 64;
-  const double tiles = keys / 64 * (qt == 2 ? 1.5 : dh == 64 ? 0.5 : 0.75);
-  const double join = double(Nq) * Hq * dh * 8 / 4e6;
-  int best = 1;
-  double cost = tiles;
-  for (int n = 2; n <= most; ++n) {
-    const double t = tiles / n + 5 + n * join;
-    if (t < cost) cost = t, best = n;
-  }
-  return best;
-}
-PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
-  // 256 rows share each tile read from LDS, which costs least power (long rows are bound by that), but
-  // leave the chip's 256 places unevenly filled and nothing to run while a workgroup starts and ends
-  // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least 9
-  // of 10 places, in pieces of at least 1024, and that are many if their rows differ in length.
-  // Measured, 256 rows against 128, 32/8 heads of 128: 16384 tokens 1.76 / 1.87 ms, 512 after 15872 126
-  // / 138 us, 256 after 16000 75 / 80 us; but 64 after 16000 37 / 31 us, 200 after 4000 31 / 28 us,
-  // 4096 tokens of 16/4 heads 98 / 74 us, 2048 tokens 52 / 44 us, 11 documents in 8192 tokens 110 / 105
-  // us, 12000 tokens of 4/1 heads in 2 documents 205 / 153 us. Heads of 64, which the vector unit
-  // bounds: 8191 tokens, window 2048, 188 / 145 us.
-  PackedPlan p{1, 0, 1, 0, false};
-  if (dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
-    const int pieces = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, window);
-    const long wgs = packed_wgs(2, n_seq, Nq, Hq, Hkv), n = wgs * pieces;
-    const long seen = packed_seen(n_seq, Nq, Nk, window);
-    if (seen >= 1024 * pieces && 10 * n >= 9 * 256 * ((n + 255) / 256) &&
-        (wgs >= 384 || 4 * packed_keys(n_seq, Nk, window) <= 5 * seen))
-      p.qt = 2;
-  }
-  const long rows = long(Nq) * (Hq / Hkv);
-  p.tiles = n_seq == 1 ? int((rows + 128 * p.qt - 1) / (128 * p.qt)) : int(rows / (128 * p.qt)) + n_seq;
-  p.splits = packed_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
-  // Row tiles are taken from the last on, so that the longest rows start first. Where all workgroups
-  // start at once, two on a compute unit (three of heads of 64), those past the first 256 come in the
-  // opposite order, so that each unit has long and short ones: 2048 tokens of 32/8 heads of 128 44 ->
-  // 42 us, 1800 38 -> 35.6, 4000 of 8/4 heads of 64 46 -> 44 us.
-  const long wgs = packed_wgs(p.qt, n_seq, Nq, Hq, Hkv) * p.splits;
-  // Sequences with most keys first, where workgroups go more than once around the chip and so few times that
-  // the last to start counts, and finding the order (30 clocks a sequence in each) is little beside a row's
-  // tiles. Ordered / not, means over six draws of lengths: 16/8 heads of 128, 8 .. 14 sequences in 8800 tokens
-  // (1100 workgroups) 0.92 .. 0.94, in 16000 (2000) 0.95 .. 0.98; 32/8 heads, 5 .. 14 in 3200 .. 8000 tokens
-  // (800 .. 2000) 0.96 .. 1.005, 16 in 4096 0.99; 16/4 of 64 in 12000 (1500) 0.87 .. 0.96. But 5 .. 16 in 512 tokens (under 300)
-  // 1.02 .. 1.15, 24 in 4400 tokens (3 tiles a row) 1.10, 16 in 16384 with a window of 512 (4600) 1.06.
-  p.longest = n_seq > 1 && n_seq <= 16 && n_seq <= 4 * (packed_keys(n_seq, Nk, window) / AP_BN) &&
-              wgs > 512 && wgs <= 3200;
-  p.half = p.qt == 1 && wgs > 256 && wgs <= (dh == 64 ? 768 : 512) ? 256 / (Hkv * p.splits) : p.tiles;
-  return p;
-}
-}  // namespace
-
 size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh) {
-  // the window is not known here; with one there are no more pieces than without
-  const int a = packed_splits(1, n_seq, Nq, Nk, Hq, Hkv, dh, 0);
-  const int b = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, 0);
-  const int n = a > b ? a : b;
-  return n > 1 ? size_t(n) * Nq * Hq * (dh + 2) * 4 : 0;
+  return packed_workspace(n_seq, Nq, Nk, Hq, Hkv, dh);
 }
 
 hipError_t attention_packed(const PackedArgs& a) {

@@ -18,12 +18,13 @@
 #include <type_traits>
 
 #include "attn.hpp"
+#include "attn_plan.hpp"
 #include "launch.hpp"
 
 namespace ttt {
 namespace {
 
-constexpr int DC_BN = 32, DC_MAX_SPLITS = 64;
+constexpr int DC_BN = 32;
 
 // a row of zeros: what stands for the tokens of a page that does not exist
 __device__ const uint4 dc_zeros[16] = {};
@@ -400,41 +401,12 @@ __global__ __launch_bounds__(256) void k_attention_join_few(const float* part, i
   if (lse && ch == 0) lse[rr] = log_sum(lt, mx, scale);
 }
 
-// What a call launches: waves per workgroup and pieces per sequence, from the most that the page
-// table can hold, since only the device knows the lengths.
-struct DecodePlan {
-  int waves, splits;
-};
-DecodePlan decode_plan(int n_seq, int max_pages, int page, int Hkv, int G, int dh, int window) {
-  const long wgs = long(n_seq) * Hkv * ((G + 31) / 32);
-  long keys = long(max_pages) * page;
-  if (window > 0 && window < keys) keys = window;
-  // The ring of 4 waves of heads of 128 takes a compute unit's LDS; with 2 waves, one workgroup starts
-  // or ends while the other streams, which counts when each unit has several: from 1536 tokens per
-  // unit on. 4 / 2 waves, 32/8 heads of 128: 100 x 512 tokens 47 / 39 us, 200 x 500 96 / 91, 64 x
-  // 1000 45 / 43, but 1 x 32768 28 / 29, 1 x 4096 8.3 / 9.8.
-  const int waves = dh == 128 && wgs * keys >= 256 * 1536 ? 2 : 4;
-  // As many pieces as fill the chip, of at least 128 tokens (a tile per wave), and up to four times
-  // as many, since lengths differ and the last to end counts, where a piece still has 1024 (heads of
-  // 64, whose tiles are half as large: 512). Measured in pieces for four times the chip's workgroups
-  // of 4 waves / for once, without the second limit: 16 x 32768 tokens 365 / 374 us, 33 of up to 5000,
-  // 16/4 heads of 64, 21 / 33 us, but 64 x 1000 52 / 45 us, 4 x 2000 11.8 / 9.6 us.
-  const auto pieces = [&](long want, long least) {
-    const long n = (want + wgs - 1) / wgs, most = keys / least;
-    return n < most ? n : most;
-  };
-  const long chip = 1024 / waves;
-  const long a = pieces(chip, 128), b = pieces(4 * chip, dh == 128 ? 1024 : 512), n = a > b ? a : b;
-  return {waves, int(n < 1 ? 1 : n > DC_MAX_SPLITS ? DC_MAX_SPLITS : n)};
-}
-
 }  // namespace
 
 hipError_t attention_join(const float* part, int splits, const int* cu_q, int n_seq, long nrows,
                           int Hq, int Hkv, int dh, void* O, long os, float* lse, float scale,
                           hipStream_t stream) {
-  // few rows: a wave per workgroup, on as many compute units
-  const int rows = splits <= 8 ? 1024 / dh : nrows < 1024 ? 1 : 4;  // per workgroup
+  const int rows = join_rows(splits, nrows, dh);  // per workgroup
   const long per_head = nrows / Hkv;
   const dim3 grid(unsigned((per_head + rows - 1) / rows * Hkv)), block(splits <= 8 ? 256 : 64 * rows);
   const auto k = splits <= 8 ? (dh == 128 ? k_attention_join_few<128> : k_attention_join_few<64>)
@@ -446,9 +418,7 @@ hipError_t attention_join(const float* part, int splits, const int* cu_q, int n_
 }
 
 size_t attention_decode_workspace(int n_seq, int max_pages, int page, int Hq, int Hkv, int dh) {
-  // the window is not known here: without one there are no fewer pieces than with it
-  const int ns = decode_plan(n_seq, max_pages, page, Hkv, Hq / Hkv, dh, 0).splits;
-  return ns > 1 ? size_t(ns) * n_seq * Hq * (dh + 2) * 4 : 0;
+  return decode_workspace(n_seq, max_pages, page, Hq, Hkv, dh);
 }
 
 hipError_t attention_decode(const DecodeArgs& a) {
