@@ -549,16 +549,27 @@ def _int_in(value, name: str, lo: int, hi: int) -> int:
     return value
 
 
+@functools.lru_cache(maxsize=1)
+def _device_calls(internals=None):
+    """(the current device's index, a device's current stream as a handle). torch's own functions where it
+    has them, since torch.cuda.current_stream() builds an object, 4 us of a 16 us call; they are not part
+    of its interface, so the public ones otherwise."""
+    torch = _torch()
+    internals = torch._C if internals is None else internals
+    return (getattr(internals, "_cuda_getDevice", None) or torch.cuda.current_device,
+            getattr(internals, "_cuda_getCurrentRawStream", None) or
+            (lambda index: torch.cuda.current_stream(index).cuda_stream))
+
+
 def _launch(fn, args, device):
     """Calls fn(*args, stream) with `device` current and its current stream; checks the status."""
-    # the raw stream handle: torch.cuda.current_stream() builds an object, 4 us of a 16 us call
-    torch = _torch()
+    current, stream = _device_calls()
     index = device.index
-    if torch._C._cuda_getDevice() == index:
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if current() == index:
+        code = fn(*args, stream(index))
     else:
-        with torch.cuda.device(device):
-            code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        with _torch().cuda.device(device):
+            code = fn(*args, stream(index))
     if code != 0:
         raise TTTError(status_string(code))
 
@@ -659,7 +670,8 @@ def attention_packed(Q, K, V, cu_q, cu_k=None, *, scale=None, window: int = 0, O
 def attention_decode(Q, K_cache, V_cache, page_table, lengths, page_size: int, *, scale=None,
                      window: int = 0, O=None, with_lse: bool = False, lse=None, workspace=None):
     """One-token attention over a paged cache. Q [S,Hq,dh] bf16; K_cache, V_cache
-    [n_slots,Hkv,dh] (rows of page p: p * page_size ..); page_table [S,max_pages] int32;
+    [n_slots,Hkv,dh] (rows of page p: p * page_size ..; rows behind the last whole page are not read, and
+    tokens of a page that is not there are left out); page_table [S,max_pages] int32;
     lengths [S] int32: cached tokens of each sequence, its query's own among them. Returns
     O [S,Hq,dh], with (with_lse, or lse given) lse [S,Hq] fp32 beside it."""
     torch = _torch()

@@ -282,3 +282,24 @@ def test_packed_sequences_taken_longest_first(Hq, Hkv, dh, more):
     _check(O[tokens][:, heads], L[tokens][:, heads],
            _some_rows(q, k, v, cu_q, cu_k, dh ** -0.5, 0, tokens, heads),
            _logit_size(q[tokens], k, dh ** -0.5)[:, heads], dh, "longest first")
+
+
+def test_a_call_on_another_stream_without_torchs_own_functions(monkeypatch):
+    """The public way to the stream gives the same handle, and a call through it the same bits."""
+    import torch
+    print("case: streams by the public interface", flush=True)
+    current, stream = ttt._device_calls.__wrapped__(object())
+    own = ttt._device_calls()
+    side = torch.cuda.Stream()
+    rng = np.random.default_rng(20)
+    q, k, v = (dev(_draw(rng, 50, 2, 64), "bf16") for _ in range(3))
+    want = host_bits(ttt.attention_packed(q, k, v, _i32([0, 50])))
+    torch.cuda.synchronize()
+    for s in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(s):
+            assert current() == own[0]() == 0 and stream(0) == own[1](0) == s.cuda_stream
+            monkeypatch.setattr(ttt, "_device_calls", lambda: (current, stream))
+            got = ttt.attention_packed(q, k, v, _i32([0, 50]))
+            monkeypatch.undo()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(host_bits(got), want)
