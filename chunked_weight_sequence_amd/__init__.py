@@ -606,6 +606,8 @@ def qk_norm_rope(Q, K, pos, inv_freq, *, q_weight=None, k_weight=None, eps: floa
             raise ValueError("slots needs V, K_cache and V_cache")
         _vec(slots, "slots", (N,), torch.int32, dev)
         vs = _rows(V, "V", Hkv, dh, dt, dev, N)
+        if K_cache.dim() != 3:
+            raise ValueError(f"K_cache must be [n_slots, Hkv, dh], got {tuple(K_cache.shape)}")
         n_slots = K_cache.shape[0]
         _vec(K_cache, "K_cache", (n_slots, Hkv, dh), dt, dev)
         _vec(V_cache, "V_cache", (n_slots, Hkv, dh), dt, dev)
@@ -643,6 +645,8 @@ def attention_packed(Q, K, V, cu_q, cu_k=None, *, scale=None, window: int = 0, O
     if Nk >= 1 << 31:
         raise ValueError(f"K has too many tokens: {Nk}")
     vs = _rows(V, "V", Hkv, dh, dt, dev, Nk)
+    if cu_q.dim() != 1:
+        raise ValueError(f"cu_q must be [n_seq + 1], got {tuple(cu_q.shape)}")
     n_seq = cu_q.shape[0] - 1
     _vec(cu_q, "cu_q", (n_seq + 1,), torch.int32, dev)
     if cu_k is None:
@@ -678,6 +682,8 @@ def attention_decode(Q, K_cache, V_cache, page_table, lengths, page_size: int, *
     qs = _rows(Q, "Q")
     S, Hq, dh = Q.shape
     dt, dev = Q.dtype, Q.device
+    if K_cache.dim() != 3:
+        raise ValueError(f"K_cache must be [n_slots, Hkv, dh], got {tuple(K_cache.shape)}")
     n_slots, Hkv = K_cache.shape[0], K_cache.shape[1]
     _vec(K_cache, "K_cache", (n_slots, Hkv, dh), dt, dev)
     _vec(V_cache, "V_cache", (n_slots, Hkv, dh), dt, dev)

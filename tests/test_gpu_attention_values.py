@@ -303,3 +303,22 @@ def test_a_call_on_another_stream_without_torchs_own_functions(monkeypatch):
             monkeypatch.undo()
         torch.cuda.synchronize()
         np.testing.assert_array_equal(host_bits(got), want)
+
+
+def test_tensors_of_other_ranks_are_refused():
+    import torch
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu, n = _i32([0, 4]), _i32([4] * 4)
+    for bad in (cu[0], cu[None]):
+        with pytest.raises(ValueError):
+            ttt.attention_packed(q, q, q, bad)
+        with pytest.raises(ValueError):
+            ttt.attention_packed(q, q, q, cu, bad)
+    f = torch.zeros(0, dtype=torch.float64, device="cuda")
+    for bad in (q[0, 0, 0], q[0, 0], q[0], q[None]):
+        with pytest.raises(ValueError):
+            ttt.attention_decode(q, bad, q, _i32([[0]] * 4), n, 16)
+        with pytest.raises(ValueError):
+            ttt.attention_packed(q, bad, q, cu)
+        with pytest.raises(ValueError):
+            ttt.qk_norm_rope(q.clone(), q.clone(), _i32([0] * 4), f, V=q, K_cache=bad, V_cache=q, slots=n)
