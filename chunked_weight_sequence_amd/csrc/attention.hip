@@ -220,8 +220,8 @@ struct ApPlan {
 // multiply a value that a row does not see by a weight of 0, and 0 times an infinity or a NaN is a NaN. Here
 // such values are multiplied as 0, and what the rows that see them get is found by products of 1 and 0:
 // which of +inf, -inf and NaN a row sees at all. The maxima and sums of the first pass are right and stay;
-// the weights are divided by their sum (inv: 1 / sum) before they meet the values, so that finite values,
-// whose mean is finite, do not pass fp32 on the way. By the wave alone, 32 keys [j, j + 32) of [j0, j1) at a
+// the weights are lower by a power of two (headroom), so that sums of finite values, whose mean is finite, do
+// not pass fp32 on the way. By the wave alone, 32 keys [j, j + 32) of [j0, j1) at a
 // time: K straight into registers, V by way of its own 32 rows of LDS. 16384 tokens of 32/8 heads of 128
 // take 1.7 .. 2.3 ms; with one infinity in the last token 2.9 ms, in the first, which every row of a head sees,
 // 9.6 ms, with nothing but NaN in V 44 ms.
@@ -254,7 +254,7 @@ __device__ __forceinline__ f32x16 ap_again(int d, const bf16x8 (&qf)[KS], const 
       if (k % 4 == 3) ap_fence();  // not all loads at once: the registers are the main loop's
     }
     asm volatile("s_nop 15\n\ts_nop 15" : "+v"(s));
-    uint32_t pw[8], seen = 0;  // bit i: the row sees its i-th key
+    uint32_t pw[8], seen = 0;  // weights as bf16 pairs, as in the main loop; bit i: the row sees its i-th key
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       float p[2];
@@ -262,7 +262,7 @@ __device__ __forceinline__ f32x16 ap_again(int d, const bf16x8 (&qf)[KS], const 
       for (int e = 0; e < 2; ++e) {
         const int key = j + 8 * (i / 4) + 4 * h + (i & 3) + e;
         const bool in = key >= lo && key <= hi && key < j1;
-        p[e] = in ? exp2_fast(fmaf(s[i + e], c, -base)) * inv : 0.f;
+        p[e] = in ? exp2_fast(fmaf(s[i + e], c, -base) - headroom(inv)) : 0.f;
         seen |= uint32_t(in) << (i + e);
       }
       pw[i / 2] = pack2bf(p[0], p[1]);
@@ -568,7 +568,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
     constexpr bool NEXT = decltype(next)::value;
     constexpr int BUF = decltype(buf)::value;
     constexpr Plan plan{};
-    uint32_t pw[2][QT][8];  // bf16 pairs: [key block][query block]
+    uint32_t pw[2][QT][8];  // the weights as bf16 pairs (attn.hpp: why bf16): [key block][query block]
     float p0 = 0.f, p1 = 0.f;
     // the tile's own sums, added to the row's once: 2^20 equal weights one by one lose 0.4%, and no time is won
     float lt[QT][2] = {};
@@ -735,14 +735,15 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
         bool odd = false;
 #pragma unroll
         for (int i = 0; i < 16; ++i) odd = odd || !(fabsf(o[d][b][i]) < INFINITY);
+        float f = inv;
         if (__any(odd && lt == lt)) {
           o[d][b] = ap_again<DH>(d, qf[b], out + 32 * b * DH * 2, a.K + long(k0) * a.ks + kvh * DH, a.ks,
                                  a.V + long(k0) * a.vs + kvh * DH, a.vs, t0 * AP_BN, min(t1 * AP_BN, lk),
                                  lo[b], hi[b], c, base[b], inv, ln);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[d][b][i] *= inv;
+          f *= exp2_fast(headroom(inv));
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][b][i] = in_range(o[d][b][i] * f);
       }
       inv = 1.f;
     }

@@ -139,8 +139,7 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
 
   // The weights are relative to the running maximum and divided by their sum at the end, so sums of finite
   // values can pass fp32 on the way although their mean does not. Where that shows in the results, they are
-  // taken a second time, with the weights divided by the sum of the first: exponents are lower by `add`, its
-  // logarithm.
+  // taken a second time, with the weights lower by a power of two, 2^-add, above the sum of the first.
   float* js = reinterpret_cast<float*>(&sm[0][0][0][0]);
   const long nrows = long(a.n_seq) * a.Hq;
   float add = 0.f, whole = 0.f;
@@ -194,7 +193,7 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= al;
 #pragma unroll
-      for (int s2 = 0; s2 < 2; ++s2) {
+      for (int s2 = 0; s2 < 2; ++s2) {  // the weights as bf16 (attn.hpp: why)
         const uint4 pf = make_uint4(pack2bf(p[8 * s2], p[8 * s2 + 1]), pack2bf(p[8 * s2 + 2], p[8 * s2 + 3]),
                                     pack2bf(p[8 * s2 + 4], p[8 * s2 + 5]), pack2bf(p[8 * s2 + 6], p[8 * s2 + 7]));
 #pragma unroll
@@ -234,13 +233,14 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < W; ++w) {  // the wave's weight in the mean before its values: finite stays finite
-        const float f = (again ? part[w] * ml_s[w][g].y : part[w]) * inv;
+        const float f = (again ? part[w] * exp2_fast(headroom(inverse_sum(ml_s[w][g].y, ml_s[w][g].x))) : part[w]) * inv;
         const float4 v = *reinterpret_cast<const float4*>(js + (w * 32 + g) * DH + d4);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);
         acc.w = fmaf(f, v.w, acc.w);
       }
+      if (again) acc = make_float4(in_range(acc.x), in_range(acc.y), in_range(acc.z), in_range(acc.w));
       if (lt < INFINITY && acc.x * 0.f + acc.y * 0.f + acc.z * 0.f + acc.w * 0.f != 0.f) odd_s = true;
       const int hq = kvh * a.G + g0 + g;
       const long rr = long(seq) * a.Hq + hq;
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
     if (!__builtin_amdgcn_readfirstlane(odd_s)) break;
     again = true;
     whole = l;
-    add = l > 0.f && l < INFINITY ? __log2f(l) : 0.f;
+    add = headroom(inverse_sum(l, m));
     l = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)

@@ -322,3 +322,27 @@ def test_tensors_of_other_ranks_are_refused():
             ttt.attention_packed(q, bad, q, cu)
         with pytest.raises(ValueError):
             ttt.qk_norm_rope(q.clone(), q.clone(), _i32([0] * 4), f, V=q, K_cache=bad, V_cache=q, slots=n)
+
+
+@pytest.mark.parametrize("dh,more,sign", [(64, 0, 1), (128, 0, -1), (128, 3000, 1)])
+def test_means_of_the_largest_value_are_that_value(dh, more, sign):
+    """Keys that all weigh the same and all hold bf16's largest value: however their weights round, the
+    result does not pass it."""
+    import torch
+    print(f"case: largest values, dh {dh}, past {more}", flush=True)
+    N, top = 300, float(torch.finfo(torch.bfloat16).max)
+    Q = torch.zeros(N, 2, dh, dtype=torch.bfloat16, device="cuda")
+    K = torch.zeros(N + more, 1, dh, dtype=torch.bfloat16, device="cuda")
+    V = torch.full_like(K, sign * top)
+    O = host_f64(ttt.attention_packed(Q, K, V, _i32([0, N]), _i32([0, N + more])))
+    # every row: half a step of the weights, then of the result
+    assert np.isfinite(O).all() and (np.abs(O - sign * top) <= 2.0 ** -7 * top).all()
+    lens, page = list(range(1, 200)) + [more + N], 16
+    pages = -(-(more + N) // page)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(len(lens), pages).contiguous()
+    C, D = (torch.zeros(pages * page, 1, dh, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    D.fill_(sign * top)
+    q = torch.zeros(len(lens), 2, dh, dtype=torch.bfloat16, device="cuda")
+    O = host_f64(ttt.attention_decode(q, C, D, table, _i32(lens), page))
+    torch.cuda.synchronize()
+    assert np.isfinite(O).all() and (np.abs(O - sign * top) <= 2.0 ** -7 * top).all()
