@@ -13,8 +13,8 @@
 // Copies are whole rows, so each instruction reads 1 KB in full lines. Rows that are masked
 // (behind the last token, before the window) are replaced by a visible row of the tile in the
 // copy itself: what lies in them, NaN included, never enters a product. 32/8 heads of 128: 16 sequences
-// of 32768 tokens, 2.1 GB, 365 us (5.8 TB/s; a copy reaches 4.9), 1 of 4096 8.2 us in two launches; 33 of up
-// to 5000, 16/4 heads of 64, 86 MB, 21 us.
+// of 32768 tokens, 2.1 GB, 365 .. 378 us (5.7 TB/s; a copy reaches 4.9), 1 of 4096 8.2 us in two launches; 33 of
+// up to 5000, 16/4 heads of 64, 86 MB, 22 .. 25 us.
 #include <type_traits>
 
 #include "attn.hpp"

@@ -17,7 +17,7 @@
 // and cosines are computed once per token (one angle per thread) and shared through LDS.
 // Bound by HBM: each input is read once and each output written once. 32768 tokens of 32/8 heads of 128
 // bf16 with the cache write, 872 MB: 166 us, 5.25 TB/s (a copy of 2 GiB: 4.9); 1023 tokens of 16/16 heads
-// of 64 in fp32, 17 MB: 6.2 us; 1 token 3.8 us, of which an empty launch is 2.
+// of 64 in fp32, 17 MB: 6.4 us; 1 token 3.9 us, of which an empty launch is 2.
 #include <type_traits>
 
 #include "common.hpp"
