@@ -16,9 +16,9 @@
 // the matrix pipe, and by power where rows are long (the clock falls to 1.6 .. 2.0 GHz), heads of 64 by
 // the vector unit. 32/8 heads of 128: 16384 tokens 1.69 .. 1.88 ms (1170 .. 1300 TFLOP/s over the visible
 // pairs; a large matrix product 1350 .. 1550), 11 documents in 8192 tokens 90 .. 118 us by their lengths, 512
-// tokens after 15872 122 .. 127 us with the join; 32/32 heads of 64, 8191 tokens, window 2048: 139 .. 154 us. A workgroup takes 4 us
-// to its first round (its sequence 0.6, set up 0.6, copies 1.5, queries to registers 0.5, first scores
-// 0.9), 1.2 .. 1.5 per tile of 128 rows with two on a unit, and 2 to write its rows.
+// tokens after 15872 122 .. 127 us with the join; 32/32 heads of 64, 8191 tokens, window 2048: 139 .. 154 us.
+// A workgroup takes 4 us to its first round (its sequence 0.6, set up 0.6, copies 1.5, queries to registers
+// 0.5, first scores 0.9), 1.2 .. 1.5 per tile of 128 rows with two on a unit, and 2 to write its rows.
 #include <type_traits>
 
 #include "attn.hpp"

@@ -233,7 +233,8 @@ __global__ __launch_bounds__(64 * W) void k_attention_decode(DecodeDev a) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < W; ++w) {  // the wave's weight in the mean before its values: finite stays finite
-        const float f = (again ? part[w] * exp2_fast(headroom(inverse_sum(ml_s[w][g].y, ml_s[w][g].x))) : part[w]) * inv;
+        float f = part[w] * inv;
+        if (again) f *= exp2_fast(headroom(inverse_sum(ml_s[w][g].y, ml_s[w][g].x)));
         const float4 v = *reinterpret_cast<const float4*>(js + (w * 32 + g) * DH + d4);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);

@@ -246,7 +246,8 @@ hipError_t norm_rope(const NormRopeArgs& a) {
   // in a graph, 32/8 heads of 128 with the cache write: 1024 tokens 7.1 / 7.2 / 9.5 us, 1280 9.4 / 8.3 / 10.1,
   // 2048 12.3 / 10.3 / 11.6, 2560 14.6 / 13.4 / 13.3, 8192 35.2 / 33.9 / 35.0; fp32 1024 tokens 12.2 / 11.6 /
   // 12.1; 32/32 heads 1024 10.5 / 12.1 / 15.4, 2048 19.0 / 19.5 / 20.7; 8/8 of 256 without it 1024 5.3 / 5.8 /
-  // 7.6, 2048 8.9 / 8.1 / 8.8, 4096 15.2 / 13.9 / 12.9. 2 / 1 of 16/4 heads of 64: 2048 5.1 / 5.7, 2560 6.6 / 6.2.
+  // 7.6, 2048 8.9 / 8.1 / 8.8, 4096 15.2 / 13.9 / 12.9. 2 / 1 of 16/4 heads of 64: 2048 5.1 / 5.7,
+  // 2560 6.6 / 6.2.
   const int waves = (((a.Hq + a.Hkv + (a.Vc ? a.Hkv : 0)) << lsh) + 63) / 64;
   int wsh = waves < 2 ? 0 : waves < 4 ? 1 : 2;
   while (wsh > 0 && long(a.N) << wsh > 4096) --wsh;

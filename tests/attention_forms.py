@@ -16,6 +16,8 @@ PACKED = [
     (([3000], [3000], 60, 30, 128, 2300), dict(qt=2, splits=1)),
     (([1000], [3000], 32, 32, 128, 2500), dict(qt=2, splits=2, join=8)),
     (([250], [4200], 64, 8, 128, 0), dict(qt=2, splits=4, join=8)),
+    (([2200, 0, 1, 1500], [3000, 900, 2000, 3500], 48, 12, 128, 0), dict(qt=2, splits=1, longest=True)),
+    (([700, 0, 1, 1500], [300, 900, 2000, 3500], 32, 16, 128, 900), dict(qt=1, splits=1, longest=True)),
     (([1030], [0], 32, 8, 128, 0), dict(qt=1, splits=1, reversed=True)),
     (([1000, 1040], [0, 50], 16, 4, 128, 0), dict(qt=1, splits=1, reversed=True)),
     (([3000], [0], 16, 8, 64, 0), dict(qt=1, splits=1, reversed=True)),

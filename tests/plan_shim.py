@@ -41,7 +41,7 @@ class Plan:
         Nk = sum(max(a + b, 0) for a, b in zip(lq, more))
         p = self._ask(self.lib.packed, (len(lq), sum(lq), max(Nk, 1), Hq, Hkv, dh, window),
                       ("qt", "splits", "tiles", "half", "longest", "join", "workspace"))
-        p["reversed"] = p["half"] < p["tiles"]
+        p["reversed"], p["longest"] = p["half"] < p["tiles"], bool(p["longest"])
         return p
 
     def decode(self, n_seq, max_pages, page, Hq, Hkv, dh, window):

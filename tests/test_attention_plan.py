@@ -38,6 +38,7 @@ def test_the_forms_are_all_there():
         (64, 16), (64, 1), (64, 4), (128, 8), (128, 1), (128, 4)}
     assert {c[4] for c, f in PACKED if f.get("reversed")} == {64, 128}
     assert {f["qt"] for c, f in PACKED if c[5] and f["splits"] > 1} == {1, 2}
+    assert {f["qt"] for c, f in PACKED if f.get("longest")} == {1, 2}
     decode = {(c[5], f["waves"], f["splits"] > 1, c[6] > 0) for c, f in DECODE}
     assert decode >= {(128, 2, s, w) for s in (False, True) for w in (False, True)}
     assert decode >= {(64, 4, True, True), (128, 4, True, True), (64, 4, True, False), (128, 4, True, False)}
