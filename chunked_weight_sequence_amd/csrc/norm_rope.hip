@@ -207,7 +207,22 @@ __global__ __launch_bounds__(256) void k_norm_rope(NormRopeArgs a, int lsh, int 
 #pragma unroll
       for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
       for (int d = 1; d < L; d *= 2) ss += __shfl_xor(ss, d);
-      const float rs = rsqrtf(ss * inv_dh + a.eps);
+      float eps = a.eps;
+      // Squares that leave fp32 (values past 2^63, or all below 2^-40 where eps does not hide them): the head
+      // is scaled by a power of two first. All lanes of a head decide alike.
+      const bool large = !(ss < 0x1p126f), small = ss < 0x1p-80f && eps < 0x1p-80f;
+      if (__builtin_expect(__any(large || small), 0)) {
+        const float s = large ? 0x1p-72f : small ? 0x1p96f : 1.f;
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          x[i] *= s;
+          ss = fmaf(x[i], x[i], ss);
+        }
+        for (int d = 1; d < L; d *= 2) ss += __shfl_xor(ss, d);
+        eps = eps * s * s;
+      }
+      const float rs = rsqrtf(ss * inv_dh + eps);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = x[i] * rs * w.at(i);
     }
