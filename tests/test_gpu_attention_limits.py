@@ -1,4 +1,5 @@
-"""Norm and rotation at the stated limits: sizes of heads whose squares leave fp32."""
+"""Norm and rotation, packed and one-token attention at the stated limits: sizes of heads whose squares
+leave fp32, very many sequences and tokens."""
 import numpy as np
 import pytest
 
@@ -6,7 +7,7 @@ import chunked_weight_sequence_amd as ttt
 import gen
 import oracle.attention as oa
 from helpers import dev, host_f64, requires_gpu
-from test_gpu_attention import _f, _i32
+from test_gpu_attention import _check, _cu, _draw, _f, _i32, _logit_size, _packed
 
 pytestmark = [pytest.mark.gpu, requires_gpu]
 
@@ -37,3 +38,86 @@ def test_norms_of_very_large_and_small_heads(dtype, dh, by, eps):
     off = np.abs(host_f64(Q) - want) / bound
     print(f"  {off.max():.3f} of the bound", flush=True)
     assert np.isfinite(host_f64(Q)).all() and off.max() <= 1.0
+
+
+@pytest.mark.parametrize("n", [64, 4097, 5000])
+def test_packed_thousands_of_sequences(n):
+    print(f"case: {n} sequences", flush=True)
+    rng = np.random.default_rng(n)
+    lq = rng.integers(0, 4, n)
+    more = rng.integers(-1, 5, n)
+    lk = np.maximum(lq + more, 0)
+    cu_q, cu_k = _cu(lq), _cu(lk)
+    Q = _draw(rng, max(cu_q[-1], 1), 2, 64)
+    K, V = _draw(rng, max(cu_k[-1], 1), 1, 64), _draw(rng, max(cu_k[-1], 1), 1, 64)
+    O, L = _packed(Q, K, V, cu_q, cu_k, 0.2, 0)
+    _check(O, L, oa.packed(_f(Q), _f(K), _f(V), cu_q, cu_k, 0.2), _logit_size(_f(Q), _f(K), 0.2), 64, "many")
+
+
+@pytest.mark.parametrize("n,dh", [(300001, 64), (1 << 20, 64), (70000, 128)])
+def test_packed_sequences_of_one_token_return_their_values(n, dh):
+    """Up to 2^20 sequences, the most there may be: a query with one key gets that key's value, bit for bit,
+    and its logit."""
+    import torch
+    print(f"case: {n} sequences of one token, dh {dh}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    q, k, v = (torch.randn((n, 1, dh), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    O, L = ttt.attention_packed(q, k, v, cu, scale=0.5, with_lse=True)
+    assert torch.equal(O, v)
+    x = 0.5 * (q.double() * k.double()).sum(-1)
+    X = 0.5 * (q.double() * k.double()).abs().sum(-1)
+    assert ((L - x).abs() <= (dh + 8) * 2.0 ** -24 * X + 2.0 ** -20).all()
+
+
+def test_packed_as_many_tokens_as_there_may_be():
+    """2^26 tokens in 2^20 sequences of unlike lengths, in which every key of a sequence is the same: a query's
+    result is the mean of the values it sees, here of ones and of its sequence's number."""
+    import torch
+    print("case: 2^26 tokens", flush=True)
+    n, N, dh = 1 << 20, 1 << 26, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    cuts = torch.randint(0, N + 1, (n - 1,), generator=g, device="cuda").sort().values
+    cu = torch.cat([cuts.new_zeros(1), cuts, cuts.new_full((1,), N)]).to(torch.int32)
+    owner = torch.bucketize(torch.arange(N, device="cuda"), cu[1:].long(), right=True)
+    q = torch.ones((N, 1, dh), dtype=torch.bfloat16, device="cuda")
+    k, v = torch.zeros_like(q), torch.ones_like(q)
+    v[:, 0, 1] = (owner % 251).to(torch.bfloat16)  # whole numbers that bf16 holds
+    O, L = ttt.attention_packed(q, k, v, cu, with_lse=True)
+    assert torch.equal(O, v)
+    seen = torch.arange(N, device="cuda") - cu[:-1].long()[owner] + 1
+    assert float((L[:, 0].double() - seen.double().log()).abs().max()) <= 2.0 ** -18
+
+
+def test_decode_as_many_sequences_as_there_may_be():
+    import torch
+    print("case: 2^20 sequences of one token", flush=True)
+    S, Hq, dh, page = 1 << 20, 8, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    pages = 1 << 14
+    K, V = (torch.randn((pages * page, 1, dh), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((S, Hq, dh), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.randint(0, pages, (S, 1), generator=g, device="cuda").to(torch.int32)
+    lens = torch.randint(0, 2, (S,), generator=g, device="cuda").to(torch.int32)
+    O, L = ttt.attention_decode(q, K, V, table, lens, page, with_lse=True)
+    want = torch.where(lens[:, None, None] > 0, V[table[:, 0].long() * page], torch.zeros_like(V[:1]))
+    assert torch.equal(O, want.expand(S, Hq, dh).contiguous())
+    assert torch.equal(torch.isneginf(L), (lens <= 0)[:, None].expand(S, Hq))
+
+
+def test_rotation_of_as_many_tokens_as_there_may_be():
+    """2^25 tokens: a quarter turn more each, so the pair (1, 0) goes through four places."""
+    import torch
+    print("case: 2^25 tokens of norm and rotation", flush=True)
+    N, dh = 1 << 25, 16
+    x = torch.zeros((N, 1, dh), dtype=torch.bfloat16, device="cuda")
+    x[:, 0, :8] = 1
+    freq = torch.full((8,), np.pi / 2, dtype=torch.float64, device="cuda")
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    Q, K = ttt.qk_norm_rope(x, x, pos, freq)
+    turn = torch.tensor([[1, 0], [0, 1], [-1, 0], [0, -1]], dtype=torch.float32, device="cuda")[pos % 4]
+    for y in (Q, K):
+        got = y[:, 0].float()
+        assert float((got[:, 0] - turn[:, 0]).abs().max()) <= 2.0 ** -20
+        assert float((got[:, 8] - turn[:, 1]).abs().max()) <= 2.0 ** -20
+        assert torch.equal(got[:, :1].expand(N, 8), got[:, :8]) and torch.equal(got[:, 8:9].expand(N, 8), got[:, 8:])
