@@ -430,8 +430,9 @@ ttt_status ttt_qk_norm_rope(const void* Q, long long q_stride, const void* K, lo
  *     j <= i + lk - lq   and, with window > 0,   j > i + lk - lq - window
  * and query head h reads key head h / (Hq / Hkv):
  *     o = sum_j softmax_j(scale * q . k_j) v_j        lse = ln sum_j exp(scale * q . k_j)
- * A query that sees nothing (or only logits of -inf) gets o = 0 and lse = -inf; one whose largest
- * logit times log2(e) passes fp32 gets NaN.
+ * A query that sees nothing (or only logits of -inf) gets o = 0 and lse = -inf. The products q . k
+ * are fp32 and infinite past its range; a query with a logit of +inf, or whose largest logit times
+ * log2(e) passes fp32, gets NaN.
  * Logits, exponentials, maxima and sums in fp32; the weights enter the value product as bf16.
  *   Q  [Nq, Hq, dh], K and V [Nk, Hkv, dh], O [Nq, Hq, dh], all dtype (TTT_BF16; TTT_F32 gives
  *      TTT_E_UNSUPPORTED); token t at + t * stride

@@ -121,3 +121,47 @@ def test_rotation_of_as_many_tokens_as_there_may_be():
         assert float((got[:, 0] - turn[:, 0]).abs().max()) <= 2.0 ** -20
         assert float((got[:, 8] - turn[:, 1]).abs().max()) <= 2.0 ** -20
         assert torch.equal(got[:, :1].expand(N, 8), got[:, :8]) and torch.equal(got[:, 8:9].expand(N, 8), got[:, 8:])
+
+
+@pytest.mark.parametrize("Nq,window", [(1, 0), (130, 0), (3, (1 << 26) - 77)])
+def test_packed_as_many_keys_as_there_may_be(Nq, window):
+    """2^26 keys of one logit: the values' mean, and the logarithm of their number. Each piece's sums are exact
+    (weights of 1), the halves of channel 1 cancel."""
+    import torch
+    print(f"case: {Nq} queries, 2^26 keys, window {window}", flush=True)
+    Nk, dh = 1 << 26, 64
+    q = torch.ones((Nq, 2, dh), dtype=torch.bfloat16, device="cuda")
+    k, v = torch.zeros((Nk, 1, dh), dtype=torch.bfloat16, device="cuda"), torch.ones(
+        (Nk, 1, dh), dtype=torch.bfloat16, device="cuda")
+    v[: Nk // 2, 0, 1] = -1
+    v[-1, 0, 2] = 2.0 ** 26  # the last key's value is seen by the last query alone
+    O, L = ttt.attention_packed(q, k, v, _i32([0, Nq]), _i32([0, Nk]), window=window, with_lse=True)
+    last = Nk - Nq + np.arange(Nq)
+    seen = np.minimum(last + 1, window) if window else last + 1
+    assert np.abs(host_f64(L) - np.log(seen)[:, None]).max() <= 2.0 ** -18
+    got = host_f64(O)
+    first = last + 1 - seen
+    one = (seen - 2 * np.maximum(Nk // 2 - first, 0)) / seen
+    assert np.abs(got[..., 0] - 1).max() <= 2.0 ** -8
+    assert np.abs(got[..., 1] - one[:, None]).max() <= 2.0 ** -8 * np.abs(one).max() + 2.0 ** -20
+    assert (got[:-1, :, 2] == 1).all() and np.abs(got[-1, :, 2] - 2).max() <= 2.0 ** -6
+
+
+def test_decode_as_many_tokens_as_a_table_may_hold():
+    """2^30 tokens: 16384 pages of 65536, three of them over and over, the last one once. Equal logits; each
+    wave's sums of ones are whole numbers below 2^24."""
+    import torch
+    print("case: 2^30 tokens of one sequence", flush=True)
+    page, pages, dh = 65536, 1 << 14, 64
+    K = torch.zeros((4 * page, 1, dh), dtype=torch.bfloat16, device="cuda")
+    V = torch.ones_like(K)
+    V[page:2 * page, 0, 1] = -1
+    V[3 * page:, 0, 2] = 2.0 ** 14
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None] % 2
+    table[0, -1] = 3
+    q = torch.ones((1, 3, dh), dtype=torch.bfloat16, device="cuda")
+    O, L = ttt.attention_decode(q, K, V, table.contiguous(), _i32([1 << 30]), page, with_lse=True)
+    got = host_f64(O)[0]
+    assert np.abs(host_f64(L) - np.log(2.0 ** 30)).max() <= 2.0 ** -18
+    assert np.abs(got[:, 0] - 1).max() <= 2.0 ** -8 and np.abs(got[:, 1] - 2.0 ** -13).max() <= 2.0 ** -20
+    assert np.abs(got[:, 2] - (2.0 - 2.0 ** -14)).max() <= 2.0 ** -6
