@@ -16,6 +16,11 @@ The attention half of a block, over a packed prompt and then token by token:
     q, k = qk_norm_rope(Q, K, pos, inv_freq, V=V, K_cache=Kc, V_cache=Vc, slots=slots)
     O = attention_packed(q, k, V, cu_seqlens)
     O = attention_decode(q, Kc, Vc, page_table, lengths, page_size=64)
+
+Between the halves, and fast weights that forget:
+
+    y, _, x = add_rms_norm(O, weight, residual=x)
+    O, states = gated_delta_decode(Q, K, V, g, beta, states, slots=slots)
 """
 from __future__ import annotations
 
@@ -29,7 +34,8 @@ __all__ = [
     "chunk_scan", "chunk_scan_workspace_bytes", "chunk_scan_profile",
     "linear_minibatch", "surprisal_route", "lm_target", "gated_z", "cache_readout", "chunk_scan_docs",
     "chunk_scan_handover_timeouts", "scan_test_overrides", "chunk_scan_noalloc",
-    "rope_frequencies", "qk_norm_rope", "attention_packed", "attention_decode", "EXPORTED",
+    "rope_frequencies", "qk_norm_rope", "attention_packed", "attention_decode",
+    "add_rms_norm", "gated_delta_decode", "EXPORTED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -72,6 +78,9 @@ EXPORTED = {
     "ttt_attention_decode": (_i, [_p, _ll, _p, _p, _i, _p, _ll, _p, _p, _i, _i, _i, _p,
                                   _i, _i, _i, _i, _f, _i, _p, _sz, _p]),
     "ttt_attention_decode_workspace": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "ttt_add_rms_norm": (_i, [_p, _ll, _p, _ll, _i, _p, _f, _p, _ll, _p, _ll, _p, _i, _i, _i, _p]),
+    "ttt_gated_delta_decode": (_i, [_p, _ll, _p, _ll, _p, _ll, _i, _p, _p, _p, _ll, _p, _p, _p, _ll,
+                                    _i, _i, _i, _i, _i, _f, _i, _f, _p]),
     "ttt_status_string": (ctypes.c_char_p, [_i]),
     "ttt_abi_version": (_i, []),
 }
@@ -710,6 +719,125 @@ def attention_decode(Q, K_cache, V_cache, page_table, lengths, page_size: int, *
              n_slots // page_size, lengths.data_ptr(), S, Hq, Hkv, dh,
              dh ** -0.5 if scale is None else scale, window, _ptr(ws), ws_bytes), dev)
     return O if lse is None else (O, lse)
+
+
+def _matrix(t, name: str, N, D, dtype, device):
+    """Checks a [N, D] GPU tensor whose rows may lie apart; returns its row stride in elements."""
+    if t.shape != (N, D):
+        raise ValueError(f"{name} must be [{N}, {D}], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.stride(1) != 1 and D > 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    return t.stride(0) if N > 1 else D
+
+
+def add_rms_norm(X, weight=None, *, residual=None, eps: float = 1e-6, e4m3: bool = False, group: int = 0,
+                 S=None, Y=None, scales=None):
+    """RMS norm of X [N,D] (bf16 or fp32; rows may be slices of one buffer), or of X + residual, times weight
+    [D] fp32. Returns (Y, scales, S): Y [N,D] in X's dtype and scales None, or (e4m3) Y in
+    torch.float8_e4m3fn with the fp32 scales it was divided by, one a row ([N]) or one for each `group`
+    channels ([N, D / group]); S [N,D] the sum X + residual, None without a residual. S may be X or
+    residual (in place)."""
+    torch = _torch()
+    if X.dim() != 2 or not X.is_cuda:
+        raise ValueError("X must be a [N, D] GPU tensor")
+    N, D = X.shape
+    dt, dev = X.dtype, X.device
+    code = _dtype_code(dt)
+    if N >= 1 << 31 or D >= 1 << 31:
+        raise ValueError(f"X is too large: {(N, D)}")
+    xs = _matrix(X, "X", N, D, dt, dev)
+    rs = ss = 0
+    if residual is not None:
+        rs = _matrix(residual, "residual", N, D, dt, dev)
+        if S is None:
+            S, ss = torch.empty((N, D), dtype=dt, device=dev), D
+        else:
+            ss = _matrix(S, "S", N, D, dt, dev)
+    elif S is not None:
+        raise ValueError("S is for a call with a residual")
+    if weight is not None:
+        _vec(weight, "weight", (D,), torch.float32, dev)
+    group = _int_in(group, "group", 0, 1 << 30)
+    out = torch.float8_e4m3fn if e4m3 else dt
+    if Y is None:
+        Y, ys = torch.empty((N, D), dtype=out, device=dev), D
+    else:
+        ys = _matrix(Y, "Y", N, D, out, dev)
+    if e4m3:
+        if group and D % group:
+            raise ValueError(f"group must divide D = {D}, got {group}")
+        shape = (N, D // group) if group else (N,)
+        if scales is None:
+            scales = torch.empty(shape, dtype=torch.float32, device=dev)
+        else:
+            _vec(scales, "scales", shape, torch.float32, dev)
+    elif scales is not None or group:
+        raise ValueError("scales and group are for an output in e4m3")
+    _launch(lib().ttt_add_rms_norm,
+            (X.data_ptr(), xs, _ptr(residual), rs, code, _ptr(weight), eps, _ptr(S), ss, Y.data_ptr(), ys,
+             _ptr(scales), group, N, D), dev)
+    return Y, scales, S
+
+
+def _delta_inputs(Q, K, V, g, beta, O):
+    """Checks the tensors that both calls of the gated delta rule take; returns (O, the arguments up to it,
+    tokens, Hk, Hv, dk, dv)."""
+    torch = _torch()
+    qs = _rows(Q, "Q")
+    N, Hk, dk = Q.shape
+    dt, dev = Q.dtype, Q.device
+    ks = _rows(K, "K", Hk, dk, dt, dev, N)
+    if V.dim() != 3:
+        raise ValueError(f"V must be [tokens, heads, dv], got {tuple(V.shape)}")
+    Hv, dv = V.shape[1:]
+    vs = _rows(V, "V", Hv, dv, dt, dev, N)
+    _vec(g, "g", (N, Hv), torch.float32, dev)
+    _vec(beta, "beta", (N, Hv), torch.float32, dev)
+    if O is None:
+        O, os_ = torch.empty((N, Hv, dv), dtype=dt, device=dev), Hv * dv
+    else:
+        os_ = _rows(O, "O", Hv, dv, dt, dev, N)
+    return O, (Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs, _dtype_code(dt), g.data_ptr(),
+               beta.data_ptr(), O.data_ptr(), os_), N, Hk, Hv, dk, dv
+
+
+def _delta_states(state, state_out, slots, n_seq, Hv, dk, dv, device):
+    """Checks the pools of states; returns how many slots they have."""
+    torch = _torch()
+    n_slots = None
+    for t, name in ((state, "state"), (state_out, "state_out")):
+        if t is None:
+            continue
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [n_slots, Hv, dk, dv], got {tuple(t.shape)}")
+        n_slots = t.shape[0] if n_slots is None else n_slots
+        _vec(t, name, (n_slots, Hv, dk, dv), torch.float32, device)
+    if slots is not None:
+        _vec(slots, "slots", (n_seq,), torch.int32, device)
+    elif n_slots is not None and n_slots < n_seq:
+        raise ValueError(f"{n_seq} sequences need as many states, got {n_slots}")
+    return n_slots or 0
+
+
+def gated_delta_decode(Q, K, V, g, beta, state, *, state_out=None, slots=None, scale=None,
+                       normalize: bool = True, norm_eps: float = 1e-6, O=None):
+    """The gated delta rule for one token of each of S sequences: per value head, with a = exp(g),
+    u = beta (v - a W^T k), W <- a W + k u^T, o = scale W^T q; q and k divided by their norm first
+    (normalize). Q, K [S,Hk,dk], V [S,Hv,dv] bf16 (tokens may be slices of one buffer), g and beta [S,Hv] fp32;
+    state [n_slots,Hv,dk,dv] fp32, of which sequence s has slot slots[s] (int32; slots None: s; outside: starts
+    at zero, nothing kept). The new states go to the same slots of state_out, in place if that is None.
+    scale: 1 / sqrt(dk) by default. Returns (O [S,Hv,dv], state_out)."""
+    O, args, S, Hk, Hv, dk, dv = _delta_inputs(Q, K, V, g, beta, O)
+    state_out = state if state_out is None else state_out
+    n_slots = _delta_states(state, state_out, slots, S, Hv, dk, dv, Q.device)
+    _launch(lib().ttt_gated_delta_decode,
+            args + (state.data_ptr(), state_out.data_ptr(), _ptr(slots), n_slots, S, Hk, Hv, dk, dv,
+                    dk ** -0.5 if scale is None else scale, int(bool(normalize)), norm_eps), Q.device)
+    return O, state_out
 
 
 @functools.lru_cache(maxsize=4096)

@@ -1,0 +1,250 @@
+// RMS norm of a residual stream with the residual's addition, in one pass, to the input's type or to 8
+// bits with scales.
+//
+// For row n of D channels:
+//     h = x + r                                        (h = x without a residual), written as S
+//     y = h * rsqrt(mean(h^2) + eps) * w               (w = 1 where none is given)
+// Y holds y in the input's type, or, for an output in 8 bits, e4m3(y / scale) with
+//     scale = max(max |y| / 448, 2^-126)               of the row, or of each group of channels.
+// fp32 arithmetic on the unrounded sum h, each output rounded once (448 is e4m3's largest value, so nothing
+// saturates; 2^-126 keeps scales normal numbers, and rows of zeros from dividing by zero).
+//
+// Bound by HBM: each input is read once and each output written once. A row is held in registers by one
+// wave, or by a workgroup's four where there are few rows or long ones, 8 channels of a lane side by side,
+// and is read while the one before it is worked on. The weights stay in registers from row to row: read
+// again for each, they would be as many bytes through L2 as a bf16 row itself. The largest |h w| of a scale is
+// found together with the sum of squares, since the factor between h w and y is one of the whole row.
+#include <type_traits>
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace ttt {
+namespace {
+
+// 8 channels as they lie in memory.
+template <typename T>
+struct Eight {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+  }
+  __device__ __forceinline__ void unpack(float (&x)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[4 * i] = __uint_as_float(v[i].x);
+        x[4 * i + 1] = __uint_as_float(v[i].y);
+        x[4 * i + 2] = __uint_as_float(v[i].z);
+        x[4 * i + 3] = __uint_as_float(v[i].w);
+      }
+    }
+  }
+  __device__ __forceinline__ void pack(const float (&x)[8]) {
+    if constexpr (sizeof(T) == 2) {
+      v[0] = make_uint4(pack2bf(x[0], x[1]), pack2bf(x[2], x[3]), pack2bf(x[4], x[5]), pack2bf(x[6], x[7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]),
+                          __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]));
+    }
+  }
+};
+
+// 8 values in e4m3, rounded to nearest even.
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8]) {
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
+  return make_uint2(uint32_t(lo), uint32_t(hi));
+}
+
+// W waves to a row, CH times 8 channels to a lane.
+template <typename T, bool E4M3, int W, int CH>
+__global__ __launch_bounds__(256) void k_add_norm(AddNormArgs a) {
+  __shared__ float2 part[2][4];  // of every second row in turn, so that one barrier a row is enough
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int li = W == 1 ? lane : tid, D = a.D, n8 = D >> 3;
+  const float inv_d = 1.f / float(D);
+  const T *X = static_cast<const T*>(a.X), *R = static_cast<const T*>(a.R);
+
+  bool on[CH];
+  float w[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    on[i] = i * 64 * W + li < n8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
+  }
+  const long step = long(gridDim.x) * (4 / W);
+  long n = long(blockIdx.x) * (4 / W) + (W == 1 ? wave : 0);
+  Eight<T> x[CH], r[CH];
+  const auto load = [&](long row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (on[i]) {
+        x[i].load(X + row * a.xs + 8 * (i * 64 * W + li));
+        if (R) r[i].load(R + row * a.rs + 8 * (i * 64 * W + li));
+      }
+  };
+  if (n < a.N) load(n);
+  if (a.w) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (on[i]) {
+        const float4* p = reinterpret_cast<const float4*>(a.w + 8 * (i * 64 * W + li));
+        const float4 u = p[0], v = p[1];
+        w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+        w[i][4] = v.x, w[i][5] = v.y, w[i][6] = v.z, w[i][7] = v.w;
+      }
+  }
+  // sum of squares and largest |h w| of the row
+  int turn = 0;
+  const auto reduce = [&](float& ss, float& top) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      ss += __shfl_xor(ss, d);
+      if (E4M3) top = fmaxf(top, __shfl_xor(top, d));
+    }
+    if constexpr (W > 1) {
+      if (lane == 0) part[turn][wave] = make_float2(ss, top);
+      __syncthreads();
+      ss = part[turn][0].x;
+      top = part[turn][0].y;
+#pragma unroll
+      for (int i = 1; i < W; ++i) {
+        ss += part[turn][i].x;
+        top = fmaxf(top, part[turn][i].y);
+      }
+      turn ^= 1;
+    }
+  };
+  for (; n < a.N; n += step) {  // the same rows for all waves of a row
+    float h[CH][8];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
+      if (!on[i]) continue;
+      x[i].unpack(h[i]);
+      if (R) {
+        float b[8];
+        r[i].unpack(b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] += b[e];
+      }
+      if (a.S) {
+        Eight<T> s;
+        s.pack(h[i]);
+        s.store(static_cast<T*>(a.S) + n * a.ss + 8 * (i * 64 * W + li));
+      }
+    }
+    if (n + step < a.N) load(n + step);
+    float ss = 0.f, top = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ss = fmaf(h[i][e], h[i][e], ss);
+        if (E4M3) top = fmaxf(top, fabsf(h[i][e] * w[i][e]));
+      }
+    reduce(ss, top);
+    float eps = a.eps;
+    // Squares that leave fp32 (values past 2^63, or all below 2^-40 where eps does not hide them): the row is
+    // scaled by a power of two first. All lanes of a row decide alike.
+    const bool large = !(ss < 0x1p126f), small = ss < 0x1p-80f && eps < 0x1p-80f;
+    if (__builtin_expect(large || small, 0)) {
+      const float s = large ? 0x1p-72f : 0x1p96f;
+      ss = top = 0.f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[i][e] *= s;
+          ss = fmaf(h[i][e], h[i][e], ss);
+          if (E4M3) top = fmaxf(top, fabsf(h[i][e] * w[i][e]));
+        }
+      reduce(ss, top);
+      eps = eps * s * s;
+    }
+    const float rs = rsqrtf(ss * inv_d + eps);
+    if constexpr (E4M3) {
+      const int per = a.group >> 3;  // lanes to a group, a power of two
+      const long sn = a.group ? n * (D / a.group) : n;
+      float scale = fmaxf(top * rs / 448.f, 0x1p-126f), inv = 1.f / scale;
+      if (!a.group && li == 0) a.scales[sn] = scale;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        float y[8], g = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = h[i][e] * rs * w[i][e];
+          g = fmaxf(g, fabsf(y[e]));
+        }
+        if (a.group) {  // a group's lanes are all on or all off
+          for (int d = 1; d < per; d *= 2) g = fmaxf(g, __shfl_xor(g, d));
+          scale = fmaxf(g / 448.f, 0x1p-126f);
+          inv = 1.f / scale;
+          const int c = i * 64 * W + li;
+          if (on[i] && (c & (per - 1)) == 0) a.scales[sn + c / per] = scale;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= inv;
+        if (on[i])
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + n * a.ys + 8 * (i * 64 * W + li)) = pack8_e4m3(y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = h[i][e] * rs * w[i][e];
+        Eight<T> o;
+        o.pack(y);
+        if (on[i]) o.store(static_cast<T*>(a.Y) + n * a.ys + 8 * (i * 64 * W + li));
+      }
+    }
+  }
+}
+
+template <typename T, bool E4M3, int W>
+void launch(const AddNormArgs& a, int ch, dim3 grid) {
+  const dim3 block(256);
+  if (ch <= 1) hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 1>), grid, block, 0, a.stream, a);
+  else if (ch <= 2) hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 2>), grid, block, 0, a.stream, a);
+  else if (ch <= 3) hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 3>), grid, block, 0, a.stream, a);
+  else if (ch <= 5) hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 5>), grid, block, 0, a.stream, a);
+  else hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 8>), grid, block, 0, a.stream, a);
+}
+
+}  // namespace
+
+hipError_t add_norm(const AddNormArgs& a) {
+  const int n8 = a.D / 8;
+  const int w = a.N >= 2048 && n8 <= 8 * 64 ? 1 : 4;
+  const int ch = (n8 + 64 * w - 1) / (64 * w);
+  const long wgs = (a.N + 4 / w - 1) / (4 / w);
+  const dim3 grid(unsigned(wgs < 1024 ? wgs : 1024));
+  if (a.bf16 && a.e4m3) w == 1 ? launch<uint16_t, true, 1>(a, ch, grid) : launch<uint16_t, true, 4>(a, ch, grid);
+  else if (a.bf16) w == 1 ? launch<uint16_t, false, 1>(a, ch, grid) : launch<uint16_t, false, 4>(a, ch, grid);
+  else if (a.e4m3) w == 1 ? launch<float, true, 1>(a, ch, grid) : launch<float, true, 4>(a, ch, grid);
+  else w == 1 ? launch<float, false, 1>(a, ch, grid) : launch<float, false, 4>(a, ch, grid);
+  return hipGetLastError();
+}
+
+}  // namespace ttt

@@ -811,6 +811,126 @@ TTT_EXPORT ttt_status ttt_attention_decode(const void* Q, long long q_stride, co
   return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
 }
 
+TTT_EXPORT ttt_status ttt_add_rms_norm(const void* X, long long x_stride, const void* R, long long r_stride,
+                                       ttt_dtype dtype, const float* weight, float eps, void* S,
+                                       long long s_stride, void* Y, long long y_stride, float* scales,
+                                       int group, int N, int D, hipStream_t stream) {
+  if (!valid_dtype(dtype)) return TTT_E_DTYPE;
+  if (!X || !Y) return TTT_E_NULL;
+  if (N < 1 || N > (1 << 30) || D < 8 || D > 16384 || D % 8 || !(eps >= 0.f) || !std::isfinite(eps))
+    return TTT_E_SHAPE;
+  if (group && (!scales || group < 16 || group > 512 || (group & (group - 1)) || D % group)) return TTT_E_SHAPE;
+  const size_t esz = dsize(dtype), ysz = scales ? 1 : esz;
+  const long long most = 1ll << 31;
+  if (!stride_ok(x_stride, D, esz, most) || (R && !stride_ok(r_stride, D, esz, most)) ||
+      (S && !stride_ok(s_stride, D, esz, most)) || y_stride < D || y_stride > most ||
+      (size_t(y_stride) * ysz) % (scales ? 8 : 16))
+    return TTT_E_SHAPE;
+  for (const void* p : {X, R, (const void*)weight, (const void*)S, (const void*)Y, (const void*)scales})
+    if (!aligned16(p)) return TTT_E_ALIGN;
+  const size_t n = size_t(N), row = size_t(D) * esz;
+  const Rows rx{X, n, size_t(x_stride) * esz, row}, rr{R, R ? n : 0, size_t(r_stride) * esz, row},
+      rs{S, S ? n : 0, size_t(s_stride) * esz, row}, ry{Y, n, size_t(y_stride) * ysz, size_t(D) * ysz};
+  const Rows ins[] = {rx, rr, whole(weight, size_t(D) * 4)};
+  const Rows outs[] = {rs, ry, whole(scales, n * (group ? D / group : 1) * 4)};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      // in place: the same rows, each channel read by the lane that writes it
+      const bool same = outs[o].p == ins[i].p && outs[o].stride == ins[i].stride;
+      if (same && i < 2 && (o == 0 || (o == 1 && !scales))) continue;
+      if (overlap(outs[o], ins[i])) return TTT_E_ALIAS;
+    }
+    for (int p = 0; p < o; ++p)
+      if (overlap(outs[o], outs[p])) return TTT_E_ALIAS;
+  }
+  ttt::AddNormArgs a{X, R, long(x_stride), long(r_stride), weight, eps, S, Y, long(s_stride), long(y_stride),
+                     scales, group, N, D, dtype == TTT_BF16, scales != nullptr, stream};
+  (void)hipGetLastError();
+  const hipError_t e = ttt::add_norm(a);
+  return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
+}
+
+namespace {
+// What a call of the gated delta rule gets, and what it asks of that.
+struct DeltaCall {
+  const void *Q, *K, *V;
+  long long q_stride, k_stride, v_stride;
+  ttt_dtype dtype;
+  const float *g, *beta;
+  void* O;
+  long long o_stride;
+  const float* state_in;
+  float* state_out;
+  const int* slots;
+  long long n_slots;
+  int tokens, n_seq, Hk, Hv, dk, dv;
+  float scale, eps;
+  long long most;  // tokens * Hv * dv, exclusive: a launch counts its threads in 32 bits
+};
+bool delta_shape_ok(int tokens, int n_seq, int Hk, int Hv, int dk, int dv) {
+  return tokens >= 1 && n_seq >= 1 && n_seq <= (1 << 20) && Hk >= 1 && Hv >= 1 && Hv <= (1 << 16) &&
+         Hv % Hk == 0 && dk >= 1 && dv >= 1 && dk <= 65536 && dv <= 65536 &&
+         (long long)Hk * dk <= (1 << 22) && (long long)Hv * dv <= (1 << 22);
+}
+bool delta_supported(int dk, int dv) { return (dk == 64 || dk == 128) && dv % 64 == 0 && dv <= 512; }
+ttt_status delta_check(const DeltaCall& c, Rows cu, Rows ws) {
+  if (!valid_dtype(c.dtype)) return TTT_E_DTYPE;
+  if (!c.Q || !c.K || !c.V || !c.g || !c.beta || !c.O) return TTT_E_NULL;
+  if (!delta_shape_ok(c.tokens, c.n_seq, c.Hk, c.Hv, c.dk, c.dv) ||
+      (long long)c.tokens * c.Hv * c.dv >= c.most || !std::isfinite(c.scale) || !(c.eps >= 0.f) ||
+      !std::isfinite(c.eps))
+    return TTT_E_SHAPE;
+  if (c.dtype != TTT_BF16 || !delta_supported(c.dk, c.dv)) return TTT_E_UNSUPPORTED;
+  const long long most = 1ll << 31, wk = (long long)c.Hk * c.dk, wv = (long long)c.Hv * c.dv;
+  if (!stride_ok(c.q_stride, wk, 2, most) || !stride_ok(c.k_stride, wk, 2, most) ||
+      !stride_ok(c.v_stride, wv, 2, most) || !stride_ok(c.o_stride, wv, 2, most))
+    return TTT_E_SHAPE;
+  const bool pool = c.state_in || c.state_out;
+  if (pool && (c.n_slots < (c.slots ? 1 : c.n_seq) || c.n_slots > 0x7FFFFFFFll)) return TTT_E_SHAPE;
+  for (const void* p : {c.Q, c.K, c.V, (const void*)c.g, (const void*)c.beta, (const void*)c.O,
+                        (const void*)c.state_in, (const void*)c.state_out, (const void*)c.slots, cu.p, ws.p})
+    if (!aligned16(p)) return TTT_E_ALIGN;
+  const size_t n = size_t(c.tokens), states = pool ? size_t(c.n_slots) * wv * c.dk * 4 : 0;
+  const Rows ins[] = {whole(c.state_in, states),
+                      {c.Q, n, size_t(c.q_stride) * 2, size_t(wk) * 2},
+                      {c.K, n, size_t(c.k_stride) * 2, size_t(wk) * 2},
+                      {c.V, n, size_t(c.v_stride) * 2, size_t(wv) * 2},
+                      whole(c.g, n * c.Hv * 4), whole(c.beta, n * c.Hv * 4),
+                      whole(c.slots, size_t(c.n_seq) * 4), cu};
+  const Rows outs[] = {whole(c.state_out, states), {c.O, n, size_t(c.o_stride) * 2, size_t(wv) * 2}, ws};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 8; ++i) {
+      if (i == 0 && o == 0 && c.state_in == c.state_out) continue;  // in place
+      if (overlap(outs[o], ins[i])) return TTT_E_ALIAS;
+    }
+    for (int p = 0; p < o; ++p)
+      if (overlap(outs[o], outs[p])) return TTT_E_ALIAS;
+  }
+  return TTT_OK;
+}
+ttt::DeltaArgs delta_args(const DeltaCall& c, int normalize, hipStream_t stream) {
+  return {c.Q, c.K, c.V, long(c.q_stride), long(c.k_stride), long(c.v_stride), c.g, c.beta, c.O,
+          long(c.o_stride), c.state_in, c.state_out, c.slots, long(c.n_slots), c.n_seq, c.Hk, c.Hv, c.dk,
+          c.dv, c.scale, normalize != 0, c.eps, stream};
+}
+}  // namespace
+
+TTT_EXPORT ttt_status ttt_gated_delta_decode(const void* Q, long long q_stride, const void* K,
+                                             long long k_stride, const void* V, long long v_stride,
+                                             ttt_dtype dtype, const float* g, const float* beta, void* O,
+                                             long long o_stride, const float* state_in, float* state_out,
+                                             const int* slots, long long n_slots, int n_seq, int Hk, int Hv,
+                                             int dk, int dv, float scale, int normalize, float eps,
+                                             hipStream_t stream) {
+  const DeltaCall c{Q, K, V, q_stride, k_stride, v_stride, dtype, g, beta, O, o_stride, state_in, state_out,
+                    slots, n_slots, n_seq, n_seq, Hk, Hv, dk, dv, scale, eps, 1ll << 30};
+  const ttt_status s = delta_check(c, whole(nullptr, 0), whole(nullptr, 0));
+  if (s != TTT_OK) return s;
+  (void)hipGetLastError();
+  const hipError_t e = ttt::delta_step(delta_args(c, normalize, stream));
+  return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
+}
+
 TTT_EXPORT const char* ttt_status_string(ttt_status s) {
   switch (s) {
     case TTT_OK: return "TTT_OK: success";

@@ -266,4 +266,39 @@ struct DecodeArgs {
 size_t attention_decode_workspace(int n_seq, int max_pages, int page, int Hq, int Hkv, int dh);
 hipError_t attention_decode(const DecodeArgs& a);
 
+// RMS norm with the residual's addition; Y in the input's type or, with scales, e4m3. Strides in elements.
+struct AddNormArgs {
+  const void *X, *R;             // [N, D], R may be null
+  long xs, rs;
+  const float* w;                // [D] or null
+  float eps;
+  void *S, *Y;                   // S may be null
+  long ss, ys;
+  float* scales;                 // [N] or [N, D / group]
+  int group;                     // 0: the whole row
+  int N, D;
+  bool bf16, e4m3;
+  hipStream_t stream;
+};
+hipError_t add_norm(const AddNormArgs& a);
+
+// The gated delta rule. Strides in elements.
+struct DeltaArgs {
+  const void *Q, *K, *V;         // token t's heads at + t * stride, bf16
+  long qs, ks, vs;
+  const float *g, *beta;         // [tokens, Hv]
+  void* O;
+  long os;
+  const float* state_in;         // [n_slots, Hv, dk, dv] or null
+  float* state_out;              // the same, or null
+  const int* slots;              // [n_seq] or null
+  long n_slots;
+  int n_seq, Hk, Hv, dk, dv;
+  float scale;
+  bool norm;                     // divide q and k by their norm
+  float eps;
+  hipStream_t stream;
+};
+hipError_t delta_step(const DeltaArgs& a);  // one token per sequence
+
 }  // namespace ttt

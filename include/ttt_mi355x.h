@@ -18,7 +18,8 @@
  * resets and update clipping), ttt_lm_target (the LM-aligned target), ttt_gated_z (the scan's
  * input Z) and ttt_cache_readout (the residual-cache readout); and the attention half of the
  * blocks whose MLP half the scan is: ttt_qk_norm_rope, ttt_attention_packed and
- * ttt_attention_decode.
+ * ttt_attention_decode. A serving loop that takes prompts in pieces has, beside these,
+ * ttt_add_rms_norm between the halves and ttt_gated_delta_decode.
  *
  * Conventions shared by every entry point:
  *   - Tensor pointers are DEVICE pointers owned by the caller; the library never allocates,
@@ -46,7 +47,7 @@
 extern "C" {
 #endif
 
-#define TTT_ABI_VERSION 8
+#define TTT_ABI_VERSION 9
 
 typedef enum {
   TTT_OK = 0,
@@ -487,6 +488,59 @@ ttt_status ttt_attention_decode(const void* Q, long long q_stride, const void* K
                                 size_t workspace_bytes, hipStream_t stream);
 size_t ttt_attention_decode_workspace(int n_seq, int max_pages, int page_size, int Hq, int Hkv,
                                       int dh);
+
+/* ------------------------------------------------------------------------------------------ */
+/* RMS norm of a residual stream with the residual's addition, in one pass: for row n of D channels
+ *     h = x + r                                   (h = x where R is NULL)
+ *     S = h                                       (written where S is given)
+ *     y = h * rsqrt(mean(h^2) + eps) * w          (w = 1 where weight is NULL)
+ * Without scales Y [N, D] is y in dtype. With scales it is y in 8 bits, e4m3 (the OCP format with infinities
+ * left out, largest value 448), one byte a channel, rounded to nearest even:
+ *     scale = max(max |y| / 448, 2^-126)          Y = e4m3(y / scale)
+ * over the whole row (group = 0, scales [N]) or over each `group` channels (scales [N, D / group]).
+ * fp32 arithmetic on the unrounded h, whose sum of squares may pass fp32; S and Y are rounded once. A NaN or
+ * an infinity stays in its row; in 8 bits it is NaN there, and an infinite y makes its scale infinite.
+ *   X, R, S  [N, D] dtype (TTT_F32 or TTT_BF16), row n at + n * stride elements; R and S may be NULL
+ *   weight   [D] fp32 or NULL;  Y [N, D], row n at + n * y_stride of its own elements
+ *   group    0, or a power of two 16 .. 512 that divides D; 0 without scales
+ *   D: a multiple of 8 up to 16384; 1 <= N <= 2^30; strides at least D, multiples of 16 bytes (8 for an
+ *   output in 8 bits), at most 2^31;
+ *   eps >= 0, finite (else TTT_E_SHAPE).
+ *   In place: S may be X or R, and Y without scales may be X or R, with the same stride. Any other overlap of
+ *   an output with an input or another output gives TTT_E_ALIAS. */
+ttt_status ttt_add_rms_norm(const void* X, long long x_stride, const void* R, long long r_stride,
+                            ttt_dtype dtype, const float* weight, float eps, void* S,
+                            long long s_stride, void* Y, long long y_stride, float* scales, int group,
+                            int N, int D, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* The gated delta rule: fast weights that forget, the per-token form of TTT-Linear's gradient step (at a
+ * mini-batch of one token that step is the delta rule: TTT layers page, ai-jitan-hub, on
+ * arXiv 2407.04620) with a decay. Value head h of a sequence has the state S [dk, dv], fp32, and reads the
+ * queries and keys of head h / (Hv / Hk). Token by token, with a = exp(g):
+ *     u = beta (v - a S^T k)      S <- a S + k u^T      o = scale S^T q
+ * and, where normalize is set, q and k replaced by x * rsqrt(sum(x^2) + eps) of theirs.
+ *
+ * ttt_gated_delta_decode takes one token of each of n_seq sequences.
+ *   Q, K     [n_seq, Hk, dk], V and O [n_seq, Hv, dv], dtype (TTT_BF16; TTT_F32 gives TTT_E_UNSUPPORTED);
+ *            sequence s at + s * stride
+ *   g, beta  [n_seq, Hv] fp32: the log of the decay (0 keeps all, -inf forgets all) and the step
+ *   state_in, state_out  [n_slots, Hv, dk, dv] fp32; sequence s reads and writes slot slots[s] (its own number
+ *            where slots is NULL: n_slots >= n_seq then). A slot outside [0, n_slots) is a sequence that starts
+ *            at zero and whose state is not kept (padding). The slots inside have to be distinct where states
+ *            are written. state_in NULL: all start at zero; state_out NULL: none is kept. Other slots of
+ *            state_out are left as they were. In place: state_out may be state_in.
+ * fp32 arithmetic, O rounded once. Sums of squares are fp32 and infinite past its range. What is not finite
+ * in a sequence stays in it.
+ *   Hv % Hk == 0; dk 64 or 128; dv a multiple of 64 up to 512 (else TTT_E_UNSUPPORTED); n_seq * Hv * dv < 2^30;
+ *   n_slots < 2^31; strides in elements: at least heads * width, multiples of 8, at most 2^31; scale finite;
+ *   eps >= 0, finite (else TTT_E_SHAPE). An output must not overlap anything else (TTT_E_ALIAS). */
+ttt_status ttt_gated_delta_decode(const void* Q, long long q_stride, const void* K, long long k_stride,
+                                  const void* V, long long v_stride, ttt_dtype dtype, const float* g,
+                                  const float* beta, void* O, long long o_stride, const float* state_in,
+                                  float* state_out, const int* slots, long long n_slots, int n_seq,
+                                  int Hk, int Hv, int dk, int dv, float scale, int normalize, float eps,
+                                  hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
 const char* ttt_status_string(ttt_status s);  /* static string, never NULL */
