@@ -17,6 +17,10 @@ The attention half of a block, over a packed prompt and then token by token:
     O = attention_packed(q, k, V, cu_seqlens)
     O = attention_decode(q, Kc, Vc, page_table, lengths, page_size=64)
 
+or prompts in pieces, mixed with single tokens, over the same cache:
+
+    O = attention_paged(q, Kc, Vc, cu_q, page_table, lengths, page_size=64)
+
 Between the halves, and fast weights that forget:
 
     y, _, x = add_rms_norm(O, weight, residual=x)
@@ -35,7 +39,7 @@ __all__ = [
     "linear_minibatch", "surprisal_route", "lm_target", "gated_z", "cache_readout", "chunk_scan_docs",
     "chunk_scan_handover_timeouts", "scan_test_overrides", "chunk_scan_noalloc",
     "rope_frequencies", "qk_norm_rope", "attention_packed", "attention_decode",
-    "add_rms_norm", "gated_delta_decode", "EXPORTED",
+    "attention_paged", "add_rms_norm", "gated_delta_decode", "EXPORTED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -78,6 +82,9 @@ EXPORTED = {
     "ttt_attention_decode": (_i, [_p, _ll, _p, _p, _i, _p, _ll, _p, _p, _i, _i, _i, _p,
                                   _i, _i, _i, _i, _f, _i, _p, _sz, _p]),
     "ttt_attention_decode_workspace": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "ttt_attention_paged": (_i, [_p, _ll, _p, _p, _i, _p, _ll, _p, _p, _p, _i, _i, _i, _p,
+                                 _i, _i, _i, _i, _i, _f, _i, _p, _sz, _p]),
+    "ttt_attention_paged_workspace": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "ttt_add_rms_norm": (_i, [_p, _ll, _p, _ll, _i, _p, _f, _p, _ll, _p, _ll, _p, _i, _i, _i, _p]),
     "ttt_gated_delta_decode": (_i, [_p, _ll, _p, _ll, _p, _ll, _i, _p, _p, _p, _ll, _p, _p, _p, _ll,
                                     _i, _i, _i, _i, _i, _f, _i, _f, _p]),
@@ -718,6 +725,51 @@ def attention_decode(Q, K_cache, V_cache, page_table, lengths, page_size: int, *
              O.data_ptr(), os_, _ptr(lse), page_table.data_ptr(), max_pages, page_size,
              n_slots // page_size, lengths.data_ptr(), S, Hq, Hkv, dh,
              dh ** -0.5 if scale is None else scale, window, _ptr(ws), ws_bytes), dev)
+    return O if lse is None else (O, lse)
+
+
+def attention_paged(Q, K_cache, V_cache, cu_q, page_table, lengths, page_size: int, *, scale=None,
+                    window: int = 0, O=None, with_lse: bool = False, lse=None, workspace=None):
+    """Attention of new tokens over a paged cache that holds them already. Q [Nq,Hq,dh] bf16, the tokens of
+    sequence s from cu_q[s] to cu_q[s+1] (cu_q [n_seq + 1] int32 on the GPU; any numbers of them, 0 and 1
+    too); lengths [n_seq] int32: the cached tokens of each sequence, of which the last is its last query's
+    own. The caches, page_table [n_seq,max_pages] and page_size as in attention_decode; what a query sees,
+    window and the results as in attention_packed."""
+    torch = _torch()
+    qs = _rows(Q, "Q")
+    Nq, Hq, dh = Q.shape
+    dt, dev = Q.dtype, Q.device
+    if K_cache.dim() != 3:
+        raise ValueError(f"K_cache must be [n_slots, Hkv, dh], got {tuple(K_cache.shape)}")
+    n_slots, Hkv = K_cache.shape[0], K_cache.shape[1]
+    _vec(K_cache, "K_cache", (n_slots, Hkv, dh), dt, dev)
+    _vec(V_cache, "V_cache", (n_slots, Hkv, dh), dt, dev)
+    if cu_q.dim() != 1:
+        raise ValueError(f"cu_q must be [n_seq + 1], got {tuple(cu_q.shape)}")
+    n_seq = cu_q.shape[0] - 1
+    _vec(cu_q, "cu_q", (n_seq + 1,), torch.int32, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seq, max_pages]")
+    max_pages = page_table.shape[1]
+    _vec(page_table, "page_table", (n_seq, max_pages), torch.int32, dev)
+    _vec(lengths, "lengths", (n_seq,), torch.int32, dev)
+    page_size = _int_in(page_size, "page_size", 1, 65536)
+    window = _int_in(window, "window", 0, 1 << 30)
+    if O is None:
+        O, os_ = torch.empty_like(Q), Hq * dh
+    else:
+        os_ = _rows(O, "O", Hq, dh, dt, dev, Nq)
+    if lse is not None:
+        _vec(lse, "lse", (Nq, Hq), torch.float32, dev)
+    elif with_lse:
+        lse = torch.empty(Nq, Hq, dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(workspace, _workspace_bytes(
+        "ttt_attention_paged_workspace", n_seq, Nq, max_pages, page_size, Hq, Hkv, dh), dev)
+    _launch(lib().ttt_attention_paged,
+            (Q.data_ptr(), qs, K_cache.data_ptr(), V_cache.data_ptr(), _dtype_code(dt), O.data_ptr(), os_,
+             _ptr(lse), cu_q.data_ptr(), page_table.data_ptr(), max_pages, page_size, n_slots // page_size,
+             lengths.data_ptr(), n_seq, Nq, Hq, Hkv, dh, dh ** -0.5 if scale is None else scale, window,
+             _ptr(ws), ws_bytes), dev)
     return O if lse is None else (O, lse)
 
 

@@ -811,6 +811,58 @@ TTT_EXPORT ttt_status ttt_attention_decode(const void* Q, long long q_stride, co
   return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
 }
 
+namespace {
+bool paged_ok(int n_seq, int Nq, int max_pages, int page, int Hq, int Hkv, int dh) {
+  return packed_ok(n_seq, Nq, 1, Hq, Hkv, dh) && max_pages >= 1 && page >= 1 &&
+         (long long)max_pages * page <= (1 << 30);
+}
+}  // namespace
+
+TTT_EXPORT size_t ttt_attention_paged_workspace(int n_seq, int Nq, int max_pages, int page_size, int Hq,
+                                                int Hkv, int dh) {
+  if (!paged_ok(n_seq, Nq, max_pages, page_size, Hq, Hkv, dh) || !page_ok(page_size) || (dh != 64 && dh != 128))
+    return 0;
+  return ttt::attention_paged_workspace(n_seq, Nq, max_pages, page_size, Hq, Hkv, dh);
+}
+
+TTT_EXPORT ttt_status ttt_attention_paged(const void* Q, long long q_stride, const void* K_cache,
+                                          const void* V_cache, ttt_dtype dtype, void* O, long long o_stride,
+                                          float* lse, const int* cu_q, const int* page_table, int max_pages,
+                                          int page_size, int n_pages, const int* lengths, int n_seq, int Nq,
+                                          int Hq, int Hkv, int dh, float scale, int window, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream) {
+  if (!valid_dtype(dtype)) return TTT_E_DTYPE;
+  if (!Q || !K_cache || !V_cache || !O || !cu_q || !page_table || !lengths) return TTT_E_NULL;
+  if (!paged_ok(n_seq, Nq, max_pages, page_size, Hq, Hkv, dh) || n_pages < 1 ||
+      (long long)n_pages * page_size > (1ll << 36) || window < 0 || window > (1 << 30) || !scale_ok(scale))
+    return TTT_E_SHAPE;
+  if (dtype != TTT_BF16 || (dh != 64 && dh != 128) || !page_ok(page_size)) return TTT_E_UNSUPPORTED;
+  const long long most = 1 << 23, wq = (long long)Hq * dh, wk = (long long)Hkv * dh;
+  if (!stride_ok(q_stride, wq, 2, most) || !stride_ok(o_stride, wq, 2, most)) return TTT_E_SHAPE;
+  for (const void* p : {Q, K_cache, V_cache, (const void*)O, (const void*)lse, (const void*)cu_q,
+                        (const void*)page_table, (const void*)lengths, (const void*)workspace})
+    if (!aligned16(p)) return TTT_E_ALIGN;
+  const size_t need = ttt::attention_paged_workspace(n_seq, Nq, max_pages, page_size, Hq, Hkv, dh);
+  if (need && (!workspace || workspace_bytes < need)) return TTT_E_WORKSPACE;
+  const size_t nq = size_t(Nq), ns = size_t(n_seq), cache = size_t(n_pages) * page_size * wk * 2;
+  const Rows ins[] = {{Q, nq, size_t(q_stride) * 2, size_t(wq) * 2}, whole(K_cache, cache),
+                      whole(V_cache, cache), whole(cu_q, (ns + 1) * 4), whole(page_table, ns * max_pages * 4),
+                      whole(lengths, ns * 4)};
+  const Rows outs[] = {{O, nq, size_t(o_stride) * 2, size_t(wq) * 2},
+                       whole(lse, nq * Hq * 4), whole(need ? workspace : nullptr, need)};
+  for (int o = 0; o < 3; ++o) {
+    for (const Rows& i : ins)
+      if (overlap(outs[o], i)) return TTT_E_ALIAS;
+    for (int p = 0; p < o; ++p)
+      if (overlap(outs[o], outs[p])) return TTT_E_ALIAS;
+  }
+  const ttt::PackedArgs a{Q, K_cache, V_cache, long(q_stride), long(wk), long(wk), O, long(o_stride), lse,
+                          cu_q, nullptr, n_seq, Nq, 0, Hq, Hkv, dh, scale, window, workspace, stream};
+  (void)hipGetLastError();
+  const hipError_t e = ttt::attention_paged(a, {page_table, lengths, max_pages, page_size, n_pages});
+  return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
+}
+
 TTT_EXPORT ttt_status ttt_add_rms_norm(const void* X, long long x_stride, const void* R, long long r_stride,
                                        ttt_dtype dtype, const float* weight, float eps, void* S,
                                        long long s_stride, void* Y, long long y_stride, float* scales,

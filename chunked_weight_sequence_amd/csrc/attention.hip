@@ -46,20 +46,26 @@ struct PackedDev {
   int tiles, splits;
   int half;     // pieces of work from here on are taken from the other end (packed_plan)
   bool longest;  // sequences in the order of their keys (packed_plan)
+  // paged: K and V are caches [n_pages << psh][Hkv][DH], a sequence has lengths[s] keys
+  const int *table, *lengths;
+  int max_pages, psh, n_pages;
   float* part;  // splits > 1: [splits][Nq * Hq][dh] means, then [splits][Nq * Hq] (m, l)
 };
 
 // The w-th piece of work: a sequence's offsets (clamped to the buffers) and which of its row tiles, its
 // last one first.
 struct Work {
-  int q0, q1, k0, k1, r;  // r < 0: there is no such tile
+  int q0, q1, k0, k1, r;  // r < 0: there is no such tile; paged: k0 is 0
+  int s;                  // paged: the sequence
 };
+template <bool PAGED>
 __device__ __forceinline__ Work ap_find(const PackedDev& a, int w, int BM, int lane) {
   // of sequences one after the other: s owns the ids [base(s), base(s + 1)), at least as many as it has
   // tiles
   const auto base = [&](int cu, int s) { return int(uint32_t(cu) * uint32_t(a.G) / uint32_t(BM)) + s; };
   const auto clampq = [&](int s) { return min(max(a.cu_q[s], 0), a.Nq); };
   const auto clampk = [&](int s) { return min(max(a.cu_k[s], 0), a.Nk); };
+  const auto cached = [&](int s) { return min(max(a.lengths[s], 0), a.max_pages << a.psh); };
   const int tile = a.tiles - 1 - w;
   Work p;
   p.r = -1;
@@ -70,17 +76,17 @@ __device__ __forceinline__ Work ap_find(const PackedDev& a, int w, int BM, int l
   if (a.n_seq == 1) {
     p.q0 = clampq(0);
     p.q1 = clampq(1);
-    p.k0 = clampk(0);
-    p.k1 = clampk(1);
+    p.k0 = PAGED ? 0 : clampk(0);
+    p.k1 = PAGED ? cached(0) : clampk(1);
     p.r = tiles(p.q1 - p.q0) - 1 - w;
   } else if (a.n_seq < 64) {  // one load for everything: lane s has sequence s
     const int s = min(lane, a.n_seq);
-    const int cq = clampq(s), ck = clampk(s);
+    const int cq = clampq(s), ck = PAGED ? cached(min(lane, a.n_seq - 1)) : clampk(s);
     if (a.longest) {
       // the sequence with most keys first, so that what starts last is short (otherwise the last one first)
       const int cq1 = __builtin_amdgcn_update_dpp(0, cq, 0x130, 0xF, 0xF, true);  // of the lane above
       const int ck1 = __builtin_amdgcn_update_dpp(0, ck, 0x130, 0xF, 0xF, true);
-      const int lk = max(ck1 - ck, 0);
+      const int lk = PAGED ? ck : max(ck1 - ck, 0);
       const int n = tiles(cq1 - cq);
       int before = 0;  // row tiles of the sequences that come first
       for (int j = 0; j < a.n_seq; ++j) {
@@ -99,8 +105,8 @@ __device__ __forceinline__ Work ap_find(const PackedDev& a, int w, int BM, int l
     }
     p.q0 = __builtin_amdgcn_readlane(cq, at);
     p.q1 = __builtin_amdgcn_readlane(cq, at + 1);
-    p.k0 = __builtin_amdgcn_readlane(ck, at);
-    p.k1 = __builtin_amdgcn_readlane(ck, at + 1);
+    p.k0 = PAGED ? 0 : __builtin_amdgcn_readlane(ck, at);
+    p.k1 = __builtin_amdgcn_readlane(ck, PAGED ? at : at + 1);
   } else {  // 64-way search
     int lo = 0, len = a.n_seq;
     bool some = true;
@@ -117,12 +123,13 @@ __device__ __forceinline__ Work ap_find(const PackedDev& a, int w, int BM, int l
     at = __builtin_amdgcn_readfirstlane(at);
     p.q0 = clampq(at);
     p.q1 = clampq(at + 1);
-    p.k0 = clampk(at);
-    p.k1 = clampk(at + 1);
+    p.k0 = PAGED ? 0 : clampk(at);
+    p.k1 = PAGED ? cached(at) : clampk(at + 1);
     if (some) p.r = tile - base(p.q0, at);
   }
   p.q1 = max(p.q1, p.q0);
   p.k1 = max(p.k1, p.k0);
+  p.s = at;
   return p;
 }
 
@@ -225,10 +232,12 @@ struct ApPlan {
 // time: K straight into registers, V by way of its own 32 rows of LDS. 16384 tokens of 32/8 heads of 128
 // take 1.7 .. 2.3 ms; with one infinity in the last token 2.9 ms, in the first, which every row of a head sees,
 // 9.6 ms, with nothing but NaN in V 44 ms.
-template <int DH, int KS>
+// row(j): the row of key j; there(j): whether the 16 keys j .. exist (j a multiple of 16).
+template <int DH, int KS, class Row, class There>
 __device__ __forceinline__ f32x16 ap_again(int d, const bf16x8 (&qf)[KS], const char* tile,
-                                           const uint16_t* K, long ks, const uint16_t* V, long vs, int j0,
-                                           int j1, int lo, int hi, float c, float base, float inv, int lane) {
+                                           const uint16_t* K, long ks, const uint16_t* V, long vs, Row row,
+                                           There there, int j0, int j1, int lo, int hi, float c, float base,
+                                           float inv, int lane) {
   constexpr int RPI = 1024 / (DH * 2);
   asm volatile("" : "+v"(lane));  // nothing of this is worked out before
   const char* const place = tile + FragOff<DH>::channels(lane, d);
@@ -242,9 +251,10 @@ __device__ __forceinline__ f32x16 ap_again(int d, const bf16x8 (&qf)[KS], const 
 #pragma unroll 1
     for (int i = 0; i < 32 / RPI; ++i) {
       const int r = i * RPI + lane / (64 / RPI), ch = (lane % (64 / RPI)) ^ vsw<DH>(r);
-      dma16_far(V + min(j + r, j1 - 1) * vs + 8 * ch, __builtin_amdgcn_readfirstlane(lds + i * 1024));
+      dma16_far(V + row(min(j + r, j1 - 1)) * vs + 8 * ch, __builtin_amdgcn_readfirstlane(lds + i * 1024));
     }
-    const uint16_t* kp = K + min(j + (lane & 31), j1 - 1) * ks + 8 * h;
+    const uint16_t* kp = K + row(min(j + (lane & 31), j1 - 1)) * ks + 8 * h;
+    const bool good[2] = {there(j), there(min(j + 16, j1 - 1) & ~15)};
     f32x16 s;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
@@ -261,7 +271,7 @@ __device__ __forceinline__ f32x16 ap_again(int d, const bf16x8 (&qf)[KS], const 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int key = j + 8 * (i / 4) + 4 * h + (i & 3) + e;
-        const bool in = key >= lo && key <= hi && key < j1;
+        const bool in = key >= lo && key <= hi && key < j1 && good[i / 8];
         p[e] = in ? exp2_fast(fmaf(s[i + e], c, -base) - headroom(inv)) : 0.f;
         seen |= uint32_t(in) << (i + e);
       }
@@ -318,7 +328,12 @@ __device__ __forceinline__ f32x16 ap_again(int d, const bf16x8 (&qf)[KS], const 
   return o;
 }
 
-template <int DH, int QT>
+// The page table through the scalar cache: a vector load would count with the copies in flight.
+typedef const __attribute__((address_space(4))) int const_int;
+
+// PAGED: the keys and values of a sequence lie in pages of a cache. The 16 rows of a tile that a wave copies are
+// in one page, since pages hold 2^psh >= 16 tokens: what differs is where a copy's base comes from.
+template <int DH, int QT, bool PAGED>
 __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(PackedDev a) {
   constexpr int BM = 128 * QT, TILE = AP_BN * DH * 2, KS = DH / 16, DT = DH / 32;
   // [stage][K / V]; then, with 256 rows, one region per wave that holds its queries at the start and its
@@ -333,7 +348,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   const int split = rest % a.splits;
   const int turn = rest / a.splits;
 
-  const Work wk = ap_find(a, turn < a.half ? turn : a.tiles - 1 - (turn - a.half), BM, lane);
+  const Work wk = ap_find<PAGED>(a, turn < a.half ? turn : a.tiles - 1 - (turn - a.half), BM, lane);
   if (wk.r < 0) return;
   const int q0 = wk.q0, k0 = wk.k0, G = a.G;
   const int rows = (wk.q1 - q0) * G, lk = wk.k1 - k0, off = lk - (wk.q1 - q0);
@@ -385,23 +400,57 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   uint32_t koff[NI], voff[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int r = crow + i * RPI;
-    koff[i] = r * kstep + ((cp ^ ksw<DH>(r)) << 4) + (BACK - 1024 * i);
-    voff[i] = r * vstep + ((cp ^ vsw<DH>(r)) << 4) + (BACK - 1024 * i);
+    const int r = crow + i * RPI, from = PAGED ? r - wave * (AP_BN / 4) : r;
+    koff[i] = from * kstep + ((cp ^ ksw<DH>(r)) << 4) + (BACK - 1024 * i);
+    voff[i] = from * vstep + ((cp ^ vsw<DH>(r)) << 4) + (BACK - 1024 * i);
   }
   const int tlast = t1 - 1, over = (tlast + 1) * AP_BN - lk;  // rows of the last tile that are not there
   auto cut = [&](uint32_t (&off)[NI], uint32_t step) AP_INLINE {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const uint32_t d = uint32_t(max(crow + i * RPI - (AP_BN - 1 - over), 0)) * step;
+      // PAGED: the wave's rows are counted from the 16 that hold the sequence's last key, if they lie behind it
+      const int r = crow + i * RPI - wave * (AP_BN / 4), g = tlast * AP_BN + wave * (AP_BN / 4);
+      const uint32_t d = PAGED ? uint32_t(r - (min(g + r, lk - 1) - min(g, (lk - 1) & ~15))) * step
+                               : uint32_t(max(crow + i * RPI - (AP_BN - 1 - over), 0)) * step;
       asm volatile("v_sub_u32 %0, %0, %1" : "+v"(off[i]) : "v"(d));
     }
   };
   const uint32_t lds0 = lds + wave * (TILE / 4);
   // the next tiles to copy; K stays at the last one, which is then copied again and not read
-  const char* kp = reinterpret_cast<const char*>(a.K + (long(k0) + t0 * AP_BN) * a.ks + kvh * DH) - BACK;
-  const char* vp = reinterpret_cast<const char*>(a.V + (long(k0) + t0 * AP_BN) * a.vs + kvh * DH) - BACK;
+  const char* kp = reinterpret_cast<const char*>(a.K + (PAGED ? 0 : (long(k0) + t0 * AP_BN) * a.ks) + kvh * DH) - BACK;
+  const char* vp = reinterpret_cast<const char*>(a.V + (PAGED ? 0 : (long(k0) + t0 * AP_BN) * a.vs) + kvh * DH) - BACK;
   const size_t ktile = size_t(AP_BN) * kstep, vtile = size_t(AP_BN) * vstep;
+  // PAGED: the pages of a tile's four groups of 16 keys, and from them the wave's base and which groups exist.
+  // What a group that does not exist is copied from, the first page, is masked.
+  const char *const kc = kp, *const vc = vp;
+  const_int* const table =
+      (const_int*)(reinterpret_cast<uintptr_t>(a.table) + size_t(PAGED ? wk.s : 0) * a.max_pages * 4);
+  struct Pages {
+    int p[4], t;
+  };
+  const auto pages = [&](int t) AP_INLINE {
+    Pages x;
+    x.t = min(t, t1 - 1);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      x.p[g] = table[__builtin_amdgcn_readfirstlane(min(x.t * AP_BN + 16 * g, (lk - 1) & ~15) >> a.psh)];
+    return x;
+  };
+  const auto exists = [&](int page) AP_INLINE { return uint32_t(page) < uint32_t(a.n_pages); };
+  const auto groups = [&](const Pages& x) AP_INLINE {  // bit g: group g exists
+    int good = 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) good |= int(exists(x.p[g])) << g;
+    return good;
+  };
+  const auto first_row = [&](const Pages& x) AP_INLINE {  // of the wave's group
+    const int page = wave == 0 ? x.p[0] : wave == 1 ? x.p[1] : wave == 2 ? x.p[2] : x.p[3];
+    const int j = min(x.t * AP_BN + wave * (AP_BN / 4), (lk - 1) & ~15) & ((1 << a.psh) - 1);
+    return (long(exists(page) ? page : 0) << a.psh) + j;
+  };
+  Pages ahead = {};      // of the tile after the one whose K is copied next
+  long krow = 0;         // the wave's first row of that tile
+  int good0 = 15, good1 = 15;  // groups that exist of the tile whose scores come next, and of the one after it
   auto copy_k = [&](auto i, int buf) AP_INLINE {
     constexpr int I = decltype(i)::value;
     dma16_at<I>(koff[I], kp, lds0 + buf * 2 * TILE);
@@ -447,8 +496,18 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   };
   auto mask = [&](int t, f32x16 (&s)[2][QT], float (&mx)[QT]) AP_INLINE {
     const int kv0 = t * AP_BN;
-    const bool after = kv0 + AP_BN - 1 > hi_min, before = kv0 < lo_max;
-    if (after || before) {
+    const bool after = kv0 + AP_BN - 1 > hi_min, before = kv0 < lo_max, holes = PAGED && good0 != 15;
+    if (after || before || holes) {
+      if (holes) {
+#pragma unroll
+        for (int b = 0; b < QT; ++b)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x = s[e >> 4][b][e & 15];
+            ap_hide_before(x, 0, good0 >> (2 * (e >> 4) + (e & 15) / 8) & 1 ? 0 : 1);
+            s[e >> 4][b][e & 15] = x;
+          }
+      }
       if (after) {
 #pragma unroll
         for (int b = 0; b < QT; ++b)
@@ -507,6 +566,16 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
       cut(koff, kstep);
       cut(voff, vstep);
     }
+    if (PAGED) {
+      const Pages x = pages(t0), y = pages(t0 + 1);
+      ahead = pages(t0 + 2);
+      good0 = groups(x);
+      good1 = groups(y);
+      const long row = first_row(x);
+      krow = first_row(y);
+      kp = kc + row * kstep;
+      vp = vc + row * vstep;
+    }
     each([&](auto i) AP_INLINE { copy_k(i, 0); });
     const uint16_t* Qh = a.Q + long(q0 + qa) * a.qs + long(kvh) * G * DH;
     const uint32_t qdst = lds + uint32_t(mine - smem);
@@ -518,7 +587,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
     }
     each([&](auto i) AP_INLINE { copy_v(i, 0); });
     if (OWN && t0 < tlast) {
-      kp += ktile;
+      kp = PAGED ? kc + krow * kstep : kp + ktile;
       if (t0 + 1 == tlast) cut(koff, kstep);
       each([&](auto i) AP_INLINE { copy_k(i, 1); });
       wait_vm<2 * NI>();
@@ -672,8 +741,17 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) AP_INLINE {
     constexpr int B = decltype(buf)::value;
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    vp += vtile;
-    if (t + 2 < t1) kp += ktile;
+    if (PAGED) {  // K of tile t + 2 (the last one again where there is none) and V of tile t + 1
+      vp = vc + krow * vstep;
+      krow = first_row(ahead);
+      kp = kc + krow * kstep;
+      good0 = good1;
+      good1 = groups(ahead);
+      ahead = pages(t + 3);
+    } else {
+      vp += vtile;
+      if (t + 2 < t1) kp += ktile;
+    }
     if (t + 2 >= tlast) {
       if (t + 2 == tlast) cut(koff, kstep);
       if (t + 1 == tlast) cut(voff, vstep);
@@ -686,7 +764,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
     // every wave's part of the first K tile is there, every wave has its queries
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (!OWN && t0 < tlast) {
-      kp += ktile;
+      kp = PAGED ? kc + krow * kstep : kp + ktile;
       if (t0 + 1 == tlast) cut(koff, kstep);
       each([&](auto i) AP_INLINE { copy_k(i, 1); });
     }
@@ -737,9 +815,17 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
         for (int i = 0; i < 16; ++i) odd = odd || !(fabsf(o[d][b][i]) < INFINITY);
         float f = inv;
         if (__any(odd && lt == lt)) {
+          const auto row = [&](int j) AP_INLINE {
+            if (!PAGED) return long(j);
+            const int page = a.table[size_t(wk.s) * a.max_pages + (j >> a.psh)];
+            return (long(exists(page) ? page : 0) << a.psh) + (j & ((1 << a.psh) - 1));
+          };
+          const auto there = [&](int j) AP_INLINE {
+            return !PAGED || exists(a.table[size_t(wk.s) * a.max_pages + (j >> a.psh)]);
+          };
           o[d][b] = ap_again<DH>(d, qf[b], out + 32 * b * DH * 2, a.K + long(k0) * a.ks + kvh * DH, a.ks,
-                                 a.V + long(k0) * a.vs + kvh * DH, a.vs, t0 * AP_BN, min(t1 * AP_BN, lk),
-                                 lo[b], hi[b], c, base[b], inv, ln);
+                                 a.V + long(k0) * a.vs + kvh * DH, a.vs, row, there, t0 * AP_BN,
+                                 min(t1 * AP_BN, lk), lo[b], hi[b], c, base[b], inv, ln);
           f *= exp2_fast(headroom(inv));
         }
 #pragma unroll
@@ -794,24 +880,50 @@ size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, in
   return packed_workspace(n_seq, Nq, Nk, Hq, Hkv, dh);
 }
 
-hipError_t attention_packed(const PackedArgs& a) {
-  const PackedPlan p = packed_plan(a.n_seq, a.Nq, a.Nk, a.Hq, a.Hkv, a.dh, a.window);
-  const PackedDev d{static_cast<const uint16_t*>(a.Q), static_cast<const uint16_t*>(a.K),
-                    static_cast<const uint16_t*>(a.V), a.qs, a.ks, a.vs,
-                    static_cast<uint16_t*>(a.O), a.os, a.lse, a.cu_q, a.cu_k, a.n_seq, a.Nq, a.Nk,
-                    a.Hq, a.Hkv, a.Hq / a.Hkv, a.scale, a.window, p.tiles, p.splits, p.half, p.longest,
-                    static_cast<float*>(a.ws)};
+namespace {
+
+template <bool PAGED>
+hipError_t ap_launch(const PackedArgs& a, const PackedPlan& p, const PackedDev& d) {
   const dim3 grid(unsigned(p.tiles) * a.Hkv * p.splits);
   if (p.qt == 2)
-    hipLaunchKernelGGL((k_attention_packed<128, 2>), grid, dim3(256), 0, a.stream, d);
+    hipLaunchKernelGGL((k_attention_packed<128, 2, PAGED>), grid, dim3(256), 0, a.stream, d);
   else if (a.dh == 128)
-    hipLaunchKernelGGL((k_attention_packed<128, 1>), grid, dim3(256), 0, a.stream, d);
+    hipLaunchKernelGGL((k_attention_packed<128, 1, PAGED>), grid, dim3(256), 0, a.stream, d);
   else
-    hipLaunchKernelGGL((k_attention_packed<64, 1>), grid, dim3(256), 0, a.stream, d);
+    hipLaunchKernelGGL((k_attention_packed<64, 1, PAGED>), grid, dim3(256), 0, a.stream, d);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   return attention_join(d.part, p.splits, a.cu_q, a.n_seq, long(a.Nq) * a.Hq, a.Hq, a.Hkv, a.dh, a.O, a.os,
                         a.lse, a.scale, a.stream);
+}
+
+PackedDev ap_device(const PackedArgs& a, const PackedPlan& p) {
+  return {static_cast<const uint16_t*>(a.Q), static_cast<const uint16_t*>(a.K), static_cast<const uint16_t*>(a.V),
+          a.qs, a.ks, a.vs, static_cast<uint16_t*>(a.O), a.os, a.lse, a.cu_q, a.cu_k, a.n_seq, a.Nq, a.Nk, a.Hq,
+          a.Hkv, a.Hq / a.Hkv, a.scale, a.window, p.tiles, p.splits, p.half, p.longest, nullptr, nullptr, 0, 0, 0,
+          static_cast<float*>(a.ws)};
+}
+
+}  // namespace
+
+hipError_t attention_packed(const PackedArgs& a) {
+  const PackedPlan p = packed_plan(a.n_seq, a.Nq, a.Nk, a.Hq, a.Hkv, a.dh, a.window);
+  return ap_launch<false>(a, p, ap_device(a, p));
+}
+
+size_t attention_paged_workspace(int n_seq, int Nq, int max_pages, int page, int Hq, int Hkv, int dh) {
+  return packed_workspace(n_seq, Nq, paged_keys(n_seq, max_pages, page), Hq, Hkv, dh);
+}
+
+hipError_t attention_paged(const PackedArgs& a, const Paged& g) {
+  const PackedPlan p = packed_plan(a.n_seq, a.Nq, paged_keys(a.n_seq, g.max_pages, g.page), a.Hq, a.Hkv, a.dh, a.window);
+  PackedDev d = ap_device(a, p);
+  d.table = g.table;
+  d.lengths = g.lengths;
+  d.max_pages = g.max_pages;
+  d.psh = __builtin_ctz(unsigned(g.page));
+  d.n_pages = g.n_pages;
+  return ap_launch<true>(a, p, d);
 }
 
 }  // namespace ttt

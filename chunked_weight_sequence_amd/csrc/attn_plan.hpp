@@ -13,12 +13,12 @@ struct PackedPlan {
   bool longest;
 };
 // Keys that an average row sees.
-inline long packed_seen(int n_seq, int Nq, int Nk, int window) {
+inline long packed_seen(int n_seq, int Nq, long Nk, int window) {
   const long seen = (Nk > Nq / 2 ? Nk - Nq / 2 : Nk) / n_seq;
   return window > 0 && window < seen ? window : seen;
 }
 // Keys that the last row sees.
-inline long packed_keys(int n_seq, int Nk, int window) {
+inline long packed_keys(int n_seq, long Nk, int window) {
   const long keys = Nk / n_seq;
   return window > 0 && window < keys ? window : keys;
 }
@@ -33,7 +33,7 @@ inline long packed_wgs(int qt, int n_seq, int Nq, int Hq, int Hkv) {
 // Measured, 32/8 heads of 128: 512 tokens after 15872, 323 us whole, 125 us in 4; 64 tokens after 16000,
 // 35 us in 32 pieces, 31 us in 16; 1024 tokens 20 us whole, 35 us in 2; 2048 tokens of 8/4 heads of 64
 // 24 us whole, 28 us in 2.
-inline int packed_splits(int qt, int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
+inline int packed_splits(int qt, int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh, int window) {
   const long keys = packed_keys(n_seq, Nk, window);
   // a compute unit each, where a workgroup counts for as much as an average row has of the longest
   const long seen = packed_seen(n_seq, Nq, Nk, window);
@@ -50,7 +50,7 @@ inline int packed_splits(int qt, int n_seq, int Nq, int Nk, int Hq, int Hkv, int
   }
   return best;
 }
-inline PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh, int window) {
+inline PackedPlan packed_plan(int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh, int window) {
   // 256 rows share each tile read from LDS, which costs least power (long rows are bound by that), but
   // leave the chip's 256 places unevenly filled and nothing to run while a workgroup starts and ends
   // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least 9
@@ -90,7 +90,11 @@ inline PackedPlan packed_plan(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh
   return p;
 }
 
-inline size_t packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh) {
+// The keys that a plan for a paged cache is made for: as many as the page tables can hold, since only the
+// device knows the lengths.
+inline long paged_keys(int n_seq, int max_pages, int page) { return long(n_seq) * max_pages * page; }
+
+inline size_t packed_workspace(int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh) {
   // the window is not known here; with one there are no more pieces than without
   const int a = packed_splits(1, n_seq, Nq, Nk, Hq, Hkv, dh, 0);
   const int b = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, 0);

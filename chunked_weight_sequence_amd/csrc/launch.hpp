@@ -238,6 +238,15 @@ struct PackedArgs {
 size_t attention_packed_workspace(int n_seq, int Nq, int Nk, int Hq, int Hkv, int dh);
 hipError_t attention_packed(const PackedArgs& a);
 
+// The same with the keys and values in pages of a cache: K and V of PackedArgs are the caches
+// [n_pages * page, Hkv, dh] (dense), cu_k and Nk are not used.
+struct Paged {
+  const int *table, *lengths;    // [n_seq, max_pages], [n_seq]
+  int max_pages, page, n_pages;
+};
+size_t attention_paged_workspace(int n_seq, int Nq, int max_pages, int page, int Hq, int Hkv, int dh);
+hipError_t attention_paged(const PackedArgs& a, const Paged& g);
+
 // Joins `splits` (<= 64) partial results of nrows = tokens * Hq rows: part holds each piece's
 // weighted mean of its values in fp32 [splits][nrows][dh], then (maximum logit, sum of the weights)
 // [splits][nrows][2] (decode.hip). With cu_q,

@@ -19,7 +19,7 @@
  * input Z) and ttt_cache_readout (the residual-cache readout); and the attention half of the
  * blocks whose MLP half the scan is: ttt_qk_norm_rope, ttt_attention_packed and
  * ttt_attention_decode. A serving loop that takes prompts in pieces has, beside these,
- * ttt_add_rms_norm between the halves and ttt_gated_delta_decode.
+ * ttt_attention_paged, ttt_add_rms_norm between the halves and ttt_gated_delta_decode.
  *
  * Conventions shared by every entry point:
  *   - Tensor pointers are DEVICE pointers owned by the caller; the library never allocates,
@@ -488,6 +488,23 @@ ttt_status ttt_attention_decode(const void* Q, long long q_stride, const void* K
                                 size_t workspace_bytes, hipStream_t stream);
 size_t ttt_attention_decode_workspace(int n_seq, int max_pages, int page_size, int Hq, int Hkv,
                                       int dh);
+
+/* Attention of new tokens over a paged cache that holds them already: a piece of a prompt, drafted tokens
+ * to be checked, or a batch of both with single tokens. Sequence s has the queries [cu_q[s], cu_q[s+1]), any
+ * number of them, and lengths[s] cached tokens, the queries' own among them: its last query stands at its last
+ * token. What a query sees, and the results, are those of ttt_attention_packed; where a token lies, and what
+ * lengths, pages and rows that are not seen may hold, is as for ttt_attention_decode.
+ *   Q  [Nq, Hq, dh], O [Nq, Hq, dh], lse [Nq, Hq] fp32 or NULL; cu_q as for ttt_attention_packed: rows before
+ *   cu_q[0] and from cu_q[n_seq] on are left as they were.
+ *   The limits are those of the two calls; the workspace as above. */
+ttt_status ttt_attention_paged(const void* Q, long long q_stride, const void* K_cache,
+                               const void* V_cache, ttt_dtype dtype, void* O, long long o_stride,
+                               float* lse, const int* cu_q, const int* page_table, int max_pages,
+                               int page_size, int n_pages, const int* lengths, int n_seq, int Nq, int Hq,
+                               int Hkv, int dh, float scale, int window, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+size_t ttt_attention_paged_workspace(int n_seq, int Nq, int max_pages, int page_size, int Hq, int Hkv,
+                                     int dh);
 
 /* ------------------------------------------------------------------------------------------ */
 /* RMS norm of a residual stream with the residual's addition, in one pass: for row n of D channels

@@ -1,5 +1,6 @@
-"""The residual stream's norm, in the input's type or in 8 bits, and the gated delta rule, fp64 oracle (test
-infrastructure only). Plain loops over tokens and heads, straight from the formulas.
+"""Attention of new tokens over a paged cache, the residual stream's norm, in the input's type or in 8 bits,
+and the gated delta rule, fp64 oracle (test infrastructure only). Plain loops over tokens and heads,
+straight from the formulas.
 
 The gated delta rule is the fast weight of TTT-Linear at a mini-batch of one token (TTT layers page: the
 delta rule) with a decay of the state before each token.
@@ -10,7 +11,31 @@ import math
 
 import numpy as np
 
+from .attention import attend
+
 f64 = np.float64
+
+
+def paged(Q, Kc, Vc, cu_q, table, lengths, page, scale, window=0, rows=None):
+    """Q [Nq, Hq, dh], caches [n_slots, Hkv, dh]: (O, lse, the sums of weight * |v|), of the queries `rows`
+    (None: all); other rows, and those of no sequence, are NaN. Tokens of a page that is not there are left
+    out."""
+    Q, Kc, Vc = (np.asarray(x, f64) for x in (Q, Kc, Vc))
+    Nq, Hq, dh = Q.shape
+    G, n_pages = Hq // Kc.shape[1], len(Kc) // page
+    O, A, L = (np.full(s, np.nan) for s in ((Nq, Hq, dh), (Nq, Hq, dh), (Nq, Hq)))
+    for s in range(len(cu_q) - 1):
+        lq, n = cu_q[s + 1] - cu_q[s], min(max(int(lengths[s]), 0), table.shape[1] * page)
+        for i in range(lq):
+            t, last = cu_q[s] + i, i + n - lq
+            if rows is not None and t not in rows:
+                continue
+            first = max(0, last - window + 1) if window else 0
+            at = [int(table[s, j // page]) * page + j % page for j in range(first, last + 1)
+                  if 0 <= table[s, j // page] < n_pages]
+            for h in range(Hq):
+                O[t, h], L[t, h], A[t, h] = attend(Q[t, h], Kc[at, h // G], Vc[at, h // G], scale)
+    return O, L, A
 
 
 def e4m3_values():

@@ -5,6 +5,7 @@ import math
 import numpy as np
 import pytest
 
+import oracle.attention as oa
 import oracle.serving as osv
 import oracle.ttt_linear as ol
 
@@ -14,6 +15,31 @@ def test_e4m3_codes():
     assert v[0] == 0 and v[1] == 2.0 ** -9 and v[7] == 7 * 2.0 ** -9 and v[8] == 2.0 ** -6
     assert v[0x38] == 1 and v[0x3C] == 1.5 and v[0x7E] == 448 and math.isnan(v[0x7F]) and v[0xFE] == -448
     assert (np.diff(v[:0x7F]) > 0).all()
+
+
+def test_paged_is_packed_on_gathered_keys_and_decode_on_single_tokens():
+    r = np.random.default_rng(2)
+    page, Hq, Hkv, dh = 4, 4, 2, 6
+    Kc, Vc = r.standard_normal((2, 8 * page, Hkv, dh))
+    table, lens, new = np.array([[5, 1, 7], [0, 3, 2]]), [11, 6], [4, 6]
+    Q, cu = r.standard_normal((10, Hq, dh)), [0, 4, 10]
+    rows = [[t * page + i for t in table[s] for i in range(page)][:lens[s]] for s in range(2)]
+    cat = rows[0] + rows[1]
+    for window in (0, 3):
+        got = osv.paged(Q, Kc, Vc, cu, table, lens, page, 0.4, window)
+        want = oa.packed(Q, Kc[cat], Vc[cat], cu, [0, 11, 17], 0.4, window)
+        for a, b in zip(got, want):
+            np.testing.assert_allclose(a, b)
+        one = osv.paged(Q[:2], Kc, Vc, [0, 1, 2], table, lens, page, 0.4, window)
+        for a, b in zip(one, oa.decode(Q[:2], Kc, Vc, table, lens, page, 0.4, window)):
+            np.testing.assert_allclose(a, b if a.ndim == b.ndim else b)
+    hole = table.copy()
+    hole[0, 1] = 99  # left out: the other keys' weights, of the same logits
+    o, lse, _ = osv.paged(Q, Kc, Vc, cu, hole, lens, page, 0.4)
+    keep = rows[0][:4] + rows[0][8:11]
+    w = np.exp(0.4 * Kc[keep, 0] @ Q[3, 1])
+    np.testing.assert_allclose(o[3, 1], w @ Vc[keep, 0] / w.sum())
+    np.testing.assert_allclose(lse[3, 1], np.log(w.sum()))
 
 
 def test_norm_closed_forms():

@@ -1,5 +1,5 @@
-"""ttt_add_rms_norm and ttt_gated_delta_decode refuse bad arguments on the host, before anything is enqueued
-(no GPU: every call below fails validation)."""
+"""ttt_attention_paged, ttt_add_rms_norm and ttt_gated_delta_decode refuse bad arguments on the host, before anything is enqueued
+(no GPU: every call below fails validation), and report their workspaces."""
 import pytest
 
 import chunked_weight_sequence_amd as ttt
@@ -70,3 +70,46 @@ DELTA = [
     (dict(sl=None, n=63), E_SHAPE), (dict(S=1 << 20, Hk=8, Hv=8), E_SHAPE)])
 def test_step_rejects_bad_arguments(kw, code):
     assert step(**kw) == code
+
+
+def paged(**kw):
+    a = dict(Q=A, qs=None, Kc=A + 64 * MB, Vc=A + 96 * MB, dt=BF16, O=A + 128 * MB, os=None, lse=A + 192 * MB,
+             cu=A + 200 * MB, tab=A + 208 * MB, mp=64, page=16, np=512, lens=A + 216 * MB, n=8, Nq=300, Hq=16, Hkv=4,
+             dh=64, scale=0.1, window=0, ws=A + 512 * MB, wsb=None)
+    a.update(kw)
+    for k in ("qs", "os"):
+        a[k] = a["Hq"] * a["dh"] if a[k] is None else a[k]
+    need = ttt.lib().ttt_attention_paged_workspace(a["n"], a["Nq"], a["mp"], a["page"], a["Hq"], a["Hkv"], a["dh"])
+    a["wsb"] = need if a["wsb"] is None else a["wsb"]
+    return ttt.lib().ttt_attention_paged(
+        a["Q"], a["qs"], a["Kc"], a["Vc"], a["dt"], a["O"], a["os"], a["lse"], a["cu"], a["tab"], a["mp"], a["page"],
+        a["np"], a["lens"], a["n"], a["Nq"], a["Hq"], a["Hkv"], a["dh"], a["scale"], a["window"], a["ws"], a["wsb"],
+        None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=2), E_DTYPE), (dict(dt=F32), E_UNSUP), (dict(Q=None), E_NULL), (dict(Kc=None), E_NULL),
+    (dict(Vc=None), E_NULL), (dict(O=None), E_NULL), (dict(cu=None), E_NULL), (dict(tab=None), E_NULL),
+    (dict(lens=None), E_NULL), (dict(n=0), E_SHAPE), (dict(n=(1 << 20) + 1), E_SHAPE), (dict(Nq=0), E_SHAPE),
+    (dict(Nq=(1 << 26) + 1), E_SHAPE), (dict(Hq=15), E_SHAPE), (dict(Hkv=0), E_SHAPE), (dict(mp=0), E_SHAPE),
+    (dict(mp=1 << 27), E_SHAPE), (dict(np=0), E_SHAPE), (dict(np=1 << 30, page=128), E_SHAPE),
+    (dict(window=-1), E_SHAPE), (dict(window=(1 << 30) + 1), E_SHAPE), (dict(scale=0.0), E_SHAPE),
+    (dict(scale=INF), E_SHAPE), (dict(Nq=1 << 26, Hq=32, Hkv=4), E_SHAPE), (dict(dh=96), E_UNSUP),
+    (dict(page=24), E_UNSUP), (dict(page=8), E_UNSUP), (dict(page=1 << 17), E_UNSUP), (dict(qs=1016), E_SHAPE),
+    (dict(os=1028), E_SHAPE), (dict(Q=A + 2), E_ALIGN), (dict(tab=A + 208 * MB + 4), E_ALIGN),
+    (dict(O=A), E_ALIAS), (dict(O=A + 64 * MB), E_ALIAS), (dict(lse=A + 128 * MB), E_ALIAS),
+    (dict(lse=A + 216 * MB), E_ALIAS), (dict(O=A + 96 * MB + 1024), E_ALIAS),
+])
+def test_paged_rejects_bad_arguments(kw, code):
+    assert paged(**kw) == code
+
+
+def test_paged_workspace():
+    L = ttt.lib().ttt_attention_paged_workspace
+    assert L(0, 16, 4, 16, 8, 8, 64) == 0 and L(1, 16, 4, 24, 8, 8, 64) == 0 and L(1, 16, 4, 16, 8, 8, 96) == 0
+    assert L(1, 32768, 512, 64, 32, 8, 128) == 0      # row tiles enough
+    need = L(1, 64, 512, 64, 32, 8, 128)              # few rows, many keys: partial results of each piece
+    assert need > 0 and need % (64 * 32 * 130 * 4) == 0
+    big = dict(n=1, Nq=64, mp=512, page=64, Hq=32, Hkv=8, dh=128)
+    assert paged(**big, wsb=need - 1) == E_WS and paged(**big, ws=None) == E_WS
+    assert paged(**big, ws=A) == E_ALIAS
