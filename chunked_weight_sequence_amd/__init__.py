@@ -24,6 +24,7 @@ or prompts in pieces, mixed with single tokens, over the same cache:
 Between the halves, and fast weights that forget:
 
     y, _, x = add_rms_norm(O, weight, residual=x)
+    O, states = gated_delta_packed(Q, K, V, g, beta, cu_seqlens, state=states, slots=slots)
     O, states = gated_delta_decode(Q, K, V, g, beta, states, slots=slots)
 """
 from __future__ import annotations
@@ -39,7 +40,7 @@ __all__ = [
     "linear_minibatch", "surprisal_route", "lm_target", "gated_z", "cache_readout", "chunk_scan_docs",
     "chunk_scan_handover_timeouts", "scan_test_overrides", "chunk_scan_noalloc",
     "rope_frequencies", "qk_norm_rope", "attention_packed", "attention_decode",
-    "attention_paged", "add_rms_norm", "gated_delta_decode", "EXPORTED",
+    "attention_paged", "add_rms_norm", "gated_delta_packed", "gated_delta_decode", "EXPORTED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -88,6 +89,9 @@ EXPORTED = {
     "ttt_add_rms_norm": (_i, [_p, _ll, _p, _ll, _i, _p, _f, _p, _ll, _p, _ll, _p, _i, _i, _i, _p]),
     "ttt_gated_delta_decode": (_i, [_p, _ll, _p, _ll, _p, _ll, _i, _p, _p, _p, _ll, _p, _p, _p, _ll,
                                     _i, _i, _i, _i, _i, _f, _i, _f, _p]),
+    "ttt_gated_delta_packed": (_i, [_p, _ll, _p, _ll, _p, _ll, _i, _p, _p, _p, _ll, _p, _p, _p, _ll, _p,
+                                    _i, _i, _i, _i, _i, _i, _f, _i, _f, _p, _sz, _p]),
+    "ttt_gated_delta_packed_workspace": (_sz, [_i, _i, _i, _i, _i, _i]),
     "ttt_status_string": (ctypes.c_char_p, [_i]),
     "ttt_abi_version": (_i, []),
 }
@@ -873,6 +877,40 @@ def _delta_states(state, state_out, slots, n_seq, Hv, dk, dv, device):
     elif n_slots is not None and n_slots < n_seq:
         raise ValueError(f"{n_seq} sequences need as many states, got {n_slots}")
     return n_slots or 0
+
+
+def gated_delta_packed(Q, K, V, g, beta, cu, *, state=None, state_out=None, slots=None, scale=None,
+                       normalize: bool = True, norm_eps: float = 1e-6, final_state: bool = True, O=None,
+                       workspace=None):
+    """The gated delta rule (see gated_delta_decode) over packed sequences: Q, K [N,Hk,dk], V [N,Hv,dv] bf16,
+    g and beta [N,Hv] fp32, the tokens of sequence s from cu[s] to cu[s+1] (cu [n_seq + 1] int32 on the GPU; may
+    be empty). Sequences start from their slots of state [n_slots,Hv,dk,dv] fp32 (None: from zero) and leave
+    their last states in state_out: in state itself if that is None, in a new [n_seq,Hv,dk,dv] if there is
+    neither, nowhere with final_state=False. Returns (O [N,Hv,dv], state_out or None)."""
+    torch = _torch()
+    O, args, N, Hk, Hv, dk, dv = _delta_inputs(Q, K, V, g, beta, O)
+    dev = Q.device
+    if cu.dim() != 1:
+        raise ValueError(f"cu must be [n_seq + 1], got {tuple(cu.shape)}")
+    n_seq = cu.shape[0] - 1
+    _vec(cu, "cu", (n_seq + 1,), torch.int32, dev)
+    if not final_state:
+        if state_out is not None:
+            raise ValueError("state_out is for a call with final_state")
+    elif state_out is None and state is not None:
+        state_out = state
+    elif state_out is None:
+        if slots is not None:
+            raise ValueError("slots needs state or state_out")
+        state_out = torch.empty((n_seq, Hv, dk, dv), dtype=torch.float32, device=dev)
+    n_slots = _delta_states(state, state_out, slots, n_seq, Hv, dk, dv, dev)
+    ws, ws_bytes = _workspace(workspace, _workspace_bytes(
+        "ttt_gated_delta_packed_workspace", n_seq, N, Hk, Hv, dk, dv), dev)
+    _launch(lib().ttt_gated_delta_packed,
+            args + (_ptr(state), _ptr(state_out), _ptr(slots), n_slots, cu.data_ptr(), n_seq, N, Hk, Hv, dk, dv,
+                    dk ** -0.5 if scale is None else scale, int(bool(normalize)), norm_eps, _ptr(ws), ws_bytes),
+            dev)
+    return O, state_out
 
 
 def gated_delta_decode(Q, K, V, g, beta, state, *, state_out=None, slots=None, scale=None,

@@ -22,7 +22,7 @@ ARCH = "gfx950"
 
 SOURCES = ["scan_simt.hip", "scan_mfma.hip", "linear.hip", "linear_b32.hip", "linear_chunk.hip",
            "route.hip", "target.hip", "gated_z.hip", "readout.hip", "clip.hip", "noalloc.hip",
-           "norm_rope.hip", "attention.hip", "decode.hip", "add_norm.hip", "delta_step.hip",
+           "norm_rope.hip", "attention.hip", "decode.hip", "add_norm.hip", "delta_step.hip", "delta_chunk.hip",
            "api.cpp"]
 # per-file options: routing decisions must round every operation on its own (no fused
 # multiply-add), and its latency-bound kernel schedules better for instruction-level parallelism
@@ -39,6 +39,7 @@ PER_FILE = {
     # the chunked kernel: same results under both schedulers; scheduled for instruction-level
     # parallelism it runs b = 16 about 3% faster (b = 64 the same)
     "linear_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form", "-mllvm", "-amdgpu-sched-strategy=max-ilp"],
+    "delta_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form", "-mllvm", "-amdgpu-sched-strategy=max-ilp"],
 }
 
 FLAGS = [

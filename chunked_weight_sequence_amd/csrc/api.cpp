@@ -983,6 +983,43 @@ TTT_EXPORT ttt_status ttt_gated_delta_decode(const void* Q, long long q_stride, 
   return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
 }
 
+namespace {
+bool delta_packed_ok(int n_seq, int N, int Hk, int Hv, int dk, int dv) {
+  return delta_shape_ok(N, n_seq, Hk, Hv, dk, dv) && N <= (1 << 26) &&
+         // a launch counts its threads in 32 bits: 256 per 64 tokens and head, 128 per 32 columns
+         ((long long)N / 64 + n_seq) * Hv < (1 << 24) && (long long)n_seq * Hv * dv < (1 << 28);
+}
+}  // namespace
+
+TTT_EXPORT size_t ttt_gated_delta_packed_workspace(int n_seq, int N, int Hk, int Hv, int dk, int dv) {
+  if (!delta_packed_ok(n_seq, N, Hk, Hv, dk, dv) || !delta_supported(dk, dv)) return 0;
+  return ttt::delta_packed_workspace(n_seq, N, Hv);
+}
+
+TTT_EXPORT ttt_status ttt_gated_delta_packed(const void* Q, long long q_stride, const void* K,
+                                             long long k_stride, const void* V, long long v_stride,
+                                             ttt_dtype dtype, const float* g, const float* beta, void* O,
+                                             long long o_stride, const float* state_in, float* state_out,
+                                             const int* slots, long long n_slots, const int* cu, int n_seq,
+                                             int N, int Hk, int Hv, int dk, int dv, float scale,
+                                             int normalize, float eps, void* workspace,
+                                             size_t workspace_bytes, hipStream_t stream) {
+  if (!valid_dtype(dtype)) return TTT_E_DTYPE;
+  if (!cu) return TTT_E_NULL;
+  if (!delta_packed_ok(n_seq, N, Hk, Hv, dk, dv)) return TTT_E_SHAPE;
+  const long long most = 1 << 23;  // 64 rows' offsets in 32 bits
+  if (q_stride > most || k_stride > most || v_stride > most || o_stride > most) return TTT_E_SHAPE;
+  const size_t need = delta_supported(dk, dv) ? ttt::delta_packed_workspace(n_seq, N, Hv) : 0;
+  const DeltaCall c{Q, K, V, q_stride, k_stride, v_stride, dtype, g, beta, O, o_stride, state_in, state_out,
+                    slots, n_slots, N, n_seq, Hk, Hv, dk, dv, scale, eps, 1ll << 62};
+  const ttt_status s = delta_check(c, whole(cu, size_t(n_seq + 1) * 4), whole(workspace, need));
+  if (s != TTT_OK) return s;
+  if (!workspace || workspace_bytes < need) return TTT_E_WORKSPACE;
+  (void)hipGetLastError();
+  const hipError_t e = ttt::delta_packed({delta_args(c, normalize, stream), cu, N, workspace});
+  return e == hipSuccess ? TTT_OK : TTT_E_LAUNCH;
+}
+
 TTT_EXPORT const char* ttt_status_string(ttt_status s) {
   switch (s) {
     case TTT_OK: return "TTT_OK: success";

@@ -310,4 +310,13 @@ struct DeltaArgs {
 };
 hipError_t delta_step(const DeltaArgs& a);  // one token per sequence
 
+struct DeltaPackedArgs {
+  DeltaArgs d;
+  const int* cu;                 // [n_seq + 1]
+  int N;
+  void* ws;
+};
+size_t delta_packed_workspace(int n_seq, int N, int Hv);
+hipError_t delta_packed(const DeltaPackedArgs& a);
+
 }  // namespace ttt

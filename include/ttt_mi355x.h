@@ -19,7 +19,8 @@
  * input Z) and ttt_cache_readout (the residual-cache readout); and the attention half of the
  * blocks whose MLP half the scan is: ttt_qk_norm_rope, ttt_attention_packed and
  * ttt_attention_decode. A serving loop that takes prompts in pieces has, beside these,
- * ttt_attention_paged, ttt_add_rms_norm between the halves and ttt_gated_delta_decode.
+ * ttt_attention_paged, ttt_add_rms_norm between the halves, ttt_gated_delta_packed and
+ * ttt_gated_delta_decode.
  *
  * Conventions shared by every entry point:
  *   - Tensor pointers are DEVICE pointers owned by the caller; the library never allocates,
@@ -558,6 +559,28 @@ ttt_status ttt_gated_delta_decode(const void* Q, long long q_stride, const void*
                                   float* state_out, const int* slots, long long n_slots, int n_seq,
                                   int Hk, int Hv, int dk, int dv, float scale, int normalize, float eps,
                                   hipStream_t stream);
+
+/* The same over packed sequences: sequence s has the tokens [cu[s], cu[s+1]) of N (cu [n_seq + 1] int32 on the
+ * device, clamped and read as cu_q of ttt_attention_packed; empty sequences are allowed: their state is handed
+ * on as it is). Q, K [N, Hk, dk], V, O [N, Hv, dv], g, beta [N, Hv]; rows of O before cu[0] and from cu[n_seq] on
+ * are left as they were. States and slots are those of ttt_gated_delta_decode, read before a sequence's first
+ * token and written after its last, so prompts can be taken in pieces.
+ * 64 tokens at a time, counted from the sequence's first: products on the matrix cores with fp32 accumulation,
+ * the state and what is added to it at fp32's precision (about 1e-6 of its size), O from bf16 roundings of both,
+ * rounded once. Gates are meant to be at most 0; below -1000 they count as -1000. What is not finite in a
+ * sequence stays in it, and reaches from its chunk of 64 tokens on, earlier tokens of that chunk among them.
+ *   strides in elements: at most 2^23; N <= 2^26; (N / 64 + n_seq) * Hv < 2^24 and n_seq * Hv * dv < 2^28;
+ *   the other limits as above.
+ *   workspace: at least ttt_gated_delta_packed_workspace(...) bytes (25 KB for each 64 tokens and value head);
+ *   contents on entry do not matter. Calls that overlap in time need one each. */
+ttt_status ttt_gated_delta_packed(const void* Q, long long q_stride, const void* K, long long k_stride,
+                                  const void* V, long long v_stride, ttt_dtype dtype, const float* g,
+                                  const float* beta, void* O, long long o_stride, const float* state_in,
+                                  float* state_out, const int* slots, long long n_slots, const int* cu,
+                                  int n_seq, int N, int Hk, int Hv, int dk, int dv, float scale,
+                                  int normalize, float eps, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+size_t ttt_gated_delta_packed_workspace(int n_seq, int N, int Hk, int Hv, int dk, int dv);
 
 /* ------------------------------------------------------------------------------------------ */
 const char* ttt_status_string(ttt_status s);  /* static string, never NULL */

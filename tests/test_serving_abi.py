@@ -1,4 +1,4 @@
-"""ttt_attention_paged, ttt_add_rms_norm and ttt_gated_delta_decode refuse bad arguments on the host, before anything is enqueued
+"""ttt_attention_paged, ttt_add_rms_norm, ttt_gated_delta_packed and ttt_gated_delta_decode refuse bad arguments on the host, before anything is enqueued
 (no GPU: every call below fails validation), and report their workspaces."""
 import pytest
 
@@ -70,6 +70,36 @@ DELTA = [
     (dict(sl=None, n=63), E_SHAPE), (dict(S=1 << 20, Hk=8, Hv=8), E_SHAPE)])
 def test_step_rejects_bad_arguments(kw, code):
     assert step(**kw) == code
+
+
+def delta(**kw):
+    a = dict(Q=A, qs=2048, K=A + 64 * MB, ks=2048, V=A + 128 * MB, vs=4096, dt=BF16, g=A + 192 * MB,
+             b=A + 193 * MB, O=A + 256 * MB, os=4096, si=A + 1024 * MB, so=A + 4096 * MB, sl=A + 320 * MB,
+             n=100, cu=A + 321 * MB, S=64, N=1000, Hk=16, Hv=32, dk=128, dv=128, scale=0.1, norm=1, eps=1e-6,
+             ws=A + 8192 * MB, wsb=None)
+    a.update(kw)
+    need = ttt.lib().ttt_gated_delta_packed_workspace(a["S"], a["N"], a["Hk"], a["Hv"], a["dk"], a["dv"])
+    a["wsb"] = need if a["wsb"] is None else a["wsb"]
+    return ttt.lib().ttt_gated_delta_packed(
+        a["Q"], a["qs"], a["K"], a["ks"], a["V"], a["vs"], a["dt"], a["g"], a["b"], a["O"], a["os"], a["si"],
+        a["so"], a["sl"], a["n"], a["cu"], a["S"], a["N"], a["Hk"], a["Hv"], a["dk"], a["dv"], a["scale"],
+        a["norm"], a["eps"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,code", DELTA + [
+    (dict(cu=None), E_NULL), (dict(N=0), E_SHAPE), (dict(N=(1 << 26) + 1), E_SHAPE), (dict(sl=None, n=63), E_SHAPE),
+    (dict(N=1 << 25), E_SHAPE), (dict(qs=(1 << 23) + 8), E_SHAPE), (dict(os=(1 << 23) + 8), E_SHAPE),
+    (dict(ws=None), E_WS), (dict(wsb=100), E_WS), (dict(cu=A + 321 * MB + 4), E_ALIGN), (dict(ws=A + 8192 * MB + 8), E_ALIGN),
+    (dict(cu=A + 256 * MB), E_ALIAS), (dict(ws=A), E_ALIAS), (dict(ws=A + 1024 * MB), E_ALIAS), (dict(ws=A + 256 * MB), E_ALIAS)])
+def test_packed_delta_rejects_bad_arguments(kw, code):
+    assert delta(**kw) == code
+
+
+def test_packed_delta_workspace():
+    W = ttt.lib().ttt_gated_delta_packed_workspace
+    assert W(0, 64, 1, 1, 64, 64) == 0 and W(1, 64, 1, 1, 96, 64) == 0 and W(1, 64, 1, 1, 64, 32) == 0
+    assert W(1, 64, 2, 2, 64, 64) == 2 * W(1, 64, 1, 1, 64, 64) > 0
+    assert W(1, 32768, 32, 32, 128, 128) <= 513 * 32 * 25600
 
 
 def paged(**kw):
