@@ -10,10 +10,10 @@
 //
 // Two launches. k_delta_prepare, one workgroup per chunk and head: T and A, and the factors of the rows.
 // k_delta_scan, one workgroup per sequence, head and some columns of the state: the recurrence over the
-// chunks. A wave keeps 16 NB columns of S in accumulators from the first chunk to the last and needs
-// nothing of the other waves, which only share the tiles in LDS: a product's result [rows, columns] has the lane
+// chunks. S stays in accumulators from the first chunk to the last: a product's result [rows, columns] has the lane
 // layout of the next product's operand [contraction, columns] if the 32 rows of a contraction are taken in the
-// order 16 (e / 4) + 4 (l / 16) + e % 4, e = 0..7, in both operands.
+// order 16 (e / 4) + 4 (l / 16) + e % 4, e = 0..7, in both operands. Rows of S are channels in such an order
+// (dl_channel) that K and Q need none: a lane's 8 channels lie side by side.
 //
 // Precision: what is not bf16 enters a product as a sum of bf16 planes, S as two, T, V - e^G K S and u as three
 // (of the nine products of planes of T and V - .., the six above 2^-24). One plane less for any of the three
@@ -69,22 +69,23 @@ __device__ __forceinline__ int dl_find(const DeltaPackedArgs& a, int id, int lan
   }
 }
 
-// Tiles of rows of W bf16 in LDS, in units of 32 bytes (16 channels); unit u of row r at slot u ^ turn(r), so that
-// 16 rows' reads of one unit, whole rows' worth of lanes, fall on all banks.
+// Tiles of rows of W bf16 in LDS, in pieces of 16 bytes; piece p of row r at slot p ^ turn(r). Reads of 8 bytes go by
+// 32 lanes: 16 rows of one piece each, or (transposed) 8 rows of two neighbouring ones; either way the turns put
+// them on all banks.
 template <int W>
 __device__ __forceinline__ int dl_turn(int r) {
-  return W >= 128 ? r & 7 : W == 64 ? (r >> 1) & 3 : (r >> 2) & 1;
+  return W == 128 ? (r & 7) << 1 | (r >> 3 & 1) : W == 64 ? (r >> 1 & 3) << 1 | (r >> 3 & 1) : 0;
 }
 template <int W>
-__device__ __forceinline__ int dl_at(int r, int unit) { return r * W * 2 + ((unit ^ dl_turn<W>(r)) << 5); }
+__device__ __forceinline__ int dl_at(int r, int piece) { return r * W * 2 + ((piece ^ dl_turn<W>(r)) << 4); }
 
 // The 1 KB number i of a 64-row tile: rows of a sequence from `src` on, `left` of which exist (the last one stands
 // for those behind it), by one wave.
 template <int W>
 __device__ __forceinline__ void dl_copy_rows(int i, const void* src, long stride, int left, uint32_t lds, int lane) {
-  constexpr int CH = W / 8, RPI = 64 / CH;  // 16-byte pieces of a row, rows of a copy
+  constexpr int CH = W / 8, RPI = 64 / CH;  // pieces of a row, rows of a copy
   const int r = i * RPI + lane / CH, p = lane % CH;
-  const uint32_t off = uint32_t(min(r, left - 1)) * uint32_t(stride * 2) + ((p ^ (dl_turn<W>(r) << 1)) << 4);
+  const uint32_t off = uint32_t(min(r, left - 1)) * uint32_t(stride * 2) + ((p ^ dl_turn<W>(r)) << 4);
   dma16(off, static_cast<const char*>(src), __builtin_amdgcn_readfirstlane(lds + i * 1024));
 }
 
@@ -94,19 +95,23 @@ typedef __attribute__((address_space(3))) dl_s16x4 dl_lds_s16x4;
 __device__ __forceinline__ uint2 dl_transposed(const char* p) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((dl_lds_s16x4*)p));
 }
-// The 4 rows 4 (l / 16) .. of row block rb, column 16 unit + l % 16.
+// The 4 rows 4 (l / 16) .. of row block rb, column 16 cb + l % 16.
 template <int W>
-__device__ __forceinline__ uint2 dl_column(const char* tile, int rb, int unit, int lane) {
+__device__ __forceinline__ uint2 dl_column(const char* tile, int rb, int cb, int lane) {
   const int r = 16 * rb + 4 * (lane >> 4) + ((lane & 15) >> 2);
-  return dl_transposed(tile + dl_at<W>(r, unit) + 8 * (lane & 3));
+  return dl_transposed(tile + dl_at<W>(r, 2 * cb + (lane >> 1 & 1)) + 8 * (lane & 1));
 }
-// Row 16 rb + l % 16 with the channels of contraction step ks in the order of the products' results.
+// Row 16 rb + l % 16, channels 32 ks + 8 (l / 16) ..
 template <int W>
 __device__ __forceinline__ uint4 dl_row(const char* tile, int rb, int ks, int lane) {
-  const int r = 16 * rb + (lane & 15), g = lane >> 4;
-  const uint2 lo = *reinterpret_cast<const uint2*>(tile + dl_at<W>(r, 2 * ks) + 8 * g);
-  const uint2 hi = *reinterpret_cast<const uint2*>(tile + dl_at<W>(r, 2 * ks + 1) + 8 * g);
-  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  return *reinterpret_cast<const uint4*>(tile + dl_at<W>(16 * rb + (lane & 15), 4 * ks + (lane >> 4)));
+}
+// The 4 rows 4 (l / 16) .. of row block rb, channel dl_channel(d, l % 16).
+__device__ __forceinline__ constexpr int dl_channel(int d, int m) { return 32 * (d / 2) + 8 * (m / 4) + 4 * (d % 2) + m % 4; }
+template <int W>
+__device__ __forceinline__ uint2 dl_channels(const char* tile, int rb, int d, int lane) {
+  const int r = 16 * rb + 4 * (lane >> 4) + ((lane & 15) >> 2);
+  return dl_transposed(tile + dl_at<W>(r, 4 * (d / 2) + (lane & 3)) + 8 * (d % 2));
 }
 
 // Rounds 8 values to a plane of bf16 and leaves what the rounding lost.
@@ -180,8 +185,8 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
     float kk = 0.f, qq = 0.f;
 #pragma unroll
     for (int i = 0; i < DK / 32; ++i) {  // 8 channels: any order, each once
-      const uint4 kv = *reinterpret_cast<const uint4*>(ks + r * DK * 2 + 16 * (4 * i + part));
-      const uint4 qv = *reinterpret_cast<const uint4*>(qs + r * DK * 2 + 16 * (4 * i + part));
+      const int at = r * DK * 2 + 16 * ((4 * i + part) ^ (r & (DK / 8 - 1)));
+      const uint4 kv = *reinterpret_cast<const uint4*>(ks + at), qv = *reinterpret_cast<const uint4*>(qs + at);
       const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -318,201 +323,371 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
 }
 
 // --------------------------------------------------------------------------------------------
-// W waves of 16 NB columns each.
-template <int DK, int W, int NB>
-__global__ __launch_bounds__(64 * W) void k_delta_scan(DeltaPackedArgs a) {
-  constexpr int COLS = 16 * NB * W, KT = DL_C * DK * 2, VT = DL_C * COLS * 2;
+// A split of 8 values into three planes of bf16 in 20 small steps, which stand between products.
+struct DlSplit {
+  float x[8];
+  uint32_t w[3][4];
+  __device__ __forceinline__ void step(int n) {
+    if (n < 16) {
+      const int p = n / 8, i = n % 8 / 2;
+      if (n % 2 == 0) {
+        w[p][i] = pack2bf(x[2 * i], x[2 * i + 1]);
+        x[2 * i] -= __uint_as_float(w[p][i] << 16);
+      } else {
+        x[2 * i + 1] -= __uint_as_float(w[p][i] & 0xFFFF0000u);
+      }
+    } else {
+      w[2][n - 16] = pack2bf(x[2 * (n - 16)], x[2 * (n - 16) + 1]);
+    }
+  }
+  __device__ __forceinline__ void set(int i, float v) { x[i] = v; }
+  __device__ __forceinline__ uint4 plane(int p) const { return make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]); }
+};
+__device__ __forceinline__ void dl_fence() { __builtin_amdgcn_sched_barrier(0); }
+// All waves; LDS written before is seen behind it. (The vector-memory counter is left alone.)
+__device__ __forceinline__ void dl_meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Where the waves meet. LDS written before is seen behind it; the vector-memory counter is left alone.
+template <int MOST>
+__device__ __forceinline__ void dl_meet_copied() {  // and at most MOST of the wave's copies and stores are under way
+  wait_vm<MOST>();
+  dl_meet();
+}
+
+// One workgroup: 16 columns of a state, two waves that carry it from chunk to chunk and two that do the rest, each
+// on its own SIMD. Of the carrying waves the first has the state's first half of rows and the chunk's first 32
+// tokens, the second the others: each multiplies its rows of S by all of K, hands the sums for the other's tokens
+// over, solves for its tokens' u (the second with what the first hands on) and adds all u to its rows. Their vector
+// work is dealt out between the products. The other two copy the next chunk's tiles into LDS and compute the
+// outputs, 32 tokens each, from the planes of S and the u that are left in LDS. All meet four times a chunk:
+//   B  chunk c's K is there                     1 the sums for the other's tokens, V and T; the planes of S
+//   2  the first half's V - e^G K S, in planes  3 u, and what of it the state takes, in planes
+template <int DK>
+__global__ __launch_bounds__(256, 1) void k_delta_scan(DeltaPackedArgs a) {
+  constexpr int KT = DL_C * DK * 2, VT = DL_C * 16 * 2;
   constexpr int DB = DK / 16, KS = DK / 32;  // row blocks of the state, contraction steps over them
+  constexpr int DH = DB / 2, KH = KS / 2;    // a wave's share of them
   // K, Q, the workspace's unit, V
   constexpr int AT_Q = KT, AT_U = 2 * KT, AT_V = AT_U + DL_UNIT, STAGE = AT_V + VT;
   __shared__ __align__(1024) char sm[2][STAGE];
+  __shared__ __align__(1024) char s_s[2 * KS * 1024];      // two planes of S
+  __shared__ __align__(1024) char u_s[4 * 1024];           // u, row blocks in fp32
+  __shared__ __align__(1024) char p_s[2][2 * 1024];        // sums for the tokens of the first, of the second wave
+  __shared__ __align__(1024) char r_s[3 * 1024];           // planes of the first half's V - e^G K S
+  __shared__ __align__(1024) char x_s[2][3 * 1024];        // planes of what the state takes of u
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  // the tiles of a head on one XCD: they read the same K, Q, T and A
-  const int heads = a.d.n_seq * a.d.Hv, hd = blockIdx.x % heads, tile = blockIdx.x / heads;
+  // the column tiles of a head on one XCD: they read the same K, Q, T and A
+  const int heads = a.d.n_seq * a.d.Hv, hd = blockIdx.x % heads, col = blockIdx.x / heads * 16;
   const int h = hd % a.d.Hv, s = hd / a.d.Hv, hk = h / (a.d.Hv / a.d.Hk);
   const DeltaChunk sq = dl_sequence(a, s);
+  const int me = wave & 1, g4 = 4 * (lane >> 4), c16 = lane & 15, l16 = 16 * lane;
+  const int chunks = (sq.n + DL_C - 1) / DL_C;
+
+  if (wave >= 2) {
+    constexpr int NK = KT / 1024 / 2, NU = (DL_UNIT / 1024 + 1) / 2, BACK = 3 * 1024;  // copies of a wave; NU: one may be a repetition
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(sm));
+    const uint16_t* kp = static_cast<const uint16_t*>(a.d.K) + long(sq.q0) * a.d.ks + hk * DK;
+    const uint16_t* qp = static_cast<const uint16_t*>(a.d.Q) + long(sq.q0) * a.d.qs + hk * DK;
+    const uint16_t* vp = static_cast<const uint16_t*>(a.d.V) + long(sq.q0) * a.d.vs + h * a.d.dv + col;
+    const char* up = static_cast<const char*>(a.ws) + (size_t(sq.base) * a.d.Hv + h) * DL_UNIT;
+    // A lane's offsets in 4 copies in a row of K or Q, which are 4 * 512 / DK rows and repeat then; the instruction
+    // counts 1024 i for the i-th itself, and 3 KB the base lacks, so that no offset is negative.
+    constexpr int CH = DK / 8, RPI = 64 / CH;
+    const auto offsets = [&](long stride, uint32_t (&off)[4]) DL_INLINE {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * RPI + lane / CH;
+        off[i] = uint32_t(r) * uint32_t(stride * 2) + ((lane % CH ^ dl_turn<DK>(r)) << 4) + BACK - 1024 * i;
+      }
+    };
+    uint32_t ko[4], qo[4];
+    offsets(a.d.ks, ko);
+    offsets(a.d.qs, qo);
+    const auto four = [&](const uint32_t (&off)[4], const char* base, uint32_t to) DL_INLINE {
+      dma16_at<0>(off[0], base, to);
+      dma16_at<1>(off[1], base, to);
+      dma16_at<2>(off[2], base, to);
+      dma16_at<3>(off[3], base, to);
+    };
+    // half `me` of a tile of K or Q
+    const auto rows = [&](const uint16_t* src, long stride, const uint32_t (&off)[4], int left, uint32_t to) DL_INLINE {
+      if (left >= DL_C) {
+#pragma unroll
+        for (int i = 0; i < NK; i += 4)
+          four(off, reinterpret_cast<const char*>(src + long((NK * me + i) * RPI) * stride) - BACK, to + (NK * me + i) * 1024);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) dl_copy_rows<DK>(NK * me + i, src, stride, left, to, lane);
+      }
+    };
+    // The copies of chunk c, in three parts: they are waited for one after the other, so their numbers count, and
+    // stores that follow stay behind them.
+    const auto part = [&](int which, int c) DL_INLINE {
+      const uint32_t to = lds + (c & 1) * STAGE;
+      const int left = sq.n - c * DL_C;
+      if (which == 0) rows(kp + long(c) * DL_C * a.d.ks, a.d.ks, ko, left, to);
+      if (which == 2) rows(qp + long(c) * DL_C * a.d.qs, a.d.qs, qo, left, to + AT_Q);
+      if (which == 1) {
+        dl_copy_rows<16>(me, vp + long(c) * DL_C * a.d.vs, a.d.vs, left, to + AT_V, lane);
+        const char* u = up + size_t(c) * a.d.Hv * DL_UNIT;
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          const int n = min(NU * me + i, DL_UNIT / 1024 - 1);
+          dma16(l16, u + n * 1024, to + AT_U + n * 1024);
+        }
+      }
+      asm volatile("" ::: "memory");
+      dl_fence();
+    };
+    // under way when a chunk begins: V and the unit, Q, the last outputs, behind K
+    constexpr int PER = NK + 1 + NU, STORES = 2;
+    if (chunks > 0) {
+      part(0, 0);
+      part(1, 0);
+      part(2, 0);
+    }
+    for (int c = 0; c < chunks; ++c) {
+      const bool next = c + 1 < chunks;
+      if (c > 0) dl_meet_copied<PER + STORES>();
+      else dl_meet_copied<0>();
+      if (next) part(0, c + 1);
+      const char* const qt = sm[c & 1] + AT_Q;
+      const char* const ut = sm[c & 1] + AT_U;
+      const float* const f = reinterpret_cast<const float*>(ut + DL_TOK);
+      if (next) dl_meet_copied<2 * NK + STORES>();
+      else dl_meet_copied<NK + STORES>();
+      if (next) part(1, c + 1);
+      uint4 sp[KS][2], af[2][2];
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) sp[k][p] = *reinterpret_cast<const uint4*>(s_s + (2 * k + p) * 1024 + l16);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)  // (those of the first half's second step are not used)
+          af[t][k] = *reinterpret_cast<const uint4*>(ut + (18 + (me ? dl_frag(2 + t, k) : t)) * 1024 + l16);
+      if (next) dl_meet_copied<PER + STORES>();
+      else dl_meet_copied<STORES>();
+      if (next) part(2, c + 1);
+      // O^T = S^T Q^T e^G: a lane has 4 neighbouring columns of a token
+      f32x4 o[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint4 q[2] = {dl_row<DK>(qt, 2 * me, k, lane), dl_row<DK>(qt, 2 * me + 1, k, lane)};
+#pragma unroll
+        for (int p = 1; p >= 0; --p)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) o[t] = mfma16x16x32(sp[k][p], q[t], o[t]);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) o[t] *= f[DL_OUT + 16 * (2 * me + t) + c16];
+      dl_meet();
+      // .. + u^T A^T
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (k > me) break;
+        uint4 u[2];
+        dl_planes<2>(*reinterpret_cast<const f32x4*>(u_s + 2 * k * 1024 + l16),
+                     *reinterpret_cast<const f32x4*>(u_s + (2 * k + 1) * 1024 + l16), u);
+#pragma unroll
+        for (int p = 1; p >= 0; --p)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) o[t] = mfma16x16x32(u[p], af[t][k], o[t]);
+      }
+      const int left = sq.n - c * DL_C;
+      uint16_t* p = static_cast<uint16_t*>(a.d.O) + (sq.q0 + long(c) * DL_C) * a.d.os + h * a.d.dv + col + g4;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int tok = 16 * (2 * me + t) + c16;
+        if (tok < left)
+          *reinterpret_cast<uint2*>(p + long(tok) * a.d.os) = make_uint2(pack2bf(o[t][0], o[t][1]), pack2bf(o[t][2], o[t][3]));
+      }
+    }
+    return;
+  }
+
   const long slot = a.d.slots ? a.d.slots[s] : s;
   const bool kept = slot >= 0 && slot < a.d.n_slots;
-  const int col = tile * COLS + wave * 16 * NB, g4 = 4 * (lane >> 4), c16 = lane & 15;
-  const int chunks = (sq.n + DL_C - 1) / DL_C;
   const long state = ((kept ? slot : 0) * a.d.Hv + h) * long(DK) * a.d.dv + col + c16;
-
-  f32x4 S[DB][NB];
+  const auto row = [&](int d, int r) DL_INLINE { return state + long(dl_channel(DH * me + d, g4) + r) * a.d.dv; };
+  f32x4 S[DH];
 #pragma unroll
-  for (int d = 0; d < DB; ++d)
+  for (int d = 0; d < DH; ++d)
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int r = 0; r < 4; ++r) S[d][r] = kept && a.d.state_in ? a.d.state_in[row(d, r)] : 0.f;
+  uint4 sp[KH][3];
+  DlSplit cut;
+  const auto cut_state = [&](int k, int n) DL_INLINE {  // step n of the split of the wave's rows 32 k ..
+    if (n == 0)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        S[d][b][r] = kept && a.d.state_in ? a.d.state_in[state + long(16 * d + g4 + r) * a.d.dv + 16 * b] : 0.f;
-
-  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(sm));
-  const uint16_t* kp = static_cast<const uint16_t*>(a.d.K) + long(sq.q0) * a.d.ks + hk * DK;
-  const uint16_t* qp = static_cast<const uint16_t*>(a.d.Q) + long(sq.q0) * a.d.qs + hk * DK;
-  const uint16_t* vp = static_cast<const uint16_t*>(a.d.V) + long(sq.q0) * a.d.vs + h * a.d.dv + tile * COLS;
-  const char* up = static_cast<const char*>(a.ws) + (size_t(sq.base) * a.d.Hv + h) * DL_UNIT;
-  const auto copy = [&](int c) DL_INLINE {  // of chunk c into its stage
-    const uint32_t to = lds + (c & 1) * STAGE;
-    const int left = sq.n - c * DL_C;
-    const char* u = up + size_t(c) * a.d.Hv * DL_UNIT;
+      for (int i = 0; i < 8; ++i) cut.set(i, S[2 * k + i / 4][i % 4]);
+    cut.step(n);
+    if (n == 19)
 #pragma unroll
-    for (int i = 0; i < KT / 1024 / W; ++i) {
-      dl_copy_rows<DK>(W * i + wave, kp + long(c) * DL_C * a.d.ks, a.d.ks, left, to, lane);
-      dl_copy_rows<DK>(W * i + wave, qp + long(c) * DL_C * a.d.qs, a.d.qs, left, to + AT_Q, lane);
-    }
-#pragma unroll
-    for (int i = 0; i < (DL_UNIT / 1024 + W - 1) / W; ++i)
-      if (W * i + wave < DL_UNIT / 1024)
-        dma16(uint32_t((W * i + wave) * 1024 + lane * 16), u,
-              __builtin_amdgcn_readfirstlane(to + AT_U + (W * i + wave) * 1024));
-#pragma unroll
-    for (int i = 0; i < VT / 1024 / W; ++i)
-      dl_copy_rows<COLS>(W * i + wave, vp + long(c) * DL_C * a.d.vs, a.d.vs, left, to + AT_V, lane);
+      for (int p = 0; p < 3; ++p) sp[k][p] = cut.plane(p);
   };
-  if (chunks > 0) copy(0);
+  const auto leave = [&](int k) DL_INLINE {  // two planes of the state for the outputs
+#pragma unroll
+    for (int p = 0; p < 2; ++p) *reinterpret_cast<uint4*>(s_s + (2 * (KH * me + k) + p) * 1024 + l16) = sp[k][p];
+  };
+  // steps of `op`, `total` in all, in proportion to the slots of a phase, the first `wait` of them without
+  const auto deal = [&](int at, int slots, int wait, int total, auto&& op) DL_INLINE {
+    if (at < wait) return;
+    const int n0 = (at - wait) * total / (slots - wait), n1 = (at + 1 - wait) * total / (slots - wait);
+#pragma unroll
+    for (int n = n0; n < n1; ++n) op(n);
+  };
+#pragma unroll
+  for (int k = 0; k < KH - 1; ++k)
+#pragma unroll
+    for (int n = 0; n < 20; ++n) cut_state(k, n);
+
+  constexpr int TP[6] = {2, 1, 0, 1, 0, 0}, XP[6] = {0, 1, 2, 0, 1, 0};  // planes' products from the smallest on
   for (int c = 0; c < chunks; ++c) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (c + 1 < chunks) copy(c + 1);
+    if (KH == 1)
+#pragma unroll
+      for (int n = 0; n < 20; ++n) cut_state(0, n);
+    dl_meet();  // B
     const char* const kt = sm[c & 1];
-    const char* const qt = kt + AT_Q;
     const char* const ut = kt + AT_U;
     const char* const vt = kt + AT_V;
     const float* const f = reinterpret_cast<const float*>(ut + DL_TOK);
-    const int left = sq.n - c * DL_C;
-    const auto T = [&](int p, int rb, int ks) DL_INLINE {
-      return *reinterpret_cast<const uint4*>(ut + (6 * p + dl_frag(rb, ks)) * 1024 + 16 * lane);
-    };
-
-    // S in two planes; P = K S
-    uint4 sp[KS][NB][2];
+    // P = K S over the wave's rows of S: blocks 0, 1 the other wave's tokens, 2, 3 its own; its last rows are split
+    // meanwhile
+    f32x4 x[4];
+    uint4 kf[KH][4];
+    const auto read_k = [&](int k, int b) DL_INLINE { kf[k][b] = dl_row<DK>(kt, 2 * (b < 2 ? 1 - me : me) + b % 2, KH * me + k, lane); };
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
+    for (int b = 0; b < 4; ++b) read_k(0, b);
+    dl_fence();
 #pragma unroll
-      for (int b = 0; b < NB; ++b) dl_planes<2>(S[2 * k][b], S[2 * k + 1][b], sp[k][b]);
-    f32x4 x[4][NB];
-#pragma unroll
-    for (int rb = 0; rb < 4; ++rb) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) x[rb][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint4 kf = dl_row<DK>(kt, rb, k, lane);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int p = 0; p < 2; ++p) x[rb][b] = mfma16x16x32(kf, sp[k][b][p], x[rb][b]);
+    for (int k = 0; k < 12 * KH; ++k) {
+      const int st = k / 12, p = 2 - k % 6 / 2, b = 2 * (k / 6 % 2) + k % 2;
+      if (k < 12 && k % 6 < 2) x[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+      x[b] = mfma16x16x32(kf[st][b], sp[st][p], x[b]);
+      if (KH == 2) {
+        if (k < 4) read_k(1, k);
+        if (k < 12) deal(k, 12, 0, 20, [&](int n) DL_INLINE { cut_state(KH - 1, n); });
+        if (k == 1) leave(0);
+        if (k == 14) leave(KH - 1);
+      } else if (k == 1) {
+        leave(0);
       }
-    }
-    // V - e^G P
-#pragma unroll
-    for (int rb = 0; rb < 4; ++rb) {
-      const float4 from = *reinterpret_cast<const float4*>(f + DL_FROM + 16 * rb + g4);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint2 v = dl_column<COLS>(vt, rb, wave * NB + b, lane);
-        x[rb][b] = f32x4{fmaf(-from.x, x[rb][b][0], __uint_as_float(v.x << 16)),
-                         fmaf(-from.y, x[rb][b][1], __uint_as_float(v.x & 0xFFFF0000u)),
-                         fmaf(-from.z, x[rb][b][2], __uint_as_float(v.y << 16)),
-                         fmaf(-from.w, x[rb][b][3], __uint_as_float(v.y & 0xFFFF0000u))};
+      if (k == 12 * KH - 2) {
+        *reinterpret_cast<f32x4*>(p_s[1 - me] + l16) = x[0];
+        *reinterpret_cast<f32x4*>(p_s[1 - me] + 1024 + l16) = x[1];
       }
+      dl_fence();
     }
-    uint4 xp[2][NB][3];
+    dl_meet();  // 1
+    // V - e^G P of the wave's tokens, in planes; u = T (..) of those
+    uint4 xp[3], t[2][3];
+    f32x4 u[2];
+    {
+      uint2 v[2];
+      float4 from[2];
+      f32x4 other[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int b = 0; b < NB; ++b) dl_planes<3>(x[2 * k][b], x[2 * k + 1][b], xp[k][b]);
-    // u = T (..): the planes' products from the smallest on
-#pragma unroll
-    for (int rb = 0; rb < 4; ++rb) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) x[rb][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k <= rb / 2; ++k) {
-        const uint4 t[3] = {T(0, rb, k), T(1, rb, k), T(2, rb, k)};
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          x[rb][b] = mfma16x16x32(t[2], xp[k][b][0], x[rb][b]);
-          x[rb][b] = mfma16x16x32(t[1], xp[k][b][1], x[rb][b]);
-          x[rb][b] = mfma16x16x32(t[0], xp[k][b][2], x[rb][b]);
-          x[rb][b] = mfma16x16x32(t[1], xp[k][b][0], x[rb][b]);
-          x[rb][b] = mfma16x16x32(t[0], xp[k][b][1], x[rb][b]);
-          x[rb][b] = mfma16x16x32(t[0], xp[k][b][0], x[rb][b]);
-        }
-      }
-    }
-    // one plane of u for O, and what the state takes in three
-    uint4 uh[2][NB];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint4 one[1];
-        dl_planes<1>(x[2 * k][b], x[2 * k + 1][b], one);
-        uh[k][b] = one[0];
+      for (int b = 0; b < 2; ++b) {
+        other[b] = *reinterpret_cast<const f32x4*>(p_s[me] + b * 1024 + l16);
+        from[b] = *reinterpret_cast<const float4*>(f + DL_FROM + 16 * (2 * me + b) + g4);
+        v[b] = dl_column<16>(vt, 2 * me + b, 0, lane);
       }
 #pragma unroll
-    for (int rb = 0; rb < 4; ++rb) {
-      const float4 keep = *reinterpret_cast<const float4*>(f + DL_LEFT + 16 * rb + g4);
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        x[rb][b] = f32x4{x[rb][b][0] * keep.x, x[rb][b][1] * keep.y, x[rb][b][2] * keep.z, x[rb][b][3] * keep.w};
+        for (int p = 0; p < 3; ++p)
+          t[b][p] = *reinterpret_cast<const uint4*>(ut + (6 * p + (me ? dl_frag(2 + b, 1) : b)) * 1024 + l16);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const f32x4 y = x[2 + b] + other[b];
+        x[b] = f32x4{fmaf(-from[b].x, y[0], __uint_as_float(v[b].x << 16)),
+                     fmaf(-from[b].y, y[1], __uint_as_float(v[b].x & 0xFFFF0000u)),
+                     fmaf(-from[b].z, y[2], __uint_as_float(v[b].y << 16)),
+                     fmaf(-from[b].w, y[3], __uint_as_float(v[b].y & 0xFFFF0000u))};
+      }
+      dl_planes<3>(x[0], x[1], xp);
     }
+    if (me == 0)
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(r_s + p * 1024 + l16) = xp[p];
+    float4 keep[2];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) dl_planes<3>(x[2 * k][b], x[2 * k + 1][b], xp[k][b]);
+    for (int b = 0; b < 2; ++b) keep[b] = *reinterpret_cast<const float4*>(f + DL_LEFT + 16 * (2 * me + b) + g4);
     const float whole = f[DL_WHOLE];
+    u[0] = u[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int d = 0; d < DB; ++d) {
+    for (int n = 0; n < 6; ++n)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) S[d][b] *= whole;
+      for (int b = 0; b < 2; ++b) u[b] = mfma16x16x32(t[b][TP[n]], xp[XP[n]], u[b]);
+    dl_meet();  // 2
+    const auto kc = [&](int k, int d) DL_INLINE {  // K^T of tokens 32 k .., the wave's row block d
+      const uint2 lo = dl_channels<DK>(kt, 2 * k, DH * me + d, lane), hi = dl_channels<DK>(kt, 2 * k + 1, DH * me + d, lane);
+      return make_uint4(lo.x, lo.y, hi.x, hi.y);
+    };
+    uint4 kf0[DH], kf1[DH];
+    if (me) {  // the second half's tokens see the first's
+      uint4 t0[2][3], r[3];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint2 lo = dl_column<DK>(kt, 2 * k, d, lane), hi = dl_column<DK>(kt, 2 * k + 1, d, lane);
-        const uint4 kf = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      for (int p = 0; p < 3; ++p) r[p] = *reinterpret_cast<const uint4*>(r_s + p * 1024 + l16);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int p = 2; p >= 0; --p) S[d][b] = mfma16x16x32(kf, xp[k][b][p], S[d][b]);
-      }
+        for (int p = 0; p < 3; ++p) t0[b][p] = *reinterpret_cast<const uint4*>(ut + (6 * p + dl_frag(2 + b, 0)) * 1024 + l16);
+#pragma unroll
+      for (int n = 0; n < 6; ++n)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) u[b] = mfma16x16x32(t0[b][TP[n]], r[XP[n]], u[b]);
     }
-    // O^T = S^T Q^T e^G + u^T A^T: a lane has 4 neighbouring columns of a token
 #pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      const float out = f[DL_OUT + 16 * tb + c16];
-      const int t = 16 * tb + c16;
-      f32x4 o[NB];
+    for (int d = 0; d < DH; ++d) {
+      kf0[d] = kc(me, d);  // own tokens
+      kf1[d] = kc(1 - me, d);
+    }
 #pragma unroll
-      for (int b = 0; b < NB; ++b) o[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int d = 0; d < DH; ++d) S[d] *= whole;
+    uint4 xu[3], xo[3];
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint4 qf = dl_row<DK>(qt, tb, k, lane);
+    for (int b = 0; b < 2; ++b) {
+      *reinterpret_cast<f32x4*>(u_s + (2 * me + b) * 1024 + l16) = u[b];
+      u[b] = f32x4{u[b][0] * keep[b].x, u[b][1] * keep[b].y, u[b][2] * keep[b].z, u[b][3] * keep[b].w};
+    }
+    dl_planes<3>(u[0], u[1], xu);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) o[b] = mfma16x16x32(sp[k][b][0], qf, o[b]);
-      }
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(x_s[me] + p * 1024 + l16) = xu[p];
+    if (me == 0) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) o[b] *= out;
+      for (int p = 2; p >= 0; --p)
 #pragma unroll
-      for (int k = 0; k <= tb / 2; ++k) {
-        const uint4 af = *reinterpret_cast<const uint4*>(ut + (18 + dl_frag(tb, k)) * 1024 + 16 * lane);
+        for (int d = 0; d < DH; ++d) S[d] = mfma16x16x32(kf0[d], xu[p], S[d]);
+    }
+    dl_meet();  // 3
 #pragma unroll
-        for (int b = 0; b < NB; ++b) o[b] = mfma16x16x32(uh[k][b], af, o[b]);
-      }
-      if (t < left) {
-        uint16_t* p = static_cast<uint16_t*>(a.d.O) + (sq.q0 + long(c) * DL_C + t) * a.d.os + h * a.d.dv + col + g4;
+    for (int p = 0; p < 3; ++p) xo[p] = *reinterpret_cast<const uint4*>(x_s[1 - me] + p * 1024 + l16);
+    if (me) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          *reinterpret_cast<uint2*>(p + 16 * b) = make_uint2(pack2bf(o[b][0], o[b][1]), pack2bf(o[b][2], o[b][3]));
-      }
+      for (int p = 2; p >= 0; --p)
+#pragma unroll
+        for (int d = 0; d < DH; ++d) S[d] = mfma16x16x32(kf0[d], xu[p], S[d]);
+    }
+    dl_fence();
+    // with the split of the rows that are done
+#pragma unroll
+    for (int k = 0; k < 3 * DH; ++k) {
+      const int d = 2 * (k / 6) + k % 2, p = 2 - k % 6 / 2;
+      S[d] = mfma16x16x32(kf1[d], xo[p], S[d]);
+      if (KH > 1) deal(k, 3 * DH, 8, 20 * (KH - 1), [&](int i) DL_INLINE { cut_state(i / 20, i % 20); });
+      dl_fence();
     }
   }
   if (kept && a.d.state_out)
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+    for (int d = 0; d < DH; ++d)
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) a.d.state_out[state + long(16 * d + g4 + r) * a.d.dv + 16 * b] = S[d][b][r];
+      for (int r = 0; r < 4; ++r) a.d.state_out[row(d, r)] = S[d][r];
 }
 
 long units(int n_seq, int N) { return N / DL_C + n_seq; }  // numbers of chunks
@@ -524,12 +699,7 @@ hipError_t launch(const DeltaPackedArgs& a) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const long heads = long(d.n_seq) * d.Hv;
-  if (d.dv % 128 == 0 && heads * d.dv / 64 > 512)
-    hipLaunchKernelGGL((k_delta_scan<DK, 4, 2>), dim3(unsigned(heads * (d.dv / 128))), dim3(256), 0, d.stream, a);
-  else if (heads * d.dv / 32 > 256)
-    hipLaunchKernelGGL((k_delta_scan<DK, 4, 1>), dim3(unsigned(heads * (d.dv / 64))), dim3(256), 0, d.stream, a);
-  else
-    hipLaunchKernelGGL((k_delta_scan<DK, 2, 1>), dim3(unsigned(heads * (d.dv / 32))), dim3(128), 0, d.stream, a);
+  hipLaunchKernelGGL((k_delta_scan<DK>), dim3(unsigned(heads * (d.dv / 16))), dim3(256), 0, d.stream, a);
   return hipGetLastError();
 }
 
