@@ -354,70 +354,75 @@ __device__ __forceinline__ void dl_meet_copied() {  // and at most MOST of the w
   dl_meet();
 }
 
-// One workgroup: 16 columns of a state, two waves that carry it from chunk to chunk and two that do the rest, each
-// on its own SIMD. Of the carrying waves the first has the state's first half of rows and the chunk's first 32
-// tokens, the second the others: each multiplies its rows of S by all of K, hands the sums for the other's tokens
-// over, solves for its tokens' u (the second with what the first hands on) and adds all u to its rows. Their vector
-// work is dealt out between the products. The other two copy the next chunk's tiles into LDS and compute the
-// outputs, 32 tokens each, from the planes of S and the u that are left in LDS. All meet four times a chunk:
-//   B  chunk c's K is there                     1 the sums for the other's tokens, V and T; the planes of S
-//   2  the first half's V - e^G K S, in planes  3 u, and what of it the state takes, in planes
+// One workgroup: 32 columns of a state in two tiles of 16. A tile has two waves that carry it from chunk to chunk,
+// each on a SIMD of its own, and two that do the rest beside them. Of the carrying waves the first has the state's
+// first half of rows and the chunk's first 32 tokens, the second the others: each multiplies its rows of S by all of
+// K, hands the sums for the other's tokens over, solves for its tokens' u (the second with what the first hands on)
+// and adds all u to its rows. Their vector work is dealt out between the products. The others copy the next chunk's
+// tiles into LDS and compute the outputs, 32 tokens each, from the planes of S and the u that are left in LDS. All
+// meet four times a chunk; what is there behind a meeting:
+//   B  chunk c's V, T and A                     1  the sums for the other's tokens; the planes of S
+//   2  the first half's V - e^G K S, in planes; Q of chunk c
+//   3  u, and what of it the state takes, in planes; K of chunk c + 1
 template <int DK>
-__global__ __launch_bounds__(256, 1) void k_delta_scan(DeltaPackedArgs a) {
-  constexpr int KT = DL_C * DK * 2, VT = DL_C * 16 * 2;
+__global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
+  constexpr int TILES = 2, CW = 16 * TILES, KT = DL_C * DK * 2, VT = DL_C * CW * 2;
   constexpr int DB = DK / 16, KS = DK / 32;  // row blocks of the state, contraction steps over them
   constexpr int DH = DB / 2, KH = KS / 2;    // a wave's share of them
-  // K, Q, the workspace's unit, V
-  constexpr int AT_Q = KT, AT_U = 2 * KT, AT_V = AT_U + DL_UNIT, STAGE = AT_V + VT;
+  constexpr int AT_U = KT, AT_V = AT_U + DL_UNIT, STAGE = AT_V + VT;  // K, the workspace's unit, V
+  struct Hand {
+    char s[2 * KS * 1024];  // two planes of S
+    char u[4 * 1024];       // u, row blocks in fp32
+    char r[3 * 1024];       // planes of the first half's V - e^G K S
+    char px[6 * 1024];      // sums for the tokens of the first, of the second wave; then planes of what the state takes of u
+  };
   __shared__ __align__(1024) char sm[2][STAGE];
-  __shared__ __align__(1024) char s_s[2 * KS * 1024];      // two planes of S
-  __shared__ __align__(1024) char u_s[4 * 1024];           // u, row blocks in fp32
-  __shared__ __align__(1024) char p_s[2][2 * 1024];        // sums for the tokens of the first, of the second wave
-  __shared__ __align__(1024) char r_s[3 * 1024];           // planes of the first half's V - e^G K S
-  __shared__ __align__(1024) char x_s[2][3 * 1024];        // planes of what the state takes of u
+  __shared__ __align__(1024) char q_s[KT];
+  __shared__ __align__(1024) Hand hand[TILES];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   // the column tiles of a head on one XCD: they read the same K, Q, T and A
-  const int heads = a.d.n_seq * a.d.Hv, hd = blockIdx.x % heads, col = blockIdx.x / heads * 16;
+  const int heads = a.d.n_seq * a.d.Hv, hd = blockIdx.x % heads, col0 = blockIdx.x / heads * CW;
   const int h = hd % a.d.Hv, s = hd / a.d.Hv, hk = h / (a.d.Hv / a.d.Hk);
   const DeltaChunk sq = dl_sequence(a, s);
-  const int me = wave & 1, g4 = 4 * (lane >> 4), c16 = lane & 15, l16 = 16 * lane;
+  const int me = wave & 1, tile = wave >> 1 & 1, col = col0 + 16 * tile;
+  const int g4 = 4 * (lane >> 4), c16 = lane & 15, l16 = 16 * lane;
   const int chunks = (sq.n + DL_C - 1) / DL_C;
+  char *const s_s = hand[tile].s, *const u_s = hand[tile].u, *const r_s = hand[tile].r, *const px_s = hand[tile].px;
 
-  if (wave >= 2) {
-    constexpr int NK = KT / 1024 / 2, NU = (DL_UNIT / 1024 + 1) / 2, BACK = 3 * 1024;  // copies of a wave; NU: one may be a repetition
-    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(sm));
+  if (wave >= 4) {
+    constexpr int NK = KT / 1024 / 4, NU = (DL_UNIT / 1024 + 3) / 4, BACK = 3 * 1024;  // copies of a wave; NU: some are repetitions
+    const int w = wave - 4;
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(sm)), lds_q = __builtin_amdgcn_readfirstlane(lds_u32(q_s));
     const uint16_t* kp = static_cast<const uint16_t*>(a.d.K) + long(sq.q0) * a.d.ks + hk * DK;
     const uint16_t* qp = static_cast<const uint16_t*>(a.d.Q) + long(sq.q0) * a.d.qs + hk * DK;
-    const uint16_t* vp = static_cast<const uint16_t*>(a.d.V) + long(sq.q0) * a.d.vs + h * a.d.dv + col;
+    const uint16_t* vp = static_cast<const uint16_t*>(a.d.V) + long(sq.q0) * a.d.vs + h * a.d.dv + col0;
     const char* up = static_cast<const char*>(a.ws) + (size_t(sq.base) * a.d.Hv + h) * DL_UNIT;
-    // A lane's offsets in 4 copies in a row of K or Q, which are 4 * 512 / DK rows and repeat then; the instruction
-    // counts 1024 i for the i-th itself, and 3 KB the base lacks, so that no offset is negative.
+    // A lane's offsets in the copies of 16 rows of K or Q; the instruction counts 1024 i for the i-th itself, and
+    // 3 KB the base lacks, so that no offset is negative.
     constexpr int CH = DK / 8, RPI = 64 / CH;
-    const auto offsets = [&](long stride, uint32_t (&off)[4]) DL_INLINE {
+    static_assert(NK * RPI == 16 && NK <= 4, "a wave copies 16 rows");
+    const auto offsets = [&](long stride, uint32_t (&off)[NK]) DL_INLINE {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < NK; ++i) {
         const int r = i * RPI + lane / CH;
         off[i] = uint32_t(r) * uint32_t(stride * 2) + ((lane % CH ^ dl_turn<DK>(r)) << 4) + BACK - 1024 * i;
       }
     };
-    uint32_t ko[4], qo[4];
+    uint32_t ko[NK], qo[NK];
     offsets(a.d.ks, ko);
     offsets(a.d.qs, qo);
-    const auto four = [&](const uint32_t (&off)[4], const char* base, uint32_t to) DL_INLINE {
-      dma16_at<0>(off[0], base, to);
-      dma16_at<1>(off[1], base, to);
-      dma16_at<2>(off[2], base, to);
-      dma16_at<3>(off[3], base, to);
-    };
-    // half `me` of a tile of K or Q
-    const auto rows = [&](const uint16_t* src, long stride, const uint32_t (&off)[4], int left, uint32_t to) DL_INLINE {
+    const auto rows = [&](const uint16_t* src, long stride, const uint32_t (&off)[NK], int left, uint32_t to) DL_INLINE {
       if (left >= DL_C) {
-#pragma unroll
-        for (int i = 0; i < NK; i += 4)
-          four(off, reinterpret_cast<const char*>(src + long((NK * me + i) * RPI) * stride) - BACK, to + (NK * me + i) * 1024);
+        const char* base = reinterpret_cast<const char*>(src + long(16 * w) * stride) - BACK;
+        dma16_at<0>(off[0], base, to + NK * w * 1024);
+        dma16_at<1>(off[1], base, to);
+        if constexpr (NK == 4) {
+          dma16_at<2>(off[2], base, to);
+          dma16_at<3>(off[3], base, to);
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < NK; ++i) dl_copy_rows<DK>(NK * me + i, src, stride, left, to, lane);
+        for (int i = 0; i < NK; ++i) dl_copy_rows<DK>(NK * w + i, src, stride, left, to, lane);
       }
     };
     // The copies of chunk c, in three parts: they are waited for one after the other, so their numbers count, and
@@ -426,36 +431,33 @@ __global__ __launch_bounds__(256, 1) void k_delta_scan(DeltaPackedArgs a) {
       const uint32_t to = lds + (c & 1) * STAGE;
       const int left = sq.n - c * DL_C;
       if (which == 0) rows(kp + long(c) * DL_C * a.d.ks, a.d.ks, ko, left, to);
-      if (which == 2) rows(qp + long(c) * DL_C * a.d.qs, a.d.qs, qo, left, to + AT_Q);
+      if (which == 2) rows(qp + long(c) * DL_C * a.d.qs, a.d.qs, qo, left, lds_q);
       if (which == 1) {
-        dl_copy_rows<16>(me, vp + long(c) * DL_C * a.d.vs, a.d.vs, left, to + AT_V, lane);
+        dl_copy_rows<CW>(w, vp + long(c) * DL_C * a.d.vs, a.d.vs, left, to + AT_V, lane);
         const char* u = up + size_t(c) * a.d.Hv * DL_UNIT;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-          const int n = min(NU * me + i, DL_UNIT / 1024 - 1);
+          const int n = min(NU * w + i, DL_UNIT / 1024 - 1);
           dma16(l16, u + n * 1024, to + AT_U + n * 1024);
         }
       }
       asm volatile("" ::: "memory");
       dl_fence();
     };
-    // under way when a chunk begins: V and the unit, Q, the last outputs, behind K
-    constexpr int PER = NK + 1 + NU, STORES = 2;
+    constexpr int NVU = 1 + NU, STORES = 2;
     if (chunks > 0) {
       part(0, 0);
       part(1, 0);
       part(2, 0);
     }
+    dl_meet_copied<0>();
     for (int c = 0; c < chunks; ++c) {
       const bool next = c + 1 < chunks;
-      if (c > 0) dl_meet_copied<PER + STORES>();
-      else dl_meet_copied<0>();
+      dl_meet_copied<NK + STORES>();  // B: behind V and the unit come Q and the last outputs
       if (next) part(0, c + 1);
-      const char* const qt = sm[c & 1] + AT_Q;
       const char* const ut = sm[c & 1] + AT_U;
       const float* const f = reinterpret_cast<const float*>(ut + DL_TOK);
-      if (next) dl_meet_copied<2 * NK + STORES>();
-      else dl_meet_copied<NK + STORES>();
+      dl_meet();  // 1
       if (next) part(1, c + 1);
       uint4 sp[KS][2], af[2][2];
 #pragma unroll
@@ -467,16 +469,15 @@ __global__ __launch_bounds__(256, 1) void k_delta_scan(DeltaPackedArgs a) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)  // (those of the first half's second step are not used)
           af[t][k] = *reinterpret_cast<const uint4*>(ut + (18 + (me ? dl_frag(2 + t, k) : t)) * 1024 + l16);
-      if (next) dl_meet_copied<PER + STORES>();
+      if (next) dl_meet_copied<STORES + NK + NVU>();  // 2: behind Q come the last outputs, the next K, V and unit
       else dl_meet_copied<STORES>();
-      if (next) part(2, c + 1);
       // O^T = S^T Q^T e^G: a lane has 4 neighbouring columns of a token
       f32x4 o[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const uint4 q[2] = {dl_row<DK>(qt, 2 * me, k, lane), dl_row<DK>(qt, 2 * me + 1, k, lane)};
+        const uint4 q[2] = {dl_row<DK>(q_s, 2 * me, k, lane), dl_row<DK>(q_s, 2 * me + 1, k, lane)};
 #pragma unroll
         for (int p = 1; p >= 0; --p)
 #pragma unroll
@@ -484,7 +485,9 @@ __global__ __launch_bounds__(256, 1) void k_delta_scan(DeltaPackedArgs a) {
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) o[t] *= f[DL_OUT + 16 * (2 * me + t) + c16];
-      dl_meet();
+      if (next) dl_meet_copied<NVU>();  // 3: behind the next K come V and the unit
+      else dl_meet();
+      if (next) part(2, c + 1);
       // .. + u^T A^T
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -509,6 +512,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_scan(DeltaPackedArgs a) {
     return;
   }
 
+  __builtin_amdgcn_s_setprio(3);
   const long slot = a.d.slots ? a.d.slots[s] : s;
   const bool kept = slot >= 0 && slot < a.d.n_slots;
   const long state = ((kept ? slot : 0) * a.d.Hv + h) * long(DK) * a.d.dv + col + c16;
@@ -545,7 +549,17 @@ __global__ __launch_bounds__(256, 1) void k_delta_scan(DeltaPackedArgs a) {
 #pragma unroll
     for (int n = 0; n < 20; ++n) cut_state(k, n);
 
-  constexpr int TP[6] = {2, 1, 0, 1, 0, 0}, XP[6] = {0, 1, 2, 0, 1, 0};  // planes' products from the smallest on
+  // Products of planes, the largest last but for the order in which the planes get ready.
+  constexpr int TP[6] = {2, 1, 0, 1, 0, 0}, XP[6] = {0, 0, 0, 1, 1, 2};
+  uint4 kf[KH][4];  // K: blocks 0, 1 the other wave's tokens, 2, 3 its own
+  const auto read_k = [&](const char* kt, int i) DL_INLINE {
+    const int b = i % 4;
+    kf[i / 4][b] = dl_row<DK>(kt, 2 * (b < 2 ? 1 - me : me) + b % 2, KH * me + i / 4, lane);
+  };
+  dl_meet();
+  if (chunks > 0)
+#pragma unroll
+    for (int i = 0; i < 4 * KH; ++i) read_k(sm[0], i);
   for (int c = 0; c < chunks; ++c) {
     if (KH == 1)
 #pragma unroll
@@ -555,131 +569,138 @@ __global__ __launch_bounds__(256, 1) void k_delta_scan(DeltaPackedArgs a) {
     const char* const ut = kt + AT_U;
     const char* const vt = kt + AT_V;
     const float* const f = reinterpret_cast<const float*>(ut + DL_TOK);
-    // P = K S over the wave's rows of S: blocks 0, 1 the other wave's tokens, 2, 3 its own; its last rows are split
-    // meanwhile
+    // P = K S over the wave's rows of S, whose last ones are split meanwhile; what the next steps take is read
     f32x4 x[4];
-    uint4 kf[KH][4];
-    const auto read_k = [&](int k, int b) DL_INLINE { kf[k][b] = dl_row<DK>(kt, 2 * (b < 2 ? 1 - me : me) + b % 2, KH * me + k, lane); };
-#pragma unroll
-    for (int b = 0; b < 4; ++b) read_k(0, b);
-    dl_fence();
+    uint4 t[2][3], t0[2][3], kc[2][DH];
+    uint2 v[2];
+    float4 from[2], keep[2];
+    const auto T = [&](int p, int frag) DL_INLINE { return *reinterpret_cast<const uint4*>(ut + (6 * p + frag) * 1024 + l16); };
+    const auto read_t = [&](int i) DL_INLINE { t[i % 2][2 - i / 2] = T(2 - i / 2, me ? dl_frag(2 + i % 2, 1) : i % 2); };
+    const auto read_kc = [&](int k, int d) DL_INLINE {  // K^T of tokens 32 k .., the wave's row block d
+      const uint2 lo = dl_channels<DK>(kt, 2 * k, DH * me + d, lane), hi = dl_channels<DK>(kt, 2 * k + 1, DH * me + d, lane);
+      return make_uint4(lo.x, lo.y, hi.x, hi.y);
+    };
 #pragma unroll
     for (int k = 0; k < 12 * KH; ++k) {
       const int st = k / 12, p = 2 - k % 6 / 2, b = 2 * (k / 6 % 2) + k % 2;
       if (k < 12 && k % 6 < 2) x[b] = f32x4{0.f, 0.f, 0.f, 0.f};
       x[b] = mfma16x16x32(kf[st][b], sp[st][p], x[b]);
-      if (KH == 2) {
-        if (k < 4) read_k(1, k);
-        if (k < 12) deal(k, 12, 0, 20, [&](int n) DL_INLINE { cut_state(KH - 1, n); });
-        if (k == 1) leave(0);
-        if (k == 14) leave(KH - 1);
-      } else if (k == 1) {
-        leave(0);
+      if (KH == 2 && k < 12) deal(k, 12, 0, 20, [&](int n) DL_INLINE { cut_state(KH - 1, n); });
+      if (k == 1) leave(0);
+      if (KH == 2 && k == 14) leave(1);
+      if (k >= 2 && k < 4) {
+        v[k - 2] = dl_column<CW>(vt, 2 * me + k - 2, tile, lane);
+        from[k - 2] = *reinterpret_cast<const float4*>(f + DL_FROM + 16 * (2 * me + k - 2) + g4);
+      } else if (k >= 4 && k < 10) {
+        read_t(k - 4);
+      } else if (k >= 15 && k < 17) {
+        keep[k - 15] = *reinterpret_cast<const float4*>(f + DL_LEFT + 16 * (2 * me + k - 15) + g4);
       }
       if (k == 12 * KH - 2) {
-        *reinterpret_cast<f32x4*>(p_s[1 - me] + l16) = x[0];
-        *reinterpret_cast<f32x4*>(p_s[1 - me] + 1024 + l16) = x[1];
+        *reinterpret_cast<f32x4*>(px_s + (1 - me) * 2048 + l16) = x[0];
+        *reinterpret_cast<f32x4*>(px_s + (1 - me) * 2048 + 1024 + l16) = x[1];
       }
       dl_fence();
     }
     dl_meet();  // 1
-    // V - e^G P of the wave's tokens, in planes; u = T (..) of those
-    uint4 xp[3], t[2][3];
-    f32x4 u[2];
-    {
-      uint2 v[2];
-      float4 from[2];
-      f32x4 other[2];
+    f32x4 other[2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        other[b] = *reinterpret_cast<const f32x4*>(p_s[me] + b * 1024 + l16);
-        from[b] = *reinterpret_cast<const float4*>(f + DL_FROM + 16 * (2 * me + b) + g4);
-        v[b] = dl_column<16>(vt, 2 * me + b, 0, lane);
-      }
+    for (int b = 0; b < 2; ++b) other[b] = *reinterpret_cast<const f32x4*>(px_s + me * 2048 + b * 1024 + l16);
+    if (KH == 1)
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-          t[b][p] = *reinterpret_cast<const uint4*>(ut + (6 * p + (me ? dl_frag(2 + b, 1) : b)) * 1024 + l16);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const f32x4 y = x[2 + b] + other[b];
-        x[b] = f32x4{fmaf(-from[b].x, y[0], __uint_as_float(v[b].x << 16)),
-                     fmaf(-from[b].y, y[1], __uint_as_float(v[b].x & 0xFFFF0000u)),
-                     fmaf(-from[b].z, y[2], __uint_as_float(v[b].y << 16)),
-                     fmaf(-from[b].w, y[3], __uint_as_float(v[b].y & 0xFFFF0000u))};
-      }
-      dl_planes<3>(x[0], x[1], xp);
-    }
-    if (me == 0)
-#pragma unroll
-      for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(r_s + p * 1024 + l16) = xp[p];
-    float4 keep[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) keep[b] = *reinterpret_cast<const float4*>(f + DL_LEFT + 16 * (2 * me + b) + g4);
+      for (int b = 0; b < 2; ++b) keep[b] = *reinterpret_cast<const float4*>(f + DL_LEFT + 16 * (2 * me + b) + g4);
     const float whole = f[DL_WHOLE];
+    if (me)  // the second half's tokens see the first's
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) t0[b][p] = T(p, dl_frag(2 + b, 0));
+    // V - e^G P of the wave's tokens, in planes, and u = T (..) of those
+    f32x4 u[2];
+    uint4 xp[3];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const f32x4 y = x[2 + b] + other[b];
+      cut.set(4 * b, fmaf(-from[b].x, y[0], __uint_as_float(v[b].x << 16)));
+      cut.set(4 * b + 1, fmaf(-from[b].y, y[1], __uint_as_float(v[b].x & 0xFFFF0000u)));
+      cut.set(4 * b + 2, fmaf(-from[b].z, y[2], __uint_as_float(v[b].y << 16)));
+      cut.set(4 * b + 3, fmaf(-from[b].w, y[3], __uint_as_float(v[b].y & 0xFFFF0000u)));
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) cut.step(n);
+    xp[0] = cut.plane(0);
     u[0] = u[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int n = 0; n < 6; ++n)
+    for (int k = 0; k < 12; ++k) {
+      const int n = k / 2, b = k % 2;
+      if (k == 6) xp[1] = cut.plane(1);
+      if (k == 10) xp[2] = cut.plane(2);
+      if (me == 0 && k == 10) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) u[b] = mfma16x16x32(t[b][TP[n]], xp[XP[n]], u[b]);
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(r_s + p * 1024 + l16) = xp[p];
+      }
+      u[b] = mfma16x16x32(t[b][TP[n]], xp[XP[n]], u[b]);
+      if (k < 8) deal(k, 8, 0, 12, [&](int i) DL_INLINE { cut.step(8 + i); });
+      if (k < DH) kc[0][k] = read_kc(me, k);  // own tokens
+      dl_fence();
+    }
     dl_meet();  // 2
-    const auto kc = [&](int k, int d) DL_INLINE {  // K^T of tokens 32 k .., the wave's row block d
-      const uint2 lo = dl_channels<DK>(kt, 2 * k, DH * me + d, lane), hi = dl_channels<DK>(kt, 2 * k + 1, DH * me + d, lane);
-      return make_uint4(lo.x, lo.y, hi.x, hi.y);
-    };
-    uint4 kf0[DH], kf1[DH];
-    if (me) {  // the second half's tokens see the first's
-      uint4 t0[2][3], r[3];
+#pragma unroll
+    for (int d = 0; d < DH; ++d) S[d] *= whole;
+    if (me) {
+      uint4 r[3];
 #pragma unroll
       for (int p = 0; p < 3; ++p) r[p] = *reinterpret_cast<const uint4*>(r_s + p * 1024 + l16);
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int p = 0; p < 3; ++p) t0[b][p] = *reinterpret_cast<const uint4*>(ut + (6 * p + dl_frag(2 + b, 0)) * 1024 + l16);
+      dl_fence();
 #pragma unroll
       for (int n = 0; n < 6; ++n)
 #pragma unroll
         for (int b = 0; b < 2; ++b) u[b] = mfma16x16x32(t0[b][TP[n]], r[XP[n]], u[b]);
     }
-#pragma unroll
-    for (int d = 0; d < DH; ++d) {
-      kf0[d] = kc(me, d);  // own tokens
-      kf1[d] = kc(1 - me, d);
-    }
-#pragma unroll
-    for (int d = 0; d < DH; ++d) S[d] *= whole;
     uint4 xu[3], xo[3];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+      cut.set(4 * b, u[b][0] * keep[b].x);
+      cut.set(4 * b + 1, u[b][1] * keep[b].y);
+      cut.set(4 * b + 2, u[b][2] * keep[b].z);
+      cut.set(4 * b + 3, u[b][3] * keep[b].w);
       *reinterpret_cast<f32x4*>(u_s + (2 * me + b) * 1024 + l16) = u[b];
-      u[b] = f32x4{u[b][0] * keep[b].x, u[b][1] * keep[b].y, u[b][2] * keep[b].z, u[b][3] * keep[b].w};
     }
-    dl_planes<3>(u[0], u[1], xu);
 #pragma unroll
-    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(x_s[me] + p * 1024 + l16) = xu[p];
+    for (int n = 0; n < 20; ++n) {
+      cut.step(n);
+      if (n % 8 == 7 || n == 19) {
+        xu[n / 8] = cut.plane(n / 8);
+        *reinterpret_cast<uint4*>(px_s + me * 3072 + n / 8 * 1024 + l16) = xu[n / 8];
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < DH; ++d) kc[1][d] = read_kc(1 - me, d);
+    dl_fence();
     if (me == 0) {
 #pragma unroll
       for (int p = 2; p >= 0; --p)
 #pragma unroll
-        for (int d = 0; d < DH; ++d) S[d] = mfma16x16x32(kf0[d], xu[p], S[d]);
+        for (int d = 0; d < DH; ++d) S[d] = mfma16x16x32(kc[0][d], xu[p], S[d]);
     }
     dl_meet();  // 3
 #pragma unroll
-    for (int p = 0; p < 3; ++p) xo[p] = *reinterpret_cast<const uint4*>(x_s[1 - me] + p * 1024 + l16);
+    for (int p = 0; p < 3; ++p) xo[p] = *reinterpret_cast<const uint4*>(px_s + (1 - me) * 3072 + p * 1024 + l16);
+    dl_fence();
     if (me) {
 #pragma unroll
       for (int p = 2; p >= 0; --p)
 #pragma unroll
-        for (int d = 0; d < DH; ++d) S[d] = mfma16x16x32(kf0[d], xu[p], S[d]);
+        for (int d = 0; d < DH; ++d) S[d] = mfma16x16x32(kc[0][d], xu[p], S[d]);
     }
     dl_fence();
-    // with the split of the rows that are done
+    // with the split of the rows that are done, and the next chunk's K (of the last one's: not used)
 #pragma unroll
     for (int k = 0; k < 3 * DH; ++k) {
       const int d = 2 * (k / 6) + k % 2, p = 2 - k % 6 / 2;
-      S[d] = mfma16x16x32(kf1[d], xo[p], S[d]);
-      if (KH > 1) deal(k, 3 * DH, 8, 20 * (KH - 1), [&](int i) DL_INLINE { cut_state(i / 20, i % 20); });
+      S[d] = mfma16x16x32(kc[1][d], xo[p], S[d]);
+      if (k < 4 * KH) read_k(sm[(c & 1) ^ 1], k);
+      if (KH > 1) deal(k, 3 * DH, 7, 20 * (KH - 1), [&](int i) DL_INLINE { cut_state(i / 20, i % 20); });
       dl_fence();
     }
   }
@@ -699,7 +720,7 @@ hipError_t launch(const DeltaPackedArgs& a) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const long heads = long(d.n_seq) * d.Hv;
-  hipLaunchKernelGGL((k_delta_scan<DK>), dim3(unsigned(heads * (d.dv / 16))), dim3(256), 0, d.stream, a);
+  hipLaunchKernelGGL((k_delta_scan<DK>), dim3(unsigned(heads * (d.dv / 32))), dim3(512), 0, d.stream, a);
   return hipGetLastError();
 }
 
