@@ -341,12 +341,14 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   constexpr bool OWN = QT == 2;
   __shared__ __align__(1024) char smem[4 * TILE + (OWN ? BM * DH * 2 : 0)];
   char(&sm)[2][2][TILE] = *reinterpret_cast<char(*)[2][2][TILE]>(smem);
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int h = lane >> 5;
   const int kvh = blockIdx.x % a.Hkv;
   const int rest = blockIdx.x / a.Hkv;
   const int split = rest % a.splits;
   const int turn = rest / a.splits;
+  // PAGED: the first rows, all there are of a single token, on another SIMD from one piece of work to the next
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(PAGED ? ((tid >> 6) + rest) & 3 : tid >> 6);
+  const int h = lane >> 5;
 
   const Work wk = ap_find<PAGED>(a, turn < a.half ? turn : a.tiles - 1 - (turn - a.half), BM, lane);
   if (wk.r < 0) return;
@@ -468,6 +470,69 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
     }
   };
 
+  // K of tile t + 1 and V of tile t are in LDS when round t begins; what a wave copies for the next one, and from
+  // where
+  const auto advance = [&](int t) AP_INLINE {
+    if (PAGED) {  // K of tile t + 2 (the last one again where there is none) and V of tile t + 1
+      vp = vc + krow * vstep;
+      krow = first_row(ahead);
+      kp = kc + krow * kstep;
+      good0 = good1;
+      good1 = groups(ahead);
+      ahead = pages(t + 3);
+    } else {
+      vp += vtile;
+      if (t + 2 < t1) kp += ktile;
+    }
+    if (t + 2 >= tlast) {
+      if (t + 2 == tlast) cut(koff, kstep);
+      if (t + 1 == tlast) cut(voff, vstep);
+    }
+  };
+  const auto begin = [&]() AP_INLINE {
+    if (PAGED) {
+      const Pages x = pages(t0), y = pages(t0 + 1);
+      ahead = pages(t0 + 2);
+      good0 = groups(x);
+      good1 = groups(y);
+      const long row = first_row(x);
+      krow = first_row(y);
+      kp = kc + row * kstep;
+      vp = vc + row * vstep;
+    }
+    if (t0 == tlast) {
+      cut(koff, kstep);
+      cut(voff, vstep);
+    }
+    each([&](auto i) AP_INLINE { copy_k(i, 0); });
+  };
+  const auto second_k = [&]() AP_INLINE {
+    kp = PAGED ? kc + krow * kstep : kp + ktile;
+    if (t0 + 1 == tlast) cut(koff, kstep);
+    each([&](auto i) AP_INLINE { copy_k(i, 1); });
+  };
+  // PAGED: a wave without rows copies its part of the tiles and does nothing else, which leaves the matrix pipe
+  // to others where workgroups have few rows (in 2 pieces, 512 tokens and 14 single ones on up to 12000 tokens, 32/8
+  // heads of 128, 177 -> 164 us; 16 x 5 tokens on up to 8000, 16/4 heads of 64, 59 -> 56).
+  if (PAGED && wrow >= rows_here) {
+    if (t0 >= t1) return;
+    begin();
+    each([&](auto i) AP_INLINE { copy_v(i, 0); });
+    if (OWN && t0 < tlast) second_k();
+    wait_vm<0>();
+    asm volatile("s_barrier" ::: "memory");
+    if (!OWN && t0 < tlast) second_k();
+    for (int t = t0; t + 1 < t1; ++t) {
+      asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+      advance(t);
+      const int buf = (t - t0) & 1;
+      each([&](auto i) AP_INLINE { copy_v(i, buf ^ 1); });
+      each([&](auto i) AP_INLINE { copy_k(i, buf); });
+    }
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    return;
+  }
+
   f32x16 o[DT][QT];
   // reference maximum, the largest logit that it serves, its exponent, the sum of the weights
   float m[QT], most[QT], base[QT], l[QT][2];
@@ -562,21 +627,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   // c ^ ksw(r)), V of the first tile
   bf16x8 qf[QT][KS];
   if (t0 < t1) {
-    if (t0 == tlast) {
-      cut(koff, kstep);
-      cut(voff, vstep);
-    }
-    if (PAGED) {
-      const Pages x = pages(t0), y = pages(t0 + 1);
-      ahead = pages(t0 + 2);
-      good0 = groups(x);
-      good1 = groups(y);
-      const long row = first_row(x);
-      krow = first_row(y);
-      kp = kc + row * kstep;
-      vp = vc + row * vstep;
-    }
-    each([&](auto i) AP_INLINE { copy_k(i, 0); });
+    begin();
     const uint16_t* Qh = a.Q + long(q0 + qa) * a.qs + long(kvh) * G * DH;
     const uint32_t qdst = lds + uint32_t(mine - smem);
 #pragma unroll
@@ -587,9 +638,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
     }
     each([&](auto i) AP_INLINE { copy_v(i, 0); });
     if (OWN && t0 < tlast) {
-      kp = PAGED ? kc + krow * kstep : kp + ktile;
-      if (t0 + 1 == tlast) cut(koff, kstep);
-      each([&](auto i) AP_INLINE { copy_k(i, 1); });
+      second_k();
       wait_vm<2 * NI>();
     } else {
       wait_vm<NI>();
@@ -736,26 +785,11 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
     for (int b = 0; b < QT; ++b) mx[b] = m2[b];
   };
 
-  // K of tile t + 1 and V of tile t are in LDS when round t begins
   f32x16 s1[2][QT];
   auto step = [&](int t, auto buf, f32x16 (&s)[2][QT], f32x16 (&sn)[2][QT]) AP_INLINE {
     constexpr int B = decltype(buf)::value;
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (PAGED) {  // K of tile t + 2 (the last one again where there is none) and V of tile t + 1
-      vp = vc + krow * vstep;
-      krow = first_row(ahead);
-      kp = kc + krow * kstep;
-      good0 = good1;
-      good1 = groups(ahead);
-      ahead = pages(t + 3);
-    } else {
-      vp += vtile;
-      if (t + 2 < t1) kp += ktile;
-    }
-    if (t + 2 >= tlast) {
-      if (t + 2 == tlast) cut(koff, kstep);
-      if (t + 1 == tlast) cut(voff, vstep);
-    }
+    advance(t);
     round(std::true_type(), buf, &sm[B ^ 1][0][0], &sm[B][1][0], s, sn, mx);
     mask(t + 1, sn, mx);
     rebase(mx);
@@ -763,11 +797,7 @@ __global__ __launch_bounds__(256, QT == 2 ? 1 : 2) void k_attention_packed(Packe
   if (t0 < t1) {
     // every wave's part of the first K tile is there, every wave has its queries
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (!OWN && t0 < tlast) {
-      kp = PAGED ? kc + krow * kstep : kp + ktile;
-      if (t0 + 1 == tlast) cut(koff, kstep);
-      each([&](auto i) AP_INLINE { copy_k(i, 1); });
-    }
+    if (!OWN && t0 < tlast) second_k();
     scores(&sm[0][0][0], s0);
     maxima(s0, mx);
     mask(t0, s0, mx);
@@ -912,11 +942,11 @@ hipError_t attention_packed(const PackedArgs& a) {
 }
 
 size_t attention_paged_workspace(int n_seq, int Nq, int max_pages, int page, int Hq, int Hkv, int dh) {
-  return packed_workspace(n_seq, Nq, paged_keys(n_seq, max_pages, page), Hq, Hkv, dh);
+  return paged_workspace(n_seq, Nq, max_pages, page, Hq, Hkv, dh);
 }
 
 hipError_t attention_paged(const PackedArgs& a, const Paged& g) {
-  const PackedPlan p = packed_plan(a.n_seq, a.Nq, paged_keys(a.n_seq, g.max_pages, g.page), a.Hq, a.Hkv, a.dh, a.window);
+  const PackedPlan p = paged_plan(a.n_seq, a.Nq, g.max_pages, g.page, a.Hq, a.Hkv, a.dh, a.window);
   PackedDev d = ap_device(a, p);
   d.table = g.table;
   d.lengths = g.lengths;

@@ -90,14 +90,53 @@ inline PackedPlan packed_plan(int n_seq, int Nq, long Nk, int Hq, int Hkv, int d
   return p;
 }
 
-// The keys that a plan for a paged cache is made for: as many as the page tables can hold, since only the
-// device knows the lengths.
-inline long paged_keys(int n_seq, int max_pages, int page) { return long(n_seq) * max_pages * page; }
-
 inline size_t packed_workspace(int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh) {
   // the window is not known here; with one there are no more pieces than without
   const int a = packed_splits(1, n_seq, Nq, Nk, Hq, Hkv, dh, 0);
   const int b = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, 0);
+  const int n = a > b ? a : b;
+  return n > 1 ? size_t(n) * Nq * Hq * (dh + 2) * 4 : 0;
+}
+
+// New tokens over a paged cache: the rules above with as many keys as the page tables can hold, since only the
+// device knows the lengths.
+inline long paged_keys(int n_seq, int max_pages, int page) { return long(n_seq) * max_pages * page; }
+// Pieces that the keys are split into where there are several sequences: lengths and numbers of rows differ then, so
+// a quarter more workgroups than the chip holds at once, and the joining weighs half as much again. Best, and what
+// the rule for one sequence takes, of a sweep: 16 x 5 tokens on up to 8000, 16/4 heads of 64, in 12 pieces 27 us, in 3
+// 42 us; 512 tokens and 14 single ones on up to 12000, 32/8 heads of 128, in 2 pieces 164 us (3: 175), whole 258;
+// up to 64 tokens each of 16 on up to 8000 in 3 pieces 77 us, whole 128; 4 x 500 on up to 6000 in 2 119 us, whole 143;
+// 8 x 16 on 4000 in 6 35 us, in 2 43; 2000 tokens and 30 single ones on up to 8000, 16/4 heads of 64, in 3 96 us, whole 122.
+inline int paged_splits(int qt, int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh, int window) {
+  if (n_seq == 1) return packed_splits(qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
+  const long keys = packed_keys(n_seq, Nk, window), wgs = packed_wgs(qt, n_seq, Nq, Hq, Hkv);
+  const long places = qt == 2 ? 256 : dh == 64 ? 768 : 512;
+  long most = (5 * places / 4 + wgs / 2) / wgs;
+  if (most > keys / 256) most = keys / 256;
+  if (most > PLAN_MAX_SPLITS) most = PLAN_MAX_SPLITS;
+  const double tiles = keys / 64 * (qt == 2 ? 1.5 : dh == 64 ? 0.5 : 0.75);
+  const double join = 1.5 * double(Nq) * Hq * dh * 8 / 4e6;
+  int best = 1;
+  double cost = tiles;
+  for (int n = 2; n <= most; ++n) {
+    const double t = tiles / n + 5 + n * join;
+    if (t < cost) cost = t, best = n;
+  }
+  return best;
+}
+inline PackedPlan paged_plan(int n_seq, int Nq, int max_pages, int page, int Hq, int Hkv, int dh, int window) {
+  const long Nk = paged_keys(n_seq, max_pages, page);
+  PackedPlan p = packed_plan(n_seq, Nq, Nk, Hq, Hkv, dh, window);
+  if (n_seq > 1) {
+    p.splits = paged_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
+    p.half = p.tiles;
+  }
+  return p;
+}
+inline size_t paged_workspace(int n_seq, int Nq, int max_pages, int page, int Hq, int Hkv, int dh) {
+  // the window is not known here; with one there are no more pieces than without
+  const long Nk = paged_keys(n_seq, max_pages, page);
+  const int a = paged_splits(1, n_seq, Nq, Nk, Hq, Hkv, dh, 0), b = paged_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, 0);
   const int n = a > b ? a : b;
   return n > 1 ? size_t(n) * Nq * Hq * (dh + 2) * 4 : 0;
 }

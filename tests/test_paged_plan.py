@@ -1,0 +1,65 @@
+"""The rules by which attention of new tokens over a paged cache chooses its form (csrc/attn_plan.hpp), compiled for
+the host: no call needs more workspace than the query says, and the forms that the GPU tests mean are taken."""
+import ctypes
+import random
+import subprocess
+
+import pytest
+
+import chunked_weight_sequence_amd as ttt
+from plan_shim import CSRC
+
+SOURCE = """
+#include "attn_plan.hpp"
+using namespace ttt;
+extern "C" void paged(int n, int Nq, int max_pages, int page, int Hq, int Hkv, int dh, int window, long* out) {
+  const PackedPlan p = paged_plan(n, Nq, max_pages, page, Hq, Hkv, dh, window);
+  out[0] = p.qt, out[1] = p.splits, out[2] = p.tiles, out[3] = p.half;
+  out[4] = long(paged_workspace(n, Nq, max_pages, page, Hq, Hkv, dh));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    so = str(tmp_path_factory.mktemp("paged") / "plan.so")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, "-x", "c++", "-", "-o", so],
+                   input=SOURCE, text=True, check=True)
+    fn = ctypes.CDLL(so).paged
+
+    def ask(*args):
+        out = (ctypes.c_long * 5)()
+        fn(*(ctypes.c_int(int(x)) for x in args), out)
+        return dict(zip(("qt", "splits", "tiles", "half", "workspace"), out))
+    return ask
+
+
+def test_no_call_needs_more_workspace_than_the_query_says(plan):
+    rng = random.Random(7)
+
+    def log(lo, hi):
+        return int(lo * (hi / lo) ** rng.random())
+    for _ in range(20000):
+        Hkv = rng.choice([1, 2, 3, 4, 8, 16, 32])
+        Hq, dh = Hkv * rng.choice([1, 2, 4, 7, 8, 40]), rng.choice([64, 128])
+        n, window, page = rng.choice([1, log(1, 300)]), rng.choice([0, log(1, 30000)]), rng.choice([16, 64, 256])
+        Nq, pages = log(1, 40000), log(1, 200000 // page)
+        p = plan(n, Nq, pages, page, Hq, Hkv, dh, window)
+        need = p["splits"] * Nq * Hq * (dh + 2) * 4 if p["splits"] > 1 else 0
+        assert need <= p["workspace"], (n, Nq, pages, page, Hq, Hkv, dh, window, p)
+        assert p["workspace"] == ttt.lib().ttt_attention_paged_workspace(n, Nq, pages, page, Hq, Hkv, dh)
+        assert 1 <= p["splits"] <= 64 and 0 <= p["half"] <= p["tiles"] and p["qt"] in (1, 2)
+
+
+def test_forms(plan):
+    """Rows by 128 and by 256, whole and in pieces, of one and of several sequences."""
+    got = {name: plan(*a) for name, a in dict(
+        one=(1, 512, 256, 64, 32, 8, 128, 0), drafts=(16, 48, 500, 16, 16, 4, 64, 0), whole=(4, 8000, 32, 256, 32, 32, 64, 2048),
+        mixed=(16, 526, 375, 32, 32, 8, 128, 0), wide=(8, 135, 250, 16, 32, 8, 128, 0), prompt=(1, 2100, 33, 64, 32, 8, 128, 0),
+        short=(16, 790, 19, 16, 32, 8, 128, 0)).items()}
+    assert (got["one"]["qt"], got["one"]["splits"]) == (2, 4)
+    assert got["drafts"]["qt"] == 1 and got["drafts"]["splits"] >= 8
+    assert (got["whole"]["qt"], got["whole"]["splits"]) == (1, 1)
+    assert (got["mixed"]["qt"], got["mixed"]["splits"]) == (1, 3)
+    assert got["wide"]["qt"] == 2 and got["wide"]["splits"] > 1
+    assert got["short"]["splits"] == 1 and got["prompt"]["splits"] == 1
