@@ -142,11 +142,11 @@ __device__ __forceinline__ f32x4 dl_mma_f32(float a, float b, f32x4 c) {
 // --------------------------------------------------------------------------------------------
 template <int DK>
 __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
-  constexpr int TILE = DL_C * DK * 2, LW = 68;  // row of L and T in floats
-  __shared__ __align__(1024) char kq[2 * TILE > DL_C * LW * 4 ? 2 * TILE : DL_C * LW * 4];  // K, Q; then T
+  constexpr int KS = DK / 32, LW = 68, DW = 20;  // contraction steps; rows of L, then T, and of the diagonal blocks, in floats
   __shared__ __align__(16) float ls[DL_C][LW];
-  __shared__ double gs[DL_C];
-  __shared__ float bs[DL_C], rk_s[DL_C], rq_s[DL_C];
+  __shared__ __align__(16) float ds[4][16][DW];
+  __shared__ double gs[DL_C];  // log2 of the decays, summed up
+  __shared__ __align__(16) float bs[DL_C], rk_s[DL_C], rq_s[DL_C];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int h = blockIdx.x % a.d.Hv, id = blockIdx.x / a.d.Hv;
   const DeltaChunk sq = dl_sequence(a, dl_find(a, id, lane));
@@ -154,40 +154,40 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
   if (id < sq.base || left <= 0) return;
   const int hk = h / (a.d.Hv / a.d.Hk);
   const long tok = sq.q0 + t0;
-  char* const ks = kq;
-  char* const qs = kq + TILE;
-  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(kq));
+  const int g4 = 4 * (lane >> 4), i0 = 16 * wave + (lane & 15);  // a lane's row of K and Q, and of L and A
+  // rows of K and Q as operands: lane l has row l % 16, channels 32 s + 8 (l / 16) ..; row blocks up to the wave's own
+  const auto load = [&](const void* x, long stride, int rb, uint4 (&f)[KS]) DL_INLINE {
+    const uint16_t* p = static_cast<const uint16_t*>(x) + (tok + min(16 * rb + (lane & 15), left - 1)) * stride + hk * DK + 2 * g4;
 #pragma unroll
-  for (int i = 0; i < TILE / 4096; ++i) {
-    dl_copy_rows<DK>(4 * i + wave, static_cast<const uint16_t*>(a.d.K) + tok * a.d.ks + hk * DK, a.d.ks, left, lds, lane);
-    dl_copy_rows<DK>(4 * i + wave, static_cast<const uint16_t*>(a.d.Q) + tok * a.d.qs + hk * DK, a.d.qs, left, lds + TILE, lane);
-  }
+    for (int s = 0; s < KS; ++s) f[s] = *reinterpret_cast<const uint4*>(p + 32 * s);
+  };
+  uint4 kf[4][KS], qf[KS];
+  load(a.d.K, a.d.ks, wave, kf[3]);
+  load(a.d.Q, a.d.qs, wave, qf);
+#pragma unroll
+  for (int jb = 0; jb < 3; ++jb)
+    if (jb < wave) load(a.d.K, a.d.ks, jb, kf[jb]);
   if (wave == 0) {
     // sums of the gates in fp64: their differences count, also behind a gate that forgets everything (-inf:
     // e^-1000 is 0 as well, and sums of it stay finite)
     const long at = (tok + min(lane, left - 1)) * a.d.Hv + h;
     float g = a.d.g[at];
+    const float beta = a.d.beta[at];
     g = lane < left ? (g < -1000.f ? -1000.f : g) : 0.f;
-    double G = g;
+    double G = g * 1.4426950408889634074;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
       const double up = __shfl_up(G, d);
       if (lane >= d) G += up;
     }
     gs[lane] = G;
-    bs[lane] = lane < left ? a.d.beta[at] : 0.f;
+    bs[lane] = lane < left ? beta : 0.f;
   }
-  wait_vm<0>();
-  __syncthreads();
   {
-    // the norms: four threads to a row
-    const int r = tid >> 2, part = tid & 3;
     float kk = 0.f, qq = 0.f;
 #pragma unroll
-    for (int i = 0; i < DK / 32; ++i) {  // 8 channels: any order, each once
-      const int at = r * DK * 2 + 16 * ((4 * i + part) ^ (r & (DK / 8 - 1)));
-      const uint4 kv = *reinterpret_cast<const uint4*>(ks + at), qv = *reinterpret_cast<const uint4*>(qs + at);
-      const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t kw[4] = {kf[3][s].x, kf[3][s].y, kf[3][s].z, kf[3][s].w}, qw[4] = {qf[s].x, qf[s].y, qf[s].z, qf[s].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float k0 = __uint_as_float(kw[e] << 16), k1 = __uint_as_float(kw[e] & 0xFFFF0000u);
@@ -196,13 +196,14 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
         qq = fmaf(q0, q0, fmaf(q1, q1, qq));
       }
     }
-    kk += __shfl_xor(kk, 1);
-    qq += __shfl_xor(qq, 1);
-    kk += __shfl_xor(kk, 2);
-    qq += __shfl_xor(qq, 2);
-    if (part == 0) {
-      rk_s[r] = a.d.norm ? rsqrtf(kk + a.d.eps) : 1.f;
-      rq_s[r] = a.d.scale * (a.d.norm ? rsqrtf(qq + a.d.eps) : 1.f);
+#pragma unroll
+    for (int d = 16; d < 64; d *= 2) {
+      kk += __shfl_xor(kk, d);
+      qq += __shfl_xor(qq, d);
+    }
+    if (lane < 16) {
+      rk_s[i0] = a.d.norm ? rsqrtf(kk + a.d.eps) : 1.f;
+      rq_s[i0] = a.d.scale * (a.d.norm ? rsqrtf(qq + a.d.eps) : 1.f);
     }
   }
   __syncthreads();
@@ -210,35 +211,29 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
   // Row block `wave` of L and A, as blocks [j, i] of products K K^T and K Q^T: lane l has row i = l % 16 of the
   // block and its columns j = 4 (l / 16) ..
   char* const unit = static_cast<char*>(a.ws) + (size_t(id) * a.d.Hv + h) * DL_UNIT;
-  const int g4 = 4 * (lane >> 4), i0 = 16 * wave + (lane & 15);
   {
     const double gi = gs[i0];
     const float bi = bs[i0] * rk_s[i0], qi = i0 < left ? rq_s[i0] : 0.f;
-    uint4 kf[DK / 32], qf[DK / 32];
-#pragma unroll
-    for (int s = 0; s < DK / 32; ++s) {
-      kf[s] = dl_row<DK>(ks, wave, s, lane);
-      qf[s] = dl_row<DK>(qs, wave, s, lane);
-    }
     uint2 aw[4];
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
       aw[jb] = make_uint2(0, 0);
       if (jb > wave) continue;
-      f32x4 kk = {0.f, 0.f, 0.f, 0.f}, kq2 = kk;
+      f32x4 kk = {0.f, 0.f, 0.f, 0.f}, kq = kk;
 #pragma unroll
-      for (int s = 0; s < DK / 32; ++s) {
-        const uint4 f = dl_row<DK>(ks, jb, s, lane);
-        kk = mfma16x16x32(f, kf[s], kk);
-        kq2 = mfma16x16x32(f, qf[s], kq2);
+      for (int s = 0; s < KS; ++s) {
+        const uint4 f = jb < 3 && jb < wave ? kf[jb][s] : kf[3][s];
+        kk = mfma16x16x32(f, kf[3][s], kk);
+        kq = mfma16x16x32(f, qf[s], kq);
       }
+      const float4 rk = *reinterpret_cast<const float4*>(&rk_s[16 * jb + g4]);
       float lv[4], av[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int j = 16 * jb + g4 + r;
-        const float decay = expf(float(gi - gs[j])) * rk_s[j];
+        const float decay = __builtin_amdgcn_exp2f(float(gi - gs[j])) * (r == 0 ? rk.x : r == 1 ? rk.y : r == 2 ? rk.z : rk.w);
         lv[r] = j < i0 && i0 < left ? bi * decay * kk[r] : 0.f;
-        av[r] = j <= i0 && i0 < left ? qi * decay * kq2[r] : 0.f;
+        av[r] = j <= i0 && i0 < left ? qi * decay * kq[r] : 0.f;
       }
       *reinterpret_cast<float4*>(&ls[i0][16 * jb + g4]) = make_float4(lv[0], lv[1], lv[2], lv[3]);
       aw[jb] = make_uint2(pack2bf(av[0], av[1]), pack2bf(av[2], av[3]));
@@ -249,61 +244,69 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
         *reinterpret_cast<uint4*>(unit + (18 + dl_frag(wave, s)) * 1024 + 16 * lane) =
             make_uint4(aw[2 * s].x, aw[2 * s].y, aw[2 * s + 1].x, aw[2 * s + 1].y);
   }
-  if (wave == 3) {
+  if (wave == 0) {
     float* f = reinterpret_cast<float*>(unit + DL_TOK);
     const double G = gs[lane], all = gs[DL_C - 1];
-    f[DL_FROM + lane] = expf(float(G)) * rk_s[lane];
-    f[DL_LEFT + lane] = expf(float(all - G)) * rk_s[lane];
-    f[DL_OUT + lane] = expf(float(G)) * rq_s[lane];
-    f[DL_WHOLE + lane] = expf(float(all));
+    const float from = __builtin_amdgcn_exp2f(float(G));
+    f[DL_FROM + lane] = from * rk_s[lane];
+    f[DL_LEFT + lane] = __builtin_amdgcn_exp2f(float(all - G)) * rk_s[lane];
+    f[DL_OUT + lane] = from * rq_s[lane];
+    f[DL_WHOLE + lane] = __builtin_amdgcn_exp2f(float(all));
   }
-  __syncthreads();  // L is there; K and Q have been read
-
-  // The inverse of 1 + L: the four diagonal blocks by forward substitution, a column to a lane, then block
-  // column `wave` from the top: T_ij = -T_ii sum_k L_ik T_kj.
-  float(*const ts)[LW] = reinterpret_cast<float(*)[LW]>(kq);
+  // The inverse of 1 + L: the wave's diagonal block by forward substitution, a column to a lane (lanes 16 .. 63 repeat
+  // the first 16; the rows are the wave's own)
   {
-    const int c = lane & 15, b = wave;  // lanes 16 .. 63 repeat the first 16
+    const int c = lane & 15;
     float t[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float x = i == c ? 1.f : 0.f;
+      float x[4] = {i == c ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < i; ++k) x = fmaf(-ls[16 * b + i][16 * b + k], t[k], x);
-      t[i] = x;
+      for (int k = 0; k < i; k += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(&ls[16 * wave + i][16 * wave + k]);
+        x[0] = fmaf(-l.x, t[k], x[0]);
+        if (k + 1 < i) x[1] = fmaf(-l.y, t[k + 1], x[1]);
+        if (k + 2 < i) x[2] = fmaf(-l.z, t[k + 2], x[2]);
+        if (k + 3 < i) x[3] = fmaf(-l.w, t[k + 3], x[3]);
+      }
+      t[i] = (x[0] + x[1]) + (x[2] + x[3]);
     }
     if (lane < 16)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ts[16 * b + i][16 * b + c] = t[i];
+      for (int i = 0; i < 16; ++i) ds[wave][i][c] = t[i];
   }
   __syncthreads();
-  {
-    f32x4 col[4];  // T_kj, j = wave, as operands: column l % 16, rows 4 (l / 16) ..
+  // then block column `wave` from the top: T_ij = -T_ii sum_k L_ik T_kj
+  f32x4 col[4];  // T_kj, j = wave, as operands: column l % 16, rows 4 (l / 16) ..
 #pragma unroll
-    for (int r = 0; r < 4; ++r) col[0][r] = ts[16 * wave + g4 + r][16 * wave + (lane & 15)];
+  for (int r = 0; r < 4; ++r) col[0][r] = ds[wave][g4 + r][lane & 15];
 #pragma unroll
-    for (int n = 1; n < 4; ++n) {
-      const int ib = wave + n;
-      if (ib > 3) break;
-      f32x4 y = {0.f, 0.f, 0.f, 0.f};
+  for (int n = 1; n < 4; ++n) {
+    const int ib = wave + n;
+    if (ib > 3) break;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < n; ++k) {
-        const float4 l = *reinterpret_cast<const float4*>(&ls[16 * ib + (lane & 15)][16 * (wave + k) + g4]);
-        y = dl_mma_f32(l.x, col[k][0], y);
-        y = dl_mma_f32(l.y, col[k][1], y);
-        y = dl_mma_f32(l.z, col[k][2], y);
-        y = dl_mma_f32(l.w, col[k][3], y);
-      }
-      const float4 d = *reinterpret_cast<const float4*>(&ts[16 * ib + (lane & 15)][16 * ib + g4]);
-      f32x4 z = {0.f, 0.f, 0.f, 0.f};
-      z = dl_mma_f32(d.x, -y[0], z);
-      z = dl_mma_f32(d.y, -y[1], z);
-      z = dl_mma_f32(d.z, -y[2], z);
-      z = dl_mma_f32(d.w, -y[3], z);
-      col[n] = z;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) ts[16 * ib + g4 + r][16 * wave + (lane & 15)] = z[r];
+    for (int k = 0; k < n; ++k) {
+      const float4 l = *reinterpret_cast<const float4*>(&ls[16 * ib + (lane & 15)][16 * (wave + k) + g4]);
+      y = dl_mma_f32(l.x, col[k][0], y);
+      y = dl_mma_f32(l.y, col[k][1], y);
+      y = dl_mma_f32(l.z, col[k][2], y);
+      y = dl_mma_f32(l.w, col[k][3], y);
     }
+    const float4 d = *reinterpret_cast<const float4*>(&ds[ib][lane & 15][g4]);
+    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+    z = dl_mma_f32(d.x, -y[0], z);
+    z = dl_mma_f32(d.y, -y[1], z);
+    z = dl_mma_f32(d.z, -y[2], z);
+    z = dl_mma_f32(d.w, -y[3], z);
+    col[n] = z;
+  }
+  __syncthreads();  // L has been read: T takes its place
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    if (wave + n > 3) break;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) ls[16 * (wave + n) + g4 + r][16 * wave + (lane & 15)] = col[n][r];
   }
   __syncthreads();
   // row block `wave` of T, its columns times beta, in three planes
@@ -312,9 +315,11 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
     if (s > wave / 2) break;
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int jb = 2 * s + e / 4, j = 16 * jb + g4 + e % 4;
-      x[e] = jb <= wave ? ts[i0][j] * bs[j] : 0.f;
+    for (int e = 0; e < 8; e += 4) {
+      const int jb = 2 * s + e / 4, j = 16 * jb + g4;
+      const float4 t = jb <= wave ? *reinterpret_cast<const float4*>(&ls[i0][j]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 b = *reinterpret_cast<const float4*>(&bs[j]);
+      x[e] = t.x * b.x, x[e + 1] = t.y * b.y, x[e + 2] = t.z * b.z, x[e + 3] = t.w * b.w;
     }
 #pragma unroll
     for (int p = 0; p < 3; ++p)
