@@ -10,10 +10,11 @@
 // saturates; 2^-126 keeps scales normal numbers, and rows of zeros from dividing by zero).
 //
 // Bound by HBM: each input is read once and each output written once. A row is held in registers by one
-// wave, or by a workgroup's four where there are few rows or long ones, 8 channels of a lane side by side,
-// and is read while the one before it is worked on. The weights stay in registers from row to row: read
-// again for each, they would be as many bytes through L2 as a bf16 row itself. The largest |h w| of a scale is
-// found together with the sum of squares, since the factor between h w and y is one of the whole row.
+// wave, or by a workgroup's four, 8 channels of a lane side by side; rows are taken by new workgroups, not in a
+// loop, with which fewer are under way at once. The largest |h w| of a scale is found together with the sum of
+// squares, since the factor between h w and y is one of the whole row. With a residual: 32768 x 2560 bf16 to e4m3 by
+// 128, 587 MB, 112 us (5.2 TB/s; in a loop, with the next row read ahead and the weights kept, 165), to bf16, 671 MB,
+// 125 us; 4099 x 1000 fp32, 66 MB, 14 us; 512 x 2560 bf16 6 us.
 #include <type_traits>
 
 #include "common.hpp"
@@ -77,41 +78,35 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8]) {
 // W waves to a row, CH times 8 channels to a lane.
 template <typename T, bool E4M3, int W, int CH>
 __global__ __launch_bounds__(256) void k_add_norm(AddNormArgs a) {
-  __shared__ float2 part[2][4];  // of every second row in turn, so that one barrier a row is enough
+  __shared__ float2 part[2][4];  // of the sums, and of those that are taken again
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int li = W == 1 ? lane : tid, D = a.D, n8 = D >> 3;
-  const float inv_d = 1.f / float(D);
-  const T *X = static_cast<const T*>(a.X), *R = static_cast<const T*>(a.R);
+  const long n = long(blockIdx.x) * (4 / W) + (W == 1 ? wave : 0);
+  if (n >= a.N) return;  // the same for all waves of a row
+  const T *X = static_cast<const T*>(a.X) + n * a.xs, *R = static_cast<const T*>(a.R) + n * a.rs;
+  const bool with_r = a.R != nullptr;
 
   bool on[CH];
-  float w[CH][8];
+  Eight<T> x[CH], r[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     on[i] = i * 64 * W + li < n8;
+    if (on[i]) {
+      x[i].load(X + 8 * (i * 64 * W + li));
+      if (with_r) r[i].load(R + 8 * (i * 64 * W + li));
+    }
+  }
+  float w[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
-  }
-  const long step = long(gridDim.x) * (4 / W);
-  long n = long(blockIdx.x) * (4 / W) + (W == 1 ? wave : 0);
-  Eight<T> x[CH], r[CH];
-  const auto load = [&](long row) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-      if (on[i]) {
-        x[i].load(X + row * a.xs + 8 * (i * 64 * W + li));
-        if (R) r[i].load(R + row * a.rs + 8 * (i * 64 * W + li));
-      }
-  };
-  if (n < a.N) load(n);
-  if (a.w) {
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-      if (on[i]) {
-        const float4* p = reinterpret_cast<const float4*>(a.w + 8 * (i * 64 * W + li));
-        const float4 u = p[0], v = p[1];
-        w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
-        w[i][4] = v.x, w[i][5] = v.y, w[i][6] = v.z, w[i][7] = v.w;
-      }
+    if (a.w && on[i]) {
+      const float4* p = reinterpret_cast<const float4*>(a.w + 8 * (i * 64 * W + li));
+      const float4 u = p[0], v = p[1];
+      w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+      w[i][4] = v.x, w[i][5] = v.y, w[i][6] = v.z, w[i][7] = v.w;
+    }
   }
   // sum of squares and largest |h w| of the row
   int turn = 0;
@@ -134,116 +129,120 @@ __global__ __launch_bounds__(256) void k_add_norm(AddNormArgs a) {
       turn ^= 1;
     }
   };
-  for (; n < a.N; n += step) {  // the same rows for all waves of a row
-    float h[CH][8];
+  float h[CH][8], ss = 0.f, top = 0.f;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
+  for (int i = 0; i < CH; ++i) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
-      if (!on[i]) continue;
-      x[i].unpack(h[i]);
-      if (R) {
-        float b[8];
-        r[i].unpack(b);
+    for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
+    if (!on[i]) continue;
+    x[i].unpack(h[i]);
+    if (with_r) {
+      float b[8];
+      r[i].unpack(b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] += b[e];
-      }
-      if (a.S) {
-        Eight<T> s;
-        s.pack(h[i]);
-        s.store(static_cast<T*>(a.S) + n * a.ss + 8 * (i * 64 * W + li));
-      }
+      for (int e = 0; e < 8; ++e) h[i][e] += b[e];
     }
-    if (n + step < a.N) load(n + step);
-    float ss = 0.f, top = 0.f;
+    if (a.S) {
+      Eight<T> s;
+      s.pack(h[i]);
+      s.store(static_cast<T*>(a.S) + n * a.ss + 8 * (i * 64 * W + li));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      ss = fmaf(h[i][e], h[i][e], ss);
+      if (E4M3) top = fmaxf(top, fabsf(h[i][e] * w[i][e]));
+    }
+  }
+  reduce(ss, top);
+  float eps = a.eps;
+  // Squares that leave fp32 (values past 2^63, or all below 2^-40 where eps does not hide them): the row is
+  // scaled by a power of two first. All lanes of a row decide alike.
+  const bool large = !(ss < 0x1p126f), small = ss < 0x1p-80f && eps < 0x1p-80f;
+  if (__builtin_expect(large || small, 0)) {
+    const float s = large ? 0x1p-72f : 0x1p96f;
+    ss = top = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
+        h[i][e] *= s;
         ss = fmaf(h[i][e], h[i][e], ss);
         if (E4M3) top = fmaxf(top, fabsf(h[i][e] * w[i][e]));
       }
     reduce(ss, top);
-    float eps = a.eps;
-    // Squares that leave fp32 (values past 2^63, or all below 2^-40 where eps does not hide them): the row is
-    // scaled by a power of two first. All lanes of a row decide alike.
-    const bool large = !(ss < 0x1p126f), small = ss < 0x1p-80f && eps < 0x1p-80f;
-    if (__builtin_expect(large || small, 0)) {
-      const float s = large ? 0x1p-72f : 0x1p96f;
-      ss = top = 0.f;
+    eps = eps * s * s;
+  }
+  const float rs = rsqrtf(ss / float(D) + eps);
+  if constexpr (E4M3) {
+    const int per = a.group >> 3;  // lanes to a group, a power of two
+    const long sn = a.group ? n * (D / a.group) : n;
+    float scale = fmaxf(top * rs / 448.f, 0x1p-126f), inv = 1.f / scale;
+    if (!a.group && li == 0) a.scales[sn] = scale;
 #pragma unroll
-      for (int i = 0; i < CH; ++i)
+    for (int i = 0; i < CH; ++i) {
+      float y[8], g = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          h[i][e] *= s;
-          ss = fmaf(h[i][e], h[i][e], ss);
-          if (E4M3) top = fmaxf(top, fabsf(h[i][e] * w[i][e]));
-        }
-      reduce(ss, top);
-      eps = eps * s * s;
+      for (int e = 0; e < 8; ++e) {
+        y[e] = h[i][e] * rs * w[i][e];
+        g = fmaxf(g, fabsf(y[e]));
+      }
+      if (a.group) {  // a group's lanes are all on or all off
+        for (int d = 1; d < per; d *= 2) g = fmaxf(g, __shfl_xor(g, d));
+        scale = fmaxf(g / 448.f, 0x1p-126f);
+        inv = 1.f / scale;
+        const int c = i * 64 * W + li;
+        if (on[i] && (c & (per - 1)) == 0) a.scales[sn + c / per] = scale;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= inv;
+      if (on[i])
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + n * a.ys + 8 * (i * 64 * W + li)) = pack8_e4m3(y);
     }
-    const float rs = rsqrtf(ss * inv_d + eps);
-    if constexpr (E4M3) {
-      const int per = a.group >> 3;  // lanes to a group, a power of two
-      const long sn = a.group ? n * (D / a.group) : n;
-      float scale = fmaxf(top * rs / 448.f, 0x1p-126f), inv = 1.f / scale;
-      if (!a.group && li == 0) a.scales[sn] = scale;
+  } else {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        float y[8], g = 0.f;
+    for (int i = 0; i < CH; ++i) {
+      float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = h[i][e] * rs * w[i][e];
-          g = fmaxf(g, fabsf(y[e]));
-        }
-        if (a.group) {  // a group's lanes are all on or all off
-          for (int d = 1; d < per; d *= 2) g = fmaxf(g, __shfl_xor(g, d));
-          scale = fmaxf(g / 448.f, 0x1p-126f);
-          inv = 1.f / scale;
-          const int c = i * 64 * W + li;
-          if (on[i] && (c & (per - 1)) == 0) a.scales[sn + c / per] = scale;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= inv;
-        if (on[i])
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + n * a.ys + 8 * (i * 64 * W + li)) = pack8_e4m3(y);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = h[i][e] * rs * w[i][e];
-        Eight<T> o;
-        o.pack(y);
-        if (on[i]) o.store(static_cast<T*>(a.Y) + n * a.ys + 8 * (i * 64 * W + li));
-      }
+      for (int e = 0; e < 8; ++e) y[e] = h[i][e] * rs * w[i][e];
+      Eight<T> o;
+      o.pack(y);
+      if (on[i]) o.store(static_cast<T*>(a.Y) + n * a.ys + 8 * (i * 64 * W + li));
     }
   }
 }
 
-template <typename T, bool E4M3, int W>
-void launch(const AddNormArgs& a, int ch, dim3 grid) {
-  const dim3 block(256);
-  if (ch <= 1) hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 1>), grid, block, 0, a.stream, a);
-  else if (ch <= 2) hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 2>), grid, block, 0, a.stream, a);
-  else if (ch <= 3) hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 3>), grid, block, 0, a.stream, a);
-  else if (ch <= 5) hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 5>), grid, block, 0, a.stream, a);
-  else hipLaunchKernelGGL((k_add_norm<T, E4M3, W, 8>), grid, block, 0, a.stream, a);
+template <typename T, bool E4M3, int W, int CH>
+void launch(const AddNormArgs& a) {
+  const long rows = 4 / W;
+  hipLaunchKernelGGL((k_add_norm<T, E4M3, W, CH>), dim3(unsigned((a.N + rows - 1) / rows)), dim3(256), 0, a.stream, a);
+}
+template <typename T, bool E4M3>
+void launch(const AddNormArgs& a) {
+  // Four waves to a row from 2048 channels on, and past 512 where rows are few. One wave / four, with a residual: bf16
+  // 32768 x 2560 124 / 126 us, 4096 x 4096 23.6 / 23.2, 16384 x 4096 108 / 100, 16384 x 1024 22.9 / 26.6, 4096 x 512
+  // 6.5 / 8.0, but 512 x 1536 6.3 / 5.6; fp32 16384 x 2048 107 / 103, 65536 x 128 29 / 50.
+  const int n8 = a.D / 8;
+  if (n8 >= 256 || (a.N < 2048 && n8 > 64)) {
+    const int ch = (n8 + 255) / 256;
+    if (ch <= 1) launch<T, E4M3, 4, 1>(a);
+    else if (ch <= 2) launch<T, E4M3, 4, 2>(a);
+    else if (ch <= 3) launch<T, E4M3, 4, 3>(a);
+    else if (ch <= 5) launch<T, E4M3, 4, 5>(a);
+    else launch<T, E4M3, 4, 8>(a);
+  } else {
+    const int ch = (n8 + 63) / 64;
+    if (ch <= 1) launch<T, E4M3, 1, 1>(a);
+    else if (ch <= 2) launch<T, E4M3, 1, 2>(a);
+    else if (ch <= 3) launch<T, E4M3, 1, 3>(a);
+    else launch<T, E4M3, 1, 4>(a);
+  }
 }
 
 }  // namespace
 
 hipError_t add_norm(const AddNormArgs& a) {
-  const int n8 = a.D / 8;
-  const int w = a.N >= 2048 && n8 <= 8 * 64 ? 1 : 4;
-  const int ch = (n8 + 64 * w - 1) / (64 * w);
-  const long wgs = (a.N + 4 / w - 1) / (4 / w);
-  const dim3 grid(unsigned(wgs < 1024 ? wgs : 1024));
-  if (a.bf16 && a.e4m3) w == 1 ? launch<uint16_t, true, 1>(a, ch, grid) : launch<uint16_t, true, 4>(a, ch, grid);
-  else if (a.bf16) w == 1 ? launch<uint16_t, false, 1>(a, ch, grid) : launch<uint16_t, false, 4>(a, ch, grid);
-  else if (a.e4m3) w == 1 ? launch<float, true, 1>(a, ch, grid) : launch<float, true, 4>(a, ch, grid);
-  else w == 1 ? launch<float, false, 1>(a, ch, grid) : launch<float, false, 4>(a, ch, grid);
+  if (a.bf16) a.e4m3 ? launch<uint16_t, true>(a) : launch<uint16_t, false>(a);
+  else a.e4m3 ? launch<float, true>(a) : launch<float, false>(a);
   return hipGetLastError();
 }
 
