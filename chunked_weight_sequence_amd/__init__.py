@@ -810,7 +810,7 @@ def add_rms_norm(X, weight=None, *, residual=None, eps: float = 1e-6, e4m3: bool
     if residual is not None:
         rs = _matrix(residual, "residual", N, D, dt, dev)
         if S is None:
-            S, ss = torch.empty((N, D), dtype=dt, device=dev), D
+            S, ss = torch.empty_like(X), D  # contiguous, also of a slice
         else:
             ss = _matrix(S, "S", N, D, dt, dev)
     elif S is not None:
@@ -820,7 +820,7 @@ def add_rms_norm(X, weight=None, *, residual=None, eps: float = 1e-6, e4m3: bool
     group = _int_in(group, "group", 0, 1 << 30)
     out = torch.float8_e4m3fn if e4m3 else dt
     if Y is None:
-        Y, ys = torch.empty((N, D), dtype=out, device=dev), D
+        Y, ys = torch.empty_like(X, dtype=out), D
     else:
         ys = _matrix(Y, "Y", N, D, out, dev)
     if e4m3:
@@ -854,7 +854,7 @@ def _delta_inputs(Q, K, V, g, beta, O):
     _vec(g, "g", (N, Hv), torch.float32, dev)
     _vec(beta, "beta", (N, Hv), torch.float32, dev)
     if O is None:
-        O, os_ = torch.empty((N, Hv, dv), dtype=dt, device=dev), Hv * dv
+        O, os_ = torch.empty_like(V), Hv * dv  # contiguous, also of a slice
     else:
         os_ = _rows(O, "O", Hv, dv, dt, dev, N)
     return O, (Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs, _dtype_code(dt), g.data_ptr(),

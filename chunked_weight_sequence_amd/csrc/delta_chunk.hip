@@ -36,6 +36,7 @@ constexpr int DL_FRAGS = 6;          // 16 x 32 blocks of a lower triangle: (row
                                      // step <= row block / 2, numbered row block + (row block > 1) * (row block - 2) + step
 constexpr int DL_TOK = 4 * DL_FRAGS * 1024;  // byte offset of the rows' factors behind 3 planes of T, then A
 constexpr int DL_UNIT = DL_TOK + 1024;       // bytes of a chunk and head in the workspace
+constexpr int DL_A = 3 * DL_FRAGS * 1024;    // where A begins
 // the rows' factors: e^G and the norm of k [64], e^(G_C - G) and the norm of k [64], scale e^G and the norm of
 // q [64], e^(G_C)
 constexpr int DL_FROM = 0, DL_LEFT = 64, DL_OUT = 128, DL_WHOLE = 192;
@@ -366,7 +367,7 @@ __device__ __forceinline__ void dl_meet_copied() {  // and at most MOST of the w
 // and adds all u to its rows. Their vector work is dealt out between the products. The others copy the next chunk's
 // tiles into LDS and compute the outputs, 32 tokens each, from the planes of S and the u that are left in LDS. All
 // meet four times a chunk; what is there behind a meeting:
-//   B  chunk c's V, T and A                     1  the sums for the other's tokens; the planes of S
+//   B  chunk c's V and A                        1  the sums for the other's tokens; the planes of S
 //   2  the first half's V - e^G K S, in planes; Q of chunk c
 //   3  u, and what of it the state takes, in planes; K of chunk c + 1
 template <int DK>
@@ -374,7 +375,8 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
   constexpr int TILES = 2, CW = 16 * TILES, KT = DL_C * DK * 2, VT = DL_C * CW * 2;
   constexpr int DB = DK / 16, KS = DK / 32;  // row blocks of the state, contraction steps over them
   constexpr int DH = DB / 2, KH = KS / 2;    // a wave's share of them
-  constexpr int AT_U = KT, AT_V = AT_U + DL_UNIT, STAGE = AT_V + VT;  // K, the workspace's unit, V
+  constexpr int REST = DL_UNIT - DL_A;                             // A and the rows' factors
+  constexpr int AT_U = KT, AT_V = AT_U + REST, STAGE = AT_V + VT;  // K, these, V
   struct Hand {
     char s[2 * KS * 1024];  // two planes of S
     char u[4 * 1024];       // u, row blocks in fp32
@@ -395,7 +397,7 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
   char *const s_s = hand[tile].s, *const u_s = hand[tile].u, *const r_s = hand[tile].r, *const px_s = hand[tile].px;
 
   if (wave >= 4) {
-    constexpr int NK = KT / 1024 / 4, NU = (DL_UNIT / 1024 + 3) / 4, BACK = 3 * 1024;  // copies of a wave; NU: some are repetitions
+    constexpr int NK = KT / 1024 / 4, NU = (REST / 1024 + 3) / 4, BACK = 3 * 1024;  // copies of a wave; NU: some are repetitions
     const int w = wave - 4;
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(sm)), lds_q = __builtin_amdgcn_readfirstlane(lds_u32(q_s));
     const uint16_t* kp = static_cast<const uint16_t*>(a.d.K) + long(sq.q0) * a.d.ks + hk * DK;
@@ -439,10 +441,10 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
       if (which == 2) rows(qp + long(c) * DL_C * a.d.qs, a.d.qs, qo, left, lds_q);
       if (which == 1) {
         dl_copy_rows<CW>(w, vp + long(c) * DL_C * a.d.vs, a.d.vs, left, to + AT_V, lane);
-        const char* u = up + size_t(c) * a.d.Hv * DL_UNIT;
+        const char* u = up + size_t(c) * a.d.Hv * DL_UNIT + DL_A;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-          const int n = min(NU * w + i, DL_UNIT / 1024 - 1);
+          const int n = min(NU * w + i, REST / 1024 - 1);
           dma16(l16, u + n * 1024, to + AT_U + n * 1024);
         }
       }
@@ -461,7 +463,7 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
       dl_meet_copied<NK + STORES>();  // B: behind V and the unit come Q and the last outputs
       if (next) part(0, c + 1);
       const char* const ut = sm[c & 1] + AT_U;
-      const float* const f = reinterpret_cast<const float*>(ut + DL_TOK);
+      const float* const f = reinterpret_cast<const float*>(ut + DL_TOK - DL_A);
       dl_meet();  // 1
       if (next) part(1, c + 1);
       uint4 sp[KS][2], af[2][2];
@@ -473,7 +475,7 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int k = 0; k < 2; ++k)  // (those of the first half's second step are not used)
-          af[t][k] = *reinterpret_cast<const uint4*>(ut + (18 + (me ? dl_frag(2 + t, k) : t)) * 1024 + l16);
+          af[t][k] = *reinterpret_cast<const uint4*>(ut + (me ? dl_frag(2 + t, k) : t) * 1024 + l16);
       if (next) dl_meet_copied<STORES + NK + NVU>();  // 2: behind Q come the last outputs, the next K, V and unit
       else dl_meet_copied<STORES>();
       // O^T = S^T Q^T e^G: a lane has 4 neighbouring columns of a token
@@ -561,6 +563,29 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
     const int b = i % 4;
     kf[i / 4][b] = dl_row<DK>(kt, 2 * (b < 2 ? 1 - me : me) + b % 2, KH * me + i / 4, lane);
   };
+  // T of the wave's tokens by its own (t) and, for the second, by the first's (t0): straight from the workspace, a chunk
+  // ahead (of the last one's: again)
+  uint4 t[2][3], t0[2][3];
+  const char* const up = static_cast<const char*>(a.ws) + (size_t(sq.base) * a.d.Hv + h) * DL_UNIT;
+  const auto T = [&](int c, int p, int frag) DL_INLINE {
+    return *reinterpret_cast<const uint4*>(up + size_t(min(c, chunks - 1)) * a.d.Hv * DL_UNIT + (6 * p + frag) * 1024 + l16);
+  };
+  const auto read_own = [&](int c) DL_INLINE {
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) t[b][p] = T(c, p, me ? dl_frag(2 + b, 1) : b);
+  };
+  const auto read_first = [&](int c) DL_INLINE {
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) t0[b][p] = T(c, p, dl_frag(2 + b, 0));
+  };
+  if (chunks > 0) {
+    read_own(0);
+    if (me) read_first(0);
+  }
   dl_meet();
   if (chunks > 0)
 #pragma unroll
@@ -573,14 +598,12 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
     const char* const kt = sm[c & 1];
     const char* const ut = kt + AT_U;
     const char* const vt = kt + AT_V;
-    const float* const f = reinterpret_cast<const float*>(ut + DL_TOK);
+    const float* const f = reinterpret_cast<const float*>(ut + DL_TOK - DL_A);
     // P = K S over the wave's rows of S, whose last ones are split meanwhile; what the next steps take is read
     f32x4 x[4];
-    uint4 t[2][3], t0[2][3], kc[2][DH];
+    uint4 kc[2][DH];
     uint2 v[2];
     float4 from[2], keep[2];
-    const auto T = [&](int p, int frag) DL_INLINE { return *reinterpret_cast<const uint4*>(ut + (6 * p + frag) * 1024 + l16); };
-    const auto read_t = [&](int i) DL_INLINE { t[i % 2][2 - i / 2] = T(2 - i / 2, me ? dl_frag(2 + i % 2, 1) : i % 2); };
     const auto read_kc = [&](int k, int d) DL_INLINE {  // K^T of tokens 32 k .., the wave's row block d
       const uint2 lo = dl_channels<DK>(kt, 2 * k, DH * me + d, lane), hi = dl_channels<DK>(kt, 2 * k + 1, DH * me + d, lane);
       return make_uint4(lo.x, lo.y, hi.x, hi.y);
@@ -596,8 +619,6 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
       if (k >= 2 && k < 4) {
         v[k - 2] = dl_column<CW>(vt, 2 * me + k - 2, tile, lane);
         from[k - 2] = *reinterpret_cast<const float4*>(f + DL_FROM + 16 * (2 * me + k - 2) + g4);
-      } else if (k >= 4 && k < 10) {
-        read_t(k - 4);
       } else if (k >= 15 && k < 17) {
         keep[k - 15] = *reinterpret_cast<const float4*>(f + DL_LEFT + 16 * (2 * me + k - 15) + g4);
       }
@@ -615,11 +636,6 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) keep[b] = *reinterpret_cast<const float4*>(f + DL_LEFT + 16 * (2 * me + b) + g4);
     const float whole = f[DL_WHOLE];
-    if (me)  // the second half's tokens see the first's
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) t0[b][p] = T(p, dl_frag(2 + b, 0));
     // V - e^G P of the wave's tokens, in planes, and u = T (..) of those
     f32x4 u[2];
     uint4 xp[3];
@@ -649,6 +665,7 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
       if (k < DH) kc[0][k] = read_kc(me, k);  // own tokens
       dl_fence();
     }
+    read_own(c + 1);
     dl_meet();  // 2
 #pragma unroll
     for (int d = 0; d < DH; ++d) S[d] *= whole;
@@ -661,6 +678,7 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
       for (int n = 0; n < 6; ++n)
 #pragma unroll
         for (int b = 0; b < 2; ++b) u[b] = mfma16x16x32(t0[b][TP[n]], r[XP[n]], u[b]);
+      read_first(c + 1);
     }
     uint4 xu[3], xo[3];
 #pragma unroll
