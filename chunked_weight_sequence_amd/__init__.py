@@ -918,14 +918,14 @@ def gated_delta_decode(Q, K, V, g, beta, state, *, state_out=None, slots=None, s
     """The gated delta rule for one token of each of S sequences: per value head, with a = exp(g),
     u = beta (v - a W^T k), W <- a W + k u^T, o = scale W^T q; q and k divided by their norm first
     (normalize). Q, K [S,Hk,dk], V [S,Hv,dv] bf16 (tokens may be slices of one buffer), g and beta [S,Hv] fp32;
-    state [n_slots,Hv,dk,dv] fp32, of which sequence s has slot slots[s] (int32; slots None: s; outside: starts
-    at zero, nothing kept). The new states go to the same slots of state_out, in place if that is None.
+    state [n_slots,Hv,dk,dv] fp32 (None: all start at zero), of which sequence s has slot slots[s] (int32; slots
+    None: s; outside: starts at zero, nothing kept). The new states go to the same slots of state_out, in place if that is None.
     scale: 1 / sqrt(dk) by default. Returns (O [S,Hv,dv], state_out)."""
     O, args, S, Hk, Hv, dk, dv = _delta_inputs(Q, K, V, g, beta, O)
     state_out = state if state_out is None else state_out
     n_slots = _delta_states(state, state_out, slots, S, Hv, dk, dv, Q.device)
     _launch(lib().ttt_gated_delta_decode,
-            args + (state.data_ptr(), state_out.data_ptr(), _ptr(slots), n_slots, S, Hk, Hv, dk, dv,
+            args + (_ptr(state), _ptr(state_out), _ptr(slots), n_slots, S, Hk, Hv, dk, dv,
                     dk ** -0.5 if scale is None else scale, int(bool(normalize)), norm_eps), Q.device)
     return O, state_out
 

@@ -184,33 +184,33 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
     gs[lane] = G;
     bs[lane] = lane < left ? beta : 0.f;
   }
-  {
-    float kk = 0.f, qq = 0.f;
+  // Row block `wave` of K K^T and Q K^T, as blocks [j, i] of products K K^T and K Q^T: lane l has row i = l % 16 of
+  // the block and its columns j = 4 (l / 16) .. The squares of the norms are the diagonals of K K^T and Q Q^T.
+  f32x4 kk[4], kq[4], qq = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < KS; ++s) qq = mfma16x16x32(qf[s], qf[s], qq);
+#pragma unroll
+  for (int jb = 3; jb >= 0; --jb) {
+    kk[jb] = kq[jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (jb > wave) continue;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      const uint32_t kw[4] = {kf[3][s].x, kf[3][s].y, kf[3][s].z, kf[3][s].w}, qw[4] = {qf[s].x, qf[s].y, qf[s].z, qf[s].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float k0 = __uint_as_float(kw[e] << 16), k1 = __uint_as_float(kw[e] & 0xFFFF0000u);
-        const float q0 = __uint_as_float(qw[e] << 16), q1 = __uint_as_float(qw[e] & 0xFFFF0000u);
-        kk = fmaf(k0, k0, fmaf(k1, k1, kk));
-        qq = fmaf(q0, q0, fmaf(q1, q1, qq));
-      }
+      const uint4 f = jb < 3 && jb < wave ? kf[jb][s] : kf[3][s];
+      kk[jb] = mfma16x16x32(f, kf[3][s], kk[jb]);
+      kq[jb] = mfma16x16x32(f, qf[s], kq[jb]);
     }
-#pragma unroll
-    for (int d = 16; d < 64; d *= 2) {
-      kk += __shfl_xor(kk, d);
-      qq += __shfl_xor(qq, d);
-    }
-    if (lane < 16) {
-      rk_s[i0] = a.d.norm ? rsqrtf(kk + a.d.eps) : 1.f;
-      rq_s[i0] = a.d.scale * (a.d.norm ? rsqrtf(qq + a.d.eps) : 1.f);
-    }
+  }
+  if ((lane & 15) / 4 == lane / 16) {  // has the diagonal's i = j
+    const f32x4 d = wave == 0 ? kk[0] : wave == 1 ? kk[1] : wave == 2 ? kk[2] : kk[3];
+    const int r = lane & 3;
+    const float k2 = r == 0 ? d[0] : r == 1 ? d[1] : r == 2 ? d[2] : d[3];
+    const float q2 = r == 0 ? qq[0] : r == 1 ? qq[1] : r == 2 ? qq[2] : qq[3];
+    rk_s[i0] = a.d.norm ? rsqrtf(k2 + a.d.eps) : 1.f;
+    rq_s[i0] = a.d.scale * (a.d.norm ? rsqrtf(q2 + a.d.eps) : 1.f);
   }
   __syncthreads();
 
-  // Row block `wave` of L and A, as blocks [j, i] of products K K^T and K Q^T: lane l has row i = l % 16 of the
-  // block and its columns j = 4 (l / 16) ..
+  // the same of L and A
   char* const unit = static_cast<char*>(a.ws) + (size_t(id) * a.d.Hv + h) * DL_UNIT;
   {
     const double gi = gs[i0];
@@ -220,21 +220,14 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
     for (int jb = 0; jb < 4; ++jb) {
       aw[jb] = make_uint2(0, 0);
       if (jb > wave) continue;
-      f32x4 kk = {0.f, 0.f, 0.f, 0.f}, kq = kk;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const uint4 f = jb < 3 && jb < wave ? kf[jb][s] : kf[3][s];
-        kk = mfma16x16x32(f, kf[3][s], kk);
-        kq = mfma16x16x32(f, qf[s], kq);
-      }
       const float4 rk = *reinterpret_cast<const float4*>(&rk_s[16 * jb + g4]);
       float lv[4], av[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int j = 16 * jb + g4 + r;
         const float decay = __builtin_amdgcn_exp2f(float(gi - gs[j])) * (r == 0 ? rk.x : r == 1 ? rk.y : r == 2 ? rk.z : rk.w);
-        lv[r] = j < i0 && i0 < left ? bi * decay * kk[r] : 0.f;
-        av[r] = j <= i0 && i0 < left ? qi * decay * kq[r] : 0.f;
+        lv[r] = j < i0 && i0 < left ? bi * decay * kk[jb][r] : 0.f;
+        av[r] = j <= i0 && i0 < left ? qi * decay * kq[jb][r] : 0.f;
       }
       *reinterpret_cast<float4*>(&ls[i0][16 * jb + g4]) = make_float4(lv[0], lv[1], lv[2], lv[3]);
       aw[jb] = make_uint2(pack2bf(av[0], av[1]), pack2bf(av[2], av[3]));
@@ -254,17 +247,17 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
     f[DL_OUT + lane] = from * rq_s[lane];
     f[DL_WHOLE + lane] = __builtin_amdgcn_exp2f(float(all));
   }
-  // The inverse of 1 + L: the wave's diagonal block by forward substitution, a column to a lane (lanes 16 .. 63 repeat
-  // the first 16; the rows are the wave's own)
-  {
-    const int c = lane & 15;
+  __syncthreads();
+  // The inverse of 1 + L: the four diagonal blocks by forward substitution, a column to each lane of one wave
+  if (wave == 3) {
+    const int c = lane & 15, b = lane >> 4;
     float t[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float x[4] = {i == c ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < i; k += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(&ls[16 * wave + i][16 * wave + k]);
+        const float4 l = *reinterpret_cast<const float4*>(&ls[16 * b + i][16 * b + k]);
         x[0] = fmaf(-l.x, t[k], x[0]);
         if (k + 1 < i) x[1] = fmaf(-l.y, t[k + 1], x[1]);
         if (k + 2 < i) x[2] = fmaf(-l.z, t[k + 2], x[2]);
@@ -272,9 +265,8 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
       }
       t[i] = (x[0] + x[1]) + (x[2] + x[3]);
     }
-    if (lane < 16)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ds[wave][i][c] = t[i];
+    for (int i = 0; i < 16; ++i) ds[b][i][c] = t[i];
   }
   __syncthreads();
   // then block column `wave` from the top: T_ij = -T_ii sum_k L_ik T_kj

@@ -338,3 +338,22 @@ def test_packed_refusals():
             (cu, dict(workspace=torch.empty(1000, dtype=torch.uint8, device="cuda")), ttt.TTTError)]:
         with pytest.raises(err):
             ttt.gated_delta_packed(*x, cu2, **kw)
+
+
+def test_offsets_are_clamped_and_states_may_be_missing():
+    """Offsets outside the buffers; one token without a state, kept or not."""
+    import torch
+    print("case: delta, clamped offsets, no states", flush=True)
+    rng = np.random.default_rng(15)
+    N, Hk, Hv, dk, dv = 100, 1, 2, 64, 128
+    x = _draw(rng, N, Hk, Hv, dk, dv)
+    O, st = ttt.gated_delta_packed(*_on_gpu(x), _i32([-7, 70, 1 << 30]), norm_eps=EPS)
+    torch.cuda.synchronize()
+    _packed_check(x, O, [70, 30], 0, [None, None], list(host_f64(st)), dk ** -0.5, EPS)
+    one = [a[:3] for a in x]
+    new = torch.full((3, Hv, dk, dv), 7.0, device="cuda")
+    O, st = ttt.gated_delta_decode(*_on_gpu(one), None, state_out=new, norm_eps=EPS)
+    O2, none = ttt.gated_delta_decode(*_on_gpu(one), None, norm_eps=EPS)
+    torch.cuda.synchronize()
+    assert st is new and none is None and torch.equal(O, O2)
+    _packed_check(one, O, [1, 1, 1], 0, [None] * 3, list(host_f64(new)), dk ** -0.5, EPS)
