@@ -15,11 +15,18 @@
 // order 16 (e / 4) + 4 (l / 16) + e % 4, e = 0..7, in both operands. Rows of S are channels in such an order
 // (dl_channel) that K and Q need none: a lane's 8 channels lie side by side.
 //
-// Precision: what is not bf16 enters a product as a sum of bf16 planes, S as two, T, V - e^G K S and u as three
-// (of the nine products of planes of T and V - .., the six above 2^-24). One plane less for any of the three
-// leaves 3 .. 6e-6 of the state's size after 2048 tokens, this 3 .. 7e-7 (an fp32 computation 2e-7); S
-// itself is never rounded to fewer bits, and its error in S^T k enters a chunk's u only. O, which is rounded to
-// bf16, takes one plane of S and u, and A in bf16.
+// Precision: what is not bf16 enters a product as a sum of bf16 planes, S, T, V - e^G K S and u as three each (of the
+// nine products of planes of T and V - .., the six above 2^-24). The state is then off by 2e-7 of its size after 2048
+// tokens, as an fp32 computation is; with two planes of S it was 1.2e-6, with two of the others as well 3 .. 6e-6. O,
+// which is rounded to bf16, takes two planes of S and u, and A in bf16.
+//
+// What bounds it. k_delta_prepare: memory, mostly its own 25 KB per 64 tokens and head of T, A and factors (32768
+// tokens of 32 heads, 400 MB out and 8 MB in: 203 us; three planes of T in the order in which the scan's operands lie are
+// more bytes than 4 KB of L would be, but the inverse is then computed once for a head and not in each of its column
+// tiles). k_delta_scan: the chain through S, whose 512 chunks follow each other here: 1010 us or 4700 clocks a chunk, in
+// 128 workgroups; of that 72 matrix instructions of the wave that has most, some 17 clocks each, and between them
+// splits into planes and four meetings. Smaller column tiles would use more of the card, and were slower (16
+// columns, two workgroups a CU: 1373 us): each reads K, Q, T and A again. 8192 tokens in 11 sequences: 52 + 213 us.
 #include <type_traits>
 
 #include "common.hpp"
@@ -75,7 +82,7 @@ __device__ __forceinline__ int dl_find(const DeltaPackedArgs& a, int id, int lan
 // them on all banks.
 template <int W>
 __device__ __forceinline__ int dl_turn(int r) {
-  return W == 128 ? (r & 7) << 1 | (r >> 3 & 1) : W == 64 ? (r >> 1 & 3) << 1 | (r >> 3 & 1) : 0;
+  return W == 128 ? (r & 7) << 1 | (r >> 3 & 1) : W == 64 ? (r >> 1 & 3) << 1 | (r >> 3 & 1) : (r >> 2 & 1) << 1;
 }
 template <int W>
 __device__ __forceinline__ int dl_at(int r, int piece) { return r * W * 2 + ((piece ^ dl_turn<W>(r)) << 4); }
@@ -362,6 +369,8 @@ __device__ __forceinline__ void dl_meet_copied() {  // and at most MOST of the w
 //   B  chunk c's V and A                        1  the sums for the other's tokens; the planes of S
 //   2  the first half's V - e^G K S, in planes; Q of chunk c
 //   3  u, and what of it the state takes, in planes; K of chunk c + 1
+// What u adds to the outputs is added behind the next B, where these waves have time: between 3 and B the carrying ones
+// waited 700 clocks of 4900 a chunk for it.
 template <int DK>
 __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
   constexpr int TILES = 2, CW = 16 * TILES, KT = DL_C * DK * 2, VT = DL_C * CW * 2;
@@ -444,50 +453,10 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
       dl_fence();
     };
     constexpr int NVU = 1 + NU, STORES = 2;
-    if (chunks > 0) {
-      part(0, 0);
-      part(1, 0);
-      part(2, 0);
-    }
-    dl_meet_copied<0>();
-    for (int c = 0; c < chunks; ++c) {
-      const bool next = c + 1 < chunks;
-      dl_meet_copied<NK + STORES>();  // B: behind V and the unit come Q and the last outputs
-      if (next) part(0, c + 1);
-      const char* const ut = sm[c & 1] + AT_U;
-      const float* const f = reinterpret_cast<const float*>(ut + DL_TOK - DL_A);
-      dl_meet();  // 1
-      if (next) part(1, c + 1);
-      uint4 sp[KS][2], af[2][2];
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) sp[k][p] = *reinterpret_cast<const uint4*>(s_s + (2 * k + p) * 1024 + l16);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)  // (those of the first half's second step are not used)
-          af[t][k] = *reinterpret_cast<const uint4*>(ut + (me ? dl_frag(2 + t, k) : t) * 1024 + l16);
-      if (next) dl_meet_copied<STORES + NK + NVU>();  // 2: behind Q come the last outputs, the next K, V and unit
-      else dl_meet_copied<STORES>();
-      // O^T = S^T Q^T e^G: a lane has 4 neighbouring columns of a token
-      f32x4 o[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint4 q[2] = {dl_row<DK>(q_s, 2 * me, k, lane), dl_row<DK>(q_s, 2 * me + 1, k, lane)};
-#pragma unroll
-        for (int p = 1; p >= 0; --p)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) o[t] = mfma16x16x32(sp[k][p], q[t], o[t]);
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) o[t] *= f[DL_OUT + 16 * (2 * me + t) + c16];
-      if (next) dl_meet_copied<NVU>();  // 3: behind the next K come V and the unit
-      else dl_meet();
-      if (next) part(2, c + 1);
-      // .. + u^T A^T
+    f32x4 o[2];
+    uint4 af[2][2];  // (those of the first half's second step are not used)
+    // the outputs of a chunk: what S gave, + u^T A^T
+    const auto finish = [&](int c) DL_INLINE {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (k > me) break;
@@ -507,7 +476,55 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
         if (tok < left)
           *reinterpret_cast<uint2*>(p + long(tok) * a.d.os) = make_uint2(pack2bf(o[t][0], o[t][1]), pack2bf(o[t][2], o[t][3]));
       }
+    };
+    if (chunks > 0) {
+      part(0, 0);
+      part(1, 0);
+      part(2, 0);
     }
+    dl_meet_copied<0>();
+    for (int c = 0; c < chunks; ++c) {
+      const bool next = c + 1 < chunks;
+      dl_meet_copied<NK>();  // B: behind V and A comes Q
+      if (next) part(0, c + 1);
+      if (c > 0) finish(c - 1);
+      asm volatile("" ::: "memory");  // its stores stay before the copies that follow: they are counted together
+      dl_fence();
+      const char* const ut = sm[c & 1] + AT_U;
+      const float* const f = reinterpret_cast<const float*>(ut + DL_TOK - DL_A);
+      dl_meet();  // 1
+      if (next) part(1, c + 1);
+      uint4 sp[KS][2];
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) sp[k][p] = *reinterpret_cast<const uint4*>(s_s + (2 * k + p) * 1024 + l16);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          af[t][k] = *reinterpret_cast<const uint4*>(ut + (me ? dl_frag(2 + t, k) : t) * 1024 + l16);
+      if (next) dl_meet_copied<NK + STORES + NVU>();  // 2: behind Q come the next K, the last outputs, the next V and A
+      else dl_meet_copied<STORES>();
+      // O^T = S^T Q^T e^G: a lane has 4 neighbouring columns of a token
+#pragma unroll
+      for (int t = 0; t < 2; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint4 q[2] = {dl_row<DK>(q_s, 2 * me, k, lane), dl_row<DK>(q_s, 2 * me + 1, k, lane)};
+#pragma unroll
+        for (int p = 1; p >= 0; --p)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) o[t] = mfma16x16x32(sp[k][p], q[t], o[t]);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) o[t] *= f[DL_OUT + 16 * (2 * me + t) + c16];
+      if (next) dl_meet_copied<NVU>();  // 3: behind the next K come the outputs, V and A
+      else dl_meet();
+      if (next) part(2, c + 1);
+    }
+    dl_meet();  // the last u
+    if (chunks > 0) finish(chunks - 1);
     return;
   }
 
@@ -719,6 +736,7 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
       dl_fence();
     }
   }
+  dl_meet();  // the last u
   if (kept && a.d.state_out)
 #pragma unroll
     for (int d = 0; d < DH; ++d)
