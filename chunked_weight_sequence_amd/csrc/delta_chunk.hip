@@ -20,10 +20,10 @@
 // tokens, as an fp32 computation is; with two planes of S it was 1.2e-6, with two of the others as well 3 .. 6e-6. O,
 // which is rounded to bf16, takes two planes of S and u, and A in bf16.
 //
-// What bounds it. k_delta_prepare: memory, mostly its own 25 KB per 64 tokens and head of T, A and factors (32768
-// tokens of 32 heads, 400 MB out and 8 MB in: 203 us; three planes of T in the order in which the scan's operands lie are
-// more bytes than 4 KB of L would be, but the inverse is then computed once for a head and not in each of its column
-// tiles). k_delta_scan: the chain through S, whose 512 chunks follow each other here: 1010 us or 4700 clocks a chunk, in
+// What bounds it. k_delta_prepare: memory, for the most part its own 25 KB per 64 tokens and head of T, A and factors
+// (32768 tokens of 32 heads: 419 MB out, 302 MB in, 203 us, 3.55 TB/s, where a copy reaches 4.95; three planes of T in
+// the order in which the scan's operands lie are more bytes than L would be, but the inverse is computed once for a
+// head and not in each of its column tiles). k_delta_scan: the chain through S, whose 512 chunks follow each other here: 1010 us or 4700 clocks a chunk, in
 // 128 workgroups; of that 72 matrix instructions of the wave that has most, some 17 clocks each, and between them
 // splits into planes and four meetings. Smaller column tiles would use more of the card, and were slower (16
 // columns, two workgroups a CU: 1373 us): each reads K, Q, T and A again. 8192 tokens in 11 sequences: 52 + 213 us.

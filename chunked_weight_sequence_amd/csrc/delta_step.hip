@@ -6,7 +6,8 @@
 // Bound by HBM: a head's state (64 KB at 128 x 128) is read once and written once. A workgroup takes some
 // columns of one head's state into registers, all of its loads asked for at once; the sums over the rows for
 // S^T k and S^T q are taken together, since o = scale (keep S^T q + (k . q) u), so the workgroup
-// meets once.
+// meets once. 2048 heads of 128 x 128 (64 sequences of 32): 51 us, 5.3 TB/s; a copy reaches 4.95. 32 heads: 3.6 us,
+// of which an empty kernel takes 2.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -127,15 +128,17 @@ template <int DK>
 void launch(const DeltaArgs& a, int tile) {
   const dim3 grid(unsigned(long(a.n_seq) * a.Hv * (a.dv / tile))), block(256);
   if (tile == 32) hipLaunchKernelGGL((k_delta_step<DK, 32>), grid, block, 0, a.stream, a);
-  else if (tile == 64) hipLaunchKernelGGL((k_delta_step<DK, 64>), grid, block, 0, a.stream, a);
-  else hipLaunchKernelGGL((k_delta_step<DK, 128>), grid, block, 0, a.stream, a);
+  else hipLaunchKernelGGL((k_delta_step<DK, 64>), grid, block, 0, a.stream, a);
 }
 
 }  // namespace
 
 hipError_t delta_step(const DeltaArgs& a) {
   const long heads = long(a.n_seq) * a.Hv;
-  const int tile = heads * a.dv <= 256 * 32 ? 32 : a.dv % 128 || heads * a.dv <= 512 * 128 ? 64 : 128;
+  // Columns of a workgroup: 32 while those are at most the card's 256 units, else 64. States of 128 x 128, tiles of 32
+  // and of 64 columns: 8 heads 3.4 and 3.6 us, 64 heads 3.9 and 4.1, 128 heads 6.1 and 5.9, 1024 heads 28.8 and 28.5,
+  // 4096 heads 104 and 98.6. (128 columns: 4.2, 5.1, 6.1, 30.2, 104.)
+  const int tile = heads * a.dv <= 256 * 32 ? 32 : 64;
   a.dk == 128 ? launch<128>(a, tile) : launch<64>(a, tile);
   return hipGetLastError();
 }

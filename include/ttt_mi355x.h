@@ -567,8 +567,9 @@ ttt_status ttt_gated_delta_decode(const void* Q, long long q_stride, const void*
  * token and written after its last, so prompts can be taken in pieces.
  * 64 tokens at a time, counted from the sequence's first: products on the matrix cores with fp32 accumulation,
  * the state and what is added to it at fp32's precision (at most about 1e-6 of its size), O from two bf16 planes
- * of both and bf16 weights between the tokens of a chunk, rounded once. Gates are meant to be at most 0; below -1000 they count as -1000. What is not finite in a
- * sequence stays in it, and reaches from its chunk of 64 tokens on, earlier tokens of that chunk among them.
+ * of both and bf16 weights between the tokens of a chunk, rounded once. Gates are meant to be at most 0; below
+ * -1000 they count as -1000. What is not finite in a sequence stays in it, and reaches from its chunk of 64 tokens
+ * on, earlier tokens of that chunk among them.
  *   strides in elements: at most 2^23; N <= 2^26; (N / 64 + n_seq) * Hv < 2^24 and n_seq * Hv * dv < 2^28;
  *   the other limits as above.
  *   workspace: at least ttt_gated_delta_packed_workspace(...) bytes (25 KB for each 64 tokens and value head);
