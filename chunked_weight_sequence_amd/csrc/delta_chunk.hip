@@ -26,7 +26,7 @@
 // head and not in each of its column tiles). k_delta_scan: the chain through S, whose 512 chunks follow each other here: 1010 us or 4700 clocks a chunk, in
 // 128 workgroups; of that 72 matrix instructions of the wave that has most, some 17 clocks each, and between them
 // splits into planes and four meetings. Smaller column tiles would use more of the card, and were slower (16
-// columns, two workgroups a CU: 1373 us): each reads K, Q, T and A again. 8192 tokens in 11 sequences: 52 + 213 us.
+// columns, two workgroups a CU: 1373 us): each reads K, Q, T and A again. 8192 tokens in 11 sequences: 52 + 168 us.
 #include <type_traits>
 
 #include "common.hpp"
@@ -50,13 +50,18 @@ constexpr int DL_FROM = 0, DL_LEFT = 64, DL_OUT = 128, DL_WHOLE = 192;
 
 __device__ __forceinline__ constexpr int dl_frag(int rb, int ks) { return rb + (rb > 1 ? rb - 2 : 0) + ks; }
 
+// Up to 1024 sequences are scanned in the order of their lengths, the longest first, so that none starts late:
+// k_delta_prepare leaves that order behind the units. (11 documents in 8192 tokens, 32 heads: 213 us in their own
+// order, 168 by length.) More of them give the card work enough for a long one to start late among it, and to rank
+// them takes a pass over all lengths for each.
+__host__ __device__ __forceinline__ constexpr bool dl_ranked(int n_seq) { return n_seq > 1 && n_seq <= 1024; }
+
 struct DeltaChunk {
-  int q0, n;       // first token and tokens of the sequence
-  int base, seq;   // its first chunk's number
+  int q0, n;  // first token and tokens of the sequence
+  int base;   // its first chunk's number
 };
 __device__ __forceinline__ DeltaChunk dl_sequence(const DeltaPackedArgs& a, int s) {
   DeltaChunk c;
-  c.seq = s;
   c.q0 = min(max(a.cu[s], 0), a.N);
   c.n = max(min(max(a.cu[s + 1], 0), a.N) - c.q0, 0);
   c.base = c.q0 / DL_C + s;
@@ -75,6 +80,21 @@ __device__ __forceinline__ int dl_find(const DeltaPackedArgs& a, int id, int lan
     if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
     len = min(step, len - (n - 1) * step);
   }
+}
+
+long units(int n_seq, int N) { return N / DL_C + n_seq; }  // numbers of chunks
+__device__ __forceinline__ int* dl_order(const DeltaPackedArgs& a) {
+  return reinterpret_cast<int*>(static_cast<char*>(a.ws) + size_t(a.N / DL_C + a.d.n_seq) * a.d.Hv * DL_UNIT);
+}
+// The place of sequence s among all by length. By all lanes of a wave.
+__device__ __forceinline__ int dl_rank(const DeltaPackedArgs& a, int s, int lane) {
+  const int n = dl_sequence(a, s).n;
+  int rank = 0;
+  for (int j0 = 0; j0 < a.d.n_seq; j0 += 64) {
+    const int j = j0 + lane, nj = dl_sequence(a, min(j, a.d.n_seq - 1)).n;
+    rank += __popcll(__ballot(j < a.d.n_seq && (nj > n || (nj == n && j < s))));
+  }
+  return rank;
 }
 
 // Tiles of rows of W bf16 in LDS, in pieces of 16 bytes; piece p of row r at slot p ^ turn(r). Reads of 8 bytes go by
@@ -159,6 +179,10 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaPackedArgs a) {
   const int h = blockIdx.x % a.d.Hv, id = blockIdx.x / a.d.Hv;
   const DeltaChunk sq = dl_sequence(a, dl_find(a, id, lane));
   const int t0 = (id - sq.base) * DL_C, left = min(sq.n - t0, DL_C);
+  if (wave == 2 && dl_ranked(a.d.n_seq) && int(blockIdx.x) < a.d.n_seq) {  // there are as many workgroups and more
+    const int rank = dl_rank(a, blockIdx.x, lane);
+    if (lane == 0) dl_order(a)[rank] = blockIdx.x;
+  }
   if (id < sq.base || left <= 0) return;
   const int hk = h / (a.d.Hv / a.d.Hk);
   const long tok = sq.q0 + t0;
@@ -388,9 +412,10 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
   __shared__ __align__(1024) char q_s[KT];
   __shared__ __align__(1024) Hand hand[TILES];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  // the column tiles of a head on one XCD: they read the same K, Q, T and A
-  const int heads = a.d.n_seq * a.d.Hv, hd = blockIdx.x % heads, col0 = blockIdx.x / heads * CW;
-  const int h = hd % a.d.Hv, s = hd / a.d.Hv, hk = h / (a.d.Hv / a.d.Hk);
+  // the column tiles of a head follow each other on one XCD where there are 8 heads: they read the same K, Q, T and A
+  const int wide = a.d.Hv * (a.d.dv / CW), nth = blockIdx.x / wide;
+  const int h = blockIdx.x % wide % a.d.Hv, col0 = blockIdx.x % wide / a.d.Hv * CW, hk = h / (a.d.Hv / a.d.Hk);
+  const int s = dl_ranked(a.d.n_seq) ? __builtin_amdgcn_readfirstlane(dl_order(a)[nth]) : nth;
   const DeltaChunk sq = dl_sequence(a, s);
   const int me = wave & 1, tile = wave >> 1 & 1, col = col0 + 16 * tile;
   const int g4 = 4 * (lane >> 4), c16 = lane & 15, l16 = 16 * lane;
@@ -744,8 +769,6 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
       for (int r = 0; r < 4; ++r) a.d.state_out[row(d, r)] = S[d][r];
 }
 
-long units(int n_seq, int N) { return N / DL_C + n_seq; }  // numbers of chunks
-
 template <int DK>
 hipError_t launch(const DeltaPackedArgs& a) {
   const DeltaArgs& d = a.d;
@@ -759,7 +782,9 @@ hipError_t launch(const DeltaPackedArgs& a) {
 
 }  // namespace
 
-size_t delta_packed_workspace(int n_seq, int N, int Hv) { return size_t(units(n_seq, N)) * Hv * DL_UNIT; }
+size_t delta_packed_workspace(int n_seq, int N, int Hv) {
+  return size_t(units(n_seq, N)) * Hv * DL_UNIT + (dl_ranked(n_seq) ? (n_seq * 4 + 255) / 256 * 256 : 0);
+}
 
 hipError_t delta_packed(const DeltaPackedArgs& a) { return a.d.dk == 128 ? launch<128>(a) : launch<64>(a); }
 

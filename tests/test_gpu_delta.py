@@ -247,6 +247,17 @@ def test_packed_long_and_many(lens, Hk, Hv, dk, dv):
     _packed(np.random.default_rng(len(lens)), lens, Hk, Hv, dk, dv)
 
 
+@pytest.mark.parametrize("n", [2, 63, 64, 65, 129, 1023, 1024, 1025])
+def test_packed_sequences_of_unlike_lengths(n):
+    """The longest ones last and in the middle, many of one length, empty ones: on both sides of the number up to
+    which sequences are taken in the order of their lengths."""
+    print(f"case: delta packed, {n} sequences of unlike lengths", flush=True)
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 4, n)
+    lens[n // 2], lens[-1] = 130, 300
+    _packed(rng, [int(i) for i in lens], 1, 1, 64, 64, first=1)
+
+
 def test_packed_gates_and_steps():
     """Gates of 0, of -inf (everything forgotten), of -1e5; steps of 0 and 1; keys and queries of zeros; the same
     key again and again."""
