@@ -23,10 +23,9 @@
 // What bounds it. k_delta_prepare: memory, for the most part its own 25 KB per 64 tokens and head of T, A and factors
 // (32768 tokens of 32 heads: 419 MB out, 302 MB in, 203 us, 3.55 TB/s, where a copy reaches 4.95; three planes of T in
 // the order in which the scan's operands lie are more bytes than L would be, but the inverse is computed once for a
-// head and not in each of its column tiles). k_delta_scan: the chain through S, whose 512 chunks follow each other here: 1010 us or 4700 clocks a chunk, in
-// 128 workgroups; of that 72 matrix instructions of the wave that has most, some 17 clocks each, and between them
-// splits into planes and four meetings. Smaller column tiles would use more of the card, and were slower (16
-// columns, two workgroups a CU: 1373 us): each reads K, Q, T and A again. 8192 tokens in 11 sequences: 52 + 168 us.
+// head and not in each of its column tiles). k_delta_scan: the chain through S, whose 512 chunks follow each other
+// here: 850 .. 960 us, some 4000 clocks a chunk; of that 72 matrix instructions of the wave that has most, 17 clocks
+// each, and between them splits into planes and four meetings. 8192 tokens in 11 sequences: 52 + 168 us.
 #include <type_traits>
 
 #include "common.hpp"
@@ -52,8 +51,7 @@ __device__ __forceinline__ constexpr int dl_frag(int rb, int ks) { return rb + (
 
 // Up to 1024 sequences are scanned in the order of their lengths, the longest first, so that none starts late:
 // k_delta_prepare leaves that order behind the units. (11 documents in 8192 tokens, 32 heads: 213 us in their own
-// order, 168 by length.) More of them give the card work enough for a long one to start late among it, and to rank
-// them takes a pass over all lengths for each.
+// order, 168 by length.) A place in it takes a pass over all lengths, so that more of them are taken as they lie.
 __host__ __device__ __forceinline__ constexpr bool dl_ranked(int n_seq) { return n_seq > 1 && n_seq <= 1024; }
 
 struct DeltaChunk {
@@ -102,7 +100,7 @@ __device__ __forceinline__ int dl_rank(const DeltaPackedArgs& a, int s, int lane
 // them on all banks.
 template <int W>
 __device__ __forceinline__ int dl_turn(int r) {
-  return W == 128 ? (r & 7) << 1 | (r >> 3 & 1) : W == 64 ? (r >> 1 & 3) << 1 | (r >> 3 & 1) : (r >> 2 & 1) << 1;
+  return W == 128 ? (r & 7) << 1 | (r >> 3 & 1) : W == 64 ? (r >> 1 & 3) << 1 | (r >> 3 & 1) : W == 32 ? (r >> 2 & 1) << 1 : 0;
 }
 template <int W>
 __device__ __forceinline__ int dl_at(int r, int piece) { return r * W * 2 + ((piece ^ dl_turn<W>(r)) << 4); }
@@ -383,7 +381,7 @@ __device__ __forceinline__ void dl_meet_copied() {  // and at most MOST of the w
   dl_meet();
 }
 
-// One workgroup: 32 columns of a state in two tiles of 16. A tile has two waves that carry it from chunk to chunk,
+// One workgroup: 16 or 32 columns of a state, in TILES tiles of 16. A tile has two waves that carry it from chunk to chunk,
 // each on a SIMD of its own, and two that do the rest beside them. Of the carrying waves the first has the state's
 // first half of rows and the chunk's first 32 tokens, the second the others: each multiplies its rows of S by all of
 // K, hands the sums for the other's tokens over, solves for its tokens' u (the second with what the first hands on)
@@ -395,9 +393,9 @@ __device__ __forceinline__ void dl_meet_copied() {  // and at most MOST of the w
 //   3  u, and what of it the state takes, in planes; K of chunk c + 1
 // What u adds to the outputs is added behind the next B, where these waves have time: between 3 and B the carrying ones
 // waited 700 clocks of 4900 a chunk for it.
-template <int DK>
-__global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
-  constexpr int TILES = 2, CW = 16 * TILES, KT = DL_C * DK * 2, VT = DL_C * CW * 2;
+template <int DK, int TILES>
+__global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a) {
+  constexpr int CARRY = 2 * TILES, CW = 16 * TILES, KT = DL_C * DK * 2, VT = DL_C * CW * 2;
   constexpr int DB = DK / 16, KS = DK / 32;  // row blocks of the state, contraction steps over them
   constexpr int DH = DB / 2, KH = KS / 2;    // a wave's share of them
   constexpr int REST = DL_UNIT - DL_A;                             // A and the rows' factors
@@ -417,14 +415,14 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
   const int h = blockIdx.x % wide % a.d.Hv, col0 = blockIdx.x % wide / a.d.Hv * CW, hk = h / (a.d.Hv / a.d.Hk);
   const int s = dl_ranked(a.d.n_seq) ? __builtin_amdgcn_readfirstlane(dl_order(a)[nth]) : nth;
   const DeltaChunk sq = dl_sequence(a, s);
-  const int me = wave & 1, tile = wave >> 1 & 1, col = col0 + 16 * tile;
+  const int me = wave & 1, tile = TILES == 2 ? wave >> 1 & 1 : 0, col = col0 + 16 * tile;
   const int g4 = 4 * (lane >> 4), c16 = lane & 15, l16 = 16 * lane;
   const int chunks = (sq.n + DL_C - 1) / DL_C;
   char *const s_s = hand[tile].s, *const u_s = hand[tile].u, *const r_s = hand[tile].r, *const px_s = hand[tile].px;
 
-  if (wave >= 4) {
-    constexpr int NK = KT / 1024 / 4, NU = (REST / 1024 + 3) / 4, BACK = 3 * 1024;  // copies of a wave; NU: some are repetitions
-    const int w = wave - 4;
+  if (wave >= CARRY) {
+    constexpr int NK = KT / 1024 / CARRY, NU = (REST / 1024 + CARRY - 1) / CARRY, BACK = 3 * 1024;  // copies of a wave; NU: some are repetitions
+    const int w = wave - CARRY;
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_u32(sm)), lds_q = __builtin_amdgcn_readfirstlane(lds_u32(q_s));
     const uint16_t* kp = static_cast<const uint16_t*>(a.d.K) + long(sq.q0) * a.d.ks + hk * DK;
     const uint16_t* qp = static_cast<const uint16_t*>(a.d.Q) + long(sq.q0) * a.d.qs + hk * DK;
@@ -433,25 +431,29 @@ __global__ __launch_bounds__(512, 1) void k_delta_scan(DeltaPackedArgs a) {
     // A lane's offsets in the copies of 16 rows of K or Q; the instruction counts 1024 i for the i-th itself, and
     // 3 KB the base lacks, so that no offset is negative.
     constexpr int CH = DK / 8, RPI = 64 / CH;
-    static_assert(NK * RPI == 16 && NK <= 4, "a wave copies 16 rows");
-    const auto offsets = [&](long stride, uint32_t (&off)[NK]) DL_INLINE {
+    constexpr int N16 = 16 / RPI;
+    static_assert(N16 <= 4 && NK % N16 == 0, "a wave copies 16 rows at a time");
+    const auto offsets = [&](long stride, uint32_t (&off)[N16]) DL_INLINE {
 #pragma unroll
-      for (int i = 0; i < NK; ++i) {
+      for (int i = 0; i < N16; ++i) {
         const int r = i * RPI + lane / CH;
         off[i] = uint32_t(r) * uint32_t(stride * 2) + ((lane % CH ^ dl_turn<DK>(r)) << 4) + BACK - 1024 * i;
       }
     };
-    uint32_t ko[NK], qo[NK];
+    uint32_t ko[N16], qo[N16];
     offsets(a.d.ks, ko);
     offsets(a.d.qs, qo);
-    const auto rows = [&](const uint16_t* src, long stride, const uint32_t (&off)[NK], int left, uint32_t to) DL_INLINE {
+    const auto rows = [&](const uint16_t* src, long stride, const uint32_t (&off)[N16], int left, uint32_t to) DL_INLINE {
       if (left >= DL_C) {
-        const char* base = reinterpret_cast<const char*>(src + long(16 * w) * stride) - BACK;
-        dma16_at<0>(off[0], base, to + NK * w * 1024);
-        dma16_at<1>(off[1], base, to);
-        if constexpr (NK == 4) {
-          dma16_at<2>(off[2], base, to);
-          dma16_at<3>(off[3], base, to);
+#pragma unroll
+        for (int n = 0; n < NK / N16; ++n) {
+          const char* base = reinterpret_cast<const char*>(src + long(16 * (NK / N16 * w + n)) * stride) - BACK;
+          dma16_at<0>(off[0], base, to + (NK * w + N16 * n) * 1024);
+          dma16_at<1>(off[1], base, to);
+          if constexpr (N16 == 4) {
+            dma16_at<2>(off[2], base, to);
+            dma16_at<3>(off[3], base, to);
+          }
         }
       } else {
 #pragma unroll
@@ -776,7 +778,14 @@ hipError_t launch(const DeltaPackedArgs& a) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const long heads = long(d.n_seq) * d.Hv;
-  hipLaunchKernelGGL((k_delta_scan<DK>), dim3(unsigned(heads * (d.dv / 32))), dim3(512), 0, d.stream, a);
+  // 16 columns of a workgroup where each then has one of the card's 256 units to itself, and its carrying waves a SIMD:
+  // 32 where there are more (one fits a unit). 8192 tokens of 128 x 128, both launches with 16 and with 32 columns: 4
+  // heads 204 and 250 us, 32 heads 261 and 294, 40 heads 510 and 323; 64 x 128: 8 heads 185 and 207, 32 heads 221 and
+  // 237, 40 heads 272 and 268, 64 heads 375 and 331.
+  if (heads * (d.dv / 16) <= 256)
+    hipLaunchKernelGGL((k_delta_scan<DK, 1>), dim3(unsigned(heads * (d.dv / 16))), dim3(256), 0, d.stream, a);
+  else
+    hipLaunchKernelGGL((k_delta_scan<DK, 2>), dim3(unsigned(heads * (d.dv / 32))), dim3(512), 0, d.stream, a);
   return hipGetLastError();
 }
 
