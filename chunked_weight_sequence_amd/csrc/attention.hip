@@ -19,6 +19,12 @@
 // tokens after 15872 122 .. 127 us with the join; 32/32 heads of 64, 8191 tokens, window 2048: 139 .. 154 us.
 // A workgroup takes 4 us to its first round (its sequence 0.6, set up 0.6, copies 1.5, queries to registers
 // 0.5, first scores 0.9), 1.2 .. 1.5 per tile of 128 rows with two on a unit, and 2 to write its rows.
+//
+// The paged form is the same kernel with other copies: a wave's 16 rows of a tile lie in one page (a page has at least 16),
+// so a tile takes four page numbers, read through the scalar cache a tile ahead. It costs little: 512 tokens after
+// 15872, 32/8 heads of 128, 122 .. 132 us with the join (1026 TFLOP/s), 4 pieces of 2000 tokens, 32/32 heads of 64,
+// window 2048, 172 .. 186 us. Few rows per key are bound by HBM instead: 16 x 5 tokens on up to 8000, 16/4 heads
+// of 64, 23 us (3.9 TB/s); a piece of 512 tokens and 14 single ones on up to 12000 take both in turn, 171 us.
 #include <type_traits>
 
 #include "attn.hpp"

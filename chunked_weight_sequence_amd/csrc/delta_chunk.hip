@@ -21,11 +21,12 @@
 // which is rounded to bf16, takes two planes of S and u, and A in bf16.
 //
 // What bounds it. k_delta_prepare: memory, for the most part its own 25 KB per 64 tokens and head of T, A and factors
-// (32768 tokens of 32 heads: 419 MB out, 302 MB in, 203 us, 3.55 TB/s, where a copy reaches 4.95; three planes of T in
-// the order in which the scan's operands lie are more bytes than L would be, but the inverse is computed once for a
-// head and not in each of its column tiles). k_delta_scan: the chain through S, whose 512 chunks follow each other
-// here: 850 .. 960 us, some 4000 clocks a chunk; of that 72 matrix instructions of the wave that has most, 17 clocks
-// each, and between them splits into planes and four meetings. 8192 tokens in 11 sequences: 52 + 168 us.
+// beside K and Q (32768 tokens of 32 heads: 419 MB out, 604 in, 203 us, 5 TB/s, as much as a copy reaches; three
+// planes of T in the order in which the scan's operands lie are more bytes than L would be, but the inverse is computed
+// once for a head and not in each of its column tiles). k_delta_scan: the chain through S, whose 512 chunks follow each
+// other here: 840 .. 960 us, 3550 clocks a chunk (at 2.0 GHz: power); of that 72 matrix instructions of the wave that
+// has most, 17 clocks each, and between them splits into planes and four meetings. 8192 tokens in 11 sequences of 32
+// heads: 52 + 168 us.
 #include <type_traits>
 
 #include "common.hpp"
