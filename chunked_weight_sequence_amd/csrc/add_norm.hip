@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256) void k_add_norm(AddNormArgs a) {
   __shared__ float2 part[2][4];  // of the sums, and of those that are taken again
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int li = W == 1 ? lane : tid, D = a.D, n8 = D >> 3;
-  const long n = long(blockIdx.x) * (4 / W) + (W == 1 ? wave : 0);
+  const long n = (long(blockIdx.y) * gridDim.x + blockIdx.x) * (4 / W) + (W == 1 ? wave : 0);
   if (n >= a.N) return;  // the same for all waves of a row
   const T *X = static_cast<const T*>(a.X) + n * a.xs, *R = static_cast<const T*>(a.R) + n * a.rs;
   const bool with_r = a.R != nullptr;
@@ -176,7 +176,18 @@ __global__ __launch_bounds__(256) void k_add_norm(AddNormArgs a) {
   if constexpr (E4M3) {
     const int per = a.group >> 3;  // lanes to a group, a power of two
     const long sn = a.group ? n * (D / a.group) : n;
-    float scale = fmaxf(top * rs / 448.f, 0x1p-126f), inv = 1.f / scale;
+    float most = top * rs;  // |y|
+    if (!a.group && __builtin_expect(!(top > 0x1p-100f && top < 0x1p126f), 0)) {
+      // a weight far from 1: h w leaves fp32 where y need not
+      float none = 0.f;
+      most = 0.f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(h[i][e] * rs * w[i][e]));
+      reduce(none, most);
+    }
+    float scale = fmaxf(most / 448.f, 0x1p-126f), inv = 1.f / scale;
     if (!a.group && li == 0) a.scales[sn] = scale;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -213,8 +224,9 @@ __global__ __launch_bounds__(256) void k_add_norm(AddNormArgs a) {
 
 template <typename T, bool E4M3, int W, int CH>
 void launch(const AddNormArgs& a) {
-  const long rows = 4 / W;
-  hipLaunchKernelGGL((k_add_norm<T, E4M3, W, CH>), dim3(unsigned((a.N + rows - 1) / rows)), dim3(256), 0, a.stream, a);
+  const long rows = 4 / W, n = (a.N + rows - 1) / rows, most = 1 << 23;  // a launch counts its threads along x in 32 bits
+  const dim3 grid(unsigned(n < most ? n : most), unsigned((n + most - 1) / most));
+  hipLaunchKernelGGL((k_add_norm<T, E4M3, W, CH>), grid, dim3(256), 0, a.stream, a);
 }
 template <typename T, bool E4M3>
 void launch(const AddNormArgs& a) {

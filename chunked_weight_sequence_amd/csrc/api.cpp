@@ -986,7 +986,7 @@ TTT_EXPORT ttt_status ttt_gated_delta_decode(const void* Q, long long q_stride, 
 namespace {
 bool delta_packed_ok(int n_seq, int N, int Hk, int Hv, int dk, int dv) {
   return delta_shape_ok(N, n_seq, Hk, Hv, dk, dv) && N <= (1 << 26) &&
-         // a launch counts its threads in 32 bits: 256 per 64 tokens and head, 128 per 32 columns
+         // a launch counts its threads in 32 bits: 256 per 64 tokens and head, 512 per 32 columns
          ((long long)N / 64 + n_seq) * Hv < (1 << 24) && (long long)n_seq * Hv * dv < (1 << 28);
 }
 }  // namespace

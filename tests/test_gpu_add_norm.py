@@ -110,6 +110,33 @@ def test_values_at_the_ends_of_the_range(N, e4m3):
         _check(got, x, None, w, 1e-30, "f32")
 
 
+@pytest.mark.parametrize("N,D", [(4, 256), (2100, 256), (4, 4096)])
+@pytest.mark.parametrize("size,weight", [(1e15, 1e25), (1e-15, 1e-28), (1e15, 1e-30), (1e-15, 1e30)])
+def test_scales_of_weights_far_from_one(N, D, size, weight):
+    """The product of a value and its weight may leave fp32 where the norm times the weight does not."""
+    print(f"case: norm e4m3 {N} x {D}, values of {size}, weights of {weight}", flush=True)
+    rng = np.random.default_rng(N + D)
+    x = (size * rng.standard_normal((N, D))).astype(np.float32)
+    x[1] = 0.5
+    w = (weight * rng.uniform(0.5, 2, D)).astype(np.float32)
+    for group in (0, 64):
+        _check(ttt.add_rms_norm(dev(x, "f32"), dev(w, "f32"), eps=0.0, e4m3=True, group=group), x, None, w, 0.0, "f32", group)
+
+
+def test_as_many_rows_as_a_launch_has_threads():
+    """Rows times lanes past 2^32: rows of 8 channels, whose sums of squares are exact."""
+    import torch
+    N = (1 << 26) + 5
+    print(f"case: norm, {N} rows", flush=True)
+    sign = (torch.arange(N, device="cuda") % 3 - 1).to(torch.bfloat16)  # -1, 0, 1
+    x = (2 * sign)[:, None].expand(N, 8).contiguous()
+    Y, _, _ = ttt.add_rms_norm(x, eps=2.0 ** -126)
+    assert torch.equal(Y, sign[:, None].expand(N, 8))
+    Y, s, _ = ttt.add_rms_norm(x, eps=2.0 ** -126, e4m3=True)
+    assert torch.equal(s > 2.0 ** -126, sign != 0)
+    assert torch.equal(Y.view(torch.uint8)[:, 3], torch.where(sign == 0, 0, torch.where(sign > 0, 0x7E, 0xFE)).to(torch.uint8))
+
+
 def test_infinities_and_nan_stay_in_their_rows():
     print("case: norm, infinities and NaN", flush=True)
     rng = np.random.default_rng(4)
