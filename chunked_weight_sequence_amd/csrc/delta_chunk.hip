@@ -24,9 +24,9 @@
 // beside K and Q (32768 tokens of 32 heads: 419 MB out, 604 in, 203 us, 5 TB/s, as much as a copy reaches; three
 // planes of T in the order in which the scan's operands lie are more bytes than L would be, but the inverse is computed
 // once for a head and not in each of its column tiles). k_delta_scan: the chain through S, whose 512 chunks follow each
-// other here: 840 .. 960 us, 3550 clocks a chunk (at 2.0 GHz: power); of that 72 matrix instructions of the wave that
-// has most, 17 clocks each, and between them splits into planes and four meetings. 8192 tokens in 11 sequences of 32
-// heads: 52 + 168 us.
+// other here: 860 .. 930 us, 3500 clocks a chunk (at 2.0 GHz: power); of that 72 matrix instructions of the wave that
+// has most, 17 clocks each, and between them splits into planes and three meetings. 8192 tokens in 11 sequences of 32
+// heads: 52 + 161 us.
 #include <type_traits>
 
 #include "common.hpp"
@@ -388,12 +388,11 @@ __device__ __forceinline__ void dl_meet_copied() {  // and at most MOST of the w
 // K, hands the sums for the other's tokens over, solves for its tokens' u (the second with what the first hands on)
 // and adds all u to its rows. Their vector work is dealt out between the products. The others copy the next chunk's
 // tiles into LDS and compute the outputs, 32 tokens each, from the planes of S and the u that are left in LDS. All
-// meet four times a chunk; what is there behind a meeting:
-//   B  chunk c's V and A                        1  the sums for the other's tokens; the planes of S
+// meet three times a chunk; what is there behind a meeting:
+//   1  the sums for the other's tokens; the planes of S
 //   2  the first half's V - e^G K S, in planes; Q of chunk c
-//   3  u, and what of it the state takes, in planes; K of chunk c + 1
-// What u adds to the outputs is added behind the next B, where these waves have time: between 3 and B the carrying ones
-// waited 700 clocks of 4900 a chunk for it.
+//   3  u, and what of it the state takes, in planes; K, V and A of chunk c + 1
+// What u adds to the outputs is added behind 3, while the carrying waves finish the state and begin the next chunk.
 template <int DK, int TILES>
 __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a) {
   constexpr int CARRY = 2 * TILES, CW = 16 * TILES, KT = DL_C * DK * 2, VT = DL_C * CW * 2;
@@ -405,7 +404,8 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
     char s[2 * KS * 1024];  // two planes of S
     char u[4 * 1024];       // u, row blocks in fp32
     char r[3 * 1024];       // planes of the first half's V - e^G K S
-    char px[6 * 1024];      // sums for the tokens of the first, of the second wave; then planes of what the state takes of u
+    char sum[4 * 1024];     // sums for the tokens of the first, of the second wave
+    char x[6 * 1024];       // planes of what the state takes of u
   };
   __shared__ __align__(1024) char sm[2][STAGE];
   __shared__ __align__(1024) char q_s[KT];
@@ -419,7 +419,8 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
   const int me = wave & 1, tile = TILES == 2 ? wave >> 1 & 1 : 0, col = col0 + 16 * tile;
   const int g4 = 4 * (lane >> 4), c16 = lane & 15, l16 = 16 * lane;
   const int chunks = (sq.n + DL_C - 1) / DL_C;
-  char *const s_s = hand[tile].s, *const u_s = hand[tile].u, *const r_s = hand[tile].r, *const px_s = hand[tile].px;
+  char *const s_s = hand[tile].s, *const u_s = hand[tile].u, *const r_s = hand[tile].r, *const x_s = hand[tile].x,
+       *const sum_s = hand[tile].sum;
 
   if (wave >= CARRY) {
     constexpr int NK = KT / 1024 / CARRY, NU = (REST / 1024 + CARRY - 1) / CARRY, BACK = 3 * 1024;  // copies of a wave; NU: some are repetitions
@@ -513,10 +514,9 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
     dl_meet_copied<0>();
     for (int c = 0; c < chunks; ++c) {
       const bool next = c + 1 < chunks;
-      dl_meet_copied<NK>();  // B: behind V and A comes Q
       if (next) part(0, c + 1);
       if (c > 0) finish(c - 1);
-      asm volatile("" ::: "memory");  // its stores stay before the copies that follow: they are counted together
+      asm volatile("" ::: "memory");  // its stores stay between the copies: they are counted together
       dl_fence();
       const char* const ut = sm[c & 1] + AT_U;
       const float* const f = reinterpret_cast<const float*>(ut + DL_TOK - DL_A);
@@ -547,8 +547,7 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) o[t] *= f[DL_OUT + 16 * (2 * me + t) + c16];
-      if (next) dl_meet_copied<NVU>();  // 3: behind the next K come the outputs, V and A
-      else dl_meet();
+      dl_meet_copied<0>();  // 3
       if (next) part(2, c + 1);
     }
     dl_meet();  // the last u
@@ -631,7 +630,6 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
     if (KH == 1)
 #pragma unroll
       for (int n = 0; n < 20; ++n) cut_state(0, n);
-    dl_meet();  // B
     const char* const kt = sm[c & 1];
     const char* const ut = kt + AT_U;
     const char* const vt = kt + AT_V;
@@ -660,15 +658,15 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
         keep[k - 15] = *reinterpret_cast<const float4*>(f + DL_LEFT + 16 * (2 * me + k - 15) + g4);
       }
       if (k == 12 * KH - 2) {
-        *reinterpret_cast<f32x4*>(px_s + (1 - me) * 2048 + l16) = x[0];
-        *reinterpret_cast<f32x4*>(px_s + (1 - me) * 2048 + 1024 + l16) = x[1];
+        *reinterpret_cast<f32x4*>(sum_s + (1 - me) * 2048 + l16) = x[0];
+        *reinterpret_cast<f32x4*>(sum_s + (1 - me) * 2048 + 1024 + l16) = x[1];
       }
       dl_fence();
     }
     dl_meet();  // 1
     f32x4 other[2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) other[b] = *reinterpret_cast<const f32x4*>(px_s + me * 2048 + b * 1024 + l16);
+    for (int b = 0; b < 2; ++b) other[b] = *reinterpret_cast<const f32x4*>(sum_s + me * 2048 + b * 1024 + l16);
     if (KH == 1)
 #pragma unroll
       for (int b = 0; b < 2; ++b) keep[b] = *reinterpret_cast<const float4*>(f + DL_LEFT + 16 * (2 * me + b) + g4);
@@ -731,7 +729,7 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
       cut.step(n);
       if (n % 8 == 7 || n == 19) {
         xu[n / 8] = cut.plane(n / 8);
-        *reinterpret_cast<uint4*>(px_s + me * 3072 + n / 8 * 1024 + l16) = xu[n / 8];
+        *reinterpret_cast<uint4*>(x_s + me * 3072 + n / 8 * 1024 + l16) = xu[n / 8];
       }
     }
 #pragma unroll
@@ -745,7 +743,7 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
     }
     dl_meet();  // 3
 #pragma unroll
-    for (int p = 0; p < 3; ++p) xo[p] = *reinterpret_cast<const uint4*>(px_s + (1 - me) * 3072 + p * 1024 + l16);
+    for (int p = 0; p < 3; ++p) xo[p] = *reinterpret_cast<const uint4*>(x_s + (1 - me) * 3072 + p * 1024 + l16);
     dl_fence();
     if (me) {
 #pragma unroll
@@ -780,9 +778,9 @@ hipError_t launch(const DeltaPackedArgs& a) {
   if (e != hipSuccess) return e;
   const long heads = long(d.n_seq) * d.Hv;
   // 16 columns of a workgroup where each then has one of the card's 256 units to itself, and its carrying waves a SIMD:
-  // 32 where there are more (one fits a unit). 8192 tokens of 128 x 128, both launches with 16 and with 32 columns: 4
-  // heads 204 and 250 us, 32 heads 261 and 294, 40 heads 510 and 323; 64 x 128: 8 heads 185 and 207, 32 heads 221 and
-  // 237, 40 heads 272 and 268, 64 heads 375 and 331.
+  // 32 where there are more (one fits a unit). 8192 tokens of 128 x 128, both launches with 16 and with 32 columns (with a
+  // fourth meeting): 4 heads 204 and 250 us, 32 heads 261 and 294, 40 heads 510 and 323; 64 x 128: 8 heads 185 and 207,
+  // 32 heads 221 and 237, 40 heads 272 and 268, 64 heads 375 and 331.
   if (heads * (d.dv / 16) <= 256)
     hipLaunchKernelGGL((k_delta_scan<DK, 1>), dim3(unsigned(heads * (d.dv / 16))), dim3(256), 0, d.stream, a);
   else
