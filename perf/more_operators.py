@@ -307,7 +307,8 @@ def _own_norm(s):
     case = s["case"]
     got = ttt.add_rms_norm(s["X"], s["w"], residual=s["R"], eps=EPS, e4m3=case["out"] == E4M3,
                            group=case["group"])
-    return [x for x in got if x is not None]
+    # one scale a row comes as [N]; the plain form's are [N, groups]
+    return [x if x.dim() == 2 else x[:, None] for x in got if x is not None]
 
 
 def _own_paged(s):
