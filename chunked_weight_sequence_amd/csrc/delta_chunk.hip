@@ -386,12 +386,14 @@ __device__ __forceinline__ void dl_meet_copied() {  // and at most MOST of the w
 // each on a SIMD of its own, and two that do the rest beside them. Of the carrying waves the first has the state's
 // first half of rows and the chunk's first 32 tokens, the second the others: each multiplies its rows of S by all of
 // K, hands the sums for the other's tokens over, solves for its tokens' u (the second with what the first hands on)
-// and adds all u to its rows. Their vector work is dealt out between the products. The others copy the next chunk's
-// tiles into LDS and compute the outputs, 32 tokens each, from the planes of S and the u that are left in LDS. All
+// and adds all u to its rows. Their vector work is dealt out between the products. The others copy tiles
+// into LDS and compute the outputs, 32 tokens each, from the planes of S and the u that are left in LDS. All
 // meet three times a chunk; what is there behind a meeting:
 //   1  the sums for the other's tokens; the planes of S
-//   2  the first half's V - e^G K S, in planes; Q of chunk c
-//   3  u, and what of it the state takes, in planes; K, V and A of chunk c + 1
+//   2  the first half's V - e^G K S, in planes; Q of chunk c; K, V and A of chunk c + 1
+//   3  u, and what of it the state takes, in planes
+// K, V and A are copied two chunks ahead: one ahead, the copies were late where the inputs come from HBM (32768 tokens of
+// 32 heads, both launches 1046 us, this 984; 8192 tokens 260 and 255).
 // What u adds to the outputs is added behind 3, while the carrying waves finish the state and begin the next chunk.
 template <int DK, int TILES>
 __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a) {
@@ -407,7 +409,7 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
     char sum[4 * 1024];     // sums for the tokens of the first, of the second wave
     char x[6 * 1024];       // planes of what the state takes of u
   };
-  __shared__ __align__(1024) char sm[2][STAGE];
+  __shared__ __align__(1024) char sm[3][STAGE];
   __shared__ __align__(1024) char q_s[KT];
   __shared__ __align__(1024) Hand hand[TILES];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -463,9 +465,9 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
       }
     };
     // The copies of chunk c, in three parts: they are waited for one after the other, so their numbers count, and
-    // stores that follow stay behind them.
-    const auto part = [&](int which, int c) DL_INLINE {
-      const uint32_t to = lds + (c & 1) * STAGE;
+    // stores that follow stay behind them. K, V and A go to one of three stages.
+    const auto part = [&](int which, int c, int stage = 0) DL_INLINE {
+      const uint32_t to = lds + stage * STAGE;
       const int left = sq.n - c * DL_C;
       if (which == 0) rows(kp + long(c) * DL_C * a.d.ks, a.d.ks, ko, left, to);
       if (which == 2) rows(qp + long(c) * DL_C * a.d.qs, a.d.qs, qo, left, lds_q);
@@ -511,17 +513,22 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
       part(1, 0);
       part(2, 0);
     }
+    if (chunks > 1) {
+      part(0, 1, 1);
+      part(1, 1, 1);
+    }
     dl_meet_copied<0>();
+    int at = 0, to = 2;  // c and c + 2 modulo 3
     for (int c = 0; c < chunks; ++c) {
-      const bool next = c + 1 < chunks;
-      if (next) part(0, c + 1);
+      const bool next = c + 2 < chunks;
+      if (next) part(0, c + 2, to);
       if (c > 0) finish(c - 1);
       asm volatile("" ::: "memory");  // its stores stay between the copies: they are counted together
       dl_fence();
-      const char* const ut = sm[c & 1] + AT_U;
+      const char* const ut = sm[at] + AT_U;
       const float* const f = reinterpret_cast<const float*>(ut + DL_TOK - DL_A);
       dl_meet();  // 1
-      if (next) part(1, c + 1);
+      if (next) part(1, c + 2, to);
       uint4 sp[KS][2];
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -532,7 +539,8 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           af[t][k] = *reinterpret_cast<const uint4*>(ut + (me ? dl_frag(2 + t, k) : t) * 1024 + l16);
-      if (next) dl_meet_copied<NK + STORES + NVU>();  // 2: behind Q come the next K, the last outputs, the next V and A
+      // 2: behind K, V and A of the next chunk and Q of this one come K of the one after, the last outputs, its V and A
+      if (next) dl_meet_copied<NK + STORES + NVU>();
       else dl_meet_copied<STORES>();
       // O^T = S^T Q^T e^G: a lane has 4 neighbouring columns of a token
 #pragma unroll
@@ -547,8 +555,10 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) o[t] *= f[DL_OUT + 16 * (2 * me + t) + c16];
-      dl_meet_copied<0>();  // 3
-      if (next) part(2, c + 1);
+      dl_meet();  // 3
+      if (c + 1 < chunks) part(2, c + 1);
+      to = at;
+      at = at == 2 ? 0 : at + 1;
     }
     dl_meet();  // the last u
     if (chunks > 0) finish(chunks - 1);
@@ -626,11 +636,12 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
   if (chunks > 0)
 #pragma unroll
     for (int i = 0; i < 4 * KH; ++i) read_k(sm[0], i);
-  for (int c = 0; c < chunks; ++c) {
+  for (int c = 0, at = 0; c < chunks; ++c) {
     if (KH == 1)
 #pragma unroll
       for (int n = 0; n < 20; ++n) cut_state(0, n);
-    const char* const kt = sm[c & 1];
+    const char* const kt = sm[at];
+    at = at == 2 ? 0 : at + 1;
     const char* const ut = kt + AT_U;
     const char* const vt = kt + AT_V;
     const float* const f = reinterpret_cast<const float*>(ut + DL_TOK - DL_A);
@@ -757,7 +768,7 @@ __global__ __launch_bounds__(256 * TILES, 1) void k_delta_scan(DeltaPackedArgs a
     for (int k = 0; k < 3 * DH; ++k) {
       const int d = 2 * (k / 6) + k % 2, p = 2 - k % 6 / 2;
       S[d] = mfma16x16x32(kc[1][d], xo[p], S[d]);
-      if (k < 4 * KH) read_k(sm[(c & 1) ^ 1], k);
+      if (k < 4 * KH) read_k(sm[at], k);
       if (KH > 1) deal(k, 3 * DH, 7, 20 * (KH - 1), [&](int i) DL_INLINE { cut_state(i / 20, i % 20); });
       dl_fence();
     }
