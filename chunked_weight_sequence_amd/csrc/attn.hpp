@@ -23,7 +23,7 @@
 // all banks.
 #pragma once
 #include "common.hpp"
-#include "dma.hpp"
+#include "dma_row.hpp"
 
 namespace ttt {
 

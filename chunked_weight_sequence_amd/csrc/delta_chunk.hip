@@ -30,7 +30,7 @@
 #include <type_traits>
 
 #include "common.hpp"
-#include "dma.hpp"
+#include "dma_row.hpp"
 #include "launch.hpp"
 
 namespace ttt {
