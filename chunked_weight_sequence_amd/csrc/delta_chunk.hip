@@ -24,7 +24,7 @@
 // beside K and Q (32768 tokens of 32 heads: 419 MB out, 604 in, 203 us, 5 TB/s, as much as a copy reaches; three
 // planes of T in the order in which the scan's operands lie are more bytes than L would be, but the inverse is computed
 // once for a head and not in each of its column tiles). k_delta_scan: the chain through S, whose 512 chunks follow each
-// other here: 860 .. 930 us, 3500 clocks a chunk (at 2.0 GHz: power); of that 72 matrix instructions of the wave that
+// other here: 790 .. 870 us, 3450 clocks a chunk at 2.0 GHz; of that 72 matrix instructions of the wave that
 // has most, 17 clocks each, and between them splits into planes and three meetings. 8192 tokens in 11 sequences of 32
 // heads: 52 + 161 us.
 #include <type_traits>
