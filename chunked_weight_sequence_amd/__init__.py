@@ -777,6 +777,14 @@ def attention_paged(Q, K_cache, V_cache, cu_q, page_table, lengths, page_size: i
     return O if lse is None else (O, lse)
 
 
+def _row_stride(t, name: str, N, D):
+    """The row stride in elements of an [N, D] tensor whose rows are contiguous."""
+    stride = t.stride()
+    if stride[1] != 1 and D > 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    return stride[0] if N > 1 else D
+
+
 def _matrix(t, name: str, N, D, dtype, device):
     """Checks a [N, D] GPU tensor whose rows may lie apart; returns its row stride in elements."""
     if t.shape != (N, D):
@@ -785,9 +793,7 @@ def _matrix(t, name: str, N, D, dtype, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.stride(1) != 1 and D > 1:
-        raise ValueError(f"{name}: a row must be contiguous")
-    return t.stride(0) if N > 1 else D
+    return _row_stride(t, name, N, D)
 
 
 def add_rms_norm(X, weight=None, *, residual=None, eps: float = 1e-6, e4m3: bool = False, group: int = 0,
@@ -805,7 +811,7 @@ def add_rms_norm(X, weight=None, *, residual=None, eps: float = 1e-6, e4m3: bool
     code = _dtype_code(dt)
     if N >= 1 << 31 or D >= 1 << 31:
         raise ValueError(f"X is too large: {(N, D)}")
-    xs = _matrix(X, "X", N, D, dt, dev)
+    xs = _row_stride(X, "X", N, D)
     rs = ss = 0
     if residual is not None:
         rs = _matrix(residual, "residual", N, D, dt, dev)
@@ -919,7 +925,8 @@ def gated_delta_decode(Q, K, V, g, beta, state, *, state_out=None, slots=None, s
     u = beta (v - a W^T k), W <- a W + k u^T, o = scale W^T q; q and k divided by their norm first
     (normalize). Q, K [S,Hk,dk], V [S,Hv,dv] bf16 (tokens may be slices of one buffer), g and beta [S,Hv] fp32;
     state [n_slots,Hv,dk,dv] fp32 (None: all start at zero), of which sequence s has slot slots[s] (int32; slots
-    None: s; outside: starts at zero, nothing kept). The new states go to the same slots of state_out, in place if that is None.
+    None: s; outside: starts at zero, nothing kept). The new states go to the same slots of state_out, in place if
+    that is None.
     scale: 1 / sqrt(dk) by default. Returns (O [S,Hv,dv], state_out)."""
     O, args, S, Hk, Hv, dk, dv = _delta_inputs(Q, K, V, g, beta, O)
     state_out = state if state_out is None else state_out
