@@ -50,7 +50,7 @@ inline int packed_splits(int qt, int n_seq, int Nq, long Nk, int Hq, int Hkv, in
   }
   return best;
 }
-inline PackedPlan packed_plan(int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh, int window) {
+inline PackedPlan packed_plan(int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh, int window, bool wide = true) {
   // 256 rows share each tile read from LDS, which costs least power (long rows are bound by that), but
   // leave the chip's 256 places unevenly filled and nothing to run while a workgroup starts and ends
   // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least 9
@@ -61,7 +61,7 @@ inline PackedPlan packed_plan(int n_seq, int Nq, long Nk, int Hq, int Hkv, int d
   // us, 12000 tokens of 4/1 heads in 2 documents 205 / 153 us. Heads of 64, which the vector unit
   // bounds: 8191 tokens, window 2048, 188 / 145 us.
   PackedPlan p{1, 0, 1, 0, false};
-  if (dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
+  if (wide && dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
     const int pieces = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, window);
     const long wgs = packed_wgs(2, n_seq, Nq, Hq, Hkv), n = wgs * pieces;
     const long seen = packed_seen(n_seq, Nq, Nk, window);
@@ -102,7 +102,9 @@ inline size_t packed_workspace(int n_seq, int Nq, long Nk, int Hq, int Hkv, int 
 // device knows the lengths.
 inline long paged_keys(int n_seq, int max_pages, int page) { return long(n_seq) * max_pages * page; }
 // Pieces that the keys are split into where there are several sequences: lengths and numbers of rows differ then, so
-// a quarter more workgroups than the chip holds at once, and the joining weighs half as much again. Best, and what
+// a quarter more workgroups than the chip holds at once, twice as many where a sequence has one wave's rows (HBM bounds
+// those: 15 single tokens on up to 12000 87 us in 5 pieces, 78 in 8, 16 on up to 30000 282 in 4, 265 in 8, 32 x 2 on up
+// to 8000 142 in 2, 136 in 4), and the joining weighs half as much again. Best, and what
 // the rule for one sequence takes, of a sweep: 16 x 5 tokens on up to 8000, 16/4 heads of 64, in 12 pieces 27 us, in 3
 // 42 us; 512 tokens and 14 single ones on up to 12000, 32/8 heads of 128, in 2 pieces 164 us (3: 175), whole 258;
 // up to 64 tokens each of 16 on up to 8000 in 3 pieces 77 us, whole 128; 4 x 500 on up to 6000 in 2 119 us, whole 143;
@@ -111,7 +113,8 @@ inline int paged_splits(int qt, int n_seq, int Nq, long Nk, int Hq, int Hkv, int
   if (n_seq == 1) return packed_splits(qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
   const long keys = packed_keys(n_seq, Nk, window), wgs = packed_wgs(qt, n_seq, Nq, Hq, Hkv);
   const long places = qt == 2 ? 256 : dh == 64 ? 768 : 512;
-  long most = (5 * places / 4 + wgs / 2) / wgs;
+  const bool few = long(Nq) * (Hq / Hkv) <= 32L * n_seq;
+  long most = ((few ? 2 * places : 5 * places / 4) + wgs / 2) / wgs;
   if (most > keys / 256) most = keys / 256;
   if (most > PLAN_MAX_SPLITS) most = PLAN_MAX_SPLITS;
   const double tiles = keys / 64 * (qt == 2 ? 1.5 : dh == 64 ? 0.5 : 0.75);
@@ -126,7 +129,11 @@ inline int paged_splits(int qt, int n_seq, int Nq, long Nk, int Hq, int Hkv, int
 }
 inline PackedPlan paged_plan(int n_seq, int Nq, int max_pages, int page, int Hq, int Hkv, int dh, int window) {
   const long Nk = paged_keys(n_seq, max_pages, page);
-  PackedPlan p = packed_plan(n_seq, Nq, Nk, Hq, Hkv, dh, window);
+  // 256 rows only for sequences that fill several such tiles. 256 / 128, each in its best number of pieces: 8 x 500
+  // tokens after 15500 910 / 939 us, 4 x 256 after 15744 244 / 270, but 8 x 200 after 7800 225 / 216, 16 x 60 172 / 156,
+  // 15 single tokens on up to 12000 101 / 78, 32 x 2 on up to 8000 160 / 129.
+  const bool wide = n_seq == 1 || long(Nq) * (Hq / Hkv) >= 1024L * n_seq;
+  PackedPlan p = packed_plan(n_seq, Nq, Nk, Hq, Hkv, dh, window, wide);
   if (n_seq > 1) {
     p.splits = paged_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
     p.half = p.tiles;

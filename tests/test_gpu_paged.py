@@ -83,7 +83,8 @@ def test_windows(Hq, Hkv, dh, window):
     ([1100], [5000], 256, 32, 8, 128, 0), ([600], [5000], 64, 16, 16, 64, 700), ([2100], [2100], 64, 32, 8, 128, 0),
     ([300] + [1] * 20, [4000] + [100 * i + 1 for i in range(20)], 16, 16, 4, 128, 0),
     ([5] * 16, [500 * i + 5 for i in range(16)], 16, 16, 4, 64, 0), ([2, 1] * 50, [40, 30] * 50, 16, 8, 2, 128, 0),
-    ([1] * 70, [20] * 70, 16, 4, 4, 64, 0), ([0, 0], [100, 50], 16, 8, 2, 128, 0)])
+    ([1] * 70, [20] * 70, 16, 4, 4, 64, 0), ([0, 0], [100, 50], 16, 8, 2, 128, 0),
+    ([400, 139, 500, 300, 200], [2560, 1000, 500, 2300, 2559], 16, 32, 8, 128, 0), ([1] * 15, [97 * i for i in range(15)], 32, 32, 8, 128, 0)])
 def test_long_and_many(new, lens, page, Hq, Hkv, dh, window):
     """The forms of the kernels: rows by 128 and by 256, keys split over workgroups, many sequences."""
     print(f"case: paged long {new[:4]} {lens[:4]} {Hq}/{Hkv}x{dh} page {page}", flush=True)

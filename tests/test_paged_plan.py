@@ -55,11 +55,12 @@ def test_forms(plan):
     """Rows by 128 and by 256, whole and in pieces, of one and of several sequences."""
     got = {name: plan(*a) for name, a in dict(
         one=(1, 512, 256, 64, 32, 8, 128, 0), drafts=(16, 48, 500, 16, 16, 4, 64, 0), whole=(4, 8000, 32, 256, 32, 32, 64, 2048),
-        mixed=(16, 526, 375, 32, 32, 8, 128, 0), wide=(8, 135, 250, 16, 32, 8, 128, 0), prompt=(1, 2100, 33, 64, 32, 8, 128, 0),
+        mixed=(16, 526, 375, 32, 32, 8, 128, 0), wide=(5, 1539, 160, 16, 32, 8, 128, 0), few=(8, 135, 250, 16, 32, 8, 128, 0), prompt=(1, 2100, 33, 64, 32, 8, 128, 0),
         short=(16, 790, 19, 16, 32, 8, 128, 0)).items()}
     assert (got["one"]["qt"], got["one"]["splits"]) == (2, 4)
     assert got["drafts"]["qt"] == 1 and got["drafts"]["splits"] >= 8
     assert (got["whole"]["qt"], got["whole"]["splits"]) == (1, 1)
     assert (got["mixed"]["qt"], got["mixed"]["splits"]) == (1, 3)
-    assert got["wide"]["qt"] == 2 and got["wide"]["splits"] > 1
+    assert (got["wide"]["qt"], got["wide"]["splits"]) == (2, 1)
+    assert got["few"]["qt"] == 1 and got["few"]["splits"] > 1
     assert got["short"]["splits"] == 1 and got["prompt"]["splits"] == 1
