@@ -201,3 +201,37 @@ def test_refusals():
         else:
             with pytest.raises(err):
                 ttt.add_rms_norm(*args, **kw)
+
+
+def test_values_beside_the_ties_of_eight_bits():
+    """Codes are those of the quotient y / scale, rounded once to fp32 and once to e4m3, ties to even. Rows of +1 and
+    -1 have a mean square of 1 and with eps = 0 a factor of exactly 1, so y is the weight with the row's signs, and
+    the weights here are the fp32 numbers at and beside scale * (the middle between two codes)."""
+    import torch
+    rng = np.random.default_rng(21)
+    values = osv.e4m3_values()
+    up = np.unique(np.abs(values[np.isfinite(values)]))  # 0 .. 448
+    middle = (up[1:] + up[:-1]) / 2
+    for top in (1.0, 3.7, 0.0123, 448.0, 1e-20, 7e30, 1e-30, 1e36):
+        print(f"case: norm e4m3, values beside ties, the largest {top}", flush=True)
+        top = np.float32(top)
+        scale = np.float32(top / np.float32(448))
+        at = (middle * np.float64(scale)).astype(np.float32)
+        w = np.concatenate([at, np.nextafter(at, np.float32(0)), np.nextafter(at, np.float32(np.inf))])
+        w = np.concatenate([w[w < top], np.full(512, top, np.float32)])[:512]
+        w = rng.permutation(w).astype(np.float32)
+        w[::128] = top  # every group's scale is the row's
+        x = np.where(rng.random((3, 512)) < 0.5, -1, 1).astype(np.float32)
+        q = (np.abs(w) / scale).astype(np.float64)  # fp32 quotients
+        lo = np.clip(np.searchsorted(up, q, side="right") - 1, 0, len(up) - 1)
+        hi = np.minimum(lo + 1, len(up) - 1)
+        d = (q - up[lo]) - (up[hi] - q)
+        code = np.where((d > 0) | ((d == 0) & (lo % 2 == 1)), hi, lo)  # codes of the sizes are their numbers
+        for dtype in ("f32", "bf16"):
+            xs = dev(x if dtype == "f32" else gen.f32_to_bf16_bits(x), dtype)
+            for group in (0, 128):
+                Y, s, _ = ttt.add_rms_norm(xs, dev(w, "f32"), eps=0.0, e4m3=True, group=group)
+                assert (host_f64(s) == np.float64(scale)).all()
+                got = Y.view(torch.uint8).cpu().numpy()
+                np.testing.assert_array_equal(got & 127, np.broadcast_to(code, got.shape))
+                np.testing.assert_array_equal(got >> 7 == 1, x < 0)
