@@ -50,7 +50,9 @@ inline int packed_splits(int qt, int n_seq, int Nq, long Nk, int Hq, int Hkv, in
   }
   return best;
 }
-inline PackedPlan packed_plan(int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh, int window, bool wide = true) {
+// The form, judged with the pieces that are launched: pieces(qt) of rows by 128 qt, of which 256 only where `wide`.
+template <class Pieces>
+inline PackedPlan plan_rows(int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh, int window, bool wide, Pieces pieces) {
   // 256 rows share each tile read from LDS, which costs least power (long rows are bound by that), but
   // leave the chip's 256 places unevenly filled and nothing to run while a workgroup starts and ends
   // (14000 clocks; a tile takes 2900). So: rows of at least 2048 keys whose workgroups fill at least 9
@@ -62,16 +64,15 @@ inline PackedPlan packed_plan(int n_seq, int Nq, long Nk, int Hq, int Hkv, int d
   // bounds: 8191 tokens, window 2048, 188 / 145 us.
   PackedPlan p{1, 0, 1, 0, false};
   if (wide && dh == 128 && packed_seen(n_seq, Nq, Nk, window) >= 2048) {
-    const int pieces = packed_splits(2, n_seq, Nq, Nk, Hq, Hkv, dh, window);
-    const long wgs = packed_wgs(2, n_seq, Nq, Hq, Hkv), n = wgs * pieces;
+    const long many = pieces(2), wgs = packed_wgs(2, n_seq, Nq, Hq, Hkv), n = wgs * many;
     const long seen = packed_seen(n_seq, Nq, Nk, window);
-    if (seen >= 1024 * pieces && 10 * n >= 9 * 256 * ((n + 255) / 256) &&
+    if (seen >= 1024 * many && 10 * n >= 9 * 256 * ((n + 255) / 256) &&
         (wgs >= 384 || 4 * packed_keys(n_seq, Nk, window) <= 5 * seen))
       p.qt = 2;
   }
   const long rows = long(Nq) * (Hq / Hkv);
   p.tiles = n_seq == 1 ? int((rows + 128 * p.qt - 1) / (128 * p.qt)) : int(rows / (128 * p.qt)) + n_seq;
-  p.splits = packed_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
+  p.splits = pieces(p.qt);
   // Row tiles are taken from the last on, so that the longest rows start first. Where all workgroups
   // start at once, two on a compute unit (three of heads of 64), those past the first 256 come in the
   // opposite order, so that each unit has long and short ones: 2048 tokens of 32/8 heads of 128 44 ->
@@ -88,6 +89,10 @@ inline PackedPlan packed_plan(int n_seq, int Nq, long Nk, int Hq, int Hkv, int d
               wgs > 512 && wgs <= 3200;
   p.half = p.qt == 1 && wgs > 256 && wgs <= (dh == 64 ? 768 : 512) ? 256 / (Hkv * p.splits) : p.tiles;
   return p;
+}
+inline PackedPlan packed_plan(int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh, int window) {
+  return plan_rows(n_seq, Nq, Nk, Hq, Hkv, dh, window, true,
+                   [&](int qt) { return packed_splits(qt, n_seq, Nq, Nk, Hq, Hkv, dh, window); });
 }
 
 inline size_t packed_workspace(int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh) {
@@ -129,14 +134,22 @@ inline int paged_splits(int qt, int n_seq, int Nq, long Nk, int Hq, int Hkv, int
 }
 inline PackedPlan paged_plan(int n_seq, int Nq, int max_pages, int page, int Hq, int Hkv, int dh, int window) {
   const long Nk = paged_keys(n_seq, max_pages, page);
-  // 256 rows only for sequences that fill several such tiles. 256 / 128, each in its best number of pieces: 8 x 500
-  // tokens after 15500 910 / 939 us, 4 x 256 after 15744 244 / 270, but 8 x 200 after 7800 225 / 216, 16 x 60 172 / 156,
-  // 15 single tokens on up to 12000 101 / 78, 32 x 2 on up to 8000 160 / 129.
+  // 256 rows only for sequences that fill several such tiles, and where plan_rows finds that what is launched fills the
+  // chip. 256 / 128, each in its best number of pieces, sequences alike and of unlike lengths, 32/8 heads of 128: 2 x 1024
+  // tokens on 16000 keys 469 / 477 and 276 / 286 us, 2 x 512 on 12000 192 / 201 and 120 / 123, 4 x 256 on 15744 247 / 267
+  // and 141 / 125, 8 x 500 on 15500 934 / 930 and 426 / 401, 4 x 1000 on 8000 462 / 454 and 199 / 182; 2 x 260 on 8000 in the 4
+  // pieces that are launched, which 256 rows do not fill, 118 / 103 and 69 / 65. With fewer rows 8 x 200 after 7800 225 / 216,
+  // 16 x 60 172 / 156, 15 single tokens on up to 12000 101 / 78, 32 x 2 on up to 8000 160 / 129.
   const bool wide = n_seq == 1 || long(Nq) * (Hq / Hkv) >= 1024L * n_seq;
-  PackedPlan p = packed_plan(n_seq, Nq, Nk, Hq, Hkv, dh, window, wide);
+  PackedPlan p = plan_rows(n_seq, Nq, Nk, Hq, Hkv, dh, window, wide,
+                           [&](int qt) { return paged_splits(qt, n_seq, Nq, Nk, Hq, Hkv, dh, window); });
   if (n_seq > 1) {
-    p.splits = paged_splits(p.qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
     p.half = p.tiles;
+    // In pieces, sequences are ordered where a piece has a tile for each of them. Ordered / not, means over three draws of
+    // lengths: 16 x up to 64 tokens on up to 8000 85 / 98 us, 16 x up to 16 on 16000 117 / 141, 12 x up to 200 on 9000 127 / 152,
+    // 15 single tokens on 12000 76 / 87, a piece of 512 beside 14 single tokens 164 / 166; but 16 x up to 5 on 8000, 16/4
+    // heads of 64 (7 tiles a piece), 26.6 / 25.4.
+    if (p.splits > 1) p.longest = p.longest && n_seq <= packed_keys(n_seq, Nk, window) / PLAN_TILE / p.splits;
   }
   return p;
 }

@@ -92,6 +92,17 @@ def test_long_and_many(new, lens, page, Hq, Hkv, dh, window):
     _run(rng, new, lens, page, Hq, Hkv, dh, window=window, some=40, behind=1 if not sum(new) else 0)
 
 
+@pytest.mark.parametrize("new,lens,Hq,Hkv", [
+    ([200, 9, 200], [4256, 900, 4100], 32, 4), ([1000, 224], [6560, 224], 8, 2), ([260, 260], [8000, 3900], 32, 8),
+    ([512] + [1] * 13, [6000] + [431 * i for i in range(13)], 32, 8)])
+def test_several_sequences_in_pieces(new, lens, Hq, Hkv):
+    """Rows by 256, then by 128, of several sequences whose keys are split over workgroups (test_paged_plan.py has which
+    sizes take which), the last one with the sequences in the order of their lengths."""
+    print(f"case: paged, several in pieces, {new[:3]} {lens[:3]} {Hq}/{Hkv}", flush=True)
+    rng = np.random.default_rng(sum(new) + sum(lens))
+    _run(rng, new, lens, 16, Hq, Hkv, 128, some=60, first=1, behind=2)
+
+
 @pytest.mark.parametrize("dh", [64, 128])
 @pytest.mark.parametrize("n", [100, 3000])
 def test_pages_that_are_not_there(n, dh):

@@ -64,3 +64,43 @@ def test_forms(plan):
     assert (got["wide"]["qt"], got["wide"]["splits"]) == (2, 1)
     assert got["few"]["qt"] == 1 and got["few"]["splits"] > 1
     assert got["short"]["splits"] == 1 and got["prompt"]["splits"] == 1
+
+
+def test_what_is_judged_is_what_is_launched(tmp_path):
+    """Of several sequences 256 rows are taken only where the workgroups of the pieces that are launched fill at least 9 of
+    10 places of the chip each time around, in pieces of at least 1024 keys, and an order by length only where more than
+    512 and at most 3200 are launched, each with a key tile at least for every sequence that it ranks."""
+    so = str(tmp_path / "forms.so")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, "-x", "c++", "-", "-o", so], input="""
+#include "attn_plan.hpp"
+using namespace ttt;
+extern "C" void form(int n, int Nq, int max_pages, int page, int Hq, int Hkv, int window, long* out) {
+  const PackedPlan p = paged_plan(n, Nq, max_pages, page, Hq, Hkv, 128, window);
+  const long Nk = paged_keys(n, max_pages, page), wgs = packed_wgs(p.qt, n, Nq, Hq, Hkv);
+  const long v[] = {p.qt, p.splits, p.longest, wgs, packed_seen(n, Nq, Nk, window), packed_keys(n, Nk, window)};
+  for (int i = 0; i < 6; ++i) out[i] = v[i];
+}
+""", text=True, check=True)
+    fn = ctypes.CDLL(so).form
+
+    def ask(*args):
+        out = (ctypes.c_long * 6)()
+        fn(*(ctypes.c_int(int(x)) for x in args), out)
+        return list(out)
+    rng, forms = random.Random(11), set()
+    for _ in range(40000):
+        Hkv, n = rng.choice([1, 2, 4, 8, 16]), rng.randint(2, 40)
+        a = (n, int(n * 2000 ** rng.random()), rng.randint(1, 1000), 16, Hkv * rng.choice([1, 2, 4, 8]), Hkv,
+             rng.choice([0, 0, rng.randint(1, 9000)]))
+        qt, splits, longest, wgs, seen, keys = ask(*a)
+        forms.add((qt, splits > 1, bool(longest)))
+        if qt == 2:
+            around = -(-wgs * splits // 256)
+            assert 10 * wgs * splits >= 9 * 256 * around and seen >= 1024 * splits, (a, qt, splits, wgs)
+        if longest:
+            assert 512 < wgs * splits <= 3200 and (splits == 1 or n <= keys // 64 // splits), (a, splits, wgs)
+    assert {(1, False, False), (1, False, True), (1, True, False), (1, True, True), (2, False, False), (2, True, False)} <= forms
+    # 2 x 260 tokens on 8000: 3 pieces would fill the chip, 4 are launched; the GPU tests' sequences in several pieces of 256 rows
+    assert ask(2, 520, 500, 16, 32, 8, 0)[:2] == [1, 4]
+    assert ask(3, 409, 266, 16, 32, 4, 0)[:2] == [2, 4]
+    assert ask(2, 1224, 410, 16, 8, 2, 0)[:2] == [2, 6]
