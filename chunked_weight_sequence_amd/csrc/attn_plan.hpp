@@ -140,7 +140,10 @@ inline PackedPlan paged_plan(int n_seq, int Nq, int max_pages, int page, int Hq,
   // and 141 / 125, 8 x 500 on 15500 934 / 930 and 426 / 401, 4 x 1000 on 8000 462 / 454 and 199 / 182; 2 x 260 on 8000 in the 4
   // pieces that are launched, which 256 rows do not fill, 118 / 103 and 69 / 65. With fewer rows 8 x 200 after 7800 225 / 216,
   // 16 x 60 172 / 156, 15 single tokens on up to 12000 101 / 78, 32 x 2 on up to 8000 160 / 129.
-  const bool wide = n_seq == 1 || long(Nq) * (Hq / Hkv) >= 1024L * n_seq;
+  // One sequence takes them where its rows do not fit in 128, as the sequence's key tiles are then copied once: 40 tokens on
+  // 65536 keys 76 / 87 us, 64 86 / 110; but 1 token 58 / 51, 5 on 32768 37 / 31, 32 (128 rows) 44 / 37, on 131072 127 / 126.
+  const long rows = long(Nq) * (Hq / Hkv);
+  const bool wide = n_seq == 1 ? rows > 128 : rows >= 1024L * n_seq;
   PackedPlan p = plan_rows(n_seq, Nq, Nk, Hq, Hkv, dh, window, wide,
                            [&](int qt) { return paged_splits(qt, n_seq, Nq, Nk, Hq, Hkv, dh, window); });
   if (n_seq > 1) {

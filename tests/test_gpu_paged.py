@@ -103,6 +103,15 @@ def test_several_sequences_in_pieces(new, lens, Hq, Hkv):
     _run(rng, new, lens, 16, Hq, Hkv, 128, some=60, first=1, behind=2)
 
 
+@pytest.mark.parametrize("new,n,room,Hq,Hkv", [(1, 33000, 33000, 32, 8), (5, 50000, 50000, 16, 4), (32, 700, 131072, 32, 8), (40, 1, 70000, 8, 2), (33, 33000, 33000, 16, 4)])
+def test_one_sequence_on_a_long_table(new, n, room, Hq, Hkv):
+    """A few tokens on many keys, and on few keys of a table that has room for many."""
+    print(f"case: paged, {new} tokens on {n} of {room}, {Hq}/{Hkv}", flush=True)
+    rng = np.random.default_rng(new + n)
+    kv = _pool(rng, [n], 64, Hkv, 128, most=-(-room // 64))
+    _run(rng, [new], [n], 64, Hq, Hkv, 128, kv=kv, some=8)
+
+
 @pytest.mark.parametrize("dh", [64, 128])
 @pytest.mark.parametrize("n", [100, 3000])
 def test_pages_that_are_not_there(n, dh):

@@ -104,3 +104,11 @@ extern "C" void form(int n, int Nq, int max_pages, int page, int Hq, int Hkv, in
     assert ask(2, 520, 500, 16, 32, 8, 0)[:2] == [1, 4]
     assert ask(3, 409, 266, 16, 32, 4, 0)[:2] == [2, 4]
     assert ask(2, 1224, 410, 16, 8, 2, 0)[:2] == [2, 6]
+
+
+def test_few_rows_of_one_sequence_stay_in_one_tile_of_128(plan):
+    """However long the keys, or the table that has room for them, are."""
+    for new in (1, 5, 32):
+        for keys in (4096, 32768, 49152, 131072, 1 << 20):
+            assert plan(1, new, keys // 64, 64, 32, 8, 128, 0)["qt"] == 1, (new, keys)
+    assert plan(1, 40, 1024, 64, 32, 8, 128, 0)["qt"] == 2 and plan(1, 128, 1024, 64, 8, 8, 128, 0)["qt"] == 1
