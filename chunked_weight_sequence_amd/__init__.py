@@ -896,7 +896,7 @@ def gated_delta_packed(Q, K, V, g, beta, cu, *, state=None, state_out=None, slot
     torch = _torch()
     O, args, N, Hk, Hv, dk, dv = _delta_inputs(Q, K, V, g, beta, O)
     dev = Q.device
-    if cu.dim() != 1:
+    if cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError(f"cu must be [n_seq + 1], got {tuple(cu.shape)}")
     n_seq = cu.shape[0] - 1
     _vec(cu, "cu", (n_seq + 1,), torch.int32, dev)

@@ -368,3 +368,11 @@ def test_offsets_are_clamped_and_states_may_be_missing():
     torch.cuda.synchronize()
     assert st is new and none is None and torch.equal(O, O2)
     _packed_check(one, O, [1, 1, 1], 0, [None] * 3, list(host_f64(new)), dk ** -0.5, EPS)
+
+
+def test_offsets_of_no_entry_are_refused():
+    """As such, before a state for minus one sequences is made."""
+    print("case: delta packed, no offsets", flush=True)
+    x = _on_gpu(_draw(np.random.default_rng(0), 4, 1, 1, 64, 64))
+    with pytest.raises(ValueError):
+        ttt.gated_delta_packed(*x, _i32([]))
