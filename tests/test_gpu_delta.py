@@ -376,3 +376,33 @@ def test_offsets_of_no_entry_are_refused():
     x = _on_gpu(_draw(np.random.default_rng(0), 4, 1, 1, 64, 64))
     with pytest.raises(ValueError):
         ttt.gated_delta_packed(*x, _i32([]))
+
+
+@pytest.mark.parametrize("beta,common,dk", [(0.01, 0.5, 128), (1e-4, 0.5, 64), (1.0, 3.0, 128)])
+def test_a_long_state_that_forgets_nothing(beta, common, dk):
+    """16384 tokens with gates of 0, against the recurrence in 64 bits. A chunk's products round a state's element 8 times,
+    by a third of the square of half a step each: after 256 chunks sqrt(8 * 256 / 3) * 2^-24 = 1.6e-6 of its size at most, as
+    roundings go their own ways; 2e-6 is what is stated. Tokens one by one round 64 times where a chunk does 8, and are to be
+    no nearer where that counts: a step takes beta of what a state has along its key, 1 / dk of all of it, so a rounding lasts
+    for dk / beta tokens, 100 chunks and more with steps of 0.01 and less, but two with steps of 1, whose 16 roundings are
+    no more than those of u and T themselves, of which single tokens have fewer."""
+    import torch
+    print(f"case: delta packed, long state, {beta} {common} {dk}", flush=True)
+    N, H, dv = 16384, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(N, H, dk, generator=g, device="cuda").bfloat16()
+    k = (torch.randn(N, H, dk, generator=g, device="cuda") + common * torch.randn(H, dk, generator=g, device="cuda")).bfloat16()
+    v = (torch.randn(N, H, dv, generator=g, device="cuda") + 1).bfloat16()
+    gates, steps = torch.zeros(N, H, device="cuda"), torch.full((N, H), beta, device="cuda")
+    _, whole = ttt.gated_delta_packed(q, k, v, gates, steps, _i32([0, N]), norm_eps=EPS)
+    one = torch.zeros(1, H, dk, dv, device="cuda")
+    b, u = steps[0, 0].double(), k.double()
+    u, w = u / ((u * u).sum(-1, keepdim=True) + EPS).sqrt(), v.double()
+    want = torch.zeros(H, dk, dv, dtype=torch.float64, device="cuda")
+    for t in range(N):
+        want += u[t][..., None] * (b * (w[t] - (u[t][..., None] * want).sum(1)))[:, None]
+        ttt.gated_delta_decode(q[t:t + 1], k[t:t + 1], v[t:t + 1], gates[:1], steps[:1], one, norm_eps=EPS)
+    off = lambda x: [float((x[0, h].double() - want[h]).norm() / want[h].norm()) for h in range(H)]  # noqa: E731
+    print(f"  states {max(off(whole)):.2e} off, token by token {max(off(one)):.2e}", flush=True)
+    assert max(off(whole)) <= 2e-6
+    assert beta > 0.01 or max(off(whole)) <= max(off(one))
