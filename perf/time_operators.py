@@ -1,7 +1,7 @@
-"""Times the cases of operators.py on the GPU, or runs one of them under a profiler.
+"""Times the cases of operators.py or more_operators.py on the GPU, or runs one of them under a profiler.
 
-    python perf/time_operators.py [--only NAME,NAME] [--seeds 3] [--plain]
-    rocprofv3 --pmc ... -- python3 perf/time_operators.py --once NAME [--seed 1]
+    python perf/time_operators.py [--of more_operators] [--only NAME,NAME] [--seeds 3] [--plain]
+    rocprofv3 --pmc ... -- python3 perf/time_operators.py [--of more_operators] --once NAME [--seed 1]
 
 For each case and seed: us per call of a loop of calls through the package (host and device side by side),
 and us per call of a replayed HIP graph of calls, the device alone; the least of several rounds. --plain
@@ -9,6 +9,7 @@ times the plain forms in a loop instead. --once prepares one case and calls it f
 else on the GPU but its inputs' making.
 """
 import argparse
+import importlib
 import os
 import sys
 import time
@@ -17,10 +18,9 @@ import torch
 
 sys.path[:0] = [os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                 os.path.dirname(os.path.abspath(__file__))]
-import operators as ops  # noqa: E402
 
 
-def loop_us(state, rounds=7):
+def loop_us(ops, state, rounds=7):
     ops.run(state)
     torch.cuda.synchronize()
     begin = time.perf_counter()
@@ -37,7 +37,7 @@ def loop_us(state, rounds=7):
     return 1e6 * best
 
 
-def graph_us(state, calls=30, rounds=10):
+def graph_us(ops, state, calls=30, rounds=10):
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -61,12 +61,14 @@ def graph_us(state, calls=30, rounds=10):
 
 def main():
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
+    p.add_argument("--of", default="operators", choices=["operators", "more_operators"], help="the file of the cases")
     p.add_argument("--only", default="", help="names of cases, separated by commas")
     p.add_argument("--seeds", type=int, default=3)
     p.add_argument("--plain", action="store_true")
     p.add_argument("--once", default="", metavar="NAME")
     p.add_argument("--seed", type=int, default=1, help="of --once")
     a = p.parse_args()
+    ops = importlib.import_module(a.of)
     ops.own = not a.plain
     cases = {c["name"]: c for c in ops.listed()}
     if a.once:
@@ -78,9 +80,9 @@ def main():
     for name in a.only.split(",") if a.only else cases:
         for seed in range(1, a.seeds + 1):
             state = ops.prepare(cases[name], seed)
-            line = f"{name} seed {seed}: {loop_us(state):.1f} us a call"
+            line = f"{name} seed {seed}: {loop_us(ops, state):.1f} us a call"
             if not a.plain:
-                line += f", {graph_us(state):.2f} us in a graph"
+                line += f", {graph_us(ops, state):.2f} us in a graph"
             print(line, flush=True)
             del state
 
