@@ -23,8 +23,9 @@
 // The paged form is the same kernel with other copies: a wave's 16 rows of a tile lie in one page (a page has at least 16),
 // so a tile takes four page numbers, read through the scalar cache a tile ahead. It costs little: 512 tokens after
 // 15872, 32/8 heads of 128, 122 .. 132 us with the join (1026 TFLOP/s), 4 pieces of 2000 tokens, 32/32 heads of 64,
-// window 2048, 172 .. 186 us. Few rows per key are bound by HBM instead: 16 x 5 tokens on up to 8000, 16/4 heads
-// of 64, 23 us (3.9 TB/s); a piece of 512 tokens and 14 single ones on up to 12000 take both in turn, 171 us.
+// window 2048, 169 .. 186 us. Few rows per key are bound by HBM instead: 16 x 5 tokens on up to 8000, 16/4 heads
+// of 64, 21 .. 25 us by the lengths (72 MB, 3.3 TB/s; without the join 4.2); a piece of 512 tokens and 14 single ones on up
+// to 12000 take both in turn, 138 .. 172 us by the lengths.
 #include <type_traits>
 
 #include "attn.hpp"

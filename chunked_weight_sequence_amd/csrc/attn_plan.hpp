@@ -107,13 +107,15 @@ inline size_t packed_workspace(int n_seq, int Nq, long Nk, int Hq, int Hkv, int 
 // device knows the lengths.
 inline long paged_keys(int n_seq, int max_pages, int page) { return long(n_seq) * max_pages * page; }
 // Pieces that the keys are split into where there are several sequences: lengths and numbers of rows differ then, so
-// a quarter more workgroups than the chip holds at once, twice as many where a sequence has one wave's rows (HBM bounds
-// those: 15 single tokens on up to 12000 87 us in 5 pieces, 78 in 8, 16 on up to 30000 282 in 4, 265 in 8, 32 x 2 on up
-// to 8000 142 in 2, 136 in 4), and the joining weighs half as much again. Best, and what
-// the rule for one sequence takes, of a sweep: 16 x 5 tokens on up to 8000, 16/4 heads of 64, in 12 pieces 27 us, in 3
-// 42 us; 512 tokens and 14 single ones on up to 12000, 32/8 heads of 128, in 2 pieces 164 us (3: 175), whole 258;
-// up to 64 tokens each of 16 on up to 8000 in 3 pieces 77 us, whole 128; 4 x 500 on up to 6000 in 2 119 us, whole 143;
-// 8 x 16 on 4000 in 6 35 us, in 2 43; 2000 tokens and 30 single ones on up to 8000, 16/4 heads of 64, in 3 96 us, whole 122.
+// a quarter more workgroups than the chip holds at once, twice as many where a sequence has one wave's rows, which HBM
+// bounds, and the joining weighs half as much again. Means over three draws of lengths, what is taken (in brackets) and others:
+//   few rows, 32/8 heads of 128: 15 single tokens on up to 12000 (8) 75, 5 84, 10 78 us; 16 on up to 30000 (8) 203, 4 236;
+//   32 x 2 on up to 8000 (4) 129, 2 138, 6 124. 16/4 heads of 64: 16 x 5 on up to 8000 (18) 25, 12 24, 14 26, 8 25; 16 single
+//   on up to 30000 (24) 54, 12 57, 8 62; 15 on up to 12000 (26) 27, 8 29; 4 x 6 on up to 16000 (49) 16.5, 24 18, 12 25
+//   more rows, 32/8 heads of 128: 512 tokens and 14 single ones on up to 12000 (3) 162, 2 157, 4 181, whole 243, and of the same sizes to
+//   the host 16 x up to 64 on up to 8000 (3) 83, 2 101, 4 78, whole 156; 4 x up to 500 on up to 6000 (whole) 143, 2 137, but
+//   4 x 500 on 6000 each (whole) 180, 2 197; 8 x 16 on 4000 (6) 34, 2 41; 2000 tokens and 30 single ones on up to 8000, 16/4 heads
+//   of 64, (3) 95, 4 94, whole 115
 inline int paged_splits(int qt, int n_seq, int Nq, long Nk, int Hq, int Hkv, int dh, int window) {
   if (n_seq == 1) return packed_splits(qt, n_seq, Nq, Nk, Hq, Hkv, dh, window);
   const long keys = packed_keys(n_seq, Nk, window), wgs = packed_wgs(qt, n_seq, Nq, Hq, Hkv);

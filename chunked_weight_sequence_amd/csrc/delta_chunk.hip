@@ -18,10 +18,12 @@
 // Precision: what is not bf16 enters a product as a sum of bf16 planes, S, T, V - e^G K S and u as three each (of the
 // nine products of planes of T and V - .., the six above 2^-24). The state is then off by 2e-7 of its size after 2048
 // tokens, as an fp32 computation is; with two planes of S it was 1.2e-6, with two of the others as well 3 .. 6e-6. O,
-// which is rounded to bf16, takes two planes of S and u, and A in bf16.
+// which is rounded to bf16 (1.66e-3 of its size, root of the mean square), takes two planes of S and u, which do not show
+// in it, and A in bf16: 2.0e-3 with it. A second plane of A would be 6 KB more for each chunk and head to write and read, and
+// 18 KB more of LDS, which two tiles of 128 x 16 leave no room for.
 //
 // What bounds it. k_delta_prepare: memory, for the most part its own 25 KB per 64 tokens and head of T, A and factors
-// beside K and Q (32768 tokens of 32 heads: 419 MB out, 604 in, 203 us, 5 TB/s, as much as a copy reaches; three
+// beside K and Q (32768 tokens of 32 heads: 419 MB out, 604 in, 203 .. 212 us, 5 TB/s, as much as a copy reaches; three
 // planes of T in the order in which the scan's operands lie are more bytes than L would be, but the inverse is computed
 // once for a head and not in each of its column tiles). k_delta_scan: the chain through S, whose 512 chunks follow each
 // other here: 790 .. 870 us, 3450 clocks a chunk at 2.0 GHz; of that 72 matrix instructions of the wave that
@@ -789,9 +791,10 @@ hipError_t launch(const DeltaPackedArgs& a) {
   if (e != hipSuccess) return e;
   const long heads = long(d.n_seq) * d.Hv;
   // 16 columns of a workgroup where each then has one of the card's 256 units to itself, and its carrying waves a SIMD:
-  // 32 where there are more (one fits a unit). 8192 tokens of 128 x 128, both launches with 16 and with 32 columns (with a
-  // fourth meeting): 4 heads 204 and 250 us, 32 heads 261 and 294, 40 heads 510 and 323; 64 x 128: 8 heads 185 and 207,
-  // 32 heads 221 and 237, 40 heads 272 and 268, 64 heads 375 and 331.
+  // 32 where there are more (one fits a unit). 8192 tokens, both launches with 16 and with 32 columns: 128 x 128, 4 heads 193
+  // and 229 us, 32 heads 254 and 280, 40 heads 500 and 314, 128 heads 1366 and 803; 64 x 128, 8 heads 173 and 202, 32 heads 205
+  // and 230, 40 heads 268 and 262, 64 heads 370 and 298; 128 x 64, 64 heads 325 and 357, 96 heads 648 and 419; 11 sequences in
+  // 8192 tokens, 32 heads of 128 x 128, 282 and 200.
   if (heads * (d.dv / 16) <= 256)
     hipLaunchKernelGGL((k_delta_scan<DK, 1>), dim3(unsigned(heads * (d.dv / 16))), dim3(256), 0, d.stream, a);
   else

@@ -6,8 +6,9 @@
 // Bound by HBM: a head's state (64 KB at 128 x 128) is read once and written once. A workgroup takes some
 // columns of one head's state into registers, all of its loads asked for at once; the sums over the rows for
 // S^T k and S^T q are taken together, since o = scale (keep S^T q + (k . q) u), so the workgroup
-// meets once. 2048 heads of 128 x 128 (64 sequences of 32): 51 us, 5.3 TB/s; a copy reaches 4.95. 32 heads: 3.6 us,
-// of which an empty kernel takes 2.
+// meets once. 2048 heads of 128 x 128 (64 sequences of 32): 54 us, 5.0 TB/s, as much as a copy reaches (4.95); 46 where
+// the same pool is taken again and again, of which a part stays in the last cache. 32 heads: 3.7 us, of which an empty
+// kernel takes 2.
 #include "common.hpp"
 #include "launch.hpp"
 
